@@ -68,13 +68,13 @@ typedef int32_t dq_status;
 
 #define DQ_OK 0
 #define DQ_ERR_NULL 1  /* a required pointer is NULL                         */
-#define DQ_ERR_BITS 2  /* bits outside [2, 15]                               */
-#define DQ_ERR_SHAPE 3 /* N, K or M outside the ranges above                 */
+#define DQ_ERR_BITS 2  /* bits outside [2, 15] (integer products: [2, 8])    */
+#define DQ_ERR_SHAPE 3 /* a size, count, stride or group outside its range   */
 #define DQ_ERR_ALIGN 4 /* a pointer is not aligned as required               */
-#define DQ_ERR_DTYPE 5 /* w_dtype is neither DQ_F32 nor DQ_BF16              */
+#define DQ_ERR_DTYPE 5 /* a dtype is neither DQ_F32 nor DQ_BF16              */
 #define DQ_ERR_HIP 6   /* a HIP launch or runtime call failed                */
 #define DQ_ERR_BUDGET 7 /* bit budget below every matrix at its lowest level */
-#define DQ_ERR_VALUE 8 /* a sensitivity, trace, sum or parameter count out of range */
+#define DQ_ERR_VALUE 8 /* a sensitivity, trace, sum, scale or parameter count out of range */
 #define DQ_ERR_IO 9     /* a file could not be opened, written, sized or mapped   */
 #define DQ_ERR_FORMAT 10 /* a file is not a packed-weight file, or is corrupt     */
 
@@ -251,6 +251,136 @@ dq_status dq_gemv_batched(const dq_gemv_item* items, int32_t count, int64_t M, v
  * with fp32 accumulation. */
 dq_status dq_gemm(const uint16_t* x, int64_t M, const uint32_t* packed, const float* scales,
                   int64_t N, int64_t K, int32_t bits, float* y, void* stream);
+
+/* Integer products: activations in 8 bits, one scale per token, times packed
+ * weights of at most 8 bits, one scale per channel ("量化" tutorial,
+ * "量化怎么工作", with one token as the channel of x).
+ *
+ * dq_quantize_tokens: x[M, K] -> per token s[m] = fl32(max_k |x[m,k]| / 127)
+ * (1.0 replaces a zero max before the divide), codes q = clip(rint(fl32(x / s)),
+ * -128, 127), the codes of dq_quantize_pack at bits = 8 as signed bytes, and
+ * their sum.
+ *   x       in   device, [M, K], dtype x_dtype (DQ_F32 or DQ_BF16), 16-byte aligned
+ *   codes   out  device, [M, dq_token_row_bytes(K)] int8, 16-byte aligned; the
+ *                bytes past K are 0
+ *   scales  out  device, [M] fp32
+ *   sums    out  device, [M] int32, sum_k q[m,k]
+ * A token holding a NaN or +-Inf gets scale = quiet NaN and codes 0 (its row of
+ * every product is NaN); one whose max / 127 underflows to 0 is treated like
+ * an all-zero one: scale = fl32(1/127), codes 0.
+ *
+ * dq_gemv_i8 (1 <= M <= 16) and dq_gemm_i8 (any M >= 1):
+ *   y[m,n] = x_scales[m] * scales[n] * sum_k x[m,k] (u[n,k] - z[n])
+ *   x, x_scales, x_sums  in   device, as dq_quantize_tokens writes them (the
+ *                             bytes past K must be 0, the sums those of the codes)
+ *   packed, scales       in   device, from dq_quantize_pack, or from
+ *                             dq_quantize_pack_asym together with zeros;
+ *                             2 <= bits <= 8 (else DQ_ERR_BITS)
+ *   zeros                in   device, [N] int32 in [0, 2^bits - 1]; NULL: z = 2^(bits-1)
+ *   y                    out  device, [M, N], dtype y_dtype (DQ_F32 or DQ_BF16),
+ *                             aligned to its elements
+ * The sum is exact (int32), so y differs from the formula by three fp32
+ * roundings (and one to bf16).  K <= DQ_MAX_K_I8 keeps the sum inside int32
+ * (else DQ_ERR_SHAPE).  scales, x_scales, x_sums and zeros: 4-byte aligned. */
+#define DQ_MAX_K_I8 65536
+#define DQ_MAX_BITS_I8 8
+
+/* Bytes of one token's codes: K rounded up to a multiple of 128.  Returns 0
+ * when K is outside [1, DQ_MAX_K_I8].  Host-only, no HIP call. */
+size_t dq_token_row_bytes(int64_t K);
+dq_status dq_quantize_tokens(const void* x, int32_t x_dtype, int64_t M, int64_t K, int8_t* codes,
+                             float* scales, int32_t* sums, void* stream);
+dq_status dq_gemv_i8(const int8_t* x, const float* x_scales, const int32_t* x_sums, int64_t M,
+                     const uint32_t* packed, const float* scales, const int32_t* zeros, int64_t N,
+                     int64_t K, int32_t bits, void* y, int32_t y_dtype, void* stream);
+dq_status dq_gemm_i8(const int8_t* x, const float* x_scales, const int32_t* x_sums, int64_t M,
+                     const uint32_t* packed, const float* scales, const int32_t* zeros, int64_t N,
+                     int64_t K, int32_t bits, void* y, int32_t y_dtype, void* stream);
+
+/* A key/value cache held in 4 bits.  A head's vector of D dimensions is
+ * quantized as a row of dq_quantize_pack_group with bits = 4 and groups of g
+ * dimensions (its scale, zero and non-finite rules); codes are offset binary, u =
+ * q + 8, eight to a 32-bit word from the low bits up.  The cache is a set of
+ * pages of P tokens; the caller owns its four arrays:
+ *   k_codes, v_codes    device, [pages, kv_heads, P, D / 8] uint32, 16-byte aligned
+ *   k_scales, v_scales  device, [pages, kv_heads, D / g, P] fp32, 16-byte aligned
+ * head_dim D: 64, 128 or 256; page_size P: a power of two, 16 .. 256; group g:
+ * 32, 64 or 128, at most D; 1 <= kv_heads <= DQ_CACHE4_MAX_HEADS; 1 <= pages <= 2^31-1
+ * (else DQ_ERR_SHAPE).  Inside a row the codes lie as the matrix cores take them:
+ *   keys:   dimension 32 i + 8 r + e is code e of word r (D / 32) + i, r = 0 .. 3, e = 0 .. 7;
+ *   values: dimension 16 j + c is code c (D / 16) + j of the row, c = 0 .. 15.
+ *
+ * A call works on `count` sequences (1 .. DQ_CACHE4_MAX_COUNT).  Token row t of
+ * the call's arrays belongs to sequence b where starts[b] <= t < starts[b+1];
+ * sequence b's rows are the last starts[b+1] - starts[b] of its lens[b] cached
+ * positions, and position p lies in page table[b][p / P].  starts, lens and
+ * table are read on the device: rows of no sequence are left as they were;
+ * positions that the cache does not hold (below 0, past the table, in a page
+ * outside the cache) are skipped by append, read as NaN, and make every query
+ * that sees them NaN.  Nothing outside the arrays is ever touched. */
+#define DQ_CACHE4_MAX_HEADS 1024
+#define DQ_CACHE4_MAX_COUNT 65535
+typedef struct {
+    uint32_t* k_codes;
+    uint32_t* v_codes;
+    float* k_scales;
+    float* v_scales;
+    int64_t pages;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t page_size;
+    int32_t group;
+} dq_cache4;
+
+typedef struct {
+    const int32_t* starts; /* device, [count + 1], not decreasing, 4-byte aligned      */
+    const int32_t* lens;   /* device, [count] cached tokens, the call's own included   */
+    const int32_t* table;  /* device, [count, table_width] pages in order of position  */
+    int64_t table_width;   /* pages per sequence, 1 .. 2^24 (unused entries: any value) */
+    int64_t count;
+} dq_cache4_batch;
+
+/* Quantize the call's tokens into the cache.
+ *   k, v       in  device, [tokens, kv_heads, D] of dtype (DQ_F32 or DQ_BF16),
+ *                  16-byte aligned; a token's heads are contiguous, tokens lie
+ *                  k_stride / v_stride elements apart (multiples of 8, at least
+ *                  kv_heads * D: slices of one projection's output serve as they are)
+ *   tokens         rows of k and v, 1 .. 2^31-1
+ * No two rows of a call may land on the same position of the same page. */
+dq_status dq_cache4_append(const dq_cache4* cache, const dq_cache4_batch* batch, const void* k,
+                           const void* v, int32_t dtype, int64_t tokens, int64_t k_stride,
+                           int64_t v_stride, void* stream);
+
+/* The inverse: fl32(q * s), rounded to bf16 for DQ_BF16, of the same tokens (all
+ * of a sequence's cached tokens: starts with starts[b+1] - starts[b] = lens[b]).
+ *   k, v  out  device, [tokens, kv_heads, D] contiguous, 16-byte aligned */
+dq_status dq_cache4_read(const dq_cache4* cache, const dq_cache4_batch* batch, void* k, void* v,
+                         int32_t dtype, int64_t tokens, void* stream);
+
+/* Causal attention of the call's tokens over the cache (append them first):
+ *   out[t,h] = sum_p w_p v[p] / sum_p w_p,  w_p = exp(scale * q[t,h] . k[p] - max),
+ * over the positions p up to t's own, k and v the dequantized vectors of kv
+ * head h / (q_heads / kv_heads).  A token that sees no position gives zeros.
+ *   q       in   device, [tokens, q_heads, D] bf16 bits, 16-byte aligned; tokens lie
+ *                q_stride elements apart (a multiple of 8, at least q_heads * D)
+ *   q_heads      a multiple of kv_heads, at most DQ_CACHE4_MAX_HEADS
+ *   scale        factor of the dot products, finite
+ *   max_q, max_len  the most tokens of a sequence in this call and the most
+ *                cached ones, at least 1: they size the launch (a larger sequence
+ *                is served too, only slower)
+ *   out     out  device, [tokens, q_heads, D] bf16 bits, contiguous, 16-byte aligned
+ *   workspace    device, 16-byte aligned, dq_cache4_attention_workspace bytes for the
+ *                same arguments (may be NULL where that is 0); the caller's, free
+ *                again when the call's work is done: calls that may run at the
+ *                same time need one each
+ * Codes, dot products and the softmax's statistics are exact or fp32; each
+ * weight times its value's scale is rounded once to 11 significant bits. */
+size_t dq_cache4_attention_workspace(const dq_cache4* cache, int64_t count, int64_t tokens,
+                                     int32_t q_heads, int64_t max_q, int64_t max_len);
+dq_status dq_cache4_attention(const dq_cache4* cache, const dq_cache4_batch* batch,
+                              const uint16_t* q, int64_t tokens, int64_t q_stride, int32_t q_heads,
+                              float scale, int64_t max_q, int64_t max_len, uint16_t* out,
+                              void* workspace, size_t workspace_bytes, void* stream);
 
 /* Not a step of the method: a plain streaming read of `bytes` bytes, the
  * yardstick for the bandwidth-bound entry points above (the rate a kernel

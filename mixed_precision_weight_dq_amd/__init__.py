@@ -18,6 +18,10 @@ kernels behind the C ABI declared in ``include/dq.h``):
   the asymmetric (zero-point) variant on torch tensors.
 * ``quantize_pack_group``, ``unpack_group``, ``gemv_group``, ``gemm_group``
   -- group-wise scales (one per g codes of a row) on torch tensors.
+* ``quantize_tokens``, ``gemv_i8``, ``gemm_i8`` -- int8 activations (one scale
+  per token) and their integer products with packed weights of at most 8 bits.
+* ``Cache4``, ``cache4_append``, ``cache4_read``, ``cache4_attention`` -- a paged
+  key/value cache held in 4 bits: fill it, read it back, attend over it.
 * ``sensitivity``, ``allocate_bits`` -- the host-side allocation calls on
   numpy arrays (the recipe: one bit width per matrix).
 * ``write_packed_file``, ``PackedFile`` -- the on-disk packed-weight format
@@ -45,7 +49,11 @@ __all__ = [
     "dq_gemv_asym", "dq_gemm_asym", "quantize_pack_asym", "unpack_asym", "gemv_asym",
     "gemm_asym", "dq_quantize_pack_group", "dq_unpack_group", "dq_gemv_group", "dq_gemm_group",
     "quantize_pack_group", "unpack_group", "gemv_group", "gemm_group", "DQGemvItem",
-    "GEMV_BATCH_MAX", "dq_gemv_batched", "gemv_batched",
+    "GEMV_BATCH_MAX", "dq_gemv_batched", "gemv_batched", "dq_token_row_bytes",
+    "dq_quantize_tokens", "dq_gemv_i8", "dq_gemm_i8", "quantize_tokens", "gemv_i8", "gemm_i8",
+    "DQCache4", "DQCache4Batch", "dq_cache4_append", "dq_cache4_read",
+    "dq_cache4_attention_workspace", "dq_cache4_attention", "Cache4", "cache4_append",
+    "cache4_read", "cache4_attention",
 ]
 
 (DQ_OK, DQ_ERR_NULL, DQ_ERR_BITS, DQ_ERR_SHAPE, DQ_ERR_ALIGN, DQ_ERR_DTYPE, DQ_ERR_HIP,
@@ -74,6 +82,21 @@ class DQGemvItem(ctypes.Structure):
 
 
 GEMV_BATCH_MAX = 32
+
+
+class DQCache4(ctypes.Structure):
+    """``dq_cache4`` of include/dq.h."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("group", ctypes.c_int32)]
+
+
+class DQCache4Batch(ctypes.Structure):
+    """``dq_cache4_batch`` of include/dq.h."""
+    _fields_ = [("starts", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("table_width", ctypes.c_int64), ("count", ctypes.c_int64)]
 
 
 class DQError(RuntimeError):
@@ -127,6 +150,23 @@ def load():
     lib.dq_gemv_group.restype = st
     lib.dq_gemm_group.argtypes = [vp, i64, vp, vp, i64, i64, i32, i64, vp, vp]
     lib.dq_gemm_group.restype = st
+    lib.dq_token_row_bytes.argtypes = [i64]
+    lib.dq_token_row_bytes.restype = ctypes.c_size_t
+    lib.dq_quantize_tokens.argtypes = [vp, i32, i64, i64, vp, vp, vp, vp]
+    lib.dq_quantize_tokens.restype = st
+    for fn in (lib.dq_gemv_i8, lib.dq_gemm_i8):
+        fn.argtypes = [vp, vp, vp, i64, vp, vp, vp, i64, i64, i32, vp, i32, vp]
+        fn.restype = st
+    c4, c4b = ctypes.POINTER(DQCache4), ctypes.POINTER(DQCache4Batch)
+    lib.dq_cache4_append.argtypes = [c4, c4b, vp, vp, i32, i64, i64, i64, vp]
+    lib.dq_cache4_append.restype = st
+    lib.dq_cache4_read.argtypes = [c4, c4b, vp, vp, i32, i64, vp]
+    lib.dq_cache4_read.restype = st
+    lib.dq_cache4_attention_workspace.argtypes = [c4, i64, i64, i32, i64, i64]
+    lib.dq_cache4_attention_workspace.restype = ctypes.c_size_t
+    lib.dq_cache4_attention.argtypes = [c4, c4b, vp, i64, i64, i32, ctypes.c_float, i64, i64, vp,
+                                        vp, ctypes.c_size_t, vp]
+    lib.dq_cache4_attention.restype = st
     fp = ctypes.POINTER(DQFileMatrix)
     lib.dq_file_write.argtypes = [ctypes.c_char_p, fp, i64]
     lib.dq_file_write.restype = st
@@ -249,6 +289,49 @@ def dq_gemv_batched(items: int, count: int, M: int, stream: int = 0) -> int:
 def dq_gemm(x: int, M: int, packed: int, scales: int, N: int, K: int, bits: int, y: int,
             stream: int = 0) -> int:
     return int(load().dq_gemm(x, M, packed, scales, N, K, bits, y, stream))
+
+
+def dq_token_row_bytes(K: int) -> int:
+    return int(load().dq_token_row_bytes(K))
+
+
+def dq_quantize_tokens(x: int, x_dtype: int, M: int, K: int, codes: int, scales: int, sums: int,
+                       stream: int = 0) -> int:
+    return int(load().dq_quantize_tokens(x, x_dtype, M, K, codes, scales, sums, stream))
+
+
+def dq_gemv_i8(x: int, x_scales: int, x_sums: int, M: int, packed: int, scales: int, zeros: int,
+               N: int, K: int, bits: int, y: int, y_dtype: int, stream: int = 0) -> int:
+    return int(load().dq_gemv_i8(x, x_scales, x_sums, M, packed, scales, zeros, N, K, bits, y,
+                                 y_dtype, stream))
+
+
+def dq_gemm_i8(x: int, x_scales: int, x_sums: int, M: int, packed: int, scales: int, zeros: int,
+               N: int, K: int, bits: int, y: int, y_dtype: int, stream: int = 0) -> int:
+    return int(load().dq_gemm_i8(x, x_scales, x_sums, M, packed, scales, zeros, N, K, bits, y,
+                                 y_dtype, stream))
+
+
+def dq_cache4_append(cache: DQCache4, batch: DQCache4Batch, k: int, v: int, dtype: int,
+                     tokens: int, k_stride: int, v_stride: int, stream: int = 0) -> int:
+    return int(load().dq_cache4_append(cache, batch, k, v, dtype, tokens, k_stride, v_stride, stream))
+
+
+def dq_cache4_read(cache: DQCache4, batch: DQCache4Batch, k: int, v: int, dtype: int, tokens: int,
+                   stream: int = 0) -> int:
+    return int(load().dq_cache4_read(cache, batch, k, v, dtype, tokens, stream))
+
+
+def dq_cache4_attention_workspace(cache: DQCache4, count: int, tokens: int, q_heads: int,
+                                  max_q: int, max_len: int) -> int:
+    return int(load().dq_cache4_attention_workspace(cache, count, tokens, q_heads, max_q, max_len))
+
+
+def dq_cache4_attention(cache: DQCache4, batch: DQCache4Batch, q: int, tokens: int, q_stride: int,
+                        q_heads: int, scale: float, max_q: int, max_len: int, out: int,
+                        workspace: int, workspace_bytes: int, stream: int = 0) -> int:
+    return int(load().dq_cache4_attention(cache, batch, q, tokens, q_stride, q_heads, scale, max_q,
+                                          max_len, out, workspace, workspace_bytes, stream))
 
 
 def dq_stream_read(buf: int, nbytes: int, partial: int, nparts: int, stream: int = 0) -> int:
@@ -634,6 +717,243 @@ def gemv_batched(items, ys=None):
 def gemm(x, packed, scales, K: int, bits: int, y=None):
     """y[M, N] = x . dequant(W)^T on the bf16 matrix cores (any M >= 1)."""
     return _matmul(dq_gemm, "dq_gemm", x, packed, scales, K, bits, y)
+
+
+def _dtype_code(dtype, name):
+    torch = _torch()
+    if dtype == torch.float32:
+        return DQ_F32
+    if dtype == torch.bfloat16:
+        return DQ_BF16
+    raise TypeError("%s must be torch.float32 or torch.bfloat16 (got %s)" % (name, dtype))
+
+
+def _launch(where, tensors, fn, *args):
+    """fn(*args, stream) on the tensors' device: all on one GPU, its current stream."""
+    torch = _torch()
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError("%s: all tensors must be on one GPU (%s and %s)" % (where, dev, t.device))
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if dev.index == torch.cuda.current_device():
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, stream)
+    _check(int(status), where)
+
+
+def quantize_tokens(x, codes=None, scales=None, sums=None):
+    """x[M, K] (float32 or bfloat16, on the GPU) -> (codes int8 [M, K rounded up to 128],
+    scales float32 [M], sums int32 [M]): one symmetric int8 scale per token, and each
+    token's sum of codes."""
+    torch = _torch()
+    _need(x, "x", (torch.float32, torch.bfloat16), 2)
+    M, K = x.shape
+    pitch = dq_token_row_bytes(K)
+    if pitch == 0:
+        raise DQError(DQ_ERR_SHAPE, "quantize_tokens")
+    if codes is None:
+        codes = torch.empty((M, pitch), dtype=torch.int8, device=x.device)
+    if scales is None:
+        scales = torch.empty((M,), dtype=torch.float32, device=x.device)
+    if sums is None:
+        sums = torch.empty((M,), dtype=torch.int32, device=x.device)
+    _need(codes, "codes", (torch.int8,), 2)
+    _need(scales, "scales", (torch.float32,), 1)
+    _need(sums, "sums", (torch.int32,), 1)
+    if tuple(codes.shape) != (M, pitch) or scales.shape[0] != M or sums.shape[0] != M:
+        raise ValueError("codes must be [M, %d], scales and sums [M]" % pitch)
+    _launch("dq_quantize_tokens", (x, codes, scales, sums), load().dq_quantize_tokens, x.data_ptr(),
+            DQ_BF16 if x.dtype == torch.bfloat16 else DQ_F32, M, K, codes.data_ptr(),
+            scales.data_ptr(), sums.data_ptr())
+    return codes, scales, sums
+
+
+def _matmul_i8(fn, name, codes, x_scales, x_sums, packed, scales, K, bits, zeros, y, dtype):
+    torch = _torch()
+    _need(codes, "codes", (torch.int8,), 2)
+    _need(x_scales, "x_scales", (torch.float32,), 1)
+    _need(x_sums, "x_sums", (torch.int32,), 1)
+    _need(packed, "packed", (torch.int32,), 2)
+    _need(scales, "scales", (torch.float32,), 1)
+    if zeros is not None:
+        _need(zeros, "zeros", (torch.int32,), 1)
+    M, N = codes.shape[0], packed.shape[0]
+    if K < 1 or K > 65536:
+        raise DQError(DQ_ERR_SHAPE, name)
+    if (codes.shape[1] != -(-K // 128) * 128 or x_scales.shape[0] != M or x_sums.shape[0] != M
+            or packed.shape[1] != packed_row_bytes(K, bits) // 4 or scales.shape[0] != N
+            or (zeros is not None and zeros.shape[0] != N)):
+        raise ValueError("shape mismatch between codes, x_scales, x_sums, packed, scales, zeros, K and bits")
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.float32 if dtype is None else dtype, device=codes.device)
+    elif dtype is not None and y.dtype != dtype:
+        raise TypeError("y is %s, dtype %s" % (y.dtype, dtype))
+    kind = _dtype_code(y.dtype, "y")
+    _need(y, "y", (torch.float32, torch.bfloat16), 2)
+    if tuple(y.shape) != (M, N):
+        raise ValueError("y must be [M, N]")
+    _launch(name, (codes, x_scales, x_sums, packed, scales, zeros, y), fn, codes.data_ptr(),
+            x_scales.data_ptr(), x_sums.data_ptr(), M, packed.data_ptr(), scales.data_ptr(),
+            zeros.data_ptr() if zeros is not None else None, N, K, bits, y.data_ptr(), kind)
+    return y
+
+
+def gemv_i8(codes, x_scales, x_sums, packed, scales, K: int, bits: int, zeros=None, y=None,
+            dtype=None):
+    """y[M, N] = x_scales * scales * codes . (u - z)^T for 1 <= M <= 16: ``quantize_tokens``'
+    outputs times weights from ``quantize_pack`` (or, with ``zeros``, ``quantize_pack_asym``) of
+    at most 8 bits; y float32 (the default) or bfloat16."""
+    return _matmul_i8(load().dq_gemv_i8, "dq_gemv_i8", codes, x_scales, x_sums, packed, scales, K,
+                      bits, zeros, y, dtype)
+
+
+def gemm_i8(codes, x_scales, x_sums, packed, scales, K: int, bits: int, zeros=None, y=None,
+            dtype=None):
+    """The same for any M >= 1."""
+    return _matmul_i8(load().dq_gemm_i8, "dq_gemm_i8", codes, x_scales, x_sums, packed, scales, K,
+                      bits, zeros, y, dtype)
+
+
+class Cache4:
+    """A paged key/value cache in 4 bits: k_codes, v_codes int32 [pages, kv_heads, P, D / 8]
+    and k_scales, v_scales float32 [pages, kv_heads, D / g, P], contiguous GPU tensors that
+    the caller owns (``Cache4.empty`` allocates them).  The sequences of a call are given by
+    ``starts`` int32 [count + 1] (token rows of each sequence), ``lens`` int32 [count] (cached
+    tokens, the call's own included) and ``table`` int32 [count, width] (pages)."""
+
+    def __init__(self, k_codes, v_codes, k_scales, v_scales):
+        torch = _torch()
+        for t, name in ((k_codes, "k_codes"), (v_codes, "v_codes")):
+            _need(t, name, (torch.int32,), 4)
+        for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+            _need(t, name, (torch.float32,), 4)
+        pages, heads, P, words = k_codes.shape
+        groups = k_scales.shape[2]
+        if (v_codes.shape != k_codes.shape or v_scales.shape != k_scales.shape
+                or tuple(k_scales.shape) != (pages, heads, groups, P)
+                or groups < 1 or words * 8 % groups):
+            raise ValueError("codes must be [pages, kv_heads, P, D / 8], scales [pages, kv_heads, D / g, P]")
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self.pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, P, words * 8
+        self.group = words * 8 // groups
+        self._c = DQCache4(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
+                           v_scales.data_ptr(), pages, heads, self.head_dim, P, self.group)
+
+    @classmethod
+    def empty(cls, pages: int, kv_heads: int, head_dim: int, page_size: int = 64, group: int = 32,
+              device="cuda"):
+        torch = _torch()
+        if (head_dim not in (64, 128, 256) or group not in (32, 64, 128) or group > head_dim
+                or not 16 <= page_size <= 256 or page_size & (page_size - 1)):
+            raise DQError(DQ_ERR_SHAPE, "Cache4.empty")
+        codes = (pages, kv_heads, page_size, head_dim // 8)
+        scales = (pages, kv_heads, head_dim // group, page_size)
+        return cls(*(torch.zeros(codes, dtype=torch.int32, device=device) for _ in range(2)),
+                   *(torch.zeros(scales, dtype=torch.float32, device=device) for _ in range(2)))
+
+    @property
+    def tensors(self):
+        return self.k_codes, self.v_codes, self.k_scales, self.v_scales
+
+
+def _batch4(starts, lens, table):
+    torch = _torch()
+    _need(starts, "starts", (torch.int32,), 1)
+    _need(lens, "lens", (torch.int32,), 1)
+    _need(table, "table", (torch.int32,), 2)
+    count = lens.shape[0]
+    if starts.shape[0] != count + 1 or table.shape[0] != count:
+        raise ValueError("starts must be [count + 1], lens [count], table [count, width]")
+    return DQCache4Batch(starts.data_ptr(), lens.data_ptr(), table.data_ptr(), table.shape[1], count)
+
+
+def _token_rows(t, name, heads, D, dtypes):
+    """Checks t [tokens, heads, D] with contiguous heads; returns its token stride."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.device.type != "cuda":
+        raise ValueError("%s must be a GPU tensor (got %s)" % (name, t.device))
+    if t.dtype not in dtypes:
+        raise TypeError("%s dtype %s not in %s" % (name, t.dtype, dtypes))
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+        raise ValueError("%s must be [tokens, %d, %d]" % (name, heads, D))
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+        raise ValueError("%s: the heads of a token must be contiguous" % name)
+    return t.stride(0) if t.shape[0] > 1 else heads * D
+
+
+def cache4_append(cache: Cache4, k, v, starts, lens, table) -> None:
+    """Quantize k, v [tokens, kv_heads, D] (float32 or bfloat16; tokens may be strided) into
+    the pages of their positions."""
+    torch = _torch()
+    kinds = (torch.float32, torch.bfloat16)
+    ks = _token_rows(k, "k", cache.kv_heads, cache.head_dim, kinds)
+    vs = _token_rows(v, "v", cache.kv_heads, cache.head_dim, kinds)
+    if k.dtype != v.dtype or k.shape[0] != v.shape[0]:
+        raise ValueError("k and v must have one dtype and one token count")
+    batch = _batch4(starts, lens, table)
+    _launch("dq_cache4_append", (*cache.tensors, k, v, starts, lens, table),
+            load().dq_cache4_append, cache._c, batch, k.data_ptr(), v.data_ptr(),
+            _dtype_code(k.dtype, "k"), k.shape[0], ks, vs)
+
+
+def cache4_read(cache: Cache4, tokens: int, starts, lens, table, dtype=None, k=None, v=None):
+    """The dequantized (k, v) [tokens, kv_heads, D] of a call's tokens, float32 (the default)
+    or bfloat16; rows of no sequence are left as they were."""
+    torch = _torch()
+    kind = torch.float32 if dtype is None else dtype
+    code = _dtype_code(kind, "dtype")
+    shape = (tokens, cache.kv_heads, cache.head_dim)
+    if k is None:
+        k = torch.empty(shape, dtype=kind, device=cache.k_codes.device)
+    if v is None:
+        v = torch.empty(shape, dtype=kind, device=cache.k_codes.device)
+    for t, name in ((k, "k"), (v, "v")):
+        _need(t, name, (kind,), 3)
+        if tuple(t.shape) != shape:
+            raise ValueError("%s must be [tokens, kv_heads, D]" % name)
+    batch = _batch4(starts, lens, table)
+    _launch("dq_cache4_read", (*cache.tensors, k, v, starts, lens, table), load().dq_cache4_read,
+            cache._c, batch, k.data_ptr(), v.data_ptr(), code, tokens)
+    return k, v
+
+
+def cache4_attention(cache: Cache4, q, starts, lens, table, scale=None, max_q=None, max_len=None,
+                     out=None, workspace=None):
+    """Causal attention of q [tokens, q_heads, D] (bfloat16; tokens may be strided) over the
+    cache, its tokens' keys and values already appended.  scale: D ** -0.5 unless given.
+    max_q / max_len: the most new / cached tokens of a sequence, for sizing the launch
+    (default: the whole call / the whole table).  out bfloat16 [tokens, q_heads, D];
+    workspace: uint8 tensor to use instead of a new one."""
+    torch = _torch()
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a [tokens, q_heads, D] tensor")
+    tokens, heads, D = q.shape
+    stride = _token_rows(q, "q", heads, cache.head_dim, (torch.bfloat16,))
+    batch = _batch4(starts, lens, table)
+    if out is None:
+        out = torch.empty((tokens, heads, D), dtype=torch.bfloat16, device=q.device)
+    _need(out, "out", (torch.bfloat16,), 3)
+    if tuple(out.shape) != (tokens, heads, D):
+        raise ValueError("out must be [tokens, q_heads, D]")
+    max_q = tokens if max_q is None else int(max_q)
+    max_len = table.shape[1] * cache.page_size if max_len is None else int(max_len)
+    scale = D ** -0.5 if scale is None else float(scale)
+    lib = load()
+    need = lib.dq_cache4_attention_workspace(cache._c, batch.count, tokens, heads, max_q, max_len)
+    if workspace is None:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=q.device) if need else None
+    else:
+        _need(workspace, "workspace", (torch.uint8,), 1)
+    _launch("dq_cache4_attention", (*cache.tensors, q, out, starts, lens, table, workspace),
+            lib.dq_cache4_attention, cache._c, batch, q.data_ptr(), tokens, stride, heads, scale,
+            max_q, max_len, out.data_ptr(), workspace.data_ptr() if workspace is not None else None,
+            workspace.shape[0] if workspace is not None else 0)
+    return out
 
 
 def stream_read(buf, nparts: int, partial=None):
