@@ -15,6 +15,8 @@
 //   * p * (value scale) is rounded once, to fp16, after multiplication by a
 //     power of two that puts the largest value scale seen so far in [2^14,
 //     2^15): relative error 2^-11 down to 2^-29 of the largest.
+#include <type_traits>
+
 #include "cache4.hpp"
 #include "common.hpp"
 #include "launch_serving.hpp"
@@ -54,16 +56,39 @@ __device__ __forceinline__ f16x8_t word_codes(uint32_t w)
     return __builtin_bit_cast(f16x8_t, (u32x4_t){low_codes(w), high_codes(w), low_codes(x), high_codes(x)});
 }
 
-// max over the four lanes l, l ^ 16, l ^ 32, l ^ 48
+// Reductions over the four lanes of a row (l, l ^ 16, l ^ 32, l ^ 48): a swap
+// of 32-lane halves, then of odd and even 16-lane rows, each leaving the pair's
+// two values in every lane of the pair.
+__device__ __forceinline__ void row_pair(float v, bool half, float& x, float& y)
+{
+    typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+    const uint32_t u = __float_as_uint(v);
+    const u32x2_t r = half ? __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(u, u, false, false))
+                           : __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane16_swap(u, u, false, false));
+    x = __uint_as_float(r.x);
+    y = __uint_as_float(r.y);
+}
 __device__ __forceinline__ float row_max(float v)
 {
-    v = fmaxf(v, __shfl_xor(v, 16, kWave));
-    return fmaxf(v, __shfl_xor(v, 32, kWave));
+    float x, y;
+    row_pair(v, true, x, y);
+    row_pair(fmaxf(x, y), false, x, y);
+    return fmaxf(x, y);
 }
 __device__ __forceinline__ float row_sum(float v)
 {
-    v += __shfl_xor(v, 16, kWave);
-    return v + __shfl_xor(v, 32, kWave);
+    float x, y;
+    row_pair(v, true, x, y);
+    row_pair(x + y, false, x, y);
+    return x + y;
+}
+// max over the wave of non-negative values (NaN counts as nothing)
+__device__ __forceinline__ float wave_max_abs(float v)
+{
+    v = fmaxf(v, 0.0f);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, kWave));
+    return row_max(v);
 }
 
 // 2^n for n clamped to fp32's normal range
@@ -87,65 +112,137 @@ struct AttnArgs {
     int64_t tokens;
     int32_t q_heads;
     float scale_log2;
+    int32_t row_tiles;  // 16-row tiles per (sequence, kv head) that the grid has
+    int32_t splits;     // shares of the positions per tile
+    float* part;        // splits > 1: normalised partial outputs [unit, split, 16, D]
+    float2* part_ml;    // and their maxima and sums [unit, split, 16]
 };
 
+constexpr int kWaves = 4;
+constexpr int kStep = 32;                   // positions per wave and step
+constexpr int kMinShare = kWaves * kStep;   // positions of a share, at least
+
+// Positions per share of a row tile that sees positions [0, end).
+__device__ __forceinline__ int64_t share_of(int64_t end, int splits)
+{
+    int64_t n = (end + splits - 1) / splits;
+    n = (n + kStep - 1) & ~(int64_t)(kStep - 1);
+    return n < kMinShare ? kMinShare : n;
+}
+
+// What a workgroup knows of its sequence.
+struct Rows {
+    int64_t first, nq, len;  // first token row, new tokens, cached tokens
+    bool bad;                // a length past the table
+    int per;                 // query heads of a kv head
+    __device__ __forceinline__ int64_t rows() const { return nq * per; }
+    // positions seen by the last row of the tile that starts at row r0
+    __device__ __forceinline__ int64_t end(int64_t r0) const
+    {
+        const int64_t last = r0 + 15 < rows() ? r0 + 15 : rows() - 1;
+        return len - nq + last / per + 1;
+    }
+};
+
+__device__ __forceinline__ Rows rows_of(const AttnArgs& a, int64_t b)
+{
+    Rows r;
+    cache4_rows(a.bt, b, a.tokens, r.first, r.nq);
+    r.len = a.bt.lens[b];
+    r.bad = r.len > a.bt.width << a.c.page_shift;
+    if (r.len < 0 || r.bad) r.len = 0;
+    r.per = a.q_heads / a.c.heads;
+    return r;
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float a, float b)
+{
+    return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)a) |
+           ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)b) << 16);
+}
+
+// One workgroup of four waves per (16-row tile, share of the positions, kv
+// head, sequence): wave w takes steps w, w + 4, ... of the share, and the four
+// partial results are joined through LDS in a fixed order.  A tile whose
+// positions are one share is written out here; otherwise the shares are joined
+// by cache4_join_kernel, in order.
+//
+// A step's loads are issued one step ahead, its page numbers two.  Codes come
+// straight into the registers that expand them; a step's scales come one float
+// per lane and are handed round through wave-private LDS (each lane needs the
+// scales of 8 positions and every group).
 template <int D, int G>
-__global__ __launch_bounds__(kWave) void cache4_attention_kernel(AttnArgs a)
+__global__ __launch_bounds__(kWaves* kWave) void cache4_attention_kernel(AttnArgs a)
 {
     constexpr int NC = D / 32;  // 32-dimension steps of a dot product
     constexpr int NG = D / G;   // groups of a head
     constexpr int GC = G / 32;  // steps of a group
     constexpr int NT = D / 16;  // 16-dimension tiles of the output
     constexpr int VW = D / 128 > 0 ? D / 128 : 1;  // value words a lane reads of a token
-    const int lane = threadIdx.x;
+    constexpr int NL = (NG + 3) / 4;               // scale loads per 16 positions
+    constexpr int SC = 4 * NL * 16;                // floats of 16 positions' scales in LDS
+    __shared__ __attribute__((aligned(16))) float scales[kWaves][2][2 * SC];  // keys, values
+    __shared__ __attribute__((aligned(16))) float join[kWaves / 2][(NT * 4 + 3) * kWave];
+
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int r16 = lane & 15;
     const int kg = lane >> 4;
     const int64_t b = blockIdx.z;
     const int kvh = blockIdx.y;
-    const int per = a.q_heads / a.c.heads;  // query heads of a kv head
+    const int split = blockIdx.x % a.splits;
     const int shift = a.c.page_shift;
     const int64_t P = 1LL << shift;
+    const Rows rw = rows_of(a, b);
+    const int64_t rows = rw.rows();
 
-    int64_t first, nq;
-    cache4_rows(a.bt, b, a.tokens, first, nq);
-    const int64_t rows = nq * per;
-    int64_t len = a.bt.lens[b];
-    const bool bad_len = len > a.bt.width << shift;
-    if (len < 0 || bad_len) len = 0;
+    // places of this lane's data relative to a 16-position tile of one head
+    const uint32_t k_lane = r16 * (D / 8) + kg * NC;
+    const uint32_t v_lane = 4 * kg * (D / 8) * (D == 64 ? 2 : 1) + r16 * VW;
+    uint32_t s_lane[NL];
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        const int g = 4 * i + kg < NG ? 4 * i + kg : NG - 1;
+        s_lane[i] = ((uint32_t)g << shift) + r16;
+    }
 
-    for (int64_t r0 = (int64_t)blockIdx.x * 16; r0 < rows; r0 += (int64_t)gridDim.x * 16) {
+    // tiles past the grid's are one share each, walked by the grid's last tile
+    for (int64_t tile = blockIdx.x / a.splits; tile * 16 < rows; ++tile) {
+        const bool extra = tile >= a.row_tiles;
+        if (tile > (int64_t)(blockIdx.x / a.splits) && !extra) break;
+        if (extra && split != 0) break;
+        const int64_t r0 = tile * 16;
         const int64_t row = r0 + r16;
         const bool live = row < rows;
-        const int64_t qi = live ? row / per : 0;
-        const int head = kvh * per + (live ? (int)(row % per) : 0);
-        const int64_t limit = live ? len - nq + qi : -1;  // last position the row sees
-        const int64_t last_row = r0 + 15 < rows ? r0 + 15 : rows - 1;
-        const int64_t end = len - nq + last_row / per + 1;
+        const int64_t qi = live ? row / rw.per : 0;
+        const int head = kvh * rw.per + (live ? (int)(row % rw.per) : 0);
+        const int64_t limit = live ? rw.len - rw.nq + qi : -1;  // last position the row sees
+        const int64_t end = rw.end(r0);
+        const int64_t all_see = rw.len - rw.nq + r0 / rw.per + 1;  // seen by every live row
+        const int64_t share = extra ? (end > 0 ? end : 1) : share_of(end, a.splits);
+        const bool whole = end <= share;  // one share: no joining
+        const int64_t begin = extra ? 0 : share * split;
+        const int64_t stop = begin + share < end ? begin + share : end;
+        if (begin >= end && split != 0) break;  // nothing for this share, nor for an extra tile
 
-        // q row -> fp16 operands, scaled by a power of two
-        const uint16_t* qp = a.q + (first + qi) * a.q_stride + (int64_t)head * D + 8 * kg;
+        // q row -> fp16 operands, scaled by a power of two (and by the sign of
+        // the softmax's scale, so that larger is always larger)
+        const uint16_t* qp = a.q + (rw.first + qi) * a.q_stride + (int64_t)head * D + 8 * kg;
         uint4 qr[NC];
-        float qmax = 0.0f;
+        uint32_t qmax = 0;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             qr[i] = *reinterpret_cast<const uint4*>(qp + 32 * i);
             const uint32_t u[4] = {qr[i].x, qr[i].y, qr[i].z, qr[i].w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                // as integers: a NaN is larger than everything and stays visible
-                const uint32_t lo = (u[e] << 16) & 0x7fffffffu, hi = u[e] & 0x7fff0000u;
-                qmax = __uint_as_float(max(__float_as_uint(qmax), max(lo, hi)));
-            }
+            for (int e = 0; e < 4; ++e)  // as integers: a NaN is the largest
+                qmax = max(qmax, max((u[e] << 16) & 0x7fffffffu, u[e] & 0x7fff0000u));
         }
-        {
-            uint32_t m = __float_as_uint(qmax);
-            m = max(m, (uint32_t)__shfl_xor((int)m, 16, kWave));
-            m = max(m, (uint32_t)__shfl_xor((int)m, 32, kWave));
-            qmax = __uint_as_float(m);
-        }
-        const int ue = min(14 - exponent(qmax), 126);
-        const float up = pow2(ue);
-        const float logit = a.scale_log2 * pow2(-ue);
+        qmax = max(qmax, (uint32_t)__shfl_xor((int)qmax, 16, kWave));
+        qmax = max(qmax, (uint32_t)__shfl_xor((int)qmax, 32, kWave));
+        const int ue = min(14 - exponent(__uint_as_float(qmax)), 126);
+        const float up = a.scale_log2 < 0.0f ? -pow2(ue) : pow2(ue);
+        const float logit = fabsf(a.scale_log2) * pow2(-ue);
         f16x8_t qf[NC];
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
@@ -169,72 +266,107 @@ __global__ __launch_bounds__(kWave) void cache4_attention_kernel(AttnArgs a)
 #pragma unroll
         for (int j = 0; j < NT; ++j) o[j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
 
-        for (int64_t t0 = 0; t0 < end; t0 += 32) {
-            float s[8];
-            float vs[8][NG];
-            uint32_t vw[8][VW];
+        // page of 16 positions from tt (the tile's last ones past its end)
+        auto page_of = [&](int64_t tt) {
+            if (tt >= stop) tt = (stop - 1) & ~15LL;
+            return __builtin_amdgcn_readfirstlane(a.bt.table[b * a.bt.width + (tt >> shift)]);
+        };
+        uint32_t kw[2][NC], vw[8][VW];
+        float ksl[2][NL], vsl[2][NL];
+        auto load = [&](int64_t t0, const int (&pg)[2]) __attribute__((always_inline)) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                int64_t tt = t0 + 16 * h;
+                if (tt >= stop) tt = (stop - 1) & ~15LL;
+                const bool bad = pg[h] < 0 || pg[h] >= a.c.pages;
+                const int64_t block = (int64_t)(bad ? 0 : pg[h]) * a.c.heads + kvh;
+                const int64_t off = tt & (P - 1);
+                const int64_t crow = ((block << shift) + off) * (D / 8);
+                const uint32_t* kp = a.c.k_codes + crow;
+#pragma unroll
+                for (int i = 0; i < NC; ++i) kw[h][i] = kp[k_lane + i];
+                const uint32_t* vp = a.c.v_codes + crow;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (D == 64) {
+                        vw[4 * h + e][0] = reinterpret_cast<const uint16_t*>(vp)[v_lane + e * (D / 4)];
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < VW; ++i) vw[4 * h + e][i] = vp[v_lane + e * (D / 8) + i];
+                    }
+                }
+                const float* ks = a.c.k_scales + ((block * NG) << shift) + off;
+                const float* vs = a.c.v_scales + ((block * NG) << shift) + off;
+#pragma unroll
+                for (int i = 0; i < NL; ++i) {
+                    const float x = ks[s_lane[i]];
+                    ksl[h][i] = bad ? __uint_as_float(0x7fc00000u) : x;
+                    vsl[h][i] = vs[s_lane[i]];
+                }
+            }
+        };
+        auto step = [&](int64_t t0, auto next, auto Full) __attribute__((always_inline)) {
+            constexpr bool full = decltype(Full)::value;  // every live row sees all 32
+            // value scales: none past the end, measured by a common power of two
             float vtop = 0.0f;
 #pragma unroll
-            for (int tile = 0; tile < 2; ++tile) {
-                // 16 positions of one page; past the end, the last one again
-                const int64_t tt = t0 + 16 * tile < end ? t0 + 16 * tile : (end - 1) & ~15LL;
-                int64_t page = a.bt.table[b * a.bt.width + (tt >> shift)];
-                const bool bad = page < 0 || page >= a.c.pages;
-                if (bad) page = 0;
-                const int64_t off = tt & (P - 1);
-                const int64_t block = page * a.c.heads + kvh;
-                const int64_t crow = ((block << shift) + off) * (D / 8);
-                const uint32_t* kp = a.c.k_codes + crow + r16 * (D / 8) + kg * NC;
-                uint32_t kw[NC];
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int i = 0; i < NC; ++i) kw[i] = kp[i];
-                const float* ksc = a.c.k_scales + ((block * NG) << shift) + off + 4 * kg;
-                const float* vsc = a.c.v_scales + ((block * NG) << shift) + off + 4 * kg;
+                for (int i = 0; i < NL; ++i) {
+                    if (!full && t0 + 16 * h + r16 >= end) vsl[h][i] = 0.0f;
+                    vtop = fmaxf(vtop, vsl[h][i]);
+                }
+            const int vx = exponent(__uint_as_float(
+                __builtin_amdgcn_readfirstlane(__float_as_uint(wave_max_abs(vtop)))));
+            const int vn = vx > ve ? vx : ve;
+            const float vfac = pow2(14 - vn);
+            float* lk = &scales[wave][0][0];
+            float* lv = &scales[wave][1][0];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < NL; ++i) {
+                    lk[h * SC + i * 64 + lane] = ksl[h][i];
+                    lv[h * SC + i * 64 + lane] = vsl[h][i] * vfac;
+                }
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");  // other lanes read them
+            __builtin_amdgcn_wave_barrier();
+            // S^T = K Q^T, a group at a time
+            float s[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
                 f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     f32x4_t part = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int i = 0; i < GC; ++i)
-                        part = __builtin_amdgcn_mfma_f32_16x16x32_f16(word_codes(kw[g * GC + i]),
+                        part = __builtin_amdgcn_mfma_f32_16x16x32_f16(word_codes(kw[h][g * GC + i]),
                                                                       qf[g * GC + i], part, 0, 0, 0);
-                    const float4 ks = *reinterpret_cast<const float4*>(ksc + ((int64_t)g << shift));
-                    const float4 v4 = *reinterpret_cast<const float4*>(vsc + ((int64_t)g << shift));
-                    acc[0] = fmaf(ks.x, part[0], acc[0]);
-                    acc[1] = fmaf(ks.y, part[1], acc[1]);
-                    acc[2] = fmaf(ks.z, part[2], acc[2]);
-                    acc[3] = fmaf(ks.w, part[3], acc[3]);
-                    vs[4 * tile][g] = v4.x, vs[4 * tile + 1][g] = v4.y;
-                    vs[4 * tile + 2][g] = v4.z, vs[4 * tile + 3][g] = v4.w;
+                    const f32x4_t ks = *reinterpret_cast<const f32x4_t*>(lk + h * SC + g * 16 + 4 * kg);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[e] = fmaf(ks[e], part[e], acc[e]);
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int64_t pos = t0 + 16 * tile + 4 * kg + e;
-                    float x = acc[e] * logit;
-                    if (bad) x = __uint_as_float(0x7fc00000u);
-                    s[4 * tile + e] = pos <= limit ? x : -INFINITY;
-                    if (pos < end) {
-#pragma unroll
-                        for (int g = 0; g < NG; ++g) vtop = fmaxf(vtop, vs[4 * tile + e][g]);
-                    }
-                    const uint32_t* vp = a.c.v_codes + crow + (4 * kg + e) * (D / 8);
-                    if constexpr (D == 64) {
-                        vw[4 * tile + e][0] = reinterpret_cast<const uint16_t*>(vp)[r16];
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < VW; ++i) vw[4 * tile + e][i] = vp[r16 * VW + i];
-                    }
+                    s[4 * h + e] = acc[e];
+                    if (!full && t0 + 16 * h + 4 * kg + e > limit) s[4 * h + e] = -INFINITY;
                 }
             }
-            // value scales' common power of two
-            vtop = row_max(vtop);
-            const int vn = exponent(vtop) > ve ? exponent(vtop) : ve;
-            const float vfac = pow2(14 - vn);
-            // running maximum and sum
+            // value codes of the 8 positions, out of the load registers
+            uint32_t vc[8][VW];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int i = 0; i < VW; ++i) vc[e][i] = vw[e][i];
+            next();
+            // running maximum (of logits) and sum
             float mx = s[0];
 #pragma unroll
             for (int e = 1; e < 8; ++e) mx = fmaxf(mx, s[e]);
-            const float mn = fmaxf(m, row_max(mx));
+            mx = row_max(mx);
+            // a row that sees nothing here has no maximum (0 * inf otherwise)
+            const float mn = fmaxf(m, mx == -INFINITY ? mx : mx * logit);
             const float base = mn == -INFINITY ? 0.0f : mn;
             const float alpha = __builtin_amdgcn_exp2f(m - base);
             const float oscale = alpha * pow2(ve - vn);
@@ -244,22 +376,32 @@ __global__ __launch_bounds__(kWave) void cache4_attention_kernel(AttnArgs a)
             float sum = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                p[e] = __builtin_amdgcn_exp2f(s[e] - base);
+                float x = fmaf(s[e], logit, -base);
+                if (!full && s[e] == -INFINITY) x = s[e];
+                p[e] = __builtin_amdgcn_exp2f(x);
                 sum += p[e];
             }
             l = fmaf(l, alpha, sum);
+            if (__any(oscale != 1.0f)) {
 #pragma unroll
-            for (int j = 0; j < NT; ++j) o[j] *= oscale;
+                for (int j = 0; j < NT; ++j) o[j] *= oscale;
+            }
             f16x8_t pf[NG];
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int64_t pos = t0 + 16 * (e >> 2) + 4 * kg + (e & 3);
-                    pf[g][e] = (_Float16)(pos <= limit ? p[e] * (vs[e][g] * vfac) : 0.0f);
+                for (int h = 0; h < 2; ++h) {
+                    const f32x4_t vs = *reinterpret_cast<const f32x4_t*>(lv + h * SC + g * 16 + 4 * kg);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float x = p[4 * h + e] * vs[e];
+                        // a NaN scale touches only the rows that see it
+                        if (!full && t0 + 16 * h + 4 * kg + e > limit) x = 0.0f;
+                        pf[g][4 * h + e] = (_Float16)x;
+                    }
                 }
             }
-            // tile j: nibble j of the lane's codes of 8 positions, pairs of positions
+            // O^T = V^T P^T; tile j: nibble j of the lane's codes of 8 positions, in pairs
 #pragma unroll
             for (int i = 0; i < VW; ++i) {
 #pragma unroll
@@ -268,7 +410,7 @@ __global__ __launch_bounds__(kWave) void cache4_attention_kernel(AttnArgs a)
                     uint32_t lo[4], hi[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const uint32_t v = __builtin_amdgcn_perm(vw[2 * e + 1][i], vw[2 * e][i], sel);
+                        const uint32_t v = __builtin_amdgcn_perm(vc[2 * e + 1][i], vc[2 * e][i], sel);
                         lo[e] = low_codes(v);
                         hi[e] = high_codes(v);
                     }
@@ -279,32 +421,195 @@ __global__ __launch_bounds__(kWave) void cache4_attention_kernel(AttnArgs a)
                     o[j + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vh, pf[16 * (j + 1) / G], o[j + 1], 0, 0, 0);
                 }
             }
-        }
-        l = row_sum(l);
-        float inv = l > 0.0f ? pow2(ve - 14) / l : (l == 0.0f ? 0.0f : l);  // NaN stays
-        if (bad_len) inv = __uint_as_float(0x7fc00000u);
-        if (live) {
-            uint16_t* op = a.out + ((first + qi) * a.q_heads + head) * D + 4 * kg;
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                uint32_t w[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    w[e] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)(o[j][2 * e] * inv)) |
-                           ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)(o[j][2 * e + 1] * inv)) << 16);
-                *reinterpret_cast<uint2*>(op + 16 * j) = make_uint2(w[0], w[1]);
+        };
+
+        constexpr int64_t kStride = kWaves * kStep;
+        int64_t t0 = begin + wave * kStep;
+        if (t0 < stop) {
+            int pg[2] = {page_of(t0), page_of(t0 + 16)};
+            load(t0, pg);
+            if (t0 + kStride < stop) {
+                pg[0] = page_of(t0 + kStride);
+                pg[1] = page_of(t0 + kStride + 16);
+            }
+            for (; t0 < stop; t0 += kStride) {
+                auto next = [&]() __attribute__((always_inline)) {
+                    const int64_t t1 = t0 + kStride;
+                    if (t1 < stop) {
+                        load(t1, pg);
+                        if (t1 + kStride < stop) {
+                            pg[0] = page_of(t1 + kStride);
+                            pg[1] = page_of(t1 + kStride + 16);
+                        }
+                    }
+                };
+                if (t0 + kStep <= all_see)
+                    step(t0, next, std::true_type{});
+                else
+                    step(t0, next, std::false_type{});
             }
         }
+
+        // join the waves: 2 and 3 into 0 and 1, then 1 into 0
+        auto put = [&](float* dst) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) *reinterpret_cast<f32x4_t*>(dst + (j * kWave + lane) * 4) = o[j];
+            dst[NT * 4 * kWave + lane] = m;
+            dst[(NT * 4 + 1) * kWave + lane] = l;
+            dst[(NT * 4 + 2) * kWave + lane] = __int_as_float(ve);
+        };
+        auto add = [&](const float* src) {
+            const float m2 = src[NT * 4 * kWave + lane];
+            const float l2 = src[(NT * 4 + 1) * kWave + lane];
+            const int v2 = __float_as_int(src[(NT * 4 + 2) * kWave + lane]);
+            const float mn = fmaxf(m, m2);
+            const float base = mn == -INFINITY ? 0.0f : mn;
+            const int vn = ve > v2 ? ve : v2;
+            const float w1 = __builtin_amdgcn_exp2f(m - base), w2 = __builtin_amdgcn_exp2f(m2 - base);
+            const float f1 = w1 * pow2(ve - vn), f2 = w2 * pow2(v2 - vn);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const f32x4_t x = *reinterpret_cast<const f32x4_t*>(src + (j * kWave + lane) * 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[j][e] = fmaf(x[e], f2, o[j][e] * f1);
+            }
+            l = fmaf(l2, w2, l * w1);
+            m = mn;
+            ve = vn;
+        };
+        if (wave >= 2) put(join[wave - 2]);
+        __syncthreads();
+        if (wave < 2) add(join[wave]);
+        __syncthreads();
+        if (wave == 1) put(join[0]);
+        __syncthreads();
+        if (wave == 0) {
+            add(join[0]);
+            l = row_sum(l);
+            float inv = l > 0.0f ? pow2(ve - 14) / l : (l == 0.0f ? 0.0f : l);  // NaN stays
+            if (rw.bad) inv = __uint_as_float(0x7fc00000u);
+            if (whole) {
+                if (live) {
+                    uint16_t* op = a.out + ((rw.first + qi) * a.q_heads + head) * D + 4 * kg;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+                        *reinterpret_cast<uint2*>(op + 16 * j) =
+                            make_uint2(bf16x2(o[j][0] * inv, o[j][1] * inv), bf16x2(o[j][2] * inv, o[j][3] * inv));
+                }
+            } else {
+                const int64_t at =
+                    (((b * a.c.heads + kvh) * a.row_tiles + tile) * a.splits + split) * 16 + r16;
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    *reinterpret_cast<f32x4_t*>(a.part + at * D + 16 * j + 4 * kg) = o[j] * inv;
+                if (kg == 0) a.part_ml[at] = make_float2(m, l);
+            }
+        }
+        if (tile + 1 < a.row_tiles) break;
+        __syncthreads();  // the join buffers are free for the next extra tile
     }
 }
 
-template <int D, int G>
-hipError_t launch_dg(const AttnArgs& a, int64_t max_q, hipStream_t stream)
+// Joins the shares of one row: out = sum_s w_s o_s / sum_s w_s, w_s = l_s 2^(m_s - max m).
+template <int D>
+__global__ __launch_bounds__(256) void cache4_join_kernel(AttnArgs a)
 {
-    const int64_t tiles = ceil_div(max_q * (a.q_heads / a.c.heads), 16);
-    const dim3 grid((unsigned)(tiles < 65535 ? tiles : 65535), (unsigned)a.c.heads,
-                    (unsigned)a.bt.count);
-    cache4_attention_kernel<D, G><<<grid, kWave, 0, stream>>>(a);
+    constexpr int kPer = D / 4;       // threads of a share: four dimensions each
+    constexpr int kPar = 256 / kPer;  // shares in flight
+    __shared__ float weight[256];
+    __shared__ float red[8];
+    __shared__ __attribute__((aligned(16))) f32x4_t sums[256];
+    const int tid = threadIdx.x;
+    const int64_t b = blockIdx.z;
+    const int kvh = blockIdx.y;
+    const int64_t tile = blockIdx.x >> 4;
+    const int r16 = blockIdx.x & 15;
+    const Rows rw = rows_of(a, b);
+    const int64_t r0 = tile * 16;
+    const int64_t row = r0 + r16;
+    if (row >= rw.rows()) return;
+    const int64_t end = rw.end(r0);
+    const int64_t share = share_of(end, a.splits);
+    if (end <= share) return;  // written by the attention kernel
+    const int n = (int)((end + share - 1) / share);
+    const int64_t at = ((b * a.c.heads + kvh) * a.row_tiles + tile) * a.splits;
+
+    const float2 ml = tid < n ? a.part_ml[(at + tid) * 16 + r16] : make_float2(-INFINITY, 0.0f);
+    float mx = ml.x;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o, kWave));
+    if ((tid & 63) == 0) red[tid >> 6] = mx;
+    __syncthreads();
+    mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    const float base = mx == -INFINITY ? 0.0f : mx;
+    const float w = ml.y == 0.0f ? 0.0f : ml.y * __builtin_amdgcn_exp2f(ml.x - base);
+    weight[tid] = w;
+    float tot = w;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) tot += __shfl_xor(tot, o, kWave);
+    if ((tid & 63) == 0) red[4 + (tid >> 6)] = tot;
+    __syncthreads();
+    tot = (red[4] + red[5]) + (red[6] + red[7]);
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+    const int d4 = tid % kPer;
+    for (int s = tid / kPer; s < n; s += kPar) {
+        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(a.part + ((at + s) * 16 + r16) * D + 4 * d4);
+        const float ws = weight[s];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = fmaf(ws, x[e], acc[e]);
+    }
+    sums[tid] = acc;
+    __syncthreads();
+    if (tid < kPer) {
+#pragma unroll
+        for (int i = 1; i < kPar; ++i) acc += sums[i * kPer + tid];
+        const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
+        const int64_t qi = row / rw.per;
+        const int head = kvh * rw.per + (int)(row % rw.per);
+        uint16_t* op = a.out + ((rw.first + qi) * a.q_heads + head) * D + 4 * d4;
+        *reinterpret_cast<uint2*>(op) =
+            make_uint2(bf16x2(acc[0] * inv, acc[1] * inv), bf16x2(acc[2] * inv, acc[3] * inv));
+    }
+}
+
+// The launch's shape: 16-row tiles per (sequence, kv head), and shares of the
+// positions so that about kFill workgroups are in flight, four on each of the
+// 256 CUs, with no share below kMinShare positions.
+constexpr int64_t kFill = 1024;
+constexpr int64_t kMaxSplits = 256;
+
+struct Plan {
+    int64_t tiles, splits, units;
+    size_t part_bytes, ml_bytes;
+};
+
+Plan plan_of(const Cache4& c, int64_t count, int64_t tokens, int q_heads, int64_t max_q, int64_t max_len)
+{
+    Plan p;
+    if (max_q > tokens) max_q = tokens;
+    p.tiles = ceil_div(max_q * (q_heads / c.heads), 16);
+    if (p.tiles > 65535) p.tiles = 65535;
+    p.units = count * c.heads * p.tiles;
+    const int64_t most = ceil_div(max_len, kMinShare);
+    p.splits = kFill / p.units;
+    if (p.splits > most) p.splits = most;
+    if (p.splits > kMaxSplits) p.splits = kMaxSplits;
+    if (p.splits < 1) p.splits = 1;
+    const size_t rows = p.splits > 1 ? (size_t)(p.units * p.splits) * 16 : 0;
+    p.part_bytes = rows * c.dim * sizeof(float);
+    p.ml_bytes = rows * sizeof(float2);
+    return p;
+}
+
+template <int D, int G>
+hipError_t launch_dg(const AttnArgs& a, hipStream_t stream)
+{
+    const dim3 grid((unsigned)(a.row_tiles * a.splits), (unsigned)a.c.heads, (unsigned)a.bt.count);
+    cache4_attention_kernel<D, G><<<grid, kWaves * kWave, 0, stream>>>(a);
+    if (a.splits > 1) {
+        const dim3 jgrid((unsigned)(a.row_tiles * 16), (unsigned)a.c.heads, (unsigned)a.bt.count);
+        cache4_join_kernel<D><<<jgrid, 256, 0, stream>>>(a);
+    }
     return hipGetLastError();
 }
 
@@ -313,8 +618,8 @@ hipError_t launch_dg(const AttnArgs& a, int64_t max_q, hipStream_t stream)
 size_t cache4_attention_workspace(const Cache4& c, int64_t count, int64_t tokens,
                                   int q_heads, int64_t max_q, int64_t max_len)
 {
-    (void)c, (void)count, (void)tokens, (void)q_heads, (void)max_q, (void)max_len;
-    return 0;
+    const Plan p = plan_of(c, count, tokens, q_heads, max_q, max_len);
+    return p.part_bytes + p.ml_bytes;
 }
 
 hipError_t launch_cache4_attention(const Cache4& c, const Cache4Batch& bt, const uint16_t* q,
@@ -322,18 +627,19 @@ hipError_t launch_cache4_attention(const Cache4& c, const Cache4Batch& bt, const
                                    int64_t max_q, int64_t max_len, uint16_t* out, void* workspace,
                                    hipStream_t stream)
 {
-    (void)max_len;
-    (void)workspace;
-    const AttnArgs a{c, bt, q, q_stride, out, tokens, q_heads, scale * kLog2e};
+    const Plan p = plan_of(c, bt.count, tokens, q_heads, max_q, max_len);
+    const AttnArgs a{c, bt, q, q_stride, out, tokens, q_heads, scale * kLog2e, (int32_t)p.tiles,
+                     (int32_t)p.splits, static_cast<float*>(workspace),
+                     reinterpret_cast<float2*>(static_cast<char*>(workspace) + p.part_bytes)};
     switch (c.dim * 1000 + c.group) {
-    case 64032: return launch_dg<64, 32>(a, max_q, stream);
-    case 64064: return launch_dg<64, 64>(a, max_q, stream);
-    case 128032: return launch_dg<128, 32>(a, max_q, stream);
-    case 128064: return launch_dg<128, 64>(a, max_q, stream);
-    case 128128: return launch_dg<128, 128>(a, max_q, stream);
-    case 256032: return launch_dg<256, 32>(a, max_q, stream);
-    case 256064: return launch_dg<256, 64>(a, max_q, stream);
-    case 256128: return launch_dg<256, 128>(a, max_q, stream);
+    case 64032: return launch_dg<64, 32>(a, stream);
+    case 64064: return launch_dg<64, 64>(a, stream);
+    case 128032: return launch_dg<128, 32>(a, stream);
+    case 128064: return launch_dg<128, 64>(a, stream);
+    case 128128: return launch_dg<128, 128>(a, stream);
+    case 256032: return launch_dg<256, 32>(a, stream);
+    case 256064: return launch_dg<256, 64>(a, stream);
+    case 256128: return launch_dg<256, 128>(a, stream);
     default: return hipErrorInvalidValue;
     }
 }
