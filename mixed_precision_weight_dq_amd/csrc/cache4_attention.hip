@@ -15,10 +15,9 @@
 //   * p * (value scale) is rounded once, to fp16, after multiplication by a
 //     power of two that puts the largest value scale seen so far in [2^14,
 //     2^15): relative error 2^-11 down to 2^-29 of the largest.
-#include <type_traits>
-
 #include "cache4.hpp"
 #include "common.hpp"
+#include "gemm_tiles.hpp"
 #include "launch_serving.hpp"
 
 namespace dq {
@@ -35,16 +34,34 @@ constexpr float kLog2e = 1.44269504088896340736f;
 __device__ __forceinline__ uint32_t u32_of(f16x2_t v) { return __builtin_bit_cast(uint32_t, v); }
 __device__ __forceinline__ f16x2_t f16x2_of(uint32_t v) { return __builtin_bit_cast(f16x2_t, v); }
 
+// (v & mask) | bits in one instruction: one constant in a scalar register, the
+// other in a vector register (the compiler's own choice is two instructions
+// with a literal each).
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits)
+{
+    uint32_t r;
+    asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(v), "s"(mask), "v"(bits));
+    return r;
+}
+
+// a * b, and 0 where either is 0 (a NaN or infinity beside it included)
+__device__ __forceinline__ float mul_legacy(float a, float b)
+{
+    float r;
+    asm("v_mul_legacy_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+
 // The codes in bits 0..3 and 16..19 of v as fp16 (u - 8), exact.
 __device__ __forceinline__ uint32_t low_codes(uint32_t v)
 {
-    const f16x2_t h = f16x2_of((v & 0x000f000fu) | 0x64006400u);  // 1024 + u
+    const f16x2_t h = f16x2_of(and_or(v, 0x000f000fu, 0x64006400u));  // 1024 + u
     return u32_of(h - (f16x2_t){(_Float16)1032.0f, (_Float16)1032.0f});
 }
 // The codes in bits 4..7 and 20..23.
 __device__ __forceinline__ uint32_t high_codes(uint32_t v)
 {
-    const f16x2_t h = f16x2_of((v & 0x00f000f0u) | 0x64006400u);  // 1024 + 16 u
+    const f16x2_t h = f16x2_of(and_or(v, 0x00f000f0u, 0x64006400u));  // 1024 + 16 u
     const _Float16 s = (_Float16)0.0625f, o = (_Float16)-72.0f;
     return u32_of(__builtin_elementwise_fma(h, (f16x2_t){s, s}, (f16x2_t){o, o}));
 }
@@ -82,13 +99,31 @@ __device__ __forceinline__ float row_sum(float v)
     row_pair(x + y, false, x, y);
     return x + y;
 }
-// max over the wave of non-negative values (NaN counts as nothing)
+// max over the wave of values that are not negative, NaN counting as 0; the
+// same in every lane (row_ror 8, 4, 2, 1 within 16 lanes, then across them)
+template <int kRor>
+__device__ __forceinline__ uint32_t ror_max(uint32_t u)
+{
+    const uint32_t t = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0x120 + kRor, 0xf, 0xf, false);
+    return max(u, t);
+}
 __device__ __forceinline__ float wave_max_abs(float v)
 {
-    v = fmaxf(v, 0.0f);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, kWave));
-    return row_max(v);
+    uint32_t u = v >= 0.0f ? __float_as_uint(v) : 0u;
+    u = ror_max<1>(ror_max<2>(ror_max<4>(ror_max<8>(u))));
+    float x, y;
+    row_pair(__uint_as_float(u), true, x, y);
+    u = max(__float_as_uint(x), __float_as_uint(y));
+    row_pair(__uint_as_float(u), false, x, y);
+    return __uint_as_float(max(__float_as_uint(x), __float_as_uint(y)));
+}
+
+// Keeps v computed here, in a register: a value that is used behind a branch
+// would else be computed there, its operands kept alive until then.
+template <class T>
+__device__ __forceinline__ void pin(T& v)
+{
+    asm volatile("" : "+v"(v));
 }
 
 // 2^n for n clamped to fp32's normal range
@@ -120,34 +155,38 @@ struct AttnArgs {
 
 constexpr int kWaves = 4;
 constexpr int kStep = 32;                   // positions per wave and step
-constexpr int kMinShare = kWaves * kStep;   // positions of a share, at least
+constexpr int kStride = kWaves * kStep;     // positions per workgroup and step
+constexpr int kMinShare = kStride;          // positions of a share, at least
 
 // Positions per share of a row tile that sees positions [0, end).
-__device__ __forceinline__ int64_t share_of(int64_t end, int splits)
+__device__ __forceinline__ int share_of(int end, int splits)
 {
-    int64_t n = (end + splits - 1) / splits;
-    n = (n + kStep - 1) & ~(int64_t)(kStep - 1);
+    const int n = end <= 0 ? 0 : (int)(((unsigned)(end - 1) / (unsigned)splits + kStep) & ~(unsigned)(kStep - 1));
     return n < kMinShare ? kMinShare : n;
 }
 
-// What a workgroup knows of its sequence.
+// What a workgroup knows of its sequence.  Token rows and positions are below 2^31.
 struct Rows {
-    int64_t first, nq, len;  // first token row, new tokens, cached tokens
-    bool bad;                // a length past the table
-    int per;                 // query heads of a kv head
-    __device__ __forceinline__ int64_t rows() const { return nq * per; }
+    int first, nq, len;  // first token row, new tokens, cached tokens
+    bool bad;            // a length past the table
+    int per;             // query heads of a kv head
+    __device__ __forceinline__ int64_t rows() const { return (int64_t)nq * per; }
+    // positions seen by row r (a new token's head)
+    __device__ __forceinline__ int seen(int64_t r) const { return len - nq + (int)(r / per) + 1; }
     // positions seen by the last row of the tile that starts at row r0
-    __device__ __forceinline__ int64_t end(int64_t r0) const
+    __device__ __forceinline__ int end(int64_t r0) const
     {
-        const int64_t last = r0 + 15 < rows() ? r0 + 15 : rows() - 1;
-        return len - nq + last / per + 1;
+        return seen(r0 + 15 < rows() ? r0 + 15 : rows() - 1);
     }
 };
 
 __device__ __forceinline__ Rows rows_of(const AttnArgs& a, int64_t b)
 {
     Rows r;
-    cache4_rows(a.bt, b, a.tokens, r.first, r.nq);
+    int64_t first, nq;
+    cache4_rows(a.bt, b, a.tokens, first, nq);
+    r.first = (int)first;
+    r.nq = (int)nq;
     r.len = a.bt.lens[b];
     r.bad = r.len > a.bt.width << a.c.page_shift;
     if (r.len < 0 || r.bad) r.len = 0;
@@ -161,18 +200,41 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b)
            ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)b) << 16);
 }
 
+// n consecutive words at byte offset off of a buffer.
+template <int N>
+__device__ __forceinline__ void load_n(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t (&w)[N])
+{
+    if constexpr (N == 2) {
+        const u32x2v_t v = __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0);
+        w[0] = v.x;
+        w[1] = v.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const u32x4v_t v = __builtin_amdgcn_raw_buffer_load_b128(rs, off + 4 * i, 0, 0);
+            w[i] = v.x;
+            w[i + 1] = v.y;
+            w[i + 2] = v.z;
+            w[i + 3] = v.w;
+        }
+    }
+}
+
 // One workgroup of four waves per (16-row tile, share of the positions, kv
 // head, sequence): wave w takes steps w, w + 4, ... of the share, and the four
 // partial results are joined through LDS in a fixed order.  A tile whose
 // positions are one share is written out here; otherwise the shares are joined
 // by cache4_join_kernel, in order.
 //
-// A step's loads are issued one step ahead, its page numbers two.  Codes come
+// A step's loads are issued a step ahead, as soon as the registers that they
+// fill are free, its page numbers two steps ahead (scalar loads).  Codes come
 // straight into the registers that expand them; a step's scales come one float
 // per lane and are handed round through wave-private LDS (each lane needs the
-// scales of 8 positions and every group).
+// scales of 8 positions and every group).  A tile of 16 positions lies in one
+// page, so its four arrays are buffers with scalar bases, and a lane's place
+// in them is the same in every step.
 template <int D, int G>
-__global__ __launch_bounds__(kWaves* kWave) void cache4_attention_kernel(AttnArgs a)
+__global__ __launch_bounds__(kWaves* kWave, D == 64 ? 4 : (D == 128 ? 4 : 2)) void cache4_attention_kernel(AttnArgs a)
 {
     constexpr int NC = D / 32;  // 32-dimension steps of a dot product
     constexpr int NG = D / G;   // groups of a head
@@ -188,75 +250,84 @@ __global__ __launch_bounds__(kWaves* kWave) void cache4_attention_kernel(AttnArg
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int r16 = lane & 15;
     const int kg = lane >> 4;
-    const int64_t b = blockIdx.z;
+    const int b = blockIdx.z;
     const int kvh = blockIdx.y;
-    const int split = blockIdx.x % a.splits;
+    const int split = blockIdx.x % (unsigned)a.splits;
+    const int tile0 = blockIdx.x / (unsigned)a.splits;
     const int shift = a.c.page_shift;
-    const int64_t P = 1LL << shift;
     const Rows rw = rows_of(a, b);
     const int64_t rows = rw.rows();
+    // constant address space: scalar loads, which leave the count of vector
+    // loads in flight alone
+    const __attribute__((address_space(4))) int32_t* table =
+        (const __attribute__((address_space(4))) int32_t*)(a.bt.table + b * a.bt.width);
 
-    // places of this lane's data relative to a 16-position tile of one head
-    const uint32_t k_lane = r16 * (D / 8) + kg * NC;
-    const uint32_t v_lane = 4 * kg * (D / 8) * (D == 64 ? 2 : 1) + r16 * VW;
+    // byte offsets of this lane's data in 16 positions of one head
+    const uint32_t k_lane = r16 * (D / 2) + kg * NC * 4;
+    const uint32_t v_lane = 4 * kg * (D / 2) + r16 * (D / 32);
     uint32_t s_lane[NL];
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
         const int g = 4 * i + kg < NG ? 4 * i + kg : NG - 1;
-        s_lane[i] = ((uint32_t)g << shift) + r16;
+        s_lane[i] = (((uint32_t)g << shift) + r16) * 4;
     }
 
     // tiles past the grid's are one share each, walked by the grid's last tile
-    for (int64_t tile = blockIdx.x / a.splits; tile * 16 < rows; ++tile) {
+    for (int64_t tile = tile0; tile * 16 < rows; ++tile) {
         const bool extra = tile >= a.row_tiles;
-        if (tile > (int64_t)(blockIdx.x / a.splits) && !extra) break;
         if (extra && split != 0) break;
         const int64_t r0 = tile * 16;
-        const int64_t row = r0 + r16;
-        const bool live = row < rows;
-        const int64_t qi = live ? row / rw.per : 0;
-        const int head = kvh * rw.per + (live ? (int)(row % rw.per) : 0);
-        const int64_t limit = live ? rw.len - rw.nq + qi : -1;  // last position the row sees
-        const int64_t end = rw.end(r0);
-        const int64_t all_see = rw.len - rw.nq + r0 / rw.per + 1;  // seen by every live row
-        const int64_t share = extra ? (end > 0 ? end : 1) : share_of(end, a.splits);
+        const bool live = r0 + r16 < rows;
+        const int64_t row = live ? r0 + r16 : 0;
+        const int qi = (int)(row / rw.per);
+        const int head = kvh * rw.per + (int)(row % rw.per);
+        const int seen = live ? rw.seen(row) : 0;  // positions that the row sees
+        const int end = rw.end(r0);
+        const int share = extra ? (end > 0 ? end : 1) : share_of(end, a.splits);
         const bool whole = end <= share;  // one share: no joining
-        const int64_t begin = extra ? 0 : share * split;
-        const int64_t stop = begin + share < end ? begin + share : end;
+        const int begin = extra ? 0 : share * split;
         if (begin >= end && split != 0) break;  // nothing for this share, nor for an extra tile
+        const int stop = end - begin < share ? end : begin + share;
 
         // q row -> fp16 operands, scaled by a power of two (and by the sign of
         // the softmax's scale, so that larger is always larger)
-        const uint16_t* qp = a.q + (rw.first + qi) * a.q_stride + (int64_t)head * D + 8 * kg;
-        uint4 qr[NC];
-        uint32_t qmax = 0;
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            qr[i] = *reinterpret_cast<const uint4*>(qp + 32 * i);
-            const uint32_t u[4] = {qr[i].x, qr[i].y, qr[i].z, qr[i].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)  // as integers: a NaN is the largest
-                qmax = max(qmax, max((u[e] << 16) & 0x7fffffffu, u[e] & 0x7fff0000u));
-        }
-        qmax = max(qmax, (uint32_t)__shfl_xor((int)qmax, 16, kWave));
-        qmax = max(qmax, (uint32_t)__shfl_xor((int)qmax, 32, kWave));
-        const int ue = min(14 - exponent(__uint_as_float(qmax)), 126);
-        const float up = a.scale_log2 < 0.0f ? -pow2(ue) : pow2(ue);
-        const float logit = fabsf(a.scale_log2) * pow2(-ue);
         f16x8_t qf[NC];
+        float logit;
+        {
+            const uint16_t* qp = a.q + (int64_t)(rw.first + qi) * a.q_stride + (int64_t)head * D + 8 * kg;
+            uint4 qr[NC];
+            uint32_t qmax = 0;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const uint32_t u[4] = {qr[i].x, qr[i].y, qr[i].z, qr[i].w};
-            float f[8];
+            for (int i = 0; i < NC; ++i) {
+                qr[i] = *reinterpret_cast<const uint4*>(qp + 32 * i);
+                const uint32_t u[4] = {qr[i].x, qr[i].y, qr[i].z, qr[i].w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                f[2 * e] = __uint_as_float(u[e] << 16) * up;
-                f[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u) * up;
+                for (int e = 0; e < 4; ++e)  // as integers: a NaN is the largest
+                    qmax = max(qmax, max((u[e] << 16) & 0x7fffffffu, u[e] & 0x7fff0000u));
+            }
+            qmax = max(qmax, (uint32_t)__shfl_xor((int)qmax, 16, kWave));
+            qmax = max(qmax, (uint32_t)__shfl_xor((int)qmax, 32, kWave));
+            const int ue = min(14 - exponent(__uint_as_float(qmax)), 126);
+            float up = a.scale_log2 < 0.0f ? -pow2(ue) : pow2(ue);
+            logit = fabsf(a.scale_log2) * pow2(-ue);
+            if (logit == 0.0f) {  // logits of 0 (and no 0 * -inf where positions are hidden)
+                up = 0.0f;
+                logit = 1.0f;
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {  // the order of word_codes
-                qf[i][2 * e] = (_Float16)f[e];
-                qf[i][2 * e + 1] = (_Float16)f[e + 4];
+            for (int i = 0; i < NC; ++i) {
+                const uint32_t u[4] = {qr[i].x, qr[i].y, qr[i].z, qr[i].w};
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    f[2 * e] = __uint_as_float(u[e] << 16) * up;
+                    f[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u) * up;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {  // the order of word_codes
+                    qf[i][2 * e] = (_Float16)f[e];
+                    qf[i][2 * e + 1] = (_Float16)f[e + 4];
+                }
             }
         }
 
@@ -266,72 +337,82 @@ __global__ __launch_bounds__(kWaves* kWave) void cache4_attention_kernel(AttnArg
 #pragma unroll
         for (int j = 0; j < NT; ++j) o[j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
 
-        // page of 16 positions from tt (the tile's last ones past its end)
-        auto page_of = [&](int64_t tt) {
-            if (tt >= stop) tt = (stop - 1) & ~15LL;
-            return __builtin_amdgcn_readfirstlane(a.bt.table[b * a.bt.width + (tt >> shift)]);
-        };
+        // A step's two tiles of 16 positions (the last ones again past the
+        // end): page, then (page, head) block and offset in it
         uint32_t kw[2][NC], vw[8][VW];
         float ksl[2][NL], vsl[2][NL];
-        auto load = [&](int64_t t0, const int (&pg)[2]) __attribute__((always_inline)) {
+        uint32_t bad[2];  // a NaN's bits where the page is outside the cache
+        int pg[2];
+        int64_t block[2];
+        auto tile_at = [&](int tt) { return tt < stop ? tt : (stop - 1) & ~15; };
+        auto load_pages = [&](int t0) __attribute__((always_inline)) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) pg[h] = table[tile_at(t0 + 16 * h) >> shift];
+        };
+        auto load_k = [&](int t0) __attribute__((always_inline)) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                int64_t tt = t0 + 16 * h;
-                if (tt >= stop) tt = (stop - 1) & ~15LL;
-                const bool bad = pg[h] < 0 || pg[h] >= a.c.pages;
-                const int64_t block = (int64_t)(bad ? 0 : pg[h]) * a.c.heads + kvh;
-                const int64_t off = tt & (P - 1);
-                const int64_t crow = ((block << shift) + off) * (D / 8);
-                const uint32_t* kp = a.c.k_codes + crow;
-#pragma unroll
-                for (int i = 0; i < NC; ++i) kw[h][i] = kp[k_lane + i];
-                const uint32_t* vp = a.c.v_codes + crow;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if constexpr (D == 64) {
-                        vw[4 * h + e][0] = reinterpret_cast<const uint16_t*>(vp)[v_lane + e * (D / 4)];
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < VW; ++i) vw[4 * h + e][i] = vp[v_lane + e * (D / 8) + i];
-                    }
-                }
-                const float* ks = a.c.k_scales + ((block * NG) << shift) + off;
-                const float* vs = a.c.v_scales + ((block * NG) << shift) + off;
+                const int off = tile_at(t0 + 16 * h) & ((1 << shift) - 1);
+                const bool ok = (unsigned)pg[h] < (unsigned)a.c.pages;
+                bad[h] = ok ? 0u : 0x7fc00000u;
+                block[h] = (int64_t)(ok ? pg[h] : 0) * a.c.heads + kvh;
+                const uint32_t* kc = a.c.k_codes + ((block[h] << shift) + off) * (D / 8);
+                load_n<NC>(make_rsrc(kc, 16 * (D / 2)), k_lane, kw[h]);
+                const int64_t sb = ((block[h] * NG) << shift) + off;
+                const uint32_t bytes = (((NG - 1) << shift) + 16) * 4;
+                const __amdgpu_buffer_rsrc_t ks = make_rsrc(a.c.k_scales + sb, bytes);
+                const __amdgpu_buffer_rsrc_t vs = make_rsrc(a.c.v_scales + sb, bytes);
 #pragma unroll
                 for (int i = 0; i < NL; ++i) {
-                    const float x = ks[s_lane[i]];
-                    ksl[h][i] = bad ? __uint_as_float(0x7fc00000u) : x;
-                    vsl[h][i] = vs[s_lane[i]];
+                    ksl[h][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ks, s_lane[i], 0, 0));
+                    vsl[h][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(vs, s_lane[i], 0, 0));
                 }
             }
         };
-        auto step = [&](int64_t t0, auto next, auto Full) __attribute__((always_inline)) {
-            constexpr bool full = decltype(Full)::value;  // every live row sees all 32
+        auto load_v = [&](int t0) __attribute__((always_inline)) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int off = tile_at(t0 + 16 * h) & ((1 << shift) - 1);
+                const uint32_t* vc = a.c.v_codes + ((block[h] << shift) + off) * (D / 8);
+                const __amdgpu_buffer_rsrc_t rs = make_rsrc(vc, 16 * (D / 2));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (D == 64)
+                        vw[4 * h + e][0] = __builtin_amdgcn_raw_buffer_load_b16(rs, v_lane + e * (D / 2), 0, 0);
+                    else if constexpr (D == 128)
+                        vw[4 * h + e][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, v_lane + e * (D / 2), 0, 0);
+                    else
+                        load_n<VW>(rs, v_lane + e * (D / 2), vw[4 * h + e]);
+                }
+            }
+        };
+        float* const lk = &scales[wave][0][0];
+        float* const lv = &scales[wave][1][0];
+        auto step = [&](int t0) __attribute__((always_inline)) {
             // value scales: none past the end, measured by a common power of two
             float vtop = 0.0f;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int i = 0; i < NL; ++i) {
-                    if (!full && t0 + 16 * h + r16 >= end) vsl[h][i] = 0.0f;
+                    if (t0 + 16 * h + r16 >= end) vsl[h][i] = 0.0f;
                     vtop = fmaxf(vtop, vsl[h][i]);
                 }
             const int vx = exponent(__uint_as_float(
                 __builtin_amdgcn_readfirstlane(__float_as_uint(wave_max_abs(vtop)))));
             const int vn = vx > ve ? vx : ve;
             const float vfac = pow2(14 - vn);
-            float* lk = &scales[wave][0][0];
-            float* lv = &scales[wave][1][0];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int i = 0; i < NL; ++i) {
-                    lk[h * SC + i * 64 + lane] = ksl[h][i];
+                    lk[h * SC + i * 64 + lane] = __uint_as_float(__float_as_uint(ksl[h][i]) | bad[h]);
                     lv[h * SC + i * 64 + lane] = vsl[h][i] * vfac;
                 }
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");  // other lanes read them
             __builtin_amdgcn_wave_barrier();
-            // S^T = K Q^T, a group at a time
+            // S^T = K Q^T, a group at a time; positions past the row's own at -inf
+            const int left = seen - t0 - 4 * kg;
             float s[8];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -349,24 +430,19 @@ __global__ __launch_bounds__(kWaves* kWave) void cache4_attention_kernel(AttnArg
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    s[4 * h + e] = acc[e];
-                    if (!full && t0 + 16 * h + 4 * kg + e > limit) s[4 * h + e] = -INFINITY;
+                    s[4 * h + e] = 16 * h + e < left ? acc[e] : -INFINITY;
                 }
+                __builtin_amdgcn_sched_barrier(0);
             }
-            // value codes of the 8 positions, out of the load registers
-            uint32_t vc[8][VW];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-#pragma unroll
-                for (int i = 0; i < VW; ++i) vc[e][i] = vw[e][i];
-            next();
+            __builtin_amdgcn_sched_barrier(0);  // the loads here, not where registers would be free
+            load_k(t0 + kStride);
+            __builtin_amdgcn_sched_barrier(0);
             // running maximum (of logits) and sum
             float mx = s[0];
 #pragma unroll
             for (int e = 1; e < 8; ++e) mx = fmaxf(mx, s[e]);
             mx = row_max(mx);
-            // a row that sees nothing here has no maximum (0 * inf otherwise)
-            const float mn = fmaxf(m, mx == -INFINITY ? mx : mx * logit);
+            const float mn = fmaxf(m, mx * logit);
             const float base = mn == -INFINITY ? 0.0f : mn;
             const float alpha = __builtin_amdgcn_exp2f(m - base);
             const float oscale = alpha * pow2(ve - vn);
@@ -376,12 +452,12 @@ __global__ __launch_bounds__(kWaves* kWave) void cache4_attention_kernel(AttnArg
             float sum = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float x = fmaf(s[e], logit, -base);
-                if (!full && s[e] == -INFINITY) x = s[e];
-                p[e] = __builtin_amdgcn_exp2f(x);
+                p[e] = __builtin_amdgcn_exp2f(fmaf(s[e], logit, -base));
                 sum += p[e];
             }
             l = fmaf(l, alpha, sum);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) pin(p[e]);
             if (__any(oscale != 1.0f)) {
 #pragma unroll
                 for (int j = 0; j < NT; ++j) o[j] *= oscale;
@@ -394,13 +470,14 @@ __global__ __launch_bounds__(kWaves* kWave) void cache4_attention_kernel(AttnArg
                     const f32x4_t vs = *reinterpret_cast<const f32x4_t*>(lv + h * SC + g * 16 + 4 * kg);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float x = p[4 * h + e] * vs[e];
-                        // a NaN scale touches only the rows that see it
-                        if (!full && t0 + 16 * h + 4 * kg + e > limit) x = 0.0f;
-                        pf[g][4 * h + e] = (_Float16)x;
+                        // a weight of 0 takes nothing, of a NaN scale either: that
+                        // touches only the rows that see it
+                        pf[g][4 * h + e] = (_Float16)mul_legacy(p[4 * h + e], vs[e]);
                     }
                 }
+                __builtin_amdgcn_sched_barrier(0);
             }
+            __builtin_amdgcn_sched_barrier(0);  // else the expansions of all tiles are hoisted and spill
             // O^T = V^T P^T; tile j: nibble j of the lane's codes of 8 positions, in pairs
 #pragma unroll
             for (int i = 0; i < VW; ++i) {
@@ -410,7 +487,7 @@ __global__ __launch_bounds__(kWaves* kWave) void cache4_attention_kernel(AttnArg
                     uint32_t lo[4], hi[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const uint32_t v = __builtin_amdgcn_perm(vc[2 * e + 1][i], vc[2 * e][i], sel);
+                        const uint32_t v = __builtin_amdgcn_perm(vw[2 * e + 1][i], vw[2 * e][i], sel);
                         lo[e] = low_codes(v);
                         hi[e] = high_codes(v);
                     }
@@ -419,35 +496,20 @@ __global__ __launch_bounds__(kWaves* kWave) void cache4_attention_kernel(AttnArg
                     const f16x8_t vh = __builtin_bit_cast(f16x8_t, (u32x4_t){hi[0], hi[1], hi[2], hi[3]});
                     o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vl, pf[16 * j / G], o[j], 0, 0, 0);
                     o[j + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vh, pf[16 * (j + 1) / G], o[j + 1], 0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
+            load_v(t0 + kStride);
+            load_pages(t0 + 2 * kStride);
         };
 
-        constexpr int64_t kStride = kWaves * kStep;
-        int64_t t0 = begin + wave * kStep;
+        int t0 = begin + wave * kStep;
         if (t0 < stop) {
-            int pg[2] = {page_of(t0), page_of(t0 + 16)};
-            load(t0, pg);
-            if (t0 + kStride < stop) {
-                pg[0] = page_of(t0 + kStride);
-                pg[1] = page_of(t0 + kStride + 16);
-            }
-            for (; t0 < stop; t0 += kStride) {
-                auto next = [&]() __attribute__((always_inline)) {
-                    const int64_t t1 = t0 + kStride;
-                    if (t1 < stop) {
-                        load(t1, pg);
-                        if (t1 + kStride < stop) {
-                            pg[0] = page_of(t1 + kStride);
-                            pg[1] = page_of(t1 + kStride + 16);
-                        }
-                    }
-                };
-                if (t0 + kStep <= all_see)
-                    step(t0, next, std::true_type{});
-                else
-                    step(t0, next, std::false_type{});
-            }
+            load_pages(t0);
+            load_k(t0);
+            load_v(t0);
+            load_pages(t0 + kStride);
+            for (; t0 < stop; t0 += kStride) step(t0);
         }
 
         // join the waves: 2 and 3 into 0 and 1, then 1 into 0
@@ -490,7 +552,7 @@ __global__ __launch_bounds__(kWaves* kWave) void cache4_attention_kernel(AttnArg
             if (rw.bad) inv = __uint_as_float(0x7fc00000u);
             if (whole) {
                 if (live) {
-                    uint16_t* op = a.out + ((rw.first + qi) * a.q_heads + head) * D + 4 * kg;
+                    uint16_t* op = a.out + ((int64_t)(rw.first + qi) * a.q_heads + head) * D + 4 * kg;
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
                         *reinterpret_cast<uint2*>(op + 16 * j) =
@@ -498,7 +560,7 @@ __global__ __launch_bounds__(kWaves* kWave) void cache4_attention_kernel(AttnArg
                 }
             } else {
                 const int64_t at =
-                    (((b * a.c.heads + kvh) * a.row_tiles + tile) * a.splits + split) * 16 + r16;
+                    ((((int64_t)b * a.c.heads + kvh) * a.row_tiles + tile) * a.splits + split) * 16 + r16;
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
                     *reinterpret_cast<f32x4_t*>(a.part + at * D + 16 * j + 4 * kg) = o[j] * inv;
@@ -528,10 +590,10 @@ __global__ __launch_bounds__(256) void cache4_join_kernel(AttnArgs a)
     const int64_t r0 = tile * 16;
     const int64_t row = r0 + r16;
     if (row >= rw.rows()) return;
-    const int64_t end = rw.end(r0);
-    const int64_t share = share_of(end, a.splits);
+    const int end = rw.end(r0);
+    const int share = share_of(end, a.splits);
     if (end <= share) return;  // written by the attention kernel
-    const int n = (int)((end + share - 1) / share);
+    const int n = (end - 1) / share + 1;
     const int64_t at = ((b * a.c.heads + kvh) * a.row_tiles + tile) * a.splits;
 
     const float2 ml = tid < n ? a.part_ml[(at + tid) * 16 + r16] : make_float2(-INFINITY, 0.0f);
@@ -566,7 +628,7 @@ __global__ __launch_bounds__(256) void cache4_join_kernel(AttnArgs a)
         const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
         const int64_t qi = row / rw.per;
         const int head = kvh * rw.per + (int)(row % rw.per);
-        uint16_t* op = a.out + ((rw.first + qi) * a.q_heads + head) * D + 4 * d4;
+        uint16_t* op = a.out + ((int64_t)(rw.first + qi) * a.q_heads + head) * D + 4 * d4;
         *reinterpret_cast<uint2*>(op) =
             make_uint2(bf16x2(acc[0] * inv, acc[1] * inv), bf16x2(acc[2] * inv, acc[3] * inv));
     }
