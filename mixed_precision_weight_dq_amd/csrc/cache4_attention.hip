@@ -148,7 +148,9 @@ struct AttnArgs {
     int32_t q_heads;
     float scale_log2;
     int32_t row_tiles;  // 16-row tiles per (sequence, kv head) that the grid has
+    int32_t rows_hint;  // rows per (sequence, kv head) that the launch was sized for
     int32_t splits;     // shares of the positions per tile
+    int32_t share;      // positions of a share (share_of)
     float* part;        // splits > 1: normalised partial outputs [unit, split, 16, D]
     float2* part_ml;    // and their maxima and sums [unit, split, 16]
 };
@@ -158,11 +160,13 @@ constexpr int kStep = 32;                   // positions per wave and step
 constexpr int kStride = kWaves * kStep;     // positions per workgroup and step
 constexpr int kMinShare = kStride;          // positions of a share, at least
 
-// Positions per share of a row tile that sees positions [0, end).
-__device__ __forceinline__ int share_of(int end, int splits)
+// Positions per share of a row tile that sees positions [0, end): the launch's
+// share, or more where that many shares would not cover a longer sequence.
+__device__ __forceinline__ int share_of(const AttnArgs& a, int end)
 {
-    const int n = end <= 0 ? 0 : (int)(((unsigned)(end - 1) / (unsigned)splits + kStep) & ~(unsigned)(kStep - 1));
-    return n < kMinShare ? kMinShare : n;
+    if (end <= 0) return a.share;
+    const int n = (int)(((unsigned)(end - 1) / (unsigned)a.splits + kStep) & ~(unsigned)(kStep - 1));
+    return n > a.share ? n : a.share;
 }
 
 // What a workgroup knows of its sequence.  Token rows and positions are below 2^31.
@@ -283,54 +287,14 @@ __global__ __launch_bounds__(kWaves* kWave, D == 64 ? 4 : (D == 128 ? 4 : 2)) vo
         const int head = kvh * rw.per + (int)(row % rw.per);
         const int seen = live ? rw.seen(row) : 0;  // positions that the row sees
         const int end = rw.end(r0);
-        const int share = extra ? (end > 0 ? end : 1) : share_of(end, a.splits);
+        const int share = extra ? (end > 0 ? end : 1) : share_of(a, end);
         const bool whole = end <= share;  // one share: no joining
         const int begin = extra ? 0 : share * split;
         if (begin >= end && split != 0) break;  // nothing for this share, nor for an extra tile
         const int stop = end - begin < share ? end : begin + share;
 
-        // q row -> fp16 operands, scaled by a power of two (and by the sign of
-        // the softmax's scale, so that larger is always larger)
         f16x8_t qf[NC];
-        float logit;
-        {
-            const uint16_t* qp = a.q + (int64_t)(rw.first + qi) * a.q_stride + (int64_t)head * D + 8 * kg;
-            uint4 qr[NC];
-            uint32_t qmax = 0;
-#pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                qr[i] = *reinterpret_cast<const uint4*>(qp + 32 * i);
-                const uint32_t u[4] = {qr[i].x, qr[i].y, qr[i].z, qr[i].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)  // as integers: a NaN is the largest
-                    qmax = max(qmax, max((u[e] << 16) & 0x7fffffffu, u[e] & 0x7fff0000u));
-            }
-            qmax = max(qmax, (uint32_t)__shfl_xor((int)qmax, 16, kWave));
-            qmax = max(qmax, (uint32_t)__shfl_xor((int)qmax, 32, kWave));
-            const int ue = min(14 - exponent(__uint_as_float(qmax)), 126);
-            float up = a.scale_log2 < 0.0f ? -pow2(ue) : pow2(ue);
-            logit = fabsf(a.scale_log2) * pow2(-ue);
-            if (logit == 0.0f) {  // logits of 0 (and no 0 * -inf where positions are hidden)
-                up = 0.0f;
-                logit = 1.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                const uint32_t u[4] = {qr[i].x, qr[i].y, qr[i].z, qr[i].w};
-                float f[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    f[2 * e] = __uint_as_float(u[e] << 16) * up;
-                    f[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u) * up;
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {  // the order of word_codes
-                    qf[i][2 * e] = (_Float16)f[e];
-                    qf[i][2 * e + 1] = (_Float16)f[e + 4];
-                }
-            }
-        }
-
+        float logit = 1.0f;
         float m = -INFINITY, l = 0.0f;
         int ve = -112;  // exponent that the value scales are measured against
         f32x4_t o[NT];
@@ -503,12 +467,55 @@ __global__ __launch_bounds__(kWaves* kWave, D == 64 ? 4 : (D == 128 ? 4 : 2)) vo
             load_pages(t0 + 2 * kStride);
         };
 
+        // the first step's loads go out before q is touched
         int t0 = begin + wave * kStep;
         if (t0 < stop) {
             load_pages(t0);
             load_k(t0);
             load_v(t0);
             load_pages(t0 + kStride);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // q row -> fp16 operands, scaled by a power of two (and by the sign of
+        // the softmax's scale, so that larger is always larger)
+        {
+            const uint16_t* qp = a.q + (int64_t)(rw.first + qi) * a.q_stride + (int64_t)head * D + 8 * kg;
+            uint4 qr[NC];
+            uint32_t qmax = 0;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                qr[i] = *reinterpret_cast<const uint4*>(qp + 32 * i);
+                const uint32_t u[4] = {qr[i].x, qr[i].y, qr[i].z, qr[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)  // as integers: a NaN is the largest
+                    qmax = max(qmax, max((u[e] << 16) & 0x7fffffffu, u[e] & 0x7fff0000u));
+            }
+            qmax = max(qmax, (uint32_t)__shfl_xor((int)qmax, 16, kWave));
+            qmax = max(qmax, (uint32_t)__shfl_xor((int)qmax, 32, kWave));
+            const int ue = min(14 - exponent(__uint_as_float(qmax)), 126);
+            float up = a.scale_log2 < 0.0f ? -pow2(ue) : pow2(ue);
+            logit = fabsf(a.scale_log2) * pow2(-ue);
+            if (logit == 0.0f) {  // logits of 0 (and no 0 * -inf where positions are hidden)
+                up = 0.0f;
+                logit = 1.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const uint32_t u[4] = {qr[i].x, qr[i].y, qr[i].z, qr[i].w};
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    f[2 * e] = __uint_as_float(u[e] << 16) * up;
+                    f[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u) * up;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {  // the order of word_codes
+                    qf[i][2 * e] = (_Float16)f[e];
+                    qf[i][2 * e + 1] = (_Float16)f[e + 4];
+                }
+            }
+        }
+        if (t0 < stop) {
             for (; t0 < stop; t0 += kStride) step(t0);
         }
 
@@ -558,7 +565,7 @@ __global__ __launch_bounds__(kWaves* kWave, D == 64 ? 4 : (D == 128 ? 4 : 2)) vo
                         *reinterpret_cast<uint2*>(op + 16 * j) =
                             make_uint2(bf16x2(o[j][0] * inv, o[j][1] * inv), bf16x2(o[j][2] * inv, o[j][3] * inv));
                 }
-            } else {
+            } else if (live) {
                 const int64_t at =
                     ((((int64_t)b * a.c.heads + kvh) * a.row_tiles + tile) * a.splits + split) * 16 + r16;
 #pragma unroll
@@ -584,14 +591,14 @@ __global__ __launch_bounds__(256) void cache4_join_kernel(AttnArgs a)
     const int tid = threadIdx.x;
     const int64_t b = blockIdx.z;
     const int kvh = blockIdx.y;
-    const int64_t tile = blockIdx.x >> 4;
-    const int r16 = blockIdx.x & 15;
+    const int64_t row = blockIdx.x;
+    const int64_t tile = row >> 4;
+    const int r16 = (int)(row & 15);
     const Rows rw = rows_of(a, b);
     const int64_t r0 = tile * 16;
-    const int64_t row = r0 + r16;
     if (row >= rw.rows()) return;
     const int end = rw.end(r0);
-    const int share = share_of(end, a.splits);
+    const int share = share_of(a, end);
     if (end <= share) return;  // written by the attention kernel
     const int n = (end - 1) / share + 1;
     const int64_t at = ((b * a.c.heads + kvh) * a.row_tiles + tile) * a.splits;
@@ -614,6 +621,7 @@ __global__ __launch_bounds__(256) void cache4_join_kernel(AttnArgs a)
     tot = (red[4] + red[5]) + (red[6] + red[7]);
     f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
     const int d4 = tid % kPer;
+#pragma unroll 8
     for (int s = tid / kPer; s < n; s += kPar) {
         const f32x4_t x = *reinterpret_cast<const f32x4_t*>(a.part + ((at + s) * 16 + r16) * D + 4 * d4);
         const float ws = weight[s];
@@ -634,14 +642,16 @@ __global__ __launch_bounds__(256) void cache4_join_kernel(AttnArgs a)
     }
 }
 
-// The launch's shape: 16-row tiles per (sequence, kv head), and shares of the
-// positions so that about kFill workgroups are in flight, four on each of the
-// 256 CUs, with no share below kMinShare positions.
-constexpr int64_t kFill = 1024;
+// The launch's shape: 16-row tiles per (sequence, kv head), and equal shares of
+// the positions, as many as put about kFill workgroups in flight.
+#ifndef DQ_FILL
+#define DQ_FILL 1024
+#endif
+constexpr int64_t kFill = DQ_FILL;
 constexpr int64_t kMaxSplits = 256;
 
 struct Plan {
-    int64_t tiles, splits, units;
+    int64_t rows, tiles, splits, share;
     size_t part_bytes, ml_bytes;
 };
 
@@ -649,15 +659,17 @@ Plan plan_of(const Cache4& c, int64_t count, int64_t tokens, int q_heads, int64_
 {
     Plan p;
     if (max_q > tokens) max_q = tokens;
-    p.tiles = ceil_div(max_q * (q_heads / c.heads), 16);
+    if (max_len > 0x7fffffffLL) max_len = 0x7fffffffLL;
+    p.rows = max_q * (q_heads / c.heads);
+    p.tiles = ceil_div(p.rows, 16);
     if (p.tiles > 65535) p.tiles = 65535;
-    p.units = count * c.heads * p.tiles;
-    const int64_t most = ceil_div(max_len, kMinShare);
-    p.splits = kFill / p.units;
-    if (p.splits > most) p.splits = most;
-    if (p.splits > kMaxSplits) p.splits = kMaxSplits;
-    if (p.splits < 1) p.splits = 1;
-    const size_t rows = p.splits > 1 ? (size_t)(p.units * p.splits) * 16 : 0;
+    const int64_t units = count * c.heads * p.tiles;
+    int64_t splits = kFill / units;
+    if (splits < 1) splits = 1;
+    if (splits > kMaxSplits) splits = kMaxSplits;
+    p.share = ceil_div(ceil_div(max_len, splits), kMinShare) * kMinShare;
+    p.splits = ceil_div(max_len, p.share);
+    const size_t rows = p.splits > 1 ? (size_t)(units * p.splits) * 16 : 0;
     p.part_bytes = rows * c.dim * sizeof(float);
     p.ml_bytes = rows * sizeof(float2);
     return p;
@@ -669,7 +681,7 @@ hipError_t launch_dg(const AttnArgs& a, hipStream_t stream)
     const dim3 grid((unsigned)(a.row_tiles * a.splits), (unsigned)a.c.heads, (unsigned)a.bt.count);
     cache4_attention_kernel<D, G><<<grid, kWaves * kWave, 0, stream>>>(a);
     if (a.splits > 1) {
-        const dim3 jgrid((unsigned)(a.row_tiles * 16), (unsigned)a.c.heads, (unsigned)a.bt.count);
+        const dim3 jgrid((unsigned)a.rows_hint, (unsigned)a.c.heads, (unsigned)a.bt.count);
         cache4_join_kernel<D><<<jgrid, 256, 0, stream>>>(a);
     }
     return hipGetLastError();
@@ -691,7 +703,8 @@ hipError_t launch_cache4_attention(const Cache4& c, const Cache4Batch& bt, const
 {
     const Plan p = plan_of(c, bt.count, tokens, q_heads, max_q, max_len);
     const AttnArgs a{c, bt, q, q_stride, out, tokens, q_heads, scale * kLog2e, (int32_t)p.tiles,
-                     (int32_t)p.splits, static_cast<float*>(workspace),
+                     (int32_t)(p.rows < p.tiles * 16 ? p.rows : p.tiles * 16), (int32_t)p.splits,
+                     (int32_t)p.share, static_cast<float*>(workspace),
                      reinterpret_cast<float2*>(static_cast<char*>(workspace) + p.part_bytes)};
     switch (c.dim * 1000 + c.group) {
     case 64032: return launch_dg<64, 32>(a, stream);
