@@ -147,27 +147,15 @@ struct AttnArgs {
     int64_t tokens;
     int32_t q_heads;
     float scale_log2;
-    int32_t row_tiles;  // 16-row tiles per (sequence, kv head) that the grid has
-    int32_t rows_hint;  // rows per (sequence, kv head) that the launch was sized for
-    int32_t splits;     // shares of the positions per tile
-    int32_t share;      // positions of a share (share_of)
-    float* part;        // splits > 1: normalised partial outputs [unit, split, 16, D]
-    float2* part_ml;    // and their maxima and sums [unit, split, 16]
+    float* part;      // unfinished tiles: normalised outputs [workgroup, 2, 16, D]
+    float2* part_ml;  // and their maxima and sums [workgroup, 2, 16]
+    int32_t groups;   // workgroups of the attention kernel
 };
 
 constexpr int kWaves = 4;
-constexpr int kStep = 32;                   // positions per wave and step
-constexpr int kStride = kWaves * kStep;     // positions per workgroup and step
-constexpr int kMinShare = kStride;          // positions of a share, at least
-
-// Positions per share of a row tile that sees positions [0, end): the launch's
-// share, or more where that many shares would not cover a longer sequence.
-__device__ __forceinline__ int share_of(const AttnArgs& a, int end)
-{
-    if (end <= 0) return a.share;
-    const int n = (int)(((unsigned)(end - 1) / (unsigned)a.splits + kStep) & ~(unsigned)(kStep - 1));
-    return n > a.share ? n : a.share;
-}
+constexpr int kThreads = kWaves * kWave;
+constexpr int kStep = 32;                // positions per wave and step
+constexpr int kStride = kWaves * kStep;  // positions per workgroup and step
 
 // What a workgroup knows of its sequence.  Token rows and positions are below 2^31.
 struct Rows {
@@ -198,6 +186,100 @@ __device__ __forceinline__ Rows rows_of(const AttnArgs& a, int64_t b)
     return r;
 }
 
+// The work of a call as one line of steps: sequence by sequence, in it unit by
+// unit (a kv head's 16-row tile, tiles of a head next to each other), in that
+// the sequence's steps of kStride positions (at least one, which writes rows that
+// see nothing).  Workgroup w takes an equal stretch of the line, so lengths do
+// not have to be equal, nor known to the host, for the CUs to be.
+struct Line {
+    int64_t total;   // steps of the call
+    int64_t q, r;    // a workgroup's steps: q + 1 for the first r, else q
+    int64_t before;  // steps before the found sequence
+    int b;           // the found sequence
+    __device__ __forceinline__ int64_t first(int64_t w) const { return w * q + (w < r ? w : r); }
+    // the workgroup that has step x
+    __device__ __forceinline__ int64_t group_of(int64_t x) const
+    {
+        const int64_t big = r * (q + 1);
+        return x < big ? x / (q + 1) : r + (x - big) / q;
+    }
+};
+
+__device__ __forceinline__ int steps_of(const Rows& rw) { return rw.len > 0 ? (rw.len - 1) / kStride + 1 : 1; }
+__device__ __forceinline__ int64_t tiles_of(const Rows& rw) { return (rw.rows() + 15) >> 4; }
+__device__ __forceinline__ int64_t line_steps(const AttnArgs& a, const Rows& rw)
+{
+    return tiles_of(rw) * a.c.heads * steps_of(rw);
+}
+
+// Lays the line out and finds the sequence of workgroup w's first step (b < 0:
+// it has none), or, given a sequence, the steps before it.  Every thread of
+// the workgroup takes part: each adds up a run of sequences, a scan joins them.
+template <bool kFind>
+__device__ __forceinline__ Line lay_line(const AttnArgs& a, int64_t w, int b)
+{
+    __shared__ int64_t wave_sum[kWaves];
+    __shared__ int64_t found[2];
+    Line ln;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+    const int64_t count = a.bt.count;
+    const int64_t run = (count + kThreads - 1) / kThreads;
+    const int64_t lo = run * tid < count ? run * tid : count;
+    const int64_t hi = lo + run < count ? lo + run : count;
+    int64_t mine = 0, to_b = 0;
+    for (int64_t i = lo; i < hi; ++i) {
+        if (!kFind && i == b) to_b = mine;
+        mine += line_steps(a, rows_of(a, i));
+    }
+    int64_t upto = mine;  // inclusive scan over the wave
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+        const int64_t t = __shfl_up(upto, o, kWave);
+        if (lane >= o) upto += t;
+    }
+    if (lane == kWave - 1) wave_sum[wave] = upto;
+    if (tid == 0) found[0] = -1;
+    __syncthreads();
+    int64_t base = 0;
+    ln.total = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+        if (i < wave) base += wave_sum[i];
+        ln.total += wave_sum[i];
+    }
+    ln.q = ln.total / a.groups;
+    ln.r = ln.total % a.groups;
+    int64_t before = base + upto - mine;
+    if (kFind) {
+        const int64_t x = ln.first(w);
+        if (x >= before && x < before + mine) {
+            for (int64_t i = lo; i < hi; ++i) {
+                const int64_t n = line_steps(a, rows_of(a, i));
+                if (x < before + n) {
+                    found[0] = i;
+                    found[1] = before;
+                    break;
+                }
+                before += n;
+            }
+        }
+    } else if (b >= lo && b < hi) {
+        found[0] = b;
+        found[1] = before + to_b;
+    }
+    __syncthreads();
+    ln.b = __builtin_amdgcn_readfirstlane((int)found[0]);
+    ln.before = found[1];
+    return ln;
+}
+
+__device__ __forceinline__ int64_t uniform64(int64_t v)
+{
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
 __device__ __forceinline__ uint32_t bf16x2(float a, float b)
 {
     return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)a) |
@@ -224,11 +306,11 @@ __device__ __forceinline__ void load_n(__amdgpu_buffer_rsrc_t rs, uint32_t off, 
     }
 }
 
-// One workgroup of four waves per (16-row tile, share of the positions, kv
-// head, sequence): wave w takes steps w, w + 4, ... of the share, and the four
-// partial results are joined through LDS in a fixed order.  A tile whose
-// positions are one share is written out here; otherwise the shares are joined
-// by cache4_join_kernel, in order.
+// A workgroup of four waves walks its stretch of the line: in each unit wave w
+// takes 32 of a step's 128 positions, and the four partial results are
+// joined through LDS in a fixed order.  A unit that the workgroup has whole is
+// written out here; the (at most two) that it shares with its neighbours go to
+// the workspace and are joined by cache4_join_kernel, in order.
 //
 // A step's loads are issued a step ahead, as soon as the registers that they
 // fill are free, its page numbers two steps ahead (scalar loads).  Codes come
@@ -238,7 +320,7 @@ __device__ __forceinline__ void load_n(__amdgpu_buffer_rsrc_t rs, uint32_t off, 
 // page, so its four arrays are buffers with scalar bases, and a lane's place
 // in them is the same in every step.
 template <int D, int G>
-__global__ __launch_bounds__(kWaves* kWave, D == 64 ? 4 : (D == 128 ? 4 : 2)) void cache4_attention_kernel(AttnArgs a)
+__global__ __launch_bounds__(kThreads, D == 256 ? 2 : 4) void cache4_attention_kernel(AttnArgs a)
 {
     constexpr int NC = D / 32;  // 32-dimension steps of a dot product
     constexpr int NG = D / G;   // groups of a head
@@ -254,17 +336,7 @@ __global__ __launch_bounds__(kWaves* kWave, D == 64 ? 4 : (D == 128 ? 4 : 2)) vo
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int r16 = lane & 15;
     const int kg = lane >> 4;
-    const int b = blockIdx.z;
-    const int kvh = blockIdx.y;
-    const int split = blockIdx.x % (unsigned)a.splits;
-    const int tile0 = blockIdx.x / (unsigned)a.splits;
     const int shift = a.c.page_shift;
-    const Rows rw = rows_of(a, b);
-    const int64_t rows = rw.rows();
-    // constant address space: scalar loads, which leave the count of vector
-    // loads in flight alone
-    const __attribute__((address_space(4))) int32_t* table =
-        (const __attribute__((address_space(4))) int32_t*)(a.bt.table + b * a.bt.width);
 
     // byte offsets of this lane's data in 16 positions of one head
     const uint32_t k_lane = r16 * (D / 2) + kg * NC * 4;
@@ -276,22 +348,46 @@ __global__ __launch_bounds__(kWaves* kWave, D == 64 ? 4 : (D == 128 ? 4 : 2)) vo
         s_lane[i] = (((uint32_t)g << shift) + r16) * 4;
     }
 
-    // tiles past the grid's are one share each, walked by the grid's last tile
-    for (int64_t tile = tile0; tile * 16 < rows; ++tile) {
-        const bool extra = tile >= a.row_tiles;
-        if (extra && split != 0) break;
+    // consecutive stretches (which may read the same keys) on one XCD
+    const int group = (a.groups & 7) == 0 ? (int)(blockIdx.x & 7) * (a.groups >> 3) + (int)(blockIdx.x >> 3)
+                                          : (int)blockIdx.x;
+    const Line ln = lay_line<true>(a, group, 0);
+    const int64_t x0 = uniform64(ln.first(group)), x1 = uniform64(ln.first(group + 1));
+    int b = ln.b;
+    int64_t before = uniform64(ln.before);
+    if (b < 0) return;
+
+    for (int64_t x = x0; x < x1;) {
+        const Rows rw = rows_of(a, b);
+        const int steps = steps_of(rw);
+        const int64_t tiles = tiles_of(rw);
+        if (x >= before + tiles * a.c.heads * steps) {
+            before += tiles * a.c.heads * steps;
+            ++b;
+            continue;
+        }
+        const int64_t unit = (x - before) / steps;
+        const int step0 = (int)(x - before - unit * steps);
+        const int take = (int)(x1 - x < steps - step0 ? x1 - x : steps - step0);
+        const bool whole = take == steps;
+        const int slot = x == x0 ? 0 : 1;
+        const int kvh = (int)(unit / tiles);
+        const int64_t tile = unit - kvh * tiles;
         const int64_t r0 = tile * 16;
+        const int64_t rows = rw.rows();
         const bool live = r0 + r16 < rows;
         const int64_t row = live ? r0 + r16 : 0;
         const int qi = (int)(row / rw.per);
         const int head = kvh * rw.per + (int)(row % rw.per);
         const int seen = live ? rw.seen(row) : 0;  // positions that the row sees
         const int end = rw.end(r0);
-        const int share = extra ? (end > 0 ? end : 1) : share_of(a, end);
-        const bool whole = end <= share;  // one share: no joining
-        const int begin = extra ? 0 : share * split;
-        if (begin >= end && split != 0) break;  // nothing for this share, nor for an extra tile
-        const int stop = end - begin < share ? end : begin + share;
+        const int begin = step0 * kStride;
+        const int stop = end < begin + take * kStride ? end : begin + take * kStride;
+        x += take;
+        // constant address space: scalar loads, which leave the count of vector
+        // loads in flight alone
+        const __attribute__((address_space(4))) int32_t* table =
+            (const __attribute__((address_space(4))) int32_t*)(a.bt.table + b * a.bt.width);
 
         f16x8_t qf[NC];
         float logit = 1.0f;
@@ -441,6 +537,8 @@ __global__ __launch_bounds__(kWaves* kWave, D == 64 ? 4 : (D == 128 ? 4 : 2)) vo
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
+            // page numbers after the step's last LDS read: a wait for one waits for both
+            load_pages(t0 + 2 * kStride);
             __builtin_amdgcn_sched_barrier(0);  // else the expansions of all tiles are hoisted and spill
             // O^T = V^T P^T; tile j: nibble j of the lane's codes of 8 positions, in pairs
 #pragma unroll
@@ -464,7 +562,6 @@ __global__ __launch_bounds__(kWaves* kWave, D == 64 ? 4 : (D == 128 ? 4 : 2)) vo
                 }
             }
             load_v(t0 + kStride);
-            load_pages(t0 + 2 * kStride);
         };
 
         // the first step's loads go out before q is touched
@@ -566,92 +663,157 @@ __global__ __launch_bounds__(kWaves* kWave, D == 64 ? 4 : (D == 128 ? 4 : 2)) vo
                             make_uint2(bf16x2(o[j][0] * inv, o[j][1] * inv), bf16x2(o[j][2] * inv, o[j][3] * inv));
                 }
             } else if (live) {
-                const int64_t at =
-                    ((((int64_t)b * a.c.heads + kvh) * a.row_tiles + tile) * a.splits + split) * 16 + r16;
+                const int64_t at = ((int64_t)group * 2 + slot) * 16 + r16;
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
                     *reinterpret_cast<f32x4_t*>(a.part + at * D + 16 * j + 4 * kg) = o[j] * inv;
                 if (kg == 0) a.part_ml[at] = make_float2(m, l);
             }
         }
-        if (tile + 1 < a.row_tiles) break;
-        __syncthreads();  // the join buffers are free for the next extra tile
+        __syncthreads();  // the join buffers are free for the next unit
     }
 }
 
-// Joins the shares of one row: out = sum_s w_s o_s / sum_s w_s, w_s = l_s 2^(m_s - max m).
+// Joins the parts of a unit's rows: out = sum_s w_s o_s / sum_s w_s, w_s = l_s
+// 2^(m_s - max m), s over the workgroups that share it.  Two forms:
+// cache4_join_kernel, one workgroup per row (of a sequence's new tokens and a kv
+// head's query heads), kv head and sequence, for few units of many parts; and
+// cache4_join_edges_kernel, one per neighbouring pair of stretches, for so many
+// units that each has only a part or two.
 template <int D>
-__global__ __launch_bounds__(256) void cache4_join_kernel(AttnArgs a)
+__global__ __launch_bounds__(kThreads) void cache4_join_kernel(AttnArgs a)
 {
-    constexpr int kPer = D / 4;       // threads of a share: four dimensions each
-    constexpr int kPar = 256 / kPer;  // shares in flight
-    __shared__ float weight[256];
-    __shared__ float red[8];
-    __shared__ __attribute__((aligned(16))) f32x4_t sums[256];
+    constexpr int kPer = D / 4;            // threads of a part: four dimensions each
+    constexpr int kPar = kThreads / kPer;  // parts in flight
+    __shared__ float weight[kThreads];
+    __shared__ float red[2 * kWaves];
+    __shared__ __attribute__((aligned(16))) f32x4_t sums[kThreads];
     const int tid = threadIdx.x;
-    const int64_t b = blockIdx.z;
+    const int b = blockIdx.z;
     const int kvh = blockIdx.y;
-    const int64_t row = blockIdx.x;
-    const int64_t tile = row >> 4;
-    const int r16 = (int)(row & 15);
     const Rows rw = rows_of(a, b);
-    const int64_t r0 = tile * 16;
-    if (row >= rw.rows()) return;
-    const int end = rw.end(r0);
-    const int share = share_of(a, end);
-    if (end <= share) return;  // written by the attention kernel
-    const int n = (end - 1) / share + 1;
-    const int64_t at = ((b * a.c.heads + kvh) * a.row_tiles + tile) * a.splits;
-
-    const float2 ml = tid < n ? a.part_ml[(at + tid) * 16 + r16] : make_float2(-INFINITY, 0.0f);
-    float mx = ml.x;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o, kWave));
-    if ((tid & 63) == 0) red[tid >> 6] = mx;
-    __syncthreads();
-    mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const float base = mx == -INFINITY ? 0.0f : mx;
-    const float w = ml.y == 0.0f ? 0.0f : ml.y * __builtin_amdgcn_exp2f(ml.x - base);
-    weight[tid] = w;
-    float tot = w;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) tot += __shfl_xor(tot, o, kWave);
-    if ((tid & 63) == 0) red[4 + (tid >> 6)] = tot;
-    __syncthreads();
-    tot = (red[4] + red[5]) + (red[6] + red[7]);
-    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+    if ((int64_t)blockIdx.x >= rw.rows()) return;
+    const Line ln = lay_line<false>(a, 0, b);
+    const int steps = steps_of(rw);
+    const int64_t tiles = tiles_of(rw);
     const int d4 = tid % kPer;
+
+    for (int64_t row = blockIdx.x; row < rw.rows(); row += gridDim.x) {
+        const int r16 = (int)(row & 15);
+        const int64_t x = ln.before + (kvh * tiles + (row >> 4)) * steps;
+        const int64_t g0 = ln.group_of(x), g1 = ln.group_of(x + steps - 1);
+        if (g0 == g1) continue;  // written by the attention kernel
+        const int64_t n = g1 - g0 + 1;
+        // a workgroup whose stretch begins in the unit has it in its slot 0
+        const auto slot_of = [&](int64_t s) { return ((g0 + s) * 2 + (s == 0 && ln.first(g0) != x)) * 16 + r16; };
+        float mx = -INFINITY;
+        for (int64_t s = tid; s < n; s += kThreads) mx = fmaxf(mx, a.part_ml[slot_of(s)].x);
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o, kWave));
+        if ((tid & 63) == 0) red[tid >> 6] = mx;
+        __syncthreads();
+        mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+        const float base = mx == -INFINITY ? 0.0f : mx;
+        float tot = 0.0f;
+        f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+        for (int64_t s0 = 0; s0 < n; s0 += kThreads) {
+            const float2 ml = s0 + tid < n ? a.part_ml[slot_of(s0 + tid)] : make_float2(-INFINITY, 0.0f);
+            const float w = ml.y == 0.0f ? 0.0f : ml.y * __builtin_amdgcn_exp2f(ml.x - base);
+            __syncthreads();  // the weights before are used up
+            weight[tid] = w;
+            tot += w;
+            __syncthreads();
+            const int here = (int)(n - s0 < kThreads ? n - s0 : kThreads);
 #pragma unroll 8
-    for (int s = tid / kPer; s < n; s += kPar) {
-        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(a.part + ((at + s) * 16 + r16) * D + 4 * d4);
-        const float ws = weight[s];
+            for (int s = tid / kPer; s < here; s += kPar) {
+                const f32x4_t v = *reinterpret_cast<const f32x4_t*>(a.part + slot_of(s0 + s) * D + 4 * d4);
+                const float ws = weight[s];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = fmaf(ws, x[e], acc[e]);
-    }
-    sums[tid] = acc;
-    __syncthreads();
-    if (tid < kPer) {
+                for (int e = 0; e < 4; ++e) acc[e] = fmaf(ws, v[e], acc[e]);
+            }
+        }
 #pragma unroll
-        for (int i = 1; i < kPar; ++i) acc += sums[i * kPer + tid];
-        const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
-        const int64_t qi = row / rw.per;
-        const int head = kvh * rw.per + (int)(row % rw.per);
-        uint16_t* op = a.out + ((int64_t)(rw.first + qi) * a.q_heads + head) * D + 4 * d4;
-        *reinterpret_cast<uint2*>(op) =
-            make_uint2(bf16x2(acc[0] * inv, acc[1] * inv), bf16x2(acc[2] * inv, acc[3] * inv));
+        for (int o = 32; o > 0; o >>= 1) tot += __shfl_xor(tot, o, kWave);
+        if ((tid & 63) == 0) red[kWaves + (tid >> 6)] = tot;
+        sums[tid] = acc;
+        __syncthreads();
+        if (tid < kPer) {
+            tot = (red[kWaves] + red[kWaves + 1]) + (red[kWaves + 2] + red[kWaves + 3]);
+#pragma unroll
+            for (int i = 1; i < kPar; ++i) acc += sums[i * kPer + tid];
+            const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
+            const int qi = (int)(row / rw.per);
+            const int head = kvh * rw.per + (int)(row % rw.per);
+            uint16_t* op = a.out + ((int64_t)(rw.first + qi) * a.q_heads + head) * D + 4 * d4;
+            *reinterpret_cast<uint2*>(op) =
+                make_uint2(bf16x2(acc[0] * inv, acc[1] * inv), bf16x2(acc[2] * inv, acc[3] * inv));
+        }
+        __syncthreads();
     }
 }
 
-// The launch's shape: 16-row tiles per (sequence, kv head), and equal shares of
-// the positions, as many as put about kFill workgroups in flight.
+template <int D>
+__global__ __launch_bounds__(kThreads) void cache4_join_edges_kernel(AttnArgs a)
+{
+    constexpr int N = D / 16;  // dimensions of a thread
+    const int64_t w = (int64_t)blockIdx.x + 1;
+    const Line ln = lay_line<true>(a, w, 0);
+    if (ln.b < 0) return;
+    const int64_t x = ln.first(w);
+    const Rows rw = rows_of(a, ln.b);
+    const int steps = steps_of(rw);
+    const int64_t unit = (x - ln.before) / steps;
+    const int64_t start = ln.before + unit * steps;
+    // the unit's second stretch joins it
+    if (x == start || x >= ln.total || ln.group_of(start) != w - 1) return;
+    const int64_t n = ln.group_of(start + steps - 1) - w + 2;
+    const int64_t tiles = tiles_of(rw);
+    const int kvh = (int)(unit / tiles);
+    const int r16 = threadIdx.x >> 4;
+    const int64_t row = (unit - kvh * tiles) * 16 + r16;
+    if (row >= rw.rows()) return;
+    const int d = (threadIdx.x & 15) * N;
+    const auto slot_of = [&](int64_t s) {
+        return ((w - 1 + s) * 2 + (s == 0 && ln.first(w - 1) != start)) * 16 + r16;
+    };
+    float mx = -INFINITY;
+    for (int64_t s = 0; s < n; ++s) mx = fmaxf(mx, a.part_ml[slot_of(s)].x);
+    const float base = mx == -INFINITY ? 0.0f : mx;
+    float tot = 0.0f;
+    float acc[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) acc[e] = 0.0f;
+    for (int64_t s = 0; s < n; ++s) {
+        const float2 ml = a.part_ml[slot_of(s)];
+        const float ws = ml.y == 0.0f ? 0.0f : ml.y * __builtin_amdgcn_exp2f(ml.x - base);
+        tot += ws;
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const f32x4_t v = *reinterpret_cast<const f32x4_t*>(a.part + slot_of(s) * D + d + i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i + e] = fmaf(ws, v[e], acc[i + e]);
+        }
+    }
+    const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
+    const int qi = (int)(row / rw.per);
+    const int head = kvh * rw.per + (int)(row % rw.per);
+    uint16_t* op = a.out + ((int64_t)(rw.first + qi) * a.q_heads + head) * D + d;
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+        *reinterpret_cast<uint2*>(op + i) = make_uint2(bf16x2(acc[i] * inv, acc[i + 1] * inv),
+                                                       bf16x2(acc[i + 2] * inv, acc[i + 3] * inv));
+}
+
+// The launch's shape: as many workgroups as fill the 256 CUs four deep (two
+// for heads of 256, whose registers and LDS allow no more), fewer where there
+// are not that many steps.
 #ifndef DQ_FILL
 #define DQ_FILL 1024
 #endif
 constexpr int64_t kFill = DQ_FILL;
-constexpr int64_t kMaxSplits = 256;
 
 struct Plan {
-    int64_t rows, tiles, splits, share;
+    int64_t rows, units, groups;
     size_t part_bytes, ml_bytes;
 };
 
@@ -661,28 +823,26 @@ Plan plan_of(const Cache4& c, int64_t count, int64_t tokens, int q_heads, int64_
     if (max_q > tokens) max_q = tokens;
     if (max_len > 0x7fffffffLL) max_len = 0x7fffffffLL;
     p.rows = max_q * (q_heads / c.heads);
-    p.tiles = ceil_div(p.rows, 16);
-    if (p.tiles > 65535) p.tiles = 65535;
-    const int64_t units = count * c.heads * p.tiles;
-    int64_t splits = kFill / units;
-    if (splits < 1) splits = 1;
-    if (splits > kMaxSplits) splits = kMaxSplits;
-    p.share = ceil_div(ceil_div(max_len, splits), kMinShare) * kMinShare;
-    p.splits = ceil_div(max_len, p.share);
-    const size_t rows = p.splits > 1 ? (size_t)(units * p.splits) * 16 : 0;
-    p.part_bytes = rows * c.dim * sizeof(float);
-    p.ml_bytes = rows * sizeof(float2);
+    p.units = count * c.heads * ceil_div(p.rows, 16);
+    const int64_t fill = c.dim == 256 ? kFill / 2 : kFill;
+    p.groups = p.units > fill ? fill : p.units * ceil_div(max_len, kStride);
+    if (p.groups > fill) p.groups = fill;
+    p.part_bytes = (size_t)p.groups * 2 * 16 * c.dim * sizeof(float);
+    p.ml_bytes = (size_t)p.groups * 2 * 16 * sizeof(float2);
     return p;
 }
 
 template <int D, int G>
-hipError_t launch_dg(const AttnArgs& a, hipStream_t stream)
+hipError_t launch_dg(const AttnArgs& a, const Plan& p, hipStream_t stream)
 {
-    const dim3 grid((unsigned)(a.row_tiles * a.splits), (unsigned)a.c.heads, (unsigned)a.bt.count);
-    cache4_attention_kernel<D, G><<<grid, kWaves * kWave, 0, stream>>>(a);
-    if (a.splits > 1) {
-        const dim3 jgrid((unsigned)a.rows_hint, (unsigned)a.c.heads, (unsigned)a.bt.count);
-        cache4_join_kernel<D><<<jgrid, 256, 0, stream>>>(a);
+    cache4_attention_kernel<D, G><<<(unsigned)a.groups, kThreads, 0, stream>>>(a);
+    if (a.groups > 1) {
+        if (p.units * 2 > a.groups) {
+            cache4_join_edges_kernel<D><<<(unsigned)a.groups - 1, kThreads, 0, stream>>>(a);
+        } else {
+            const dim3 jgrid((unsigned)p.rows, (unsigned)a.c.heads, (unsigned)a.bt.count);
+            cache4_join_kernel<D><<<jgrid, kThreads, 0, stream>>>(a);
+        }
     }
     return hipGetLastError();
 }
@@ -702,19 +862,19 @@ hipError_t launch_cache4_attention(const Cache4& c, const Cache4Batch& bt, const
                                    hipStream_t stream)
 {
     const Plan p = plan_of(c, bt.count, tokens, q_heads, max_q, max_len);
-    const AttnArgs a{c, bt, q, q_stride, out, tokens, q_heads, scale * kLog2e, (int32_t)p.tiles,
-                     (int32_t)(p.rows < p.tiles * 16 ? p.rows : p.tiles * 16), (int32_t)p.splits,
-                     (int32_t)p.share, static_cast<float*>(workspace),
-                     reinterpret_cast<float2*>(static_cast<char*>(workspace) + p.part_bytes)};
+    const AttnArgs a{c, bt, q, q_stride, out, tokens, q_heads, scale * kLog2e,
+                     static_cast<float*>(workspace),
+                     reinterpret_cast<float2*>(static_cast<char*>(workspace) + p.part_bytes),
+                     (int32_t)p.groups};
     switch (c.dim * 1000 + c.group) {
-    case 64032: return launch_dg<64, 32>(a, stream);
-    case 64064: return launch_dg<64, 64>(a, stream);
-    case 128032: return launch_dg<128, 32>(a, stream);
-    case 128064: return launch_dg<128, 64>(a, stream);
-    case 128128: return launch_dg<128, 128>(a, stream);
-    case 256032: return launch_dg<256, 32>(a, stream);
-    case 256064: return launch_dg<256, 64>(a, stream);
-    case 256128: return launch_dg<256, 128>(a, stream);
+    case 64032: return launch_dg<64, 32>(a, p, stream);
+    case 64064: return launch_dg<64, 64>(a, p, stream);
+    case 128032: return launch_dg<128, 32>(a, p, stream);
+    case 128064: return launch_dg<128, 64>(a, p, stream);
+    case 128128: return launch_dg<128, 128>(a, p, stream);
+    case 256032: return launch_dg<256, 32>(a, p, stream);
+    case 256064: return launch_dg<256, 64>(a, p, stream);
+    case 256128: return launch_dg<256, 128>(a, p, stream);
     default: return hipErrorInvalidValue;
     }
 }
