@@ -157,6 +157,14 @@ constexpr int kThreads = kWaves * kWave;
 constexpr int kStep = 32;                // positions per wave and step
 constexpr int kStride = kWaves * kStep;  // positions per workgroup and step
 
+// a / b of values that are not negative: the 64-bit division is some hundred
+// instructions, and these nearly always fit 32 bits.
+__device__ __forceinline__ int64_t udiv(int64_t a, int64_t b)
+{
+    if ((((uint64_t)a | (uint64_t)b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
+}
+
 // What a workgroup knows of its sequence.  Token rows and positions are below 2^31.
 struct Rows {
     int first, nq, len;  // first token row, new tokens, cached tokens
@@ -164,7 +172,7 @@ struct Rows {
     int per;             // query heads of a kv head
     __device__ __forceinline__ int64_t rows() const { return (int64_t)nq * per; }
     // positions seen by row r (a new token's head)
-    __device__ __forceinline__ int seen(int64_t r) const { return len - nq + (int)(r / per) + 1; }
+    __device__ __forceinline__ int seen(int64_t r) const { return len - nq + (int)udiv(r, per) + 1; }
     // positions seen by the last row of the tile that starts at row r0
     __device__ __forceinline__ int end(int64_t r0) const
     {
@@ -195,13 +203,14 @@ struct Line {
     int64_t total;   // steps of the call
     int64_t q, r;    // a workgroup's steps: q + 1 for the first r, else q
     int64_t before;  // steps before the found sequence
-    int b;           // the found sequence
+    int b;           // the found sequence (-1: none)
+    Rows rw;         // its rows
     __device__ __forceinline__ int64_t first(int64_t w) const { return w * q + (w < r ? w : r); }
     // the workgroup that has step x
     __device__ __forceinline__ int64_t group_of(int64_t x) const
     {
         const int64_t big = r * (q + 1);
-        return x < big ? x / (q + 1) : r + (x - big) / q;
+        return x < big ? udiv(x, q + 1) : r + udiv(x - big, q);
     }
 };
 
@@ -212,11 +221,54 @@ __device__ __forceinline__ int64_t line_steps(const AttnArgs& a, const Rows& rw)
     return tiles_of(rw) * a.c.heads * steps_of(rw);
 }
 
+__device__ __forceinline__ int64_t lane64(int64_t v, int lane)
+{
+    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, lane);
+    const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(v >> 32), lane);
+    return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
 // Lays the line out and finds the sequence of workgroup w's first step (b < 0:
 // it has none), or, given a sequence, the steps before it.  Every thread of
-// the workgroup takes part: each adds up a run of sequences, a scan joins them.
+// the workgroup takes part.  Up to 64 sequences: a lane each, every wave for
+// itself, one round of loads and no barrier (a launch's workgroups all start
+// here, so nothing else hides it).  More: each thread adds up a run of
+// sequences, and a scan over the workgroup joins the runs.
 template <bool kFind>
-__device__ __forceinline__ Line lay_line(const AttnArgs& a, int64_t w, int b)
+__device__ __forceinline__ Line lay_line_short(const AttnArgs& a, int64_t w, int b)
+{
+    Line ln;
+    const int lane = threadIdx.x & (kWave - 1);
+    const bool in = lane < a.bt.count;
+    const Rows mine = rows_of(a, in ? lane : 0);
+    const int64_t n = in ? line_steps(a, mine) : 0;
+    int64_t upto = n;
+    for (int o = 1; o < a.bt.count; o <<= 1) {
+        const int64_t t = __shfl_up(upto, o, kWave);
+        if (lane >= o) upto += t;
+    }
+    ln.total = lane64(upto, (int)a.bt.count - 1);
+    ln.q = udiv(ln.total, a.groups);
+    ln.r = ln.total - ln.q * a.groups;
+    if (kFind) {
+        const int64_t x = ln.first(w);
+        const uint64_t at = __ballot(x >= upto - n && x < upto);
+        ln.b = at ? (int)__builtin_ctzll(at) : -1;
+    } else {
+        ln.b = b;
+    }
+    const int from = ln.b < 0 ? 0 : ln.b;
+    ln.before = lane64(upto - n, from);
+    ln.rw.first = __builtin_amdgcn_readlane(mine.first, from);
+    ln.rw.nq = __builtin_amdgcn_readlane(mine.nq, from);
+    ln.rw.len = __builtin_amdgcn_readlane(mine.len, from);
+    ln.rw.bad = __builtin_amdgcn_readlane((int)mine.bad, from) != 0;
+    ln.rw.per = mine.per;
+    return ln;
+}
+
+template <bool kFind>
+__device__ __forceinline__ Line lay_line_long(const AttnArgs& a, int64_t w, int b)
 {
     __shared__ int64_t wave_sum[kWaves];
     __shared__ int64_t found[2];
@@ -247,8 +299,8 @@ __device__ __forceinline__ Line lay_line(const AttnArgs& a, int64_t w, int b)
         if (i < wave) base += wave_sum[i];
         ln.total += wave_sum[i];
     }
-    ln.q = ln.total / a.groups;
-    ln.r = ln.total % a.groups;
+    ln.q = udiv(ln.total, a.groups);
+    ln.r = ln.total - ln.q * a.groups;
     int64_t before = base + upto - mine;
     if (kFind) {
         const int64_t x = ln.first(w);
@@ -270,7 +322,14 @@ __device__ __forceinline__ Line lay_line(const AttnArgs& a, int64_t w, int b)
     __syncthreads();
     ln.b = __builtin_amdgcn_readfirstlane((int)found[0]);
     ln.before = found[1];
+    ln.rw = rows_of(a, ln.b < 0 ? 0 : ln.b);
     return ln;
+}
+
+template <bool kFind>
+__device__ __forceinline__ Line lay_line(const AttnArgs& a, int64_t w, int b)
+{
+    return a.bt.count <= kWave ? lay_line_short<kFind>(a, w, b) : lay_line_long<kFind>(a, w, b);
 }
 
 __device__ __forceinline__ int64_t uniform64(int64_t v)
@@ -357,28 +416,29 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 2 : 4) void cache4_attention_k
     int64_t before = uniform64(ln.before);
     if (b < 0) return;
 
+    Rows rw = ln.rw;
     for (int64_t x = x0; x < x1;) {
-        const Rows rw = rows_of(a, b);
         const int steps = steps_of(rw);
         const int64_t tiles = tiles_of(rw);
         if (x >= before + tiles * a.c.heads * steps) {
             before += tiles * a.c.heads * steps;
             ++b;
+            rw = rows_of(a, b);
             continue;
         }
-        const int64_t unit = (x - before) / steps;
+        const int64_t unit = udiv(x - before, steps);
         const int step0 = (int)(x - before - unit * steps);
         const int take = (int)(x1 - x < steps - step0 ? x1 - x : steps - step0);
         const bool whole = take == steps;
         const int slot = x == x0 ? 0 : 1;
-        const int kvh = (int)(unit / tiles);
+        const int kvh = (int)udiv(unit, tiles);
         const int64_t tile = unit - kvh * tiles;
         const int64_t r0 = tile * 16;
         const int64_t rows = rw.rows();
         const bool live = r0 + r16 < rows;
         const int64_t row = live ? r0 + r16 : 0;
-        const int qi = (int)(row / rw.per);
-        const int head = kvh * rw.per + (int)(row % rw.per);
+        const int qi = (int)udiv(row, rw.per);
+        const int head = kvh * rw.per + (int)(row - (int64_t)qi * rw.per);
         const int seen = live ? rw.seen(row) : 0;  // positions that the row sees
         const int end = rw.end(r0);
         const int begin = step0 * kStride;
@@ -685,15 +745,14 @@ __global__ __launch_bounds__(kThreads) void cache4_join_kernel(AttnArgs a)
 {
     constexpr int kPer = D / 4;            // threads of a part: four dimensions each
     constexpr int kPar = kThreads / kPer;  // parts in flight
-    __shared__ float weight[kThreads];
-    __shared__ float red[2 * kWaves];
+    __shared__ float2 ml_of[kPar];
     __shared__ __attribute__((aligned(16))) f32x4_t sums[kThreads];
     const int tid = threadIdx.x;
     const int b = blockIdx.z;
     const int kvh = blockIdx.y;
-    const Rows rw = rows_of(a, b);
-    if ((int64_t)blockIdx.x >= rw.rows()) return;
     const Line ln = lay_line<false>(a, 0, b);
+    const Rows rw = ln.rw;
+    if ((int64_t)blockIdx.x >= rw.rows()) return;
     const int steps = steps_of(rw);
     const int64_t tiles = tiles_of(rw);
     const int d4 = tid % kPer;
@@ -706,44 +765,57 @@ __global__ __launch_bounds__(kThreads) void cache4_join_kernel(AttnArgs a)
         const int64_t n = g1 - g0 + 1;
         // a workgroup whose stretch begins in the unit has it in its slot 0
         const auto slot_of = [&](int64_t s) { return ((g0 + s) * 2 + (s == 0 && ln.first(g0) != x)) * 16 + r16; };
-        float mx = -INFINITY;
-        for (int64_t s = tid; s < n; s += kThreads) mx = fmaxf(mx, a.part_ml[slot_of(s)].x);
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o, kWave));
-        if ((tid & 63) == 0) red[tid >> 6] = mx;
-        __syncthreads();
-        mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-        const float base = mx == -INFINITY ? 0.0f : mx;
-        float tot = 0.0f;
+        // a thread's parts, all loads of eight in flight, against their own maximum
+        float mx = -INFINITY, tot = 0.0f;
         f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-        for (int64_t s0 = 0; s0 < n; s0 += kThreads) {
-            const float2 ml = s0 + tid < n ? a.part_ml[slot_of(s0 + tid)] : make_float2(-INFINITY, 0.0f);
-            const float w = ml.y == 0.0f ? 0.0f : ml.y * __builtin_amdgcn_exp2f(ml.x - base);
-            __syncthreads();  // the weights before are used up
-            weight[tid] = w;
-            tot += w;
-            __syncthreads();
-            const int here = (int)(n - s0 < kThreads ? n - s0 : kThreads);
-#pragma unroll 8
-            for (int s = tid / kPer; s < here; s += kPar) {
-                const f32x4_t v = *reinterpret_cast<const f32x4_t*>(a.part + slot_of(s0 + s) * D + 4 * d4);
-                const float ws = weight[s];
+        for (int64_t s0 = tid / kPer; s0 < n; s0 += 8 * kPar) {
+            float2 ml[8];
+            f32x4_t v[8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[e] = fmaf(ws, v[e], acc[e]);
+            for (int i = 0; i < 8; ++i) {
+                const int64_t s = s0 + i * kPar < n ? s0 + i * kPar : s0;
+                ml[i] = a.part_ml[slot_of(s)];
+                v[i] = *reinterpret_cast<const f32x4_t*>(a.part + slot_of(s) * D + 4 * d4);
+                if (s0 + i * kPar >= n) ml[i] = make_float2(-INFINITY, 0.0f);
             }
-        }
+            float m8 = mx;
 #pragma unroll
-        for (int o = 32; o > 0; o >>= 1) tot += __shfl_xor(tot, o, kWave);
-        if ((tid & 63) == 0) red[kWaves + (tid >> 6)] = tot;
+            for (int i = 0; i < 8; ++i) m8 = fmaxf(m8, ml[i].x);
+            const float base = m8 == -INFINITY ? 0.0f : m8;
+            const float old = __builtin_amdgcn_exp2f(mx - base);
+            tot *= old;
+            acc *= old;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                // nothing seen: no weight (and a NaN sum keeps its)
+                const float w = ml[i].y == 0.0f ? 0.0f : ml[i].y * __builtin_amdgcn_exp2f(ml[i].x - base);
+                tot += w;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[e] = fmaf(w, v[i][e], acc[e]);
+            }
+            mx = m8;
+        }
         sums[tid] = acc;
+        if (d4 == 0) ml_of[tid / kPer] = make_float2(mx, tot);
         __syncthreads();
         if (tid < kPer) {
-            tot = (red[kWaves] + red[kWaves + 1]) + (red[kWaves + 2] + red[kWaves + 3]);
+            float top = -INFINITY;
 #pragma unroll
-            for (int i = 1; i < kPar; ++i) acc += sums[i * kPer + tid];
+            for (int i = 0; i < kPar; ++i) top = fmaxf(top, ml_of[i].x);
+            const float base = top == -INFINITY ? 0.0f : top;
+            tot = 0.0f;
+            acc = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < kPar; ++i) {
+                const float w = __builtin_amdgcn_exp2f(ml_of[i].x - base);
+                tot = fmaf(ml_of[i].y, w, tot);
+                const f32x4_t v = sums[i * kPer + tid];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[e] = fmaf(v[e], w, acc[e]);
+            }
             const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
-            const int qi = (int)(row / rw.per);
-            const int head = kvh * rw.per + (int)(row % rw.per);
+            const int qi = (int)udiv(row, rw.per);
+            const int head = kvh * rw.per + (int)(row - (int64_t)qi * rw.per);
             uint16_t* op = a.out + ((int64_t)(rw.first + qi) * a.q_heads + head) * D + 4 * d4;
             *reinterpret_cast<uint2*>(op) =
                 make_uint2(bf16x2(acc[0] * inv, acc[1] * inv), bf16x2(acc[2] * inv, acc[3] * inv));
@@ -760,15 +832,15 @@ __global__ __launch_bounds__(kThreads) void cache4_join_edges_kernel(AttnArgs a)
     const Line ln = lay_line<true>(a, w, 0);
     if (ln.b < 0) return;
     const int64_t x = ln.first(w);
-    const Rows rw = rows_of(a, ln.b);
+    const Rows rw = ln.rw;
     const int steps = steps_of(rw);
-    const int64_t unit = (x - ln.before) / steps;
+    const int64_t unit = udiv(x - ln.before, steps);
     const int64_t start = ln.before + unit * steps;
     // the unit's second stretch joins it
     if (x == start || x >= ln.total || ln.group_of(start) != w - 1) return;
     const int64_t n = ln.group_of(start + steps - 1) - w + 2;
     const int64_t tiles = tiles_of(rw);
-    const int kvh = (int)(unit / tiles);
+    const int kvh = (int)udiv(unit, tiles);
     const int r16 = threadIdx.x >> 4;
     const int64_t row = (unit - kvh * tiles) * 16 + r16;
     if (row >= rw.rows()) return;
@@ -795,8 +867,8 @@ __global__ __launch_bounds__(kThreads) void cache4_join_edges_kernel(AttnArgs a)
         }
     }
     const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
-    const int qi = (int)(row / rw.per);
-    const int head = kvh * rw.per + (int)(row % rw.per);
+    const int qi = (int)udiv(row, rw.per);
+    const int head = kvh * rw.per + (int)(row - (int64_t)qi * rw.per);
     uint16_t* op = a.out + ((int64_t)(rw.first + qi) * a.q_heads + head) * D + d;
 #pragma unroll
     for (int i = 0; i < N; i += 4)
