@@ -379,7 +379,7 @@ __device__ __forceinline__ void load_n(__amdgpu_buffer_rsrc_t rs, uint32_t off, 
 // page, so its four arrays are buffers with scalar bases, and a lane's place
 // in them is the same in every step.
 template <int D, int G>
-__global__ __launch_bounds__(kThreads, D == 256 ? 2 : 4) void cache4_attention_kernel(AttnArgs a)
+__global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 3 : 2)) void cache4_attention_kernel(AttnArgs a)
 {
     constexpr int NC = D / 32;  // 32-dimension steps of a dot product
     constexpr int NG = D / G;   // groups of a head
@@ -533,6 +533,13 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 2 : 4) void cache4_attention_k
             __builtin_amdgcn_wave_barrier();
             // S^T = K Q^T, a group at a time; positions past the row's own at -inf
             const int left = seen - t0 - 4 * kg;
+            f32x4_t ks[2][NG];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+                    ks[h][g] = *reinterpret_cast<const f32x4_t*>(lk + h * SC + g * 16 + 4 * kg);
+            __builtin_amdgcn_sched_barrier(0);  // all LDS reads in flight behind the expansion
             float s[8];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -544,17 +551,21 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 2 : 4) void cache4_attention_k
                     for (int i = 0; i < GC; ++i)
                         part = __builtin_amdgcn_mfma_f32_16x16x32_f16(word_codes(kw[h][g * GC + i]),
                                                                       qf[g * GC + i], part, 0, 0, 0);
-                    const f32x4_t ks = *reinterpret_cast<const f32x4_t*>(lk + h * SC + g * 16 + 4 * kg);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[e] = fmaf(ks[e], part[e], acc[e]);
+                    for (int e = 0; e < 4; ++e) acc[e] = fmaf(ks[h][g][e], part[e], acc[e]);
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     s[4 * h + e] = 16 * h + e < left ? acc[e] : -INFINITY;
                 }
-                __builtin_amdgcn_sched_barrier(0);
             }
             __builtin_amdgcn_sched_barrier(0);  // the loads here, not where registers would be free
+            f32x4_t vs[2][NG];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+                    vs[h][g] = *reinterpret_cast<const f32x4_t*>(lv + h * SC + g * 16 + 4 * kg);
             load_k(t0 + kStride);
             __builtin_amdgcn_sched_barrier(0);
             // running maximum (of logits) and sum
@@ -587,15 +598,13 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 2 : 4) void cache4_attention_k
             for (int g = 0; g < NG; ++g) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const f32x4_t vs = *reinterpret_cast<const f32x4_t*>(lv + h * SC + g * 16 + 4 * kg);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         // a weight of 0 takes nothing, of a NaN scale either: that
                         // touches only the rows that see it
-                        pf[g][4 * h + e] = (_Float16)mul_legacy(p[4 * h + e], vs[e]);
+                        pf[g][4 * h + e] = (_Float16)mul_legacy(p[4 * h + e], vs[h][g][e]);
                     }
                 }
-                __builtin_amdgcn_sched_barrier(0);
             }
             // page numbers after the step's last LDS read: a wait for one waits for both
             load_pages(t0 + 2 * kStride);
@@ -676,7 +685,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 2 : 4) void cache4_attention_k
             for (; t0 < stop; t0 += kStride) step(t0);
         }
 
-        // join the waves: 2 and 3 into 0 and 1, then 1 into 0
+        // join the waves: the upper half into the lower, and so on (the join buffers
+        // are free again after the last barrier)
         auto put = [&](float* dst) {
 #pragma unroll
             for (int j = 0; j < NT; ++j) *reinterpret_cast<f32x4_t*>(dst + (j * kWave + lane) * 4) = o[j];
@@ -703,14 +713,14 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 2 : 4) void cache4_attention_k
             m = mn;
             ve = vn;
         };
-        if (wave >= 2) put(join[wave - 2]);
-        __syncthreads();
-        if (wave < 2) add(join[wave]);
-        __syncthreads();
-        if (wave == 1) put(join[0]);
-        __syncthreads();
+#pragma unroll
+        for (int n = kWaves / 2; n > 0; n >>= 1) {
+            if (wave >= n && wave < 2 * n) put(join[wave - n]);
+            __syncthreads();
+            if (wave < n) add(join[wave]);
+            __syncthreads();
+        }
         if (wave == 0) {
-            add(join[0]);
             l = row_sum(l);
             float inv = l > 0.0f ? pow2(ve - 14) / l : (l == 0.0f ? 0.0f : l);  // NaN stays
             if (rw.bad) inv = __uint_as_float(0x7fc00000u);
@@ -730,7 +740,6 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 2 : 4) void cache4_attention_k
                 if (kg == 0) a.part_ml[at] = make_float2(m, l);
             }
         }
-        __syncthreads();  // the join buffers are free for the next unit
     }
 }
 
@@ -880,7 +889,7 @@ __global__ __launch_bounds__(kThreads) void cache4_join_edges_kernel(AttnArgs a)
 // for heads of 256, whose registers and LDS allow no more), fewer where there
 // are not that many steps.
 #ifndef DQ_FILL
-#define DQ_FILL 1024
+#define DQ_FILL 512
 #endif
 constexpr int64_t kFill = DQ_FILL;
 
