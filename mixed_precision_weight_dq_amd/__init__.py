@@ -82,6 +82,7 @@ class DQGemvItem(ctypes.Structure):
 
 
 GEMV_BATCH_MAX = 32
+MAX_K_I8 = 65536
 
 
 class DQCache4(ctypes.Structure):
@@ -355,9 +356,15 @@ def packed_row_bytes(K: int, bits: int) -> int:
     return rb
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(t):
@@ -721,27 +728,46 @@ def gemm(x, packed, scales, K: int, bits: int, y=None):
 
 def _dtype_code(dtype, name):
     torch = _torch()
-    if dtype == torch.float32:
+    if dtype is torch.float32:
         return DQ_F32
-    if dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         return DQ_BF16
     raise TypeError("%s must be torch.float32 or torch.bfloat16 (got %s)" % (name, dtype))
 
 
-def _launch(where, tensors, fn, *args):
-    """fn(*args, stream) on the tensors' device: all on one GPU, its current stream."""
+def _fast_need(t, name, dtype, ndim, dev):
+    """``_need`` for one dtype, in a few attribute reads where nothing is wrong (the calls of a
+    decode step cost the host more than their kernels take); all tensors on GPU ``dev``."""
+    try:
+        if (t.is_cuda and t.dtype is dtype and t.dim() == ndim and t.is_contiguous()
+                and t.get_device() == dev):
+            return
+    except AttributeError:
+        pass
+    _need(t, name, (dtype,), ndim)
+    raise ValueError("%s: all tensors must be on one GPU (cuda:%d and %s)" % (name, dev, t.device))
+
+
+def _gpu_index(t, name):
+    try:
+        if t.is_cuda:
+            return t.get_device()
+    except AttributeError:
+        raise TypeError("%s must be a torch.Tensor" % name) from None
+    raise ValueError("%s must be a GPU tensor (got %s)" % (name, t.device))
+
+
+def _launch(where, dev, fn, *args):
+    """fn(*args, stream) on GPU ``dev`` and its current stream."""
     torch = _torch()
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError("%s: all tensors must be on one GPU (%s and %s)" % (where, dev, t.device))
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if dev.index == torch.cuda.current_device():
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch._C._cuda_getDevice() == dev:
         status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
             status = fn(*args, stream)
-    _check(int(status), where)
+    if status != DQ_OK:
+        raise DQError(status, where)
 
 
 def quantize_tokens(x, codes=None, scales=None, sums=None):
@@ -749,55 +775,67 @@ def quantize_tokens(x, codes=None, scales=None, sums=None):
     scales float32 [M], sums int32 [M]): one symmetric int8 scale per token, and each
     token's sum of codes."""
     torch = _torch()
-    _need(x, "x", (torch.float32, torch.bfloat16), 2)
+    dev = _gpu_index(x, "x")
+    kind = _dtype_code(x.dtype, "x")
+    _fast_need(x, "x", x.dtype, 2, dev)
     M, K = x.shape
-    pitch = dq_token_row_bytes(K)
-    if pitch == 0:
+    if not 1 <= K <= MAX_K_I8:
         raise DQError(DQ_ERR_SHAPE, "quantize_tokens")
+    pitch = (K + 127) & -128
     if codes is None:
-        codes = torch.empty((M, pitch), dtype=torch.int8, device=x.device)
+        codes = x.new_empty((M, pitch), dtype=torch.int8)
+    else:
+        _fast_need(codes, "codes", torch.int8, 2, dev)
+        if tuple(codes.shape) != (M, pitch):
+            raise ValueError("codes must be [M, %d]" % pitch)
     if scales is None:
-        scales = torch.empty((M,), dtype=torch.float32, device=x.device)
+        scales = x.new_empty((M,), dtype=torch.float32)
+    else:
+        _fast_need(scales, "scales", torch.float32, 1, dev)
     if sums is None:
-        sums = torch.empty((M,), dtype=torch.int32, device=x.device)
-    _need(codes, "codes", (torch.int8,), 2)
-    _need(scales, "scales", (torch.float32,), 1)
-    _need(sums, "sums", (torch.int32,), 1)
-    if tuple(codes.shape) != (M, pitch) or scales.shape[0] != M or sums.shape[0] != M:
-        raise ValueError("codes must be [M, %d], scales and sums [M]" % pitch)
-    _launch("dq_quantize_tokens", (x, codes, scales, sums), load().dq_quantize_tokens, x.data_ptr(),
-            DQ_BF16 if x.dtype == torch.bfloat16 else DQ_F32, M, K, codes.data_ptr(),
-            scales.data_ptr(), sums.data_ptr())
+        sums = x.new_empty((M,), dtype=torch.int32)
+    else:
+        _fast_need(sums, "sums", torch.int32, 1, dev)
+    if scales.shape[0] != M or sums.shape[0] != M:
+        raise ValueError("scales and sums must be [M]")
+    _launch("dq_quantize_tokens", dev, load().dq_quantize_tokens, x.data_ptr(), kind, M, K,
+            codes.data_ptr(), scales.data_ptr(), sums.data_ptr())
     return codes, scales, sums
 
 
 def _matmul_i8(fn, name, codes, x_scales, x_sums, packed, scales, K, bits, zeros, y, dtype):
     torch = _torch()
-    _need(codes, "codes", (torch.int8,), 2)
-    _need(x_scales, "x_scales", (torch.float32,), 1)
-    _need(x_sums, "x_sums", (torch.int32,), 1)
-    _need(packed, "packed", (torch.int32,), 2)
-    _need(scales, "scales", (torch.float32,), 1)
-    if zeros is not None:
-        _need(zeros, "zeros", (torch.int32,), 1)
-    M, N = codes.shape[0], packed.shape[0]
-    if K < 1 or K > 65536:
+    dev = _gpu_index(codes, "codes")
+    _fast_need(codes, "codes", torch.int8, 2, dev)
+    _fast_need(x_scales, "x_scales", torch.float32, 1, dev)
+    _fast_need(x_sums, "x_sums", torch.int32, 1, dev)
+    _fast_need(packed, "packed", torch.int32, 2, dev)
+    _fast_need(scales, "scales", torch.float32, 1, dev)
+    (M, pitch), (N, words) = codes.shape, packed.shape
+    if not 2 <= bits <= 8:
+        raise DQError(DQ_ERR_BITS, name)
+    if not 1 <= K <= MAX_K_I8:
         raise DQError(DQ_ERR_SHAPE, name)
-    if (codes.shape[1] != -(-K // 128) * 128 or x_scales.shape[0] != M or x_sums.shape[0] != M
-            or packed.shape[1] != packed_row_bytes(K, bits) // 4 or scales.shape[0] != N
-            or (zeros is not None and zeros.shape[0] != N)):
-        raise ValueError("shape mismatch between codes, x_scales, x_sums, packed, scales, zeros, K and bits")
+    if (pitch != (K + 127) & -128 or x_scales.shape[0] != M or x_sums.shape[0] != M
+            or words != ((K * bits + 7) // 8 + 127) // 128 * 32 or scales.shape[0] != N):
+        raise ValueError("shape mismatch between codes, x_scales, x_sums, packed, scales, K and bits")
+    if zeros is not None:
+        _fast_need(zeros, "zeros", torch.int32, 1, dev)
+        if zeros.shape[0] != N:
+            raise ValueError("zeros must be [N]")
+        zeros = zeros.data_ptr()
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32 if dtype is None else dtype, device=codes.device)
-    elif dtype is not None and y.dtype != dtype:
-        raise TypeError("y is %s, dtype %s" % (y.dtype, dtype))
-    kind = _dtype_code(y.dtype, "y")
-    _need(y, "y", (torch.float32, torch.bfloat16), 2)
-    if tuple(y.shape) != (M, N):
-        raise ValueError("y must be [M, N]")
-    _launch(name, (codes, x_scales, x_sums, packed, scales, zeros, y), fn, codes.data_ptr(),
-            x_scales.data_ptr(), x_sums.data_ptr(), M, packed.data_ptr(), scales.data_ptr(),
-            zeros.data_ptr() if zeros is not None else None, N, K, bits, y.data_ptr(), kind)
+        y = codes.new_empty((M, N), dtype=torch.float32 if dtype is None else dtype)
+        kind = _dtype_code(y.dtype, "dtype")
+    else:
+        kind = _dtype_code(y.dtype, "y")
+        if dtype is not None and y.dtype != dtype:
+            raise TypeError("y is %s, dtype %s" % (y.dtype, dtype))
+        _fast_need(y, "y", y.dtype, 2, dev)
+        if tuple(y.shape) != (M, N):
+            raise ValueError("y must be [M, N]")
+    _launch(name, dev, fn, codes.data_ptr(), x_scales.data_ptr(), x_sums.data_ptr(), M,
+            packed.data_ptr(), scales.data_ptr(), zeros, N, K, bits, y.data_ptr(), kind)
     return y
 
 
@@ -826,10 +864,11 @@ class Cache4:
 
     def __init__(self, k_codes, v_codes, k_scales, v_scales):
         torch = _torch()
+        dev = _gpu_index(k_codes, "k_codes")
         for t, name in ((k_codes, "k_codes"), (v_codes, "v_codes")):
-            _need(t, name, (torch.int32,), 4)
+            _fast_need(t, name, torch.int32, 4, dev)
         for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
-            _need(t, name, (torch.float32,), 4)
+            _fast_need(t, name, torch.float32, 4, dev)
         pages, heads, P, words = k_codes.shape
         groups = k_scales.shape[2]
         if (v_codes.shape != k_codes.shape or v_scales.shape != k_scales.shape
@@ -839,6 +878,7 @@ class Cache4:
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, P, words * 8
         self.group = words * 8 // groups
+        self.device_index = dev
         self._c = DQCache4(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
                            v_scales.data_ptr(), pages, heads, self.head_dim, P, self.group)
 
@@ -859,67 +899,66 @@ class Cache4:
         return self.k_codes, self.v_codes, self.k_scales, self.v_scales
 
 
-def _batch4(starts, lens, table):
+def _batch4(starts, lens, table, dev):
     torch = _torch()
-    _need(starts, "starts", (torch.int32,), 1)
-    _need(lens, "lens", (torch.int32,), 1)
-    _need(table, "table", (torch.int32,), 2)
+    _fast_need(starts, "starts", torch.int32, 1, dev)
+    _fast_need(lens, "lens", torch.int32, 1, dev)
+    _fast_need(table, "table", torch.int32, 2, dev)
     count = lens.shape[0]
-    if starts.shape[0] != count + 1 or table.shape[0] != count:
+    rows, width = table.shape
+    if starts.shape[0] != count + 1 or rows != count:
         raise ValueError("starts must be [count + 1], lens [count], table [count, width]")
-    return DQCache4Batch(starts.data_ptr(), lens.data_ptr(), table.data_ptr(), table.shape[1], count)
+    return DQCache4Batch(starts.data_ptr(), lens.data_ptr(), table.data_ptr(), width, count)
 
 
-def _token_rows(t, name, heads, D, dtypes):
-    """Checks t [tokens, heads, D] with contiguous heads; returns its token stride."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if t.device.type != "cuda":
-        raise ValueError("%s must be a GPU tensor (got %s)" % (name, t.device))
-    if t.dtype not in dtypes:
-        raise TypeError("%s dtype %s not in %s" % (name, t.dtype, dtypes))
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+def _token_rows(t, name, heads, D, dev):
+    """Checks t [tokens, heads, D] with contiguous heads on GPU ``dev``; returns its token stride."""
+    if _gpu_index(t, name) != dev:
+        raise ValueError("%s: all tensors must be on one GPU (cuda:%d and %s)" % (name, dev, t.device))
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != D:
         raise ValueError("%s must be [tokens, %d, %d]" % (name, heads, D))
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+    token, head, dim = t.stride()
+    if dim != 1 or (heads > 1 and head != D):
         raise ValueError("%s: the heads of a token must be contiguous" % name)
-    return t.stride(0) if t.shape[0] > 1 else heads * D
+    return token if shape[0] > 1 else heads * D
 
 
 def cache4_append(cache: Cache4, k, v, starts, lens, table) -> None:
     """Quantize k, v [tokens, kv_heads, D] (float32 or bfloat16; tokens may be strided) into
     the pages of their positions."""
-    torch = _torch()
-    kinds = (torch.float32, torch.bfloat16)
-    ks = _token_rows(k, "k", cache.kv_heads, cache.head_dim, kinds)
-    vs = _token_rows(v, "v", cache.kv_heads, cache.head_dim, kinds)
-    if k.dtype != v.dtype or k.shape[0] != v.shape[0]:
+    dev = cache.device_index
+    ks = _token_rows(k, "k", cache.kv_heads, cache.head_dim, dev)
+    vs = _token_rows(v, "v", cache.kv_heads, cache.head_dim, dev)
+    kind = _dtype_code(k.dtype, "k")
+    if v.dtype != k.dtype or v.shape[0] != k.shape[0]:
         raise ValueError("k and v must have one dtype and one token count")
-    batch = _batch4(starts, lens, table)
-    _launch("dq_cache4_append", (*cache.tensors, k, v, starts, lens, table),
-            load().dq_cache4_append, cache._c, batch, k.data_ptr(), v.data_ptr(),
-            _dtype_code(k.dtype, "k"), k.shape[0], ks, vs)
+    batch = _batch4(starts, lens, table, dev)
+    _launch("dq_cache4_append", dev, load().dq_cache4_append, cache._c, batch, k.data_ptr(),
+            v.data_ptr(), kind, k.shape[0], ks, vs)
 
 
 def cache4_read(cache: Cache4, tokens: int, starts, lens, table, dtype=None, k=None, v=None):
     """The dequantized (k, v) [tokens, kv_heads, D] of a call's tokens, float32 (the default)
     or bfloat16; rows of no sequence are left as they were."""
     torch = _torch()
+    dev = cache.device_index
     kind = torch.float32 if dtype is None else dtype
     code = _dtype_code(kind, "dtype")
     shape = (tokens, cache.kv_heads, cache.head_dim)
-    if k is None:
-        k = torch.empty(shape, dtype=kind, device=cache.k_codes.device)
-    if v is None:
-        v = torch.empty(shape, dtype=kind, device=cache.k_codes.device)
+    out = []
     for t, name in ((k, "k"), (v, "v")):
-        _need(t, name, (kind,), 3)
-        if tuple(t.shape) != shape:
-            raise ValueError("%s must be [tokens, kv_heads, D]" % name)
-    batch = _batch4(starts, lens, table)
-    _launch("dq_cache4_read", (*cache.tensors, k, v, starts, lens, table), load().dq_cache4_read,
-            cache._c, batch, k.data_ptr(), v.data_ptr(), code, tokens)
-    return k, v
+        if t is None:
+            t = cache.k_codes.new_empty(shape, dtype=kind)
+        else:
+            _fast_need(t, name, kind, 3, dev)
+            if tuple(t.shape) != shape:
+                raise ValueError("%s must be [tokens, kv_heads, D]" % name)
+        out.append(t)
+    batch = _batch4(starts, lens, table, dev)
+    _launch("dq_cache4_read", dev, load().dq_cache4_read, cache._c, batch, out[0].data_ptr(),
+            out[1].data_ptr(), code, tokens)
+    return tuple(out)
 
 
 def cache4_attention(cache: Cache4, q, starts, lens, table, scale=None, max_q=None, max_len=None,
@@ -927,32 +966,39 @@ def cache4_attention(cache: Cache4, q, starts, lens, table, scale=None, max_q=No
     """Causal attention of q [tokens, q_heads, D] (bfloat16; tokens may be strided) over the
     cache, its tokens' keys and values already appended.  scale: D ** -0.5 unless given.
     max_q / max_len: the most new / cached tokens of a sequence, for sizing the launch
-    (default: the whole call / the whole table).  out bfloat16 [tokens, q_heads, D];
-    workspace: uint8 tensor to use instead of a new one."""
+    (default: an even share of the call's tokens / the whole table).  out bfloat16 [tokens,
+    q_heads, D]; workspace: uint8 tensor to use instead of a new one."""
     torch = _torch()
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be a [tokens, q_heads, D] tensor")
+    dev = cache.device_index
+    _gpu_index(q, "q")
+    if q.dtype is not torch.bfloat16 or q.dim() != 3:
+        raise TypeError("q must be a bfloat16 [tokens, q_heads, D] tensor")
     tokens, heads, D = q.shape
-    stride = _token_rows(q, "q", heads, cache.head_dim, (torch.bfloat16,))
-    batch = _batch4(starts, lens, table)
+    stride = _token_rows(q, "q", heads, cache.head_dim, dev)
+    batch = _batch4(starts, lens, table, dev)
     if out is None:
-        out = torch.empty((tokens, heads, D), dtype=torch.bfloat16, device=q.device)
-    _need(out, "out", (torch.bfloat16,), 3)
-    if tuple(out.shape) != (tokens, heads, D):
-        raise ValueError("out must be [tokens, q_heads, D]")
-    max_q = tokens if max_q is None else int(max_q)
-    max_len = table.shape[1] * cache.page_size if max_len is None else int(max_len)
-    scale = D ** -0.5 if scale is None else float(scale)
+        out = q.new_empty((tokens, heads, D))
+    else:
+        _fast_need(out, "out", torch.bfloat16, 3, dev)
+        if tuple(out.shape) != (tokens, heads, D):
+            raise ValueError("out must be [tokens, q_heads, D]")
+    if max_q is None:
+        max_q = -(-tokens // max(batch.count, 1))
+    if max_len is None:
+        max_len = batch.table_width * cache.page_size
+    if scale is None:
+        scale = D ** -0.5
     lib = load()
     need = lib.dq_cache4_attention_workspace(cache._c, batch.count, tokens, heads, max_q, max_len)
     if workspace is None:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=q.device) if need else None
+        if need:
+            workspace = q.new_empty((need,), dtype=torch.uint8)
     else:
-        _need(workspace, "workspace", (torch.uint8,), 1)
-    _launch("dq_cache4_attention", (*cache.tensors, q, out, starts, lens, table, workspace),
-            lib.dq_cache4_attention, cache._c, batch, q.data_ptr(), tokens, stride, heads, scale,
-            max_q, max_len, out.data_ptr(), workspace.data_ptr() if workspace is not None else None,
-            workspace.shape[0] if workspace is not None else 0)
+        _fast_need(workspace, "workspace", torch.uint8, 1, dev)
+        need = workspace.shape[0]
+    _launch("dq_cache4_attention", dev, lib.dq_cache4_attention, cache._c, batch, q.data_ptr(), tokens,
+            stride, heads, scale, max_q, max_len, out.data_ptr(),
+            workspace.data_ptr() if workspace is not None else None, need)
     return out
 
 
