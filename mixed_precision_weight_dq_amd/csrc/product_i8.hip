@@ -44,20 +44,20 @@ struct I8Args {
 // lane (r, g) holds, of weight row r, the chunks 2 g and 2 g + 1 of the step,
 // 2 B consecutive words, so codes go from memory to registers to the matrix
 // cores, a row's 256 codes with four lanes' neighbouring loads.  The tokens'
-// bytes of the same codes come from L1 / L2 likewise.  kDepth steps are in
-// flight per wave.
+// bytes of the same codes come from L1 / L2 likewise.  A step's loads are in
+// flight while the step before is multiplied.
+//
+// Rows per workgroup: the more, the less often the tokens' bytes are read and
+// the fewer rows are open at once, as long as every CU has a workgroup.  16 x
+// 28672 x 8192 at b = 6: 112 rows (256 workgroups) 39.5 us (4.5 TB/s of
+// weights), 64 rows 45.8, 32 rows 53.9, 16 rows 56; 1 x 4096 x 4096 at b = 4:
+// 16 rows (256 workgroups) 4.1 us, 32 rows 5.3, 64 rows 7.7.
 constexpr int kFewThreads = 256;
 constexpr int kFewWaves = kFewThreads / kWave;
 
 template <int B, int R, int T>
-struct FewTile {
-    static constexpr int kDepth = R * B <= 8 ? 4 : (R * B <= 12 && T <= 2 ? 3 : 2);
-};
-
-template <int B, int R, int T>
-__global__ __launch_bounds__(kFewThreads) void few_i8_kernel(I8Args a)
+__global__ __launch_bounds__(kFewThreads, R >= 7 || T == 4 ? 1 : (R == 1 ? 4 : 2)) void few_i8_kernel(I8Args a)
 {
-    constexpr int kDepth = FewTile<B, R, T>::kDepth;
     __shared__ __attribute__((aligned(16))) int32_t part[kFewWaves][R * T * 4 * kWave];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -89,16 +89,15 @@ __global__ __launch_bounds__(kFewThreads) void few_i8_kernel(I8Args a)
 #pragma unroll
         for (int t = 0; t < T; ++t) acc[i][t] = (i32x4_t){0, 0, 0, 0};
 
-    uint32_t w[kDepth][R][2 * B];
-    u32x4v_t x[kDepth][T][4];
-    auto load = [&](auto S, int s) __attribute__((always_inline)) {
-        constexpr int st = decltype(S)::value;
+    uint32_t w[R][2 * B];
+    u32x4v_t x[2][T][4];
+    auto load_w = [&](int i, int s) __attribute__((always_inline)) {
         // a step past the last is past the buffer: nothing is fetched
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-            buf_load_words<2 * B>(wbuf, s < steps ? woff[i] + (uint32_t)s * (32 * B) : 0xfffff000u, 0, w[st][i]);
-        // and so are the tokens' bytes past the row (the second half of a last
-        // half step too), which read as 0
+        buf_load_words<2 * B>(wbuf, s < steps ? woff[i] + (uint32_t)s * (32 * B) : 0xfffff000u, 0, w[i]);
+    };
+    auto load_x = [&](auto S, int s) __attribute__((always_inline)) {
+        constexpr int st = decltype(S)::value;
+        // likewise, and the second half of a last half step; such bytes read as 0
         const bool in = 256 * s + 64 * g < a.pitch;
 #pragma unroll
         for (int t = 0; t < T; ++t) {
@@ -107,27 +106,34 @@ __global__ __launch_bounds__(kFewThreads) void few_i8_kernel(I8Args a)
             for (int q = 0; q < 4; ++q) x[st][t][q] = buf_load_b128(xbuf, off + 16 * q, 0);
         }
     };
-    auto work = [&](auto S) __attribute__((always_inline)) {
+    // the tokens' bytes of a wave's next step are loaded at the top, a row tile's
+    // codes as soon as its words are expanded
+    auto step = [&](auto S, int s) __attribute__((always_inline)) {
         constexpr int st = decltype(S)::value;
+        load_x(std::integral_constant<int, st ^ 1>{}, s + kFewWaves);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int i = 0; i < R; ++i) {
+            i32x4_t codes[4];
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                const uint32_t(&chunk)[B] = reinterpret_cast<const uint32_t(&)[B]>(w[st][i][(q >> 1) * B]);
-                const i32x4_t codes = expand16<B>(chunk, q & 1);
+            for (int q = 0; q < 4; ++q)
+                codes[q] = expand16<B>(reinterpret_cast<const uint32_t(&)[B]>(w[i][(q >> 1) * B]), q & 1);
+            load_w(i, s + kFewWaves);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
                 for (int t = 0; t < T; ++t)
                     acc[i][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
-                        codes, __builtin_bit_cast(i32x4_t, x[st][t][q]), acc[i][t], 0, 0, 0);
-            }
+                        codes[q], __builtin_bit_cast(i32x4_t, x[st][t][q]), acc[i][t], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
-    static_for<kDepth>([&](auto S) { load(S, wave + (int)S.value * kFewWaves); });
-    for (int s = wave; s < steps; s += kFewWaves * kDepth) {
-        static_for<kDepth>([&](auto S) {
-            work(S);
-            load(S, s + ((int)S.value + kDepth) * kFewWaves);
-        });
+    load_x(std::integral_constant<int, 0>{}, wave);
+#pragma unroll
+    for (int i = 0; i < R; ++i) load_w(i, wave);
+    for (int s = wave; s < steps; s += 2 * kFewWaves) {
+        step(std::integral_constant<int, 0>{}, s);
+        step(std::integral_constant<int, 1>{}, s + kFewWaves);
     }
 
     // lane (m = lane & 15, g) holds rows 4 g + e of tile i for token 16 t + m
@@ -161,6 +167,17 @@ hipError_t launch_few(const I8Args& a, hipStream_t stream)
 {
     few_i8_kernel<B, R, T><<<dim3((unsigned)ceil_div(a.N, 16 * R)), kFewThreads, 0, stream>>>(a);
     return hipGetLastError();
+}
+
+// The most rows per workgroup that leave 224 workgroups or more for the 256 CUs.
+template <int B, int T>
+hipError_t launch_few_rows(const I8Args& a, hipStream_t stream)
+{
+    constexpr int64_t kFill = 224;
+    if (a.N >= 16 * 7 * kFill) return launch_few<B, 7, T>(a, stream);
+    if (a.N >= 16 * 4 * kFill) return launch_few<B, 4, T>(a, stream);
+    if (a.N >= 16 * 2 * kFill) return launch_few<B, 2, T>(a, stream);
+    return launch_few<B, 1, T>(a, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -407,12 +424,9 @@ template <int B>
 hipError_t launch_b(const I8Args& a, hipStream_t stream)
 {
     if (a.M <= 64) {
-        // 32 weight rows per workgroup once they fill the CUs twice over: the
-        // tokens' bytes are then read half as often
-        const bool wide = a.N >= 32 * 512;
-        if (a.M <= 16) return wide ? launch_few<B, 2, 1>(a, stream) : launch_few<B, 1, 1>(a, stream);
-        if (a.M <= 32) return wide ? launch_few<B, 2, 2>(a, stream) : launch_few<B, 1, 2>(a, stream);
-        return wide ? launch_few<B, 2, 4>(a, stream) : launch_few<B, 1, 4>(a, stream);
+        if (a.M <= 16) return launch_few_rows<B, 1>(a, stream);
+        if (a.M <= 32) return launch_few_rows<B, 2>(a, stream);
+        return launch_few_rows<B, 4>(a, stream);
     }
     // 256 x 256 tiles when they fill the 256 CUs in whole rounds (at least 80 %
     // of the last round busy)
