@@ -181,41 +181,103 @@ hipError_t launch_few_rows(const I8Args& a, hipStream_t stream)
 }
 
 // ---------------------------------------------------------------------------
-// Many tokens: bound by the matrix cores.  Four waves side by side along N;
-// wave w owns all 32 MT token rows and columns [32 NT w, 32 NT (w + 1)) of the
-// workgroup's tile, as MT x NT tiles of v_mfma_i32_32x32x32_i8.  No two waves
-// expand the same codes.
+// Many tokens: bound by the matrix cores.  4 WM waves: four side by side along
+// N, WM along M; a wave owns 32 MT token rows and 32 NT columns of the
+// workgroup's tile, as MT x NT tiles of v_mfma_i32_32x32x32_i8.
 //
-// A step is 128 codes: substep t (0 .. 3) multiplies, for lane half h, the bytes
-// 64 h + 16 t .. + 15 of it, so a lane takes its weight operands from the chunks
-// 2 h and 2 h + 1 of its row (2 B consecutive words), straight from memory
-// into registers, and its token operands from 16-byte piece 4 h + t of its row
-// in LDS.  Tokens go from memory to LDS directly, in three stages of a step,
-// piece p of row r at slot p ^ ((r >> 1) & 7), which spreads a read over the
-// banks; codes have three register stages.  Each substep's MFMAs run beside the
-// expansion and the LDS reads of the next.  Per step a wave waits for its own
-// copies of the next step's tokens (an exact count of later loads may remain in
-// flight), and one barrier makes that stage visible.
-template <int MT, int NT>
+// A step is 128 codes.  Tokens and packed codes both go from memory to LDS
+// directly, as whole 128-byte lines of a row, in two stages of a step.  (Codes
+// straight into the registers of their lanes touch 64 lines per load, eight
+// loads per line, and L1 looks up a line a cycle: 2048 x 8192 x 8192 at b = 8 took
+// 137 us so.)  Substep t (0 .. 3) multiplies, for lane half h, the bytes 64 h + 16 t ..
+// + 15 of the step: token operands are 16-byte piece 4 h + t of a row, weight
+// operands half t & 1 of chunk 2 h + (t >> 1), whose words a lane reads from LDS once
+// per step and expands a substep ahead.  Piece p of a row lies at slot p ^ f(row),
+// with f such that the rows of one LDS pass spread over all banks.  Each
+// substep's MFMAs run beside the expansion and the LDS reads of the next; after
+// the third, the step's stage has been read by every wave, and behind one
+// barrier the copies of the step after next go out into it.
+template <int MT, int NT, int WM>
 struct ManyTile {
-    static constexpr int BM = 32 * MT;
+    static constexpr int BM = 32 * MT * WM;
+    static constexpr int kThreads = 256 * WM;
     static constexpr int BN = 128 * NT;
-    static constexpr int kStages = 3;
-    static constexpr int kCopies = BM / 32;  // 16-byte pieces per thread and step
+    static constexpr int kCopies = MT;  // 16-byte pieces of tokens per thread and step
 };
 
-__device__ __forceinline__ int piece_slot(int row) { return (row >> 1) & 7; }
-
-template <int B, int MT, int NT, int kOcc>
-__global__ __launch_bounds__(256, kOcc) void many_i8_kernel(I8Args a)
+// Slot of 16-byte piece p of a row of tokens (8 pieces).
+__device__ __forceinline__ int x_slot(int row, int p) { return p ^ ((row >> 1) & 7); }
+// Slot of piece p of a row's codes (B pieces): rows of 6 and 2 pieces, and of an
+// odd number, read in 8-byte parts, spread over the banks as they are.
+template <int B>
+__device__ __forceinline__ int w_slot(int row, int p)
 {
-    using Tl = ManyTile<MT, NT>;
-    constexpr int kStages = Tl::kStages, kCopies = Tl::kCopies;
-    __shared__ __attribute__((aligned(16))) uint4 As[kStages][Tl::BM * 8];
+    if constexpr (B == 8) return p ^ ((row >> 1) & 7);
+    if constexpr (B == 4) return p ^ ((row >> 2) & 3);
+    return p;
+}
+
+// The 2 B words of half h of a row's codes in LDS.
+template <int B>
+__device__ __forceinline__ void read_words(const uint4* rows, int row, int h, uint32_t (&w)[2 * B])
+{
+    if constexpr (B % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < B / 2; ++i) {
+            const uint4 v = rows[row * B + w_slot<B>(row, h * (B / 2) + i)];
+            w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+        }
+    } else {
+        const uint2* p = reinterpret_cast<const uint2*>(rows + row * B) + h * B;
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const uint2 v = p[i];
+            w[2 * i] = v.x, w[2 * i + 1] = v.y;
+        }
+    }
+}
+
+// Waits until at most n of the wave's vector-memory operations and none of its
+// LDS operations are in flight, then for the other waves (__syncthreads would
+// wait for every copy).
+template <int n>
+__device__ __forceinline__ void join_waves()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (7 << 4));
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+}
+
+template <int B, int MT, int NT, int WM, int kOcc>
+__global__ __launch_bounds__(256 * WM, kOcc) void many_i8_kernel(I8Args a)
+{
+    using Tl = ManyTile<MT, NT, WM>;
+    constexpr int S = 2;  // stages; three, for the codes they fit, were no faster
+    constexpr int kCopies = Tl::kCopies;
+    constexpr int kWCopies = NT * B / (2 * WM);  // whole pieces of codes per thread and step
+    constexpr bool kWHalf = (NT * B) % (2 * WM) != 0;  // and one more for half of the threads
+    // an array per stage: a read of one stage is then known not to depend on the
+    // copies in flight into another (one array for all: every read waited for
+    // every copy, a whole memory latency per step)
+    __shared__ __attribute__((aligned(16))) uint4 As0[Tl::BM * 8], As1[Tl::BM * 8];
+    __shared__ __attribute__((aligned(16))) uint4 Ws0[Tl::BN * B], Ws1[Tl::BN * B];
+    auto as = [&](auto St) __attribute__((always_inline)) -> uint4* {
+        if constexpr (decltype(St)::value == 0) return As0;
+        else return As1;
+    };
+    auto ws = [&](auto St) __attribute__((always_inline)) -> uint4* {
+        if constexpr (decltype(St)::value == 0) return Ws0;
+        else return Ws1;
+    };
 
     const int tid = threadIdx.x;
     const int lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int wn = wave & 3;
+    const int wm = wave >> 2;
     const int c = lane & 31;
     const int h = lane >> 5;
 
@@ -224,8 +286,8 @@ __global__ __launch_bounds__(256, kOcc) void many_i8_kernel(I8Args a)
     const int64_t ntm = ceil_div(a.M, Tl::BM);
     const int64_t ntn = ceil_div(a.N, Tl::BN);
     const int64_t tiles = ntm * ntn;
-    int64_t L = blockIdx.x;
-    if ((tiles & 7) == 0) L = (L & 7) * (tiles >> 3) + (L >> 3);
+    const int64_t L = (int64_t)(blockIdx.x & 7) * ((tiles + 7) >> 3) + (blockIdx.x >> 3);
+    if (L >= tiles) return;
     const int64_t gm = (ntm & 3) == 0 ? 4 : ntm;
     const int64_t grp = L / (gm * ntn), rem = L % (gm * ntn);
     const int64_t m0 = (grp * gm + rem % gm) * Tl::BM;
@@ -239,20 +301,26 @@ __global__ __launch_bounds__(256, kOcc) void many_i8_kernel(I8Args a)
     for (int i = 0; i < kCopies; ++i) {
         const int slot = (wave * kCopies + i) * 64 + lane;
         const int row = slot >> 3;
-        const int p = (slot & 7) ^ piece_slot(row);
+        const int p = x_slot(row, slot & 7);
         xoff[i] = (uint32_t)((row < mrows ? row : mrows - 1) * a.pitch + 16 * p);
     }
     const int64_t nrows = a.N - n0 < Tl::BN ? a.N - n0 : Tl::BN;
-    const BufRef wbuf = uniform_buf(a.packed + n0 * a.row_words, (uint32_t)(nrows * a.row_words * 4));
-    uint32_t woff[NT];
+    const uint32_t row_bytes = (uint32_t)a.row_words * 4;
+    const BufRef wbuf = uniform_buf(a.packed + n0 * a.row_words, (uint32_t)nrows * row_bytes);
+    // 128 NT rows of B pieces, 64 pieces per wave and copy
+    constexpr int kWAll = kWCopies + (kWHalf ? 1 : 0);
+    constexpr int kStepCopies = kCopies + kWCopies;  // of the waves that copy the least
+    uint32_t woff[kWAll];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        const int64_t nl = wave * 32 * NT + j * 32 + c;
-        woff[j] = (uint32_t)((nl < nrows ? nl : nrows - 1) * a.row_words * 4 + h * (8 * B));
+    for (int i = 0; i < kWAll; ++i) {
+        const int slot = (i * 4 * WM + wave) * 64 + lane;
+        const int row = slot / B;
+        const int p = w_slot<B>(row, slot % B);
+        woff[i] = (uint32_t)(row < nrows ? row : nrows - 1) * row_bytes + 16 * p;
     }
     int abase[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) abase[t] = c * 8 + ((4 * h + t) ^ piece_slot(c));
+    for (int t = 0; t < 4; ++t) abase[t] = wm * (256 * MT) + c * 8 + x_slot(c, 4 * h + t);
 
     i32x16_t acc[MT][NT];
 #pragma unroll
@@ -262,53 +330,45 @@ __global__ __launch_bounds__(256, kOcc) void many_i8_kernel(I8Args a)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
 
-    uint32_t w[kStages][NT][2 * B];
+    uint32_t w[NT][2 * B];
     i32x4_t bq[NT];     // weight operands of the current substep
     i32x4_t aq[2][MT];  // token operands of the current and the next substep
-    auto load_x = [&](auto S, int ks) __attribute__((always_inline)) {
-        constexpr int st = decltype(S)::value;
+    auto copy = [&](auto St, int ks) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < kCopies; ++i)
-            buf_load_lds16(xbuf, &As[st][(wave * kCopies + i) * 64], xoff[i], (uint32_t)ks * 128);
-    };
-    auto load_w = [&](auto S, int ks) __attribute__((always_inline)) {
-        constexpr int st = decltype(S)::value;
+            buf_load_lds16(xbuf, as(St) + (wave * kCopies + i) * 64, xoff[i], (uint32_t)ks * 128);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) buf_load_words<2 * B>(wbuf, woff[j], (uint32_t)ks * (16 * B), w[st][j]);
+        for (int i = 0; i < kWAll; ++i)
+            if (i < kWCopies || wave < 2 * WM)
+                buf_load_lds16(wbuf, ws(St) + (i * 4 * WM + wave) * 64, woff[i] + (uint32_t)ks * (16 * B), 0);
     };
-    auto codes = [&](auto S, int j, int t) __attribute__((always_inline)) {
-        constexpr int st = decltype(S)::value;
-        return expand16<B>(reinterpret_cast<const uint32_t(&)[B]>(w[st][j][(t >> 1) * B]), t & 1);
-    };
-    auto read_a = [&](auto S, int t, i32x4_t (&dst)[MT]) __attribute__((always_inline)) {
-        constexpr int st = decltype(S)::value;
+    auto read_w = [&](auto St) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i) dst[i] = __builtin_bit_cast(i32x4_t, As[st][abase[t] + 256 * i]);
+        for (int j = 0; j < NT; ++j) read_words<B>(ws(St), (wn * NT + j) * 32 + c, h, w[j]);
     };
-    // vector-memory operations issued after the copy of step ks + 1 when step ks
-    // waits for it: the codes of step ks + 2
-    constexpr int kWLoads = NT * ((2 * B) / 4 + ((2 * B) % 4 != 0 ? 1 : 0));
-    constexpr int kWaitX = (kWLoads & 15) | ((kWLoads >> 4) << 14) | (7 << 4) | (15 << 8);
-    constexpr int kPro = kCopies + 2 * kWLoads;  // after the copy of step 0 in the prologue
-    constexpr int kWaitPro = (kPro & 15) | ((kPro >> 4) << 14) | (7 << 4) | (15 << 8);
-    static_assert(kPro < 64, "vmcnt holds at most 63");
+    auto codes = [&](int j, int t) __attribute__((always_inline)) {
+        return expand16<B>(reinterpret_cast<const uint32_t(&)[B]>(w[j][(t >> 1) * B]), t & 1);
+    };
+    auto read_a = [&](auto St, int t, i32x4_t (&dst)[MT]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) dst[i] = __builtin_bit_cast(i32x4_t, as(St)[abase[t] + 256 * i]);
+    };
 
-    auto step = [&](auto S, int ks) __attribute__((always_inline)) {
-        constexpr int st = decltype(S)::value;
-        constexpr int s1 = (st + 1) % kStages, s2 = (st + 2) % kStages;
-        const int k2 = ks + 2 < nk ? ks + 2 : nk - 1;  // past the end: in bounds, never used
-        load_w(std::integral_constant<int, s2>{}, k2);
-        __builtin_amdgcn_sched_barrier(0);
+    auto step = [&](auto St, int ks) __attribute__((always_inline)) {
+        constexpr int st = decltype(St)::value;
+        using Other = std::integral_constant<int, (st + 1) % S>;
+        const int k2 = ks + S < nk ? ks + S : nk - 1;  // past the end: in bounds, never used
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             i32x4_t nb[NT];
-            if (t < 3)
-                read_a(S, t + 1, aq[(t + 1) & 1]);
-            else
-                read_a(std::integral_constant<int, s1>{}, 0, aq[0]);
+            if (t < 3) {
+                read_a(St, t + 1, aq[(t + 1) & 1]);
+            } else {
+                read_w(Other{});
+                read_a(Other{}, 0, aq[0]);
+            }
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-                nb[j] = t < 3 ? codes(S, j, t + 1) : codes(std::integral_constant<int, s1>{}, j, 0);
+            for (int j = 0; j < NT; ++j) nb[j] = codes(j, (t + 1) & 3);
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -316,50 +376,36 @@ __global__ __launch_bounds__(256, kOcc) void many_i8_kernel(I8Args a)
                     acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(aq[t & 1][i], bq[j], acc[i][j], 0, 0, 0);
 #pragma unroll
             for (int j = 0; j < NT; ++j) bq[j] = nb[j];
-            // an MFMA covers a share of the next substep's reads and expansion
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
-#pragma unroll
-                for (int j = 1; j < NT; ++j) {
-                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                    __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
-                }
-            }
             __builtin_amdgcn_sched_barrier(0);
             if (t == 2) {
-                __builtin_amdgcn_s_waitcnt(kWaitX);
-                __syncthreads();  // stage ks + 1 is whole; stage ks + 2 is read by no wave any more
-                load_x(std::integral_constant<int, s2>{}, k2);
+                // stage ks + 1 is whole; stage ks is read by no wave any more
+                join_waves<(S - 2) * kStepCopies>();
+                copy(St, k2);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
     };
 
-    load_x(std::integral_constant<int, 0>{}, 0);
-    load_x(std::integral_constant<int, 1>{}, nk > 1 ? 1 : 0);
-    load_w(std::integral_constant<int, 0>{}, 0);
-    load_w(std::integral_constant<int, 1>{}, nk > 1 ? 1 : 0);
-    __builtin_amdgcn_s_waitcnt(kWaitPro);
-    __syncthreads();
-    read_a(std::integral_constant<int, 0>{}, 0, aq[0]);
+    using First = std::integral_constant<int, 0>;
+    static_for<S>([&](auto St) {
+        copy(St, (int)St.value < nk ? (int)St.value : nk - 1);
+        __builtin_amdgcn_sched_barrier(0);
+    });
+    join_waves<(S - 1) * kStepCopies>();
+    read_w(First{});
+    read_a(First{}, 0, aq[0]);
 #pragma unroll
-    for (int j = 0; j < NT; ++j) bq[j] = codes(std::integral_constant<int, 0>{}, j, 0);
+    for (int j = 0; j < NT; ++j) bq[j] = codes(j, 0);
     int ks = 0;
-    for (; ks + kStages <= nk; ks += kStages) {
-        step(std::integral_constant<int, 0>{}, ks);
-        step(std::integral_constant<int, 1>{}, ks + 1);
-        step(std::integral_constant<int, 2>{}, ks + 2);
-    }
-    if (ks < nk) step(std::integral_constant<int, 0>{}, ks);
-    if (ks + 1 < nk) step(std::integral_constant<int, 1>{}, ks + 1);
+    for (; ks + S <= nk; ks += S) static_for<S>([&](auto St) { step(St, ks + (int)St.value); });
+    static_for<S - 1>([&](auto St) {
+        if (ks + (int)St.value < nk) step(St, ks + (int)St.value);
+    });
 
     // the last copies into LDS have landed in every wave before the stages
     // serve for the tokens' scales and sums
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    float* const sx = reinterpret_cast<float*>(&As[0][0]);
+    join_waves<0>();
+    float* const sx = reinterpret_cast<float*>(As0);
     int32_t* const ssum = reinterpret_cast<int32_t*>(sx + Tl::BM);
     if (tid < Tl::BM) {
         const int64_t m = m0 + tid < a.M ? m0 + tid : a.M - 1;
@@ -370,11 +416,13 @@ __global__ __launch_bounds__(256, kOcc) void many_i8_kernel(I8Args a)
 
     // lane (c, h) holds column c of each tile, rows 8 (e / 4) + 4 h + e % 4
     const int64_t y_row = a.N * (a.bf16 ? 2 : 4);
-    const bool fits = Tl::BM * y_row <= 0xffffffffLL;
-    const BufRef yb = uniform_buf(static_cast<char*>(a.y) + m0 * y_row, (uint32_t)(fits ? mrows * y_row : 0));
+    // whole tiles store without checks, at scalar row offsets (the tile's rows of y
+    // must span less than 4 GiB)
+    const bool inside = Tl::BM * y_row <= 0xffffffffLL && m0 + Tl::BM <= a.M && n0 + Tl::BN <= a.N;
+    const BufRef yb = uniform_buf(static_cast<char*>(a.y) + m0 * y_row, (uint32_t)(inside ? Tl::BM * y_row : 0));
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-        const int64_t n = n0 + wave * 32 * NT + j * 32 + c;
+        const int64_t n = n0 + wn * 32 * NT + j * 32 + c;
         const bool in = n < a.N;
         const float sw = in ? a.scales[n] : 0.0f;
         const int32_t z = in ? code_shift<B>(a.zeros, n) : 0;
@@ -382,7 +430,7 @@ __global__ __launch_bounds__(256, kOcc) void many_i8_kernel(I8Args a)
         for (int i = 0; i < MT; ++i) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int row = i * 32 + 8 * q + 4 * h;
+                const int row = (wm * MT + i) * 32 + 8 * q + 4 * h;
                 const float4 s4 = *reinterpret_cast<const float4*>(sx + row);
                 const int4 t4 = *reinterpret_cast<const int4*>(ssum + row);
                 const float s[4] = {s4.x, s4.y, s4.z, s4.w};
@@ -390,10 +438,9 @@ __global__ __launch_bounds__(256, kOcc) void many_i8_kernel(I8Args a)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float v = finish_i8(acc[i][j][4 * q + e], z, t[e], s[e], sw);
-                    if (fits) {
-                        // rows past M lie past the buffer; columns past N are sent there
-                        const uint32_t voff = in ? (uint32_t)(4 * h * y_row + n * (a.bf16 ? 2 : 4)) : 0xfffffff0u;
-                        const uint32_t soff = (uint32_t)((i * 32 + 8 * q + e) * y_row);
+                    if (inside) {
+                        const uint32_t voff = (uint32_t)(4 * h * y_row + n * (a.bf16 ? 2 : 4));
+                        const uint32_t soff = (uint32_t)(((wm * MT + i) * 32 + 8 * q + e) * y_row);
                         if (a.bf16)
                             __builtin_amdgcn_raw_buffer_store_b16(bf16_round(v), make_rsrc(yb.base, yb.bytes), voff, soff, 2);
                         else
@@ -410,13 +457,13 @@ __global__ __launch_bounds__(256, kOcc) void many_i8_kernel(I8Args a)
     }
 }
 
-template <int B, int MT, int NT, int kOcc>
+template <int B, int MT, int NT, int WM, int kOcc>
 hipError_t launch_many(const I8Args& a, hipStream_t stream)
 {
-    using Tl = ManyTile<MT, NT>;
+    using Tl = ManyTile<MT, NT, WM>;
     const int64_t tiles = ceil_div(a.M, Tl::BM) * ceil_div(a.N, Tl::BN);
-    if (tiles > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-    many_i8_kernel<B, MT, NT, kOcc><<<dim3((unsigned)tiles), dim3(256), 0, stream>>>(a);
+    if (tiles > 0x7ffffff0LL) return hipErrorInvalidConfiguration;
+    many_i8_kernel<B, MT, NT, WM, kOcc><<<dim3((unsigned)((tiles + 7) & ~7LL)), dim3(Tl::kThreads), 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -428,13 +475,16 @@ hipError_t launch_b(const I8Args& a, hipStream_t stream)
         if (a.M <= 32) return launch_few_rows<B, 2>(a, stream);
         return launch_few_rows<B, 4>(a, stream);
     }
-    // 256 x 256 tiles when they fill the 256 CUs in whole rounds (at least 80 %
-    // of the last round busy)
+    // 256 x 256 tiles, eight waves, when they fill the 256 CUs in whole rounds (at
+    // least 80 % of the last round busy): 2048 x 8192 x 8192 at b = 8 122 us (2.25 POP/s)
+    // against 139 us for 128 x 128 tiles of four waves, two or three to a CU
     const int64_t wide = ceil_div(a.M, 256) * ceil_div(a.N, 256);
     if (a.M >= 256 && wide >= 256 && wide * 5 >= ceil_div(wide, 256) * 256 * 4)
-        return launch_many<B, 8, 2, 1>(a, stream);
-    if (ceil_div(a.M, 128) * ceil_div(a.N, 256) >= 400) return launch_many<B, 4, 2, 2>(a, stream);
-    return launch_many<B, 4, 1, 2>(a, stream);
+        return launch_many<B, 4, 2, 2, 2>(a, stream);
+    // 128 x 128 tiles: 333 x 17408 x 5120 at b = 5 51 us (64 x 128 67 us, 192 x 128 59 us,
+    // 128 x 256 55 us, 256 x 256 82 us); half as high while they leave CUs without one
+    if (ceil_div(a.M, 128) * ceil_div(a.N, 128) >= 256) return launch_many<B, 4, 1, 1, 3>(a, stream);
+    return launch_many<B, 2, 1, 1, 3>(a, stream);
 }
 
 }  // namespace
