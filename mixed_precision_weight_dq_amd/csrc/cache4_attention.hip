@@ -885,25 +885,454 @@ __global__ __launch_bounds__(kThreads) void cache4_join_edges_kernel(AttnArgs a)
                                                        bf16x2(acc[i + 2] * inv, acc[i + 3] * inv));
 }
 
+// ---------------------------------------------------------------------------
+// Many new tokens (a prompt, or a piece of one): bound by the matrix cores and
+// the vector units, so each code is expanded once for many rows.  NW waves of 32
+// rows each share steps of 16 NW positions.  Half of the waves expand a step's
+// keys, half its values, 32 positions each, to fp16 in LDS (code * scale, two
+// buffers, one barrier per step; a step's words are loaded two steps ahead);
+// then every wave multiplies with v_mfma_f32_32x32x16_f16, transposed as above
+// (lane & 31 is a row throughout, P^T goes in as S^T comes out).
+//
+// Here keys and values are rounded: a scale to fp16 (2^-11, after a power of
+// two common to 32 positions), its product with the code again (2^-11).  The
+// alternative, exact codes and a scale per group after the product, is 128 more
+// vector operations per 64 positions, a third of the step.  A value scale that is
+// NaN is taken as 0 and marked: its dimensions become NaN in the rows that see it.
+//
+// LDS: 16-byte pieces.  Keys: word w of position t at piece t (D / 8) + (w ^ (t & 7)).
+// Values, transposed: the 8 positions that a lane's operand holds, piece q of
+// dimension d at d (positions / 8) + (q ^ (d & 7)).  Both spread a pass's reads
+// over the banks.
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+// every wave's LDS operations done, then the barrier (loads stay in flight)
+__device__ __forceinline__ void lds_barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));  // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+template <int D, int G, int NW>
+struct PromptTile {
+    static constexpr int kRows = 32 * NW;
+    static constexpr int kTiles = NW / 2;      // of 32 positions per step
+    static constexpr int kPos = 32 * kTiles;
+    static constexpr int kOcc = D == 256 ? 1 : 2;  // waves per SIMD
+};
+
+template <int D, int G, int NW>
+__global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_prompt_kernel(AttnArgs a, int32_t grid_tiles)
+{
+    using Tl = PromptTile<D, G, NW>;
+    constexpr int NC = D / 32, NG = D / G, NT = D / 32;
+    constexpr int TT = Tl::kTiles, kPos = Tl::kPos;
+    constexpr int KW = D / 16;                     // key words of a lane: half a row
+    constexpr int VW = D / 128 > 0 ? D / 128 : 1;  // value words of a lane and position
+    constexpr int NS = (NG + 1) / 2;               // scales of a lane
+    __shared__ __attribute__((aligned(16))) uint4 Kt[2][kPos * (D / 8)];
+    __shared__ __attribute__((aligned(16))) uint4 Vt[2][D * (kPos / 8)];
+    __shared__ __attribute__((aligned(16))) _Float16 sc[NW][32 * NG];
+    __shared__ int kexp[2][TT], vexp[2][TT];
+    __shared__ uint32_t vnan[2][TT][NG];
+
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int r32 = lane & 31;
+    const int h = lane >> 5;
+    const int shift = a.c.page_shift;
+
+    // units (sequence, kv head, tile), a contiguous range of them per XCD, so that
+    // the tiles of a kv head share an L2; a head's last tiles, the longest, first
+    const int64_t units = (int64_t)a.bt.count * a.c.heads * grid_tiles;
+    const int64_t u = (int64_t)(blockIdx.x & 7) * ((units + 7) >> 3) + (blockIdx.x >> 3);
+    if (u >= units) return;
+    const int64_t head_unit = udiv(u, grid_tiles);
+    const int tile_at = grid_tiles - 1 - (int)(u - head_unit * grid_tiles);
+    const int b = (int)udiv(head_unit, a.c.heads);
+    const int kvh = (int)(head_unit - (int64_t)b * a.c.heads);
+    const Rows rw = rows_of(a, b);
+    const int64_t rows = rw.rows();
+    const __attribute__((address_space(4))) int32_t* table =
+        (const __attribute__((address_space(4))) int32_t*)(a.bt.table + b * a.bt.width);
+
+    for (int64_t tile = tile_at; tile * Tl::kRows < rows; tile += grid_tiles) {
+        const int64_t r0 = tile * Tl::kRows;
+        const int64_t w0 = r0 + wave * 32;  // the wave's first row
+        const bool live = w0 + r32 < rows;
+        const int64_t row = live ? w0 + r32 : 0;
+        const int qi = (int)udiv(row, rw.per);
+        const int head = kvh * rw.per + (int)(row - (int64_t)qi * rw.per);
+        const int seen = live ? rw.seen(row) : 0;
+        const auto seen_at = [&](int64_t r) { return rw.seen(r < rows ? r : rows - 1); };
+        const int end = seen_at(r0 + Tl::kRows - 1);                 // of the workgroup's rows
+        const int wave_end = w0 < rows ? seen_at(w0 + 31) : 0;       // of the wave's
+        const int all_see = w0 < rows ? rw.seen(w0) : 0;             // by every live row of it
+
+        // q rows: operand kk = 2 i + p holds dimensions 32 i + 8 (2 p + h) + (0 4 1 5 2 6 3 7)
+        f16x8_t qf[2 * NC];
+        float logit;
+        {
+            const uint16_t* qp = a.q + (int64_t)(rw.first + qi) * a.q_stride + (int64_t)head * D + 8 * h;
+            uint4 qr[2 * NC];
+            uint32_t qmax = 0;
+#pragma unroll
+            for (int k = 0; k < 2 * NC; ++k) {
+                qr[k] = *reinterpret_cast<const uint4*>(qp + 16 * k);
+                const uint32_t v[4] = {qr[k].x, qr[k].y, qr[k].z, qr[k].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    qmax = max(qmax, max((v[e] << 16) & 0x7fffffffu, v[e] & 0x7fff0000u));
+            }
+            qmax = max(qmax, (uint32_t)__shfl_xor((int)qmax, 32, kWave));
+            const int ue = min(14 - exponent(__uint_as_float(qmax)), 126);
+            float up = a.scale_log2 < 0.0f ? -pow2(ue) : pow2(ue);
+            logit = fabsf(a.scale_log2) * pow2(-ue);
+            if (logit == 0.0f) {
+                up = 0.0f;
+                logit = 1.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < 2 * NC; ++k) {
+                const uint32_t v[4] = {qr[k].x, qr[k].y, qr[k].z, qr[k].w};
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    f[2 * e] = __uint_as_float(v[e] << 16) * up;
+                    f[2 * e + 1] = __uint_as_float(v[e] & 0xffff0000u) * up;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    qf[k][2 * e] = (_Float16)f[e];
+                    qf[k][2 * e + 1] = (_Float16)f[e + 4];
+                }
+            }
+        }
+
+        // ---- a step's words: wave w < TT has the keys of 32 positions, w >= TT values
+        const bool keys = wave < TT;
+        const int part = keys ? wave : wave - TT;  // which 32 positions of the step
+        uint32_t kw[KW], vw[8][VW];
+        float sl[NS];
+        uint32_t bad = 0;  // a NaN's bits where the page is outside the cache
+        auto load = [&](int pos0) __attribute__((always_inline)) {
+            const int t0 = pos0 + 32 * part;
+            int pg[2], tt[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                tt[i] = t0 + 16 * i < end ? t0 + 16 * i : (end - 1) & ~15;
+                pg[i] = table[tt[i] >> shift];
+            }
+            // this lane's 16 positions: the lower or the upper half of the wave
+            const int t16 = h ? tt[1] : tt[0];
+            const int page = h ? pg[1] : pg[0];
+            const bool ok = (unsigned)page < (unsigned)a.c.pages;
+            bad = ok ? 0u : 0x7fc00000u;
+            const int64_t block = (int64_t)(ok ? page : 0) * a.c.heads + kvh;
+            const int off = t16 & ((1 << shift) - 1);
+            const int64_t code_row = (block << shift) + off;
+            if (keys) {
+                const uint32_t* kp = a.c.k_codes + (code_row + ((lane >> 1) & 15)) * (D / 8) + (lane & 1) * KW;
+#pragma unroll
+                for (int i = 0; i < KW; i += 4) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(kp + i);
+                    kw[i] = v.x, kw[i + 1] = v.y, kw[i + 2] = v.z, kw[i + 3] = v.w;
+                }
+            } else {
+                // positions 4 h' + e and 8 + 4 h' + e of the 16, h' = bit 4 of the lane
+                const int first = ((lane >> 4) & 1) * 4;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t* vp = a.c.v_codes + (code_row + first + (e & 3) + (e & 4) * 2) * (D / 8);
+                    if constexpr (D == 64) {
+                        vw[e][0] = reinterpret_cast<const uint16_t*>(vp)[lane & 15];
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < VW; ++i) vw[e][i] = vp[(lane & 15) * VW + i];
+                    }
+                }
+            }
+            // scales of position lane & 15 of the 16, groups of the parity of bit 4
+            const float* sp = (keys ? a.c.k_scales : a.c.v_scales) + ((block * NG) << shift) + off + (lane & 15);
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                const int g = 2 * i + ((lane >> 4) & 1) < NG ? 2 * i + ((lane >> 4) & 1) : NG - 1;
+                sl[i] = sp[(int64_t)g << shift];
+            }
+        };
+        // the loaded words -> fp16 pieces of buffer nb
+        auto expand = [&](int pos0, int nb) __attribute__((always_inline)) {
+            const bool past = pos0 + 32 * part + 16 * h + (lane & 15) >= end;
+            const int gpar = (lane >> 4) & 1;
+            float top = 0.0f;
+            uint64_t nan_at[NS];
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                if (past) sl[i] = 0.0f;
+                nan_at[i] = 0;
+                if (!keys) {
+                    const bool nan = sl[i] != sl[i];
+                    nan_at[i] = __ballot(nan);
+                    if (nan) sl[i] = 0.0f;
+                }
+                top = fmaxf(top, sl[i]);
+            }
+            int ex = exponent(__uint_as_float(
+                __builtin_amdgcn_readfirstlane(__float_as_uint(wave_max_abs(top)))));
+            if (ex < -104) ex = -104;
+            // values: in steps of 8, so that the running exponent seldom moves
+            if (!keys) ex |= 7;
+            const float fac = pow2(10 - ex);
+            _Float16* const s16 = sc[wave];
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                const int g = 2 * i + gpar;
+                if (g < NG) {
+                    const float x = sl[i] * fac;
+                    if (keys) {
+                        // NaN stays, and a page outside the cache is one
+                        s16[(16 * h + (lane & 15)) * NG + g] =
+                            (_Float16)__uint_as_float(__float_as_uint(x) | bad);
+                    } else {
+                        const int t = lane & 15;
+                        s16[g * 32 + (2 * h + ((t >> 2) & 1)) * 8 + (t & 3) + 4 * (t >> 3)] = (_Float16)x;
+                    }
+                }
+            }
+            if (lane == 0) {
+                if (keys) {
+                    kexp[nb][part] = ex;
+                } else {
+                    vexp[nb][part] = ex;
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        // lanes 32 s + 16 (g & 1) + t: position 16 s + t
+                        const uint64_t m = nan_at[g >> 1] >> (16 * (g & 1));
+                        vnan[nb][part][g] = (uint32_t)(m & 0xffffu) | ((uint32_t)(m >> 32) << 16);
+                    }
+                }
+            }
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            if (keys) {
+                const int t = lane >> 1;
+                uint4* const dst = &Kt[nb][(32 * part + t) * (D / 8)];
+                f16x2_t s2[NG];
+#pragma unroll
+                for (int g = 0; g < NG; ++g) s2[g] = (f16x2_t){s16[t * NG + g], s16[t * NG + g]};
+#pragma unroll
+                for (int k = 0; k < KW; ++k) {
+                    const f16x2_t s = s2[(k % NC) * 32 / G];
+                    const uint32_t x = kw[k] >> 8;
+                    const uint4 v = make_uint4(u32_of(f16x2_of(low_codes(kw[k])) * s), u32_of(f16x2_of(high_codes(kw[k])) * s),
+                                               u32_of(f16x2_of(low_codes(x)) * s), u32_of(f16x2_of(high_codes(x)) * s));
+                    dst[((lane & 1) * KW + k) ^ (t & 7)] = v;
+                }
+            } else {
+                const int tg = lane >> 4;
+                uint32_t s4[NG][4];
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(s16 + g * 32 + tg * 8);
+                    s4[g][0] = v.x, s4[g][1] = v.y, s4[g][2] = v.z, s4[g][3] = v.w;
+                }
+#pragma unroll
+                for (int i = 0; i < VW; ++i) {
+#pragma unroll
+                    for (int n = 0; n < (D == 64 ? 2 : 4); ++n) {
+                        const uint32_t sel = 0x0c000c00u | ((uint32_t)(4 + n) << 16) | (uint32_t)n;
+                        const int j = 8 * i + 2 * n;
+                        uint32_t lo[4], hi[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t v = __builtin_amdgcn_perm(vw[2 * e + 1][i], vw[2 * e][i], sel);
+                            lo[e] = u32_of(f16x2_of(low_codes(v)) * f16x2_of(s4[16 * j / G][e]));
+                            hi[e] = u32_of(f16x2_of(high_codes(v)) * f16x2_of(s4[16 * (j + 1) / G][e]));
+                        }
+                        const int d = 16 * j + (lane & 15);
+                        const int q = (4 * part + tg) ^ (d & 7);
+                        Vt[nb][d * (kPos / 8) + q] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        Vt[nb][(d + 16) * (kPos / 8) + q] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    }
+                }
+            }
+        };
+
+        float m = -INFINITY, l = 0.0f;
+        int ve = -97;  // exponent of the values in o
+        f32x16_t o[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[j][e] = 0.0f;
+
+        // 64 positions of buffer cb, the tiles 2 hp and 2 hp + 1
+        auto compute = [&](int pos, int cb, int hp) __attribute__((always_inline)) {
+            f32x16_t s[2];
+            float f[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
+                const int at = 32 * (2 * hp + t) + r32;
+#pragma unroll
+                for (int k = 0; k < 2 * NC; ++k) {
+                    const int w = (2 * (k & 1) + h) * NC + (k >> 1);
+                    s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                        __builtin_bit_cast(f16x8_t, Kt[cb][at * (D / 8) + (w ^ (at & 7))]), qf[k], s[t], 0, 0, 0);
+                }
+                // (not 0, which a hidden position's -inf would make NaN)
+                f[t] = fmaxf(logit * pow2(kexp[cb][2 * hp + t] - 10), 0x1p-126f);
+            }
+            if (pos + 64 > all_see) {
+                const int left = seen - pos - 4 * h;
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (32 * t + 8 * (e >> 2) + (e & 3) >= left) s[t][e] = -INFINITY;
+            }
+            float mx[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                mx[t] = s[t][0];
+#pragma unroll
+                for (int e = 1; e < 16; ++e) mx[t] = fmaxf(mx[t], s[t][e]);
+            }
+            float x0 = fmaxf(mx[0] * f[0], mx[1] * f[1]), x1;
+            row_pair(x0, true, x0, x1);
+            const float top = fmaxf(x0, x1);
+            // the reference only moves by more than 2^8 (weights stay below it), and
+            // the values' exponent with the largest seen
+            const int v0 = vexp[cb][2 * hp], v1 = vexp[cb][2 * hp + 1];
+            const int vn = max(ve, max(v0, v1));
+            if (__any(top > m + 8.0f) || vn != ve) {
+                const float mn = top > m + 8.0f ? top : m;
+                const float alpha = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+                const float os = alpha * pow2(ve - vn);
+                m = mn;
+                ve = vn;
+                l *= alpha;
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[j][e] *= os;
+            }
+            // weights up to 2^14: fp16's normal range then reaches 2^-20 of the largest
+            const float base = m == -INFINITY ? 0.0f : m - 6.0f;
+            f16x8_t p[2][2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int de = (t ? v1 : v0) - ve;
+                const float down = pow2(de);
+                float sum = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    s[t][e] = __builtin_amdgcn_exp2f(fmaf(s[t][e], f[t], -base));
+                    sum += s[t][e];
+                }
+                l += sum;
+                if (de != 0) {  // values of another exponent
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) s[t][e] *= down;
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) p[t][e >> 3][e & 7] = (_Float16)s[t][e];
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int d = 32 * j + r32;
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int q = (4 * (2 * hp + t) + 2 * k + h) ^ (d & 7);
+                        o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                            __builtin_bit_cast(f16x8_t, Vt[cb][d * (kPos / 8) + q]), p[t][k], o[j], 0, 0, 0);
+                    }
+            }
+            // a NaN value scale: NaN in its dimensions, in the rows that see it
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const uint32_t n0 = vnan[cb][2 * hp][32 * j / G], n1 = vnan[cb][2 * hp + 1][32 * j / G];
+                if ((n0 | n1) != 0) {
+                    const int see = seen - pos;  // positions of these 64
+                    const uint64_t mask = (uint64_t)n0 | ((uint64_t)n1 << 32);
+                    const uint64_t mine = see >= 64 ? mask : (see <= 0 ? 0 : mask & ((1ull << see) - 1));
+                    if (mine) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[j][e] = __uint_as_float(0x7fc00000u);
+                    }
+                }
+            }
+        };
+
+        if (end > 0) {
+            load(0);
+            expand(0, 0);
+            if (kPos < end) load(kPos);
+            for (int pos = 0, cb = 0; pos < end; pos += kPos, cb ^= 1) {
+                lds_barrier();  // buffer cb is whole, the other is read by no wave any more
+                if (pos + kPos < end) {
+                    expand(pos + kPos, cb ^ 1);
+                    if (pos + 2 * kPos < end) load(pos + 2 * kPos);
+                }
+#pragma unroll
+                for (int hp = 0; hp < TT / 2; ++hp)
+                    if (pos + 64 * hp < wave_end) compute(pos + 64 * hp, cb, hp);
+            }
+        }
+
+        float l0, l1;
+        row_pair(l, true, l0, l1);
+        l = l0 + l1;
+        float inv = l > 0.0f ? pow2(ve - 10) / l : (l == 0.0f ? 0.0f : l);  // NaN stays
+        if (rw.bad) inv = __uint_as_float(0x7fc00000u);
+        if (live) {
+            uint16_t* op = a.out + ((int64_t)(rw.first + qi) * a.q_heads + head) * D + 4 * h;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    *reinterpret_cast<uint2*>(op + 32 * j + 8 * e) =
+                        make_uint2(bf16x2(o[j][4 * e] * inv, o[j][4 * e + 1] * inv),
+                                   bf16x2(o[j][4 * e + 2] * inv, o[j][4 * e + 3] * inv));
+        }
+        lds_barrier();  // the buffers are free for the next tile
+    }
+}
+
 // The launch's shape: as many workgroups as fill the 256 CUs four deep (two
 // for heads of 256, whose registers and LDS allow no more), fewer where there
 // are not that many steps.
-#ifndef DQ_FILL
-#define DQ_FILL 512
-#endif
-constexpr int64_t kFill = DQ_FILL;
+constexpr int64_t kFill = 512;
+constexpr int64_t kPromptUnits = 96;  // (sequence, kv head, row tile)s for the prompt kernel
 
 struct Plan {
     int64_t rows, units, groups;
+    int prompt_waves;      // 0: cache4_attention_kernel, else waves of cache4_prompt_kernel
+    int64_t prompt_tiles;  // its row tiles per (sequence, kv head)
     size_t part_bytes, ml_bytes;
 };
 
 Plan plan_of(const Cache4& c, int64_t count, int64_t tokens, int q_heads, int64_t max_q, int64_t max_len)
 {
-    Plan p;
+    Plan p{};
     if (max_q > tokens) max_q = tokens;
     if (max_len > 0x7fffffffLL) max_len = 0x7fffffffLL;
     p.rows = max_q * (q_heads / c.heads);
+    for (int waves = 8; waves >= 4; waves /= 2) {
+        if (waves == 8 && c.dim == 256) continue;  // the buffers would not fit in LDS
+        const int64_t tiles = ceil_div(p.rows, 32 * waves);
+        const int64_t units = count * c.heads * tiles;
+        if (p.rows >= 16 * waves && units >= kPromptUnits && units <= 0x7ffffff0LL) {
+            p.prompt_waves = waves;
+            p.prompt_tiles = tiles;
+            return p;
+        }
+    }
     p.units = count * c.heads * ceil_div(p.rows, 16);
     const int64_t fill = c.dim == 256 ? kFill / 2 : kFill;
     p.groups = p.units > fill ? fill : p.units * ceil_div(max_len, kStride);
@@ -913,16 +1342,29 @@ Plan plan_of(const Cache4& c, int64_t count, int64_t tokens, int q_heads, int64_
     return p;
 }
 
+template <int D, int G, int NW>
+void launch_prompt(const AttnArgs& a, const Plan& p, hipStream_t stream)
+{
+    const int64_t units = a.bt.count * a.c.heads * p.prompt_tiles;
+    cache4_prompt_kernel<D, G, NW><<<(unsigned)((units + 7) & ~7LL), 64 * NW, 0, stream>>>(a, (int32_t)p.prompt_tiles);
+}
+
 template <int D, int G>
 hipError_t launch_dg(const AttnArgs& a, const Plan& p, hipStream_t stream)
 {
-    cache4_attention_kernel<D, G><<<(unsigned)a.groups, kThreads, 0, stream>>>(a);
-    if (a.groups > 1) {
-        if (p.units * 2 > a.groups) {
-            cache4_join_edges_kernel<D><<<(unsigned)a.groups - 1, kThreads, 0, stream>>>(a);
-        } else {
-            const dim3 jgrid((unsigned)p.rows, (unsigned)a.c.heads, (unsigned)a.bt.count);
-            cache4_join_kernel<D><<<jgrid, kThreads, 0, stream>>>(a);
+    if (p.prompt_waves == 8) {
+        if constexpr (D != 256) launch_prompt<D, G, 8>(a, p, stream);
+    } else if (p.prompt_waves == 4) {
+        launch_prompt<D, G, 4>(a, p, stream);
+    } else {
+        cache4_attention_kernel<D, G><<<(unsigned)a.groups, kThreads, 0, stream>>>(a);
+        if (a.groups > 1) {
+            if (p.units * 2 > a.groups) {
+                cache4_join_edges_kernel<D><<<(unsigned)a.groups - 1, kThreads, 0, stream>>>(a);
+            } else {
+                const dim3 jgrid((unsigned)p.rows, (unsigned)a.c.heads, (unsigned)a.bt.count);
+                cache4_join_kernel<D><<<jgrid, kThreads, 0, stream>>>(a);
+            }
         }
     }
     return hipGetLastError();

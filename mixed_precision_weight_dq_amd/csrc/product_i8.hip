@@ -483,7 +483,7 @@ hipError_t launch_b(const I8Args& a, hipStream_t stream)
         return launch_many<B, 4, 2, 2, 2>(a, stream);
     // 128 x 128 tiles: 333 x 17408 x 5120 at b = 5 51 us (64 x 128 67 us, 192 x 128 59 us,
     // 128 x 256 55 us, 256 x 256 82 us); half as high while they leave CUs without one
-    if (ceil_div(a.M, 128) * ceil_div(a.N, 128) >= 256) return launch_many<B, 4, 1, 1, 3>(a, stream);
+    if (ceil_div(a.M, 128) * ceil_div(a.N, 128) >= 256) return launch_many<B, 4, 1, 1, B <= 5 ? 3 : 2>(a, stream);
     return launch_many<B, 2, 1, 1, 3>(a, stream);
 }
 

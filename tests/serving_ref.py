@@ -126,7 +126,7 @@ def attention_ref(q, kv, batch, q_heads, scale):
     return out, W, delta
 
 
-def attention_tolerance(ref, W, delta, D, n, v_max):
+def attention_tolerance(ref, W, delta, D, n, v_max, prompt=False):
     """How far cache4_attention may be from attention_ref, from the roundings that it makes:
     * the output is rounded to bf16: 2^-8 |ref|;
     * a logit: D products are exact, their fp32 sum and the scalings round at most D + 8 times,
@@ -136,9 +136,15 @@ def attention_tolerance(ref, W, delta, D, n, v_max):
     * the hardware's exp2 is within 2^-22 of a weight;
     * weight times value scale rounds to fp32 (2^-24) and fp16 (2^-11), below fp16's normal range
       by 2^-25 of 2^14 of the largest scale: n * 2^-38 * v_max covers |code| <= 8;
-    * n products and the weights' sum accumulate in fp32: 2 n 2^-24, with the rescalings."""
+    * n products and the weights' sum accumulate in fp32: 2 n 2^-24, with the rescalings.
+    prompt: the kernel for many new tokens also rounds each scale to fp16 and its product with
+    the code again, 2 * 2^-11 of a key (so of a logit's magnitudes) and of a value; a weight below
+    fp16's normal range is off by 2^-25 of at least 2^6, a scale below it by 2^-25 of 2^10."""
     e = 2 * (D + 16) * EPS32 * delta[..., None]
     rel = EPS_F16 + 2 * (2.0 ** -22) + 4 * n * EPS32 + e
+    if prompt:
+        rel = rel + 2 * EPS_F16 + 2 * 2 * EPS_F16 * delta[..., None]
+        v_max = v_max * (1 + 2.0 ** 7)  # n 2^-38 -> n 2^-31, which covers both
     return EPS_BF16 * np.abs(ref) * (1 + 2.0 ** -7) + W * rel * (1 + 2.0 ** -6) + n * 2.0 ** -38 * v_max
 
 

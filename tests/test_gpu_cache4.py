@@ -156,7 +156,7 @@ def test_append_skips_what_the_cache_does_not_hold():
 
 
 def run_attention(seed, batch, H, per, D, g, scale=None, q_mul=2.0, max_q=None, max_len=None, tail=2,
-                  q=None):
+                  q=None, prompt=False):
     t = torch()
     cache, kv = filled(seed, batch, H, D, g)
     T = batch.tokens + tail
@@ -173,7 +173,7 @@ def run_attention(seed, batch, H, per, D, g, scale=None, q_mul=2.0, max_q=None, 
     q64 = widen(qb)[:batch.tokens, 1:].astype(np.float64)
     ref, W, delta = attention_ref(q64, kv, batch, H * per, scale)
     v_max = max([np.abs(v).max() for _, v in kv if v.size] or [0.0])
-    tol = attention_tolerance(ref, W, delta, D, int(batch.lens.max()), v_max)
+    tol = attention_tolerance(ref, W, delta, D, int(batch.lens.max()), v_max, prompt)
     bad = ~(np.abs(got[:batch.tokens] - ref) <= tol)
     if bad.any():
         at = tuple(np.argwhere(bad)[0])
@@ -227,6 +227,61 @@ def test_attention_prompt(D, g):
     batch = Batch(9, [333, 600, 128], [333, 150, 97], 64)
     report("cache4_attention prompt D=%d g=%d" % (D, g))
     run_attention(50, batch, 2, 3, D, g, max_q=333, max_len=600)
+
+
+@pytest.mark.parametrize("D,g", GEOMETRY)
+def test_attention_prompt_batches(D, g):
+    """Enough rows for the kernel of many new tokens (whose rounding of keys and values the bound
+    then counts): first prompts and later ones, ragged, empty sequences and rows that see nothing
+    among them, tiles of 256 and of 128 rows, the launch sized right and too small."""
+    rng = np.random.default_rng(D + g)
+    for i, (count, top, H, per, page) in enumerate([(13, 150, 4, 2, 32), (25, 30, 4, 3, 16)]):
+        news = [int(n) for n in rng.integers(1, top + 1, count)]
+        news[0], news[1], news[2] = top, 0, top // 2
+        lens = [n + int(k) for n, k in zip(news, rng.integers(0, 200, count))]
+        lens[2] = news[2] - 3  # its first three rows see nothing
+        lens[3] = news[3]
+        batch = Batch(i, lens, news, page)
+        for hints in (dict(max_q=top, max_len=max(lens)), dict(max_q=(top * 2) // 3, max_len=1)):
+            report("cache4_attention prompts D=%d g=%d count=%d top=%d %s" % (D, g, count, top, hints))
+            got, ref = run_attention(i + 70, batch, H, per, D, g, prompt=True, **hints)
+        s = batch.starts[2]
+        assert (got[s:s + 3] == 0).all()
+
+
+def test_attention_prompt_special():
+    """The kernel of many new tokens on what it treats apart: NaN groups, pages outside the cache,
+    values whose magnitude grows along the sequence, queries far from 1."""
+    t = torch()
+    D, g, H, per, count, n = 128, 32, 4, 2, 13, 160
+    batch = Batch(21, [n] * count, [n] * count, 16)
+    k, v = head_vectors(1, count * n, H, D), head_vectors(2, count * n, H, D)
+    v *= np.exp2(np.linspace(-30, 20, n)).astype(np.float32)[np.tile(np.arange(n), count), None, None]
+    v[3 * n + 70, 1, 40] = np.nan   # sequence 3, head 1, group 1
+    k[4 * n + 100, 2, 5] = np.inf   # sequence 4, head 2
+    cache = dq.Cache4.empty(batch.pages, H, D, 16, g)
+    full = gpu(batch.starts)
+    dq.cache4_append(cache, gpu(k), gpu(v), full, gpu(batch.lens), gpu(batch.table))
+    kd, vd = dq.cache4_read(cache, count * n, full, gpu(batch.lens), gpu(batch.table))
+    kv = [(a, b) for a, b in zip(kd.double().cpu().numpy().reshape(count, n, H, D),
+                                 vd.double().cpu().numpy().reshape(count, n, H, D))]
+    table = batch.table.copy()
+    table[5, 6] = -1  # positions 96 .. 111 of sequence 5
+    for mul, scale in ((1.0, None), (2.0 ** 90, 2.0 ** -93)):
+        qb = bf16(np.random.default_rng(3).standard_normal((count * n, H * per, D)) * mul)
+        report("cache4_attention prompts, special values, q x %g" % mul)
+        out = dq.cache4_attention(cache, bf16_gpu(qb), full, gpu(batch.lens), gpu(table), max_q=n,
+                                  max_len=n, scale=scale).double().cpu().numpy()
+        nan = np.zeros(out.shape, bool)
+        nan[3 * n + 70:4 * n, 2:4, 32:64] = True
+        nan[4 * n + 100:5 * n, 4:6] = True
+        nan[5 * n + 96:6 * n] = True
+        assert np.array_equal(np.isnan(out), nan)
+        clean = [(np.nan_to_num(a), np.nan_to_num(b)) for a, b in kv]
+        ref, W, delta = attention_ref(widen(qb).astype(np.float64), clean, batch, H * per,
+                                      D ** -0.5 if scale is None else scale)
+        tol = attention_tolerance(ref, W, delta, D, n, np.nanmax(np.abs(vd.cpu().numpy())), True)
+        assert (np.abs(out - ref) <= tol)[~nan].all()
 
 
 def test_attention_logit_range():
