@@ -900,10 +900,15 @@ __global__ __launch_bounds__(kThreads) void cache4_join_edges_kernel(AttnArgs a)
 // vector operations per 64 positions, a third of the step.  A value scale that is
 // NaN is taken as 0 and marked: its dimensions become NaN in the rows that see it.
 //
-// LDS: 16-byte pieces.  Keys: word w of position t at piece t (D / 8) + (w ^ (t & 7)).
-// Values, transposed: the 8 positions that a lane's operand holds, piece q of
-// dimension d at d (positions / 8) + (q ^ (d & 7)).  Both spread a pass's reads
-// over the banks.
+// LDS: 16-byte pieces.  Keys: word w of position t is piece w of row t; values,
+// transposed: the 8 positions that a lane's operand holds are a piece of
+// dimension d's row.  Piece p of a row lies at p ^ swizzle(row), which spreads the
+// rows of a pass over the banks (of rows of 8 pieces, two share all banks).
+template <int kPieces>
+__device__ __forceinline__ int swizzle(int row)
+{
+    return kPieces == 8 ? (row >> 1) & 7 : row & 15;
+}
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 // every wave's LDS operations done, then the barrier (loads stay in flight)
@@ -1014,7 +1019,7 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
         // ---- a step's words: wave w < TT has the keys of 32 positions, w >= TT values
         const bool keys = wave < TT;
         const int part = keys ? wave : wave - TT;  // which 32 positions of the step
-        uint32_t kw[KW], vw[8][VW];
+        uint32_t raw[KW > 8 * VW ? KW : 8 * VW];  // key words, or value words [position][word]
         float sl[NS];
         uint32_t bad = 0;  // a NaN's bits where the page is outside the cache
         auto load = [&](int pos0) __attribute__((always_inline)) {
@@ -1038,7 +1043,7 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
 #pragma unroll
                 for (int i = 0; i < KW; i += 4) {
                     const uint4 v = *reinterpret_cast<const uint4*>(kp + i);
-                    kw[i] = v.x, kw[i + 1] = v.y, kw[i + 2] = v.z, kw[i + 3] = v.w;
+                    raw[i] = v.x, raw[i + 1] = v.y, raw[i + 2] = v.z, raw[i + 3] = v.w;
                 }
             } else {
                 // positions 4 h' + e and 8 + 4 h' + e of the 16, h' = bit 4 of the lane
@@ -1047,10 +1052,10 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
                 for (int e = 0; e < 8; ++e) {
                     const uint32_t* vp = a.c.v_codes + (code_row + first + (e & 3) + (e & 4) * 2) * (D / 8);
                     if constexpr (D == 64) {
-                        vw[e][0] = reinterpret_cast<const uint16_t*>(vp)[lane & 15];
+                        raw[e] = reinterpret_cast<const uint16_t*>(vp)[lane & 15];
                     } else {
 #pragma unroll
-                        for (int i = 0; i < VW; ++i) vw[e][i] = vp[(lane & 15) * VW + i];
+                        for (int i = 0; i < VW; ++i) raw[e * VW + i] = vp[(lane & 15) * VW + i];
                     }
                 }
             }
@@ -1125,10 +1130,10 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
 #pragma unroll
                 for (int k = 0; k < KW; ++k) {
                     const f16x2_t s = s2[(k % NC) * 32 / G];
-                    const uint32_t x = kw[k] >> 8;
-                    const uint4 v = make_uint4(u32_of(f16x2_of(low_codes(kw[k])) * s), u32_of(f16x2_of(high_codes(kw[k])) * s),
+                    const uint32_t x = raw[k] >> 8;
+                    const uint4 v = make_uint4(u32_of(f16x2_of(low_codes(raw[k])) * s), u32_of(f16x2_of(high_codes(raw[k])) * s),
                                                u32_of(f16x2_of(low_codes(x)) * s), u32_of(f16x2_of(high_codes(x)) * s));
-                    dst[((lane & 1) * KW + k) ^ (t & 7)] = v;
+                    dst[((lane & 1) * KW + k) ^ swizzle<D / 8>(t)] = v;
                 }
             } else {
                 const int tg = lane >> 4;
@@ -1147,12 +1152,12 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
                         uint32_t lo[4], hi[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const uint32_t v = __builtin_amdgcn_perm(vw[2 * e + 1][i], vw[2 * e][i], sel);
+                            const uint32_t v = __builtin_amdgcn_perm(raw[(2 * e + 1) * VW + i], raw[2 * e * VW + i], sel);
                             lo[e] = u32_of(f16x2_of(low_codes(v)) * f16x2_of(s4[16 * j / G][e]));
                             hi[e] = u32_of(f16x2_of(high_codes(v)) * f16x2_of(s4[16 * (j + 1) / G][e]));
                         }
                         const int d = 16 * j + (lane & 15);
-                        const int q = (4 * part + tg) ^ (d & 7);
+                        const int q = (4 * part + tg) ^ swizzle<kPos / 8>(d);
                         Vt[nb][d * (kPos / 8) + q] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                         Vt[nb][(d + 16) * (kPos / 8) + q] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     }
@@ -1181,7 +1186,7 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
                 for (int k = 0; k < 2 * NC; ++k) {
                     const int w = (2 * (k & 1) + h) * NC + (k >> 1);
                     s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                        __builtin_bit_cast(f16x8_t, Kt[cb][at * (D / 8) + (w ^ (at & 7))]), qf[k], s[t], 0, 0, 0);
+                        __builtin_bit_cast(f16x8_t, Kt[cb][at * (D / 8) + (w ^ swizzle<D / 8>(r32))]), qf[k], s[t], 0, 0, 0);
                 }
                 // (not 0, which a hidden position's -inf would make NaN)
                 f[t] = fmaxf(logit * pow2(kexp[cb][2 * hp + t] - 10), 0x1p-126f);
@@ -1248,7 +1253,7 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const int q = (4 * (2 * hp + t) + 2 * k + h) ^ (d & 7);
+                        const int q = (4 * (2 * hp + t) + 2 * k + h) ^ swizzle<kPos / 8>(r32);
                         o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
                             __builtin_bit_cast(f16x8_t, Vt[cb][d * (kPos / 8) + q]), p[t][k], o[j], 0, 0, 0);
                     }
@@ -1275,13 +1280,19 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
             if (kPos < end) load(kPos);
             for (int pos = 0, cb = 0; pos < end; pos += kPos, cb ^= 1) {
                 lds_barrier();  // buffer cb is whole, the other is read by no wave any more
-                if (pos + kPos < end) {
-                    expand(pos + kPos, cb ^ 1);
-                    if (pos + 2 * kPos < end) load(pos + 2 * kPos);
-                }
+                // the waves of the keys expand before they multiply, those of the
+                // values after: a SIMD has one of each, and so both kinds of work
+                auto refill = [&]() __attribute__((always_inline)) {
+                    if (pos + kPos < end) {
+                        expand(pos + kPos, cb ^ 1);
+                        if (pos + 2 * kPos < end) load(pos + 2 * kPos);
+                    }
+                };
+                if (keys) refill();
 #pragma unroll
                 for (int hp = 0; hp < TT / 2; ++hp)
                     if (pos + 64 * hp < wave_end) compute(pos + 64 * hp, cb, hp);
+                if (!keys) refill();
             }
         }
 
