@@ -5,9 +5,13 @@
 // v / s)), -8, 7), code u = q + 8; a group with a NaN or an infinity gets a NaN
 // scale and q = 0.
 //
-// A thread owns 8 dimensions of one (token, kv head, keys or values) row, so a
-// row is D/8 neighbouring threads of a wave and a group g/8 of them: the
-// group's maximum is a butterfly over those lanes.
+// Both kernels are bound by memory.  A workgroup has kTokens consecutive tokens, so
+// where a token lives is worked out once, with scalars, while its elements are on
+// their way; a thread has 8 dimensions of a (kv head, keys or values) row, D/8
+// neighbouring threads of a wave a row, g/8 of them a group, whose maximum is a
+// butterfly over those lanes.  6207 tokens of 8 heads of 128 in bf16 (a token
+// each for a workgroup of as many threads, its place found by every thread, took
+// 27 us to append and 19 us to read).
 #include "cache4.hpp"
 #include "common.hpp"
 #include "launch_serving.hpp"
@@ -19,178 +23,265 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// The row that a thread works on: row = (token * heads + head) * 2 + (0 keys, 1 values).
-struct RowAt {
-    int64_t token;
-    int head;
-    bool value;
-    int part;  // which 8 dimensions
-};
-
-__device__ __forceinline__ RowAt row_at(const Cache4& c, int64_t row, int part)
+// The place of each of a workgroup's tokens from t0 on: -2 for a token of no
+// sequence (or past the call's), -1 for one that the cache does not hold.
+template <int kTokens>
+__device__ __forceinline__ void find_slots(const Cache4& c, const Cache4Batch& bt, int64_t t0,
+                                           int64_t tokens, int64_t (&slot)[kTokens])
 {
-    const int64_t th = row >> 1;
-    return RowAt{th / c.heads, (int)(th % c.heads), (row & 1) != 0, part};
+    int64_t b = cache4_sequence(bt, t0);
+    int64_t first, n;
+    cache4_rows(bt, b, tokens, first, n);
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        const int64_t t = t0 + i;
+        while (t >= first + n && b + 1 < bt.count) cache4_rows(bt, ++b, tokens, first, n);
+        slot[i] = -2;
+        if (t >= first && t < first + n)
+            slot[i] = cache4_slot(c, bt, b, (int64_t)bt.lens[b] - n + (t - first));
+    }
 }
 
-template <bool BF16>
+// This thread's row (head, keys or values) and 8 dimensions; false past the last.
+struct Part {
+    int head;
+    bool value;
+    int part;
+};
+template <int D>
+__device__ __forceinline__ bool part_of(const Cache4& c, Part* p)
+{
+    constexpr unsigned kParts = D / 8;
+    const unsigned row = (blockIdx.y * blockDim.x + threadIdx.x) / kParts;
+    p->part = threadIdx.x % kParts;
+    p->value = row & 1;
+    p->head = (int)(row >> 1);
+    return p->head < c.heads;
+}
+
+template <int D, bool BF16, int kTokens>
 __global__ __launch_bounds__(kThreads) void cache4_append_kernel(
     Cache4 c, Cache4Batch bt, const void* __restrict__ k, const void* __restrict__ v,
     int64_t tokens, int64_t k_stride, int64_t v_stride)
 {
-    __shared__ uint8_t nib[kThreads * 8];
-    const int parts = c.dim >> 3;  // threads of a row: 8, 16 or 32
-    const int rows_here = kThreads / parts;
-    const int local = threadIdx.x / parts;
-    const RowAt at = row_at(c, (int64_t)blockIdx.x * rows_here + local, threadIdx.x % parts);
-    int64_t slot = -1;
-    bool live = at.token < tokens && cache4_slot(c, bt, at.token, tokens, &slot);
-    live = live && slot >= 0;
+    constexpr int kParts = D / 8;
+    constexpr int kPer = D / 16;  // value codes of a c (cache4.hpp)
+    __shared__ __attribute__((aligned(16))) uint32_t turn[kThreads];
+    const int64_t t0 = (int64_t)blockIdx.x * kTokens;
+    Part at;
+    const bool in = part_of<D>(c, &at);
 
-    float x[8];
+    uint4 raw[kTokens][BF16 ? 1 : 2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.0f;
-    if (live) {
-        const int64_t off = at.token * (at.value ? v_stride : k_stride) + at.head * c.dim + at.part * 8;
-        const void* src = at.value ? v : k;
-        if (BF16) {
-            const uint4 d = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src) + off);
-            const uint32_t u[4] = {d.x, d.y, d.z, d.w};
+    for (int i = 0; i < kTokens; ++i) {
+        raw[i][0] = make_uint4(0, 0, 0, 0);
+        if constexpr (!BF16) raw[i][1] = make_uint4(0, 0, 0, 0);
+        if (in && t0 + i < tokens) {
+            const int64_t off = (t0 + i) * (at.value ? v_stride : k_stride) + at.head * D + at.part * 8;
+            const uint4* src = reinterpret_cast<const uint4*>(
+                static_cast<const char*>(at.value ? v : k) + off * (BF16 ? 2 : 4));
+            raw[i][0] = src[0];
+            if constexpr (!BF16) raw[i][1] = src[1];
+        }
+    }
+    int64_t slot[kTokens];
+    find_slots<kTokens>(c, bt, t0, tokens, slot);
+
+    const float margin = quotient_margin(8.0f);
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        float x[8];
+        const uint32_t u4[4] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w};
+        if constexpr (BF16) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                x[2 * e] = __uint_as_float(u[e] << 16);
-                x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+                x[2 * e] = __uint_as_float(u4[e] << 16);
+                x[2 * e + 1] = __uint_as_float(u4[e] & 0xffff0000u);
             }
         } else {
-            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(src) + off);
-            const float4 a = p[0], b = p[1];
-            x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-            x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-        }
-    }
-    uint32_t amax = 0;
+            const uint32_t w4[4] = {raw[i][1].x, raw[i][1].y, raw[i][1].z, raw[i][1].w};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t a = __float_as_uint(x[e]) & 0x7fffffffu;
-        amax = a > amax ? a : amax;
-    }
-    for (int o = c.group >> 4; o > 0; o >>= 1) {
-        const uint32_t t = (uint32_t)__shfl_xor((int)amax, o, kWave);
-        amax = t > amax ? t : amax;
-    }
-    float s;
-    bool zero = false;
-    if (amax >= 0x7f800000u) {
-        s = __uint_as_float(0x7fc00000u);
-        zero = true;
-    } else {
-        const float a = __uint_as_float(amax);
-        s = (a == 0.0f ? 1.0f : a) / 7.0f;
-        if (a == 0.0f || s == 0.0f) {
-            s = 1.0f / 7.0f;
+            for (int e = 0; e < 4; ++e) {
+                x[e] = __uint_as_float(u4[e]);
+                x[4 + e] = __uint_as_float(w4[e]);
+            }
+        }
+        uint32_t amax = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(x[e]) & 0x7fffffffu);
+        for (int o = c.group >> 4; o > 0; o >>= 1)
+            amax = max(amax, (uint32_t)__shfl_xor((int)amax, o, kWave));
+        float s;
+        bool zero = false;
+        if (amax >= 0x7f800000u) {
+            s = __uint_as_float(0x7fc00000u);
             zero = true;
+        } else {
+            const float a = __uint_as_float(amax);
+            s = (a == 0.0f ? 1.0f : a) / 7.0f;
+            if (a == 0.0f || s == 0.0f) {
+                s = 1.0f / 7.0f;
+                zero = true;
+            }
         }
-    }
-    const float r = 1.0f / s;
-    const float margin = quotient_margin(8.0f);
-    uint32_t word = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float q = fminf(fmaxf(rounded_quotient(x[e], s, r, margin), -8.0f), 7.0f);
-        const uint32_t u = zero ? 8u : (uint32_t)((int32_t)q + 8);
-        nib[threadIdx.x * 8 + e] = (uint8_t)u;
-        word |= u << (4 * e);
-    }
-    __syncthreads();  // a row's threads are inside one wave, but rows share no order otherwise
-    if (!live) return;
-    const int64_t page = slot >> c.page_shift;
-    const int64_t off = slot & ((1LL << c.page_shift) - 1);
-    const int64_t block = page * c.heads + at.head;  // (page, head)
-    const int64_t row = ((block << c.page_shift) + off) * parts;
-    if (!at.value) {
-        // dimensions 8 part .. = 32 i + 8 r: word r (D/32) + i
-        c.k_codes[row + (at.part & 3) * (c.dim >> 5) + (at.part >> 2)] = word;
-    } else {
-        // word w of the row holds codes 8 w .. 8 w + 7; code n is dimension 16 j + c, n = c (D/16) + j
-        const int per = c.dim >> 4;
-        const uint8_t* src = nib + local * c.dim;
-        uint32_t w = 0;
+        const float r = 1.0f / s;
+        uint32_t word = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int n = at.part * 8 + e;
-            w |= (uint32_t)src[16 * (n % per) + n / per] << (4 * e);
+            const float q = fminf(fmaxf(rounded_quotient(x[e], s, r, margin), -8.0f), 7.0f);
+            const uint32_t u = zero ? 8u : (uint32_t)((int32_t)q + 8);
+            word |= u << (4 * e);
         }
-        c.v_codes[row + at.part] = w;
-    }
-    const int gp = c.group >> 3;  // threads of a group
-    if (at.part % gp == 0) {
-        const int groups = c.dim / c.group;
-        float* dst = at.value ? c.v_scales : c.k_scales;
-        dst[((block * groups + at.part / gp) << c.page_shift) + off] = s;
+        // values: dimension 8 part + e is 16 j + c with j = part / 2, c = 8 (part & 1)
+        // + e; a row's words change hands through LDS, those of one half of the
+        // c's next to each other
+        const int row0 = threadIdx.x - at.part;
+        __syncthreads();
+        turn[row0 + (at.part & 1) * kPer + (at.part >> 1)] = word;
+        __syncthreads();
+        if (!in || slot[i] < 0) continue;
+        const int64_t page = slot[i] >> c.page_shift;
+        const int64_t off = slot[i] & ((1LL << c.page_shift) - 1);
+        const int64_t block = page * c.heads + at.head;  // (page, head)
+        const int64_t row = ((block << c.page_shift) + off) * kParts;
+        if (!at.value) {
+            // dimensions 8 part .. = 32 i + 8 r: word r (D/32) + i
+            c.k_codes[row + (at.part & 3) * (D / 32) + (at.part >> 2)] = word;
+        } else {
+            // word w holds the codes 8 w + n: dimension 16 j + c for 8 w + n = c (D/16) + j
+            uint32_t w = 0;
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                const int code = at.part * 8 + n;
+                const int cc = code / kPer, j = code % kPer;
+                w |= ((turn[row0 + (cc >> 3) * kPer + j] >> (4 * (cc & 7))) & 15u) << (4 * n);
+            }
+            c.v_codes[row + at.part] = w;
+        }
+        const int gp = c.group >> 3;  // threads of a group
+        if ((at.part & (gp - 1)) == 0) {
+            float* dst = at.value ? c.v_scales : c.k_scales;
+            dst[((block * (D / c.group) + at.part / gp) << c.page_shift) + off] = s;
+        }
     }
 }
 
-template <bool BF16>
+template <int D, bool BF16, int kTokens>
 __global__ __launch_bounds__(kThreads) void cache4_read_kernel(Cache4 c, Cache4Batch bt,
                                                                void* __restrict__ k,
                                                                void* __restrict__ v, int64_t tokens)
 {
-    const int parts = c.dim >> 3;
-    const int rows_here = kThreads / parts;
-    const RowAt at = row_at(c, (int64_t)blockIdx.x * rows_here + threadIdx.x / parts,
-                            threadIdx.x % parts);
-    int64_t slot = -1;
-    if (at.token >= tokens || !cache4_slot(c, bt, at.token, tokens, &slot)) return;
-    float x[8];
-    if (slot < 0) {
+    constexpr int kParts = D / 8;
+    constexpr int kWords = D / 64 * 4;  // of the 8 c's of a thread's dimensions
+    const int64_t t0 = (int64_t)blockIdx.x * kTokens;
+    Part at;
+    const bool in = part_of<D>(c, &at);
+    int64_t slot[kTokens];
+    find_slots<kTokens>(c, bt, t0, tokens, slot);
+    if (!in) return;
+
+    uint32_t w[kTokens][kWords];
+    float s[kTokens];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(0x7fc00000u);
-    } else {
-        const int64_t page = slot >> c.page_shift;
-        const int64_t off = slot & ((1LL << c.page_shift) - 1);
+    for (int i = 0; i < kTokens; ++i) {
+        if (slot[i] < 0) continue;
+        const int64_t page = slot[i] >> c.page_shift;
+        const int64_t off = slot[i] & ((1LL << c.page_shift) - 1);
         const int64_t block = page * c.heads + at.head;
-        const int64_t row = ((block << c.page_shift) + off) * parts;
-        const int groups = c.dim / c.group;
-        const float* sc = at.value ? c.v_scales : c.k_scales;
-        const float s = sc[((block * groups + at.part * 8 / c.group) << c.page_shift) + off];
+        const int64_t row = ((block << c.page_shift) + off) * kParts;
         if (!at.value) {
-            const uint32_t w = c.k_codes[row + (at.part & 3) * (c.dim >> 5) + (at.part >> 2)];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = (float)((int32_t)((w >> (4 * e)) & 15u) - 8) * s;
+            w[i][0] = c.k_codes[row + (at.part & 3) * (D / 32) + (at.part >> 2)];
         } else {
-            const int per = c.dim >> 4;
+            const uint4* src = reinterpret_cast<const uint4*>(c.v_codes + row + (at.part & 1) * kWords);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int d = at.part * 8 + e;
-                const int n = (d & 15) * per + (d >> 4);
-                x[e] = (float)((int32_t)((c.v_codes[row + (n >> 3)] >> (4 * (n & 7))) & 15u) - 8) * s;
+            for (int e = 0; e < kWords; e += 4) {
+                const uint4 x = src[e / 4];
+                w[i][e] = x.x, w[i][e + 1] = x.y, w[i][e + 2] = x.z, w[i][e + 3] = x.w;
             }
         }
+        const float* sc = at.value ? c.v_scales : c.k_scales;
+        s[i] = sc[((block * (D / c.group) + at.part * 8 / c.group) << c.page_shift) + off];
     }
-    const int64_t o = (at.token * c.heads + at.head) * c.dim + at.part * 8;
-    void* dst = at.value ? v : k;
-    if (BF16) {
-        uint32_t u[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            u[e] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[2 * e]) |
-                   ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[2 * e + 1]) << 16);
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + o) = make_uint4(u[0], u[1], u[2], u[3]);
-    } else {
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(dst) + o);
-        p[0] = make_float4(x[0], x[1], x[2], x[3]);
-        p[1] = make_float4(x[4], x[5], x[6], x[7]);
+    for (int i = 0; i < kTokens; ++i) {
+        if (slot[i] == -2) continue;
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            uint32_t u;
+            if (!at.value) {
+                u = w[i][0] >> (4 * e);
+            } else {
+                // code j = part / 2 of the e-th c
+                const int j = at.part >> 1;
+                if constexpr (D == 64)
+                    u = w[i][e / 2] >> (16 * (e & 1) + 4 * j);
+                else if constexpr (D == 128)
+                    u = w[i][e] >> (4 * j);
+                else
+                    u = (j & 8 ? w[i][2 * e + 1] : w[i][2 * e]) >> (4 * (j & 7));
+            }
+            x[e] = slot[i] < 0 ? __uint_as_float(0x7fc00000u) : (float)((int32_t)(u & 15u) - 8) * s[i];
+        }
+        const int64_t o = ((t0 + i) * c.heads + at.head) * D + at.part * 8;
+        void* dst = at.value ? v : k;
+        if constexpr (BF16) {
+            uint32_t p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                p[e] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[2 * e]) |
+                       ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x[2 * e + 1]) << 16);
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + o) = make_uint4(p[0], p[1], p[2], p[3]);
+        } else {
+            float4* p = reinterpret_cast<float4*>(static_cast<float*>(dst) + o);
+            p[0] = make_float4(x[0], x[1], x[2], x[3]);
+            p[1] = make_float4(x[4], x[5], x[6], x[7]);
+        }
     }
 }
 
-// One workgroup per kThreads / (D/8) rows of (token, head, keys | values).
-bool row_grid(const Cache4& c, int64_t tokens, unsigned* grid)
+// kTokens tokens by all rows of a token; a token each while there are fewer than
+// fill the CUs four deep.
+template <int kTokens>
+bool token_grid(const Cache4& c, int64_t tokens, dim3* grid, unsigned* threads)
 {
-    const int64_t rows = tokens * c.heads * 2;
-    const int64_t blocks = ceil_div(rows, kThreads / (c.dim >> 3));
-    if (blocks > 0x7fffffffLL) return false;
-    *grid = (unsigned)blocks;
-    return true;
+    const int64_t all = (int64_t)c.heads * 2 * (c.dim / 8);
+    *threads = all >= kThreads ? kThreads : (unsigned)ceil_div(all, kWave) * kWave;
+    const int64_t x = ceil_div(tokens, kTokens);
+    *grid = dim3((unsigned)x, (unsigned)ceil_div(all, *threads));
+    return x <= 0x7fffffffLL;
+}
+
+template <int D, bool BF16>
+hipError_t append_d(const Cache4& c, const Cache4Batch& bt, const void* k, const void* v,
+                    int64_t tokens, int64_t k_stride, int64_t v_stride, hipStream_t stream)
+{
+    dim3 grid;
+    unsigned threads;
+    if (tokens >= 4096) {
+        if (!token_grid<4>(c, tokens, &grid, &threads)) return hipErrorInvalidConfiguration;
+        cache4_append_kernel<D, BF16, 4><<<grid, threads, 0, stream>>>(c, bt, k, v, tokens, k_stride, v_stride);
+    } else {
+        if (!token_grid<1>(c, tokens, &grid, &threads)) return hipErrorInvalidConfiguration;
+        cache4_append_kernel<D, BF16, 1><<<grid, threads, 0, stream>>>(c, bt, k, v, tokens, k_stride, v_stride);
+    }
+    return hipGetLastError();
+}
+
+template <int D, bool BF16>
+hipError_t read_d(const Cache4& c, const Cache4Batch& bt, void* k, void* v, int64_t tokens,
+                  hipStream_t stream)
+{
+    dim3 grid;
+    unsigned threads;
+    if (tokens >= 4096) {
+        if (!token_grid<4>(c, tokens, &grid, &threads)) return hipErrorInvalidConfiguration;
+        cache4_read_kernel<D, BF16, 4><<<grid, threads, 0, stream>>>(c, bt, k, v, tokens);
+    } else {
+        if (!token_grid<1>(c, tokens, &grid, &threads)) return hipErrorInvalidConfiguration;
+        cache4_read_kernel<D, BF16, 1><<<grid, threads, 0, stream>>>(c, bt, k, v, tokens);
+    }
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -199,25 +290,20 @@ hipError_t launch_cache4_append(const Cache4& c, const Cache4Batch& bt, const vo
                                 const void* v, bool bf16, int64_t tokens, int64_t k_stride,
                                 int64_t v_stride, hipStream_t stream)
 {
-    unsigned grid;
-    if (!row_grid(c, tokens, &grid)) return hipErrorInvalidConfiguration;
-    if (bf16)
-        cache4_append_kernel<true><<<grid, kThreads, 0, stream>>>(c, bt, k, v, tokens, k_stride, v_stride);
-    else
-        cache4_append_kernel<false><<<grid, kThreads, 0, stream>>>(c, bt, k, v, tokens, k_stride, v_stride);
-    return hipGetLastError();
+#define CALL(D) \
+    (bf16 ? append_d<D, true>(c, bt, k, v, tokens, k_stride, v_stride, stream) \
+          : append_d<D, false>(c, bt, k, v, tokens, k_stride, v_stride, stream))
+    return c.dim == 64 ? CALL(64) : (c.dim == 128 ? CALL(128) : CALL(256));
+#undef CALL
 }
 
 hipError_t launch_cache4_read(const Cache4& c, const Cache4Batch& bt, void* k, void* v, bool bf16,
                               int64_t tokens, hipStream_t stream)
 {
-    unsigned grid;
-    if (!row_grid(c, tokens, &grid)) return hipErrorInvalidConfiguration;
-    if (bf16)
-        cache4_read_kernel<true><<<grid, kThreads, 0, stream>>>(c, bt, k, v, tokens);
-    else
-        cache4_read_kernel<false><<<grid, kThreads, 0, stream>>>(c, bt, k, v, tokens);
-    return hipGetLastError();
+#define CALL(D) \
+    (bf16 ? read_d<D, true>(c, bt, k, v, tokens, stream) : read_d<D, false>(c, bt, k, v, tokens, stream))
+    return c.dim == 64 ? CALL(64) : (c.dim == 128 ? CALL(128) : CALL(256));
+#undef CALL
 }
 
 }  // namespace dq

@@ -50,13 +50,10 @@ __device__ __forceinline__ void cache4_rows(const Cache4Batch& bt, int64_t b, in
     n = e - s;
 }
 
-// Where token row t of the call lives: false if it belongs to no sequence;
-// *slot = page * P + offset, or -1 where the cache does not hold it (a
-// position below 0 or past the table, a page outside the cache).
-__device__ __forceinline__ bool cache4_slot(const Cache4& c, const Cache4Batch& bt, int64_t t,
-                                            int64_t tokens, int64_t* slot)
+// The sequence of token row t of the call: the last one whose first row is at or
+// before t (its rows are [first, first + n); t may lie behind them).
+__device__ __forceinline__ int64_t cache4_sequence(const Cache4Batch& bt, int64_t t)
 {
-    // the last sequence whose first row is at or before t
     int64_t lo = 0, hi = bt.count;
     while (lo + 1 < hi) {
         const int64_t mid = (lo + hi) >> 1;
@@ -65,18 +62,19 @@ __device__ __forceinline__ bool cache4_slot(const Cache4& c, const Cache4Batch& 
         else
             hi = mid;
     }
-    int64_t first, n;
-    cache4_rows(bt, lo, tokens, first, n);
-    if (t < first || t >= first + n) return false;
-    const int64_t pos = (int64_t)bt.lens[lo] - n + (t - first);
-    *slot = -1;
-    if (pos < 0) return true;
+    return lo;
+}
+
+// page * P + offset of position pos of sequence b, or -1 where the cache does not
+// hold it (a position below 0 or past the table, a page outside the cache).
+__device__ __forceinline__ int64_t cache4_slot(const Cache4& c, const Cache4Batch& bt, int64_t b, int64_t pos)
+{
+    if (pos < 0) return -1;
     const int64_t idx = pos >> c.page_shift;
-    if (idx >= bt.width) return true;
-    const int64_t page = bt.table[lo * bt.width + idx];
-    if (page < 0 || page >= c.pages) return true;
-    *slot = (page << c.page_shift) + (pos & ((1LL << c.page_shift) - 1));
-    return true;
+    if (idx >= bt.width) return -1;
+    const int64_t page = bt.table[b * bt.width + idx];
+    if (page < 0 || page >= c.pages) return -1;
+    return (page << c.page_shift) + (pos & ((1LL << c.page_shift) - 1));
 }
 
 }  // namespace dq
