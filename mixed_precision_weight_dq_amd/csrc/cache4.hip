@@ -29,16 +29,18 @@ template <int kTokens>
 __device__ __forceinline__ void find_slots(const Cache4& c, const Cache4Batch& bt, int64_t t0,
                                            int64_t tokens, int64_t (&slot)[kTokens])
 {
-    int64_t b = cache4_sequence(bt, t0);
-    int64_t first, n;
+    // token i of them by the lanes whose number is i modulo kTokens
+    const int64_t t = t0 + (kTokens > 1 ? threadIdx.x % kTokens : 0);
+    const int64_t b = cache4_sequence(bt, t);
+    int64_t first, n, at = -2;
     cache4_rows(bt, b, tokens, first, n);
+    if (t >= first && t < first + n)
+        at = cache4_slot(c, bt, b, (int64_t)bt.lens[b] - n + (t - first));
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
-        const int64_t t = t0 + i;
-        while (t >= first + n && b + 1 < bt.count) cache4_rows(bt, ++b, tokens, first, n);
-        slot[i] = -2;
-        if (t >= first && t < first + n)
-            slot[i] = cache4_slot(c, bt, b, (int64_t)bt.lens[b] - n + (t - first));
+        const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)at, i);
+        const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(at >> 32), i);
+        slot[i] = (int64_t)((uint64_t)hi << 32 | lo);
     }
 }
 
@@ -124,21 +126,27 @@ __global__ __launch_bounds__(kThreads) void cache4_append_kernel(
                 zero = true;
             }
         }
-        const float r = 1.0f / s;
-        uint32_t word = 0;
+        float q[8];
+        clipped_quotients(x, s, 1.0f / s, margin, 7.0f, q);
+        // four codes at a time as the exact fp32 sum of 16^e (q + 8)
+        float lo = 34952.0f, hi = 34952.0f;  // 0x8888
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float q = fminf(fmaxf(rounded_quotient(x[e], s, r, margin), -8.0f), 7.0f);
-            const uint32_t u = zero ? 8u : (uint32_t)((int32_t)q + 8);
-            word |= u << (4 * e);
+        for (int e = 0; e < 4; ++e) {
+            lo = fmaf(q[e], (float)(1 << (4 * e)), lo);
+            hi = fmaf(q[4 + e], (float)(1 << (4 * e)), hi);
         }
+        uint32_t word = (uint32_t)hi << 16 | (uint32_t)lo;
+        if (zero) word = 0x88888888u;
         // values: dimension 8 part + e is 16 j + c with j = part / 2, c = 8 (part & 1)
         // + e; a row's words change hands through LDS, those of one half of the
         // c's next to each other
+        // (a row is within a wave, whose LDS accesses are in order)
         const int row0 = threadIdx.x - at.part;
-        __syncthreads();
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
         turn[row0 + (at.part & 1) * kPer + (at.part >> 1)] = word;
-        __syncthreads();
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
         if (!in || slot[i] < 0) continue;
         const int64_t page = slot[i] >> c.page_shift;
         const int64_t off = slot[i] & ((1LL << c.page_shift) - 1);
@@ -149,13 +157,20 @@ __global__ __launch_bounds__(kThreads) void cache4_append_kernel(
             c.k_codes[row + (at.part & 3) * (D / 32) + (at.part >> 2)] = word;
         } else {
             // word w holds the codes 8 w + n: dimension 16 j + c for 8 w + n = c (D/16) + j
+            constexpr int kRun = kPer < 8 ? kPer : 8;  // codes of one c in the word
+            const int c0 = at.part * 8 / kPer;
+            const uint4* from = reinterpret_cast<const uint4*>(
+                &turn[row0 + (c0 >> 3) * kPer + at.part * 8 % kPer]);
+            uint32_t x8[kRun];
+#pragma unroll
+            for (int e = 0; e < kRun; e += 4) {
+                const uint4 d = from[e / 4];
+                x8[e] = d.x, x8[e + 1] = d.y, x8[e + 2] = d.z, x8[e + 3] = d.w;
+            }
             uint32_t w = 0;
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
-                const int code = at.part * 8 + n;
-                const int cc = code / kPer, j = code % kPer;
-                w |= ((turn[row0 + (cc >> 3) * kPer + j] >> (4 * (cc & 7))) & 15u) << (4 * n);
-            }
+            for (int n = 0; n < 8; ++n)
+                w |= ((x8[n % kRun] >> (4 * ((c0 + n / kRun) & 7))) & 15u) << (4 * n);
             c.v_codes[row + at.part] = w;
         }
         const int gp = c.group >> 3;  // threads of a group

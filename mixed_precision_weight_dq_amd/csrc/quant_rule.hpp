@@ -39,4 +39,25 @@ __host__ __device__ __forceinline__ float rounded_quotient(float w, float s, flo
     return q;
 }
 
+// The clipped codes clip(rint(fl32(w / s)), -qmax - 1, qmax) of 8 elements of a
+// row or group whose |w| is at most fl32(s qmax)'s dividend, given r =
+// fl32(1 / s) and margin = quotient_margin(qmax + 1): one test for all of them.
+// For a normal s (r < 2^125) |w / s| <= qmax (1 + 2^-23), so rint needs no clip.
+__host__ __device__ __forceinline__ void clipped_quotients(const float (&w)[8], float s, float r,
+                                                           float margin, float qmax, float (&q)[8])
+{
+    float far = r < 0x1p125f ? 0.0f : 1.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float t = w[e] * r;
+        q[e] = rintf(t);
+        far = fmaxf(far, fabsf(t - q[e]));
+    }
+    if (!(far < margin)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            q[e] = fminf(fmaxf(rounded_quotient(w[e], s, r, margin), -qmax - 1.0f), qmax);
+    }
+}
+
 }  // namespace dq

@@ -8,7 +8,9 @@
 // codes' offset or zero point off an integer product exactly.
 //
 // One workgroup per token.  A piece is 8 elements: one 16-byte load of bf16
-// (two of fp32) and one 8-byte store of codes.
+// (two of fp32) and one 8-byte store of codes.  A thread keeps its first kHeld
+// pieces (rows of up to 8192 elements whole) in registers between the maximum and
+// the codes; of longer rows the rest is read again, from the caches by then.
 #include "common.hpp"
 #include "launch_serving.hpp"
 #include "quant_rule.hpp"
@@ -19,39 +21,77 @@ namespace {
 
 constexpr int kPiece = 8;
 constexpr int kTokenThreads = 256;
+constexpr int kHeld = 4;  // pieces per thread
 
-// The 8 elements of piece p of a row, 0 past its end.
+// The 8 elements of a piece as they lie in memory.
 template <bool BF16>
-__device__ __forceinline__ void load_piece(const void* __restrict__ x, int64_t row_off, int64_t K,
-                                           int64_t p, bool vec, float (&v)[kPiece])
+struct Piece {
+    uint32_t w[BF16 ? 4 : 8];
+    __device__ __forceinline__ void floats(float (&v)[kPiece]) const
+    {
+#pragma unroll
+        for (int e = 0; e < kPiece; ++e)
+            v[e] = __uint_as_float(!BF16 ? w[BF16 ? 0 : e] : (e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16));
+    }
+};
+
+// Piece p of a row, 0 past its end.
+template <bool BF16>
+__device__ __forceinline__ Piece<BF16> load_piece(const void* __restrict__ x, int64_t row_off,
+                                                  int64_t K, int64_t p, bool vec)
 {
+    Piece<BF16> d;
     const int64_t k0 = p * kPiece;
     if (vec && k0 + kPiece <= K) {
-        if (BF16) {
-            const uint4 d = *reinterpret_cast<const uint4*>(
-                static_cast<const uint16_t*>(x) + row_off + k0);
-            const uint32_t u[4] = {d.x, d.y, d.z, d.w};
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const char*>(x) +
+                                                          (row_off + k0) * (BF16 ? 2 : 4));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[2 * e] = __uint_as_float(u[e] << 16);
-                v[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-            }
-        } else {
-            const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(x) + row_off + k0);
-            const float4 a = q[0], b = q[1];
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        for (int h = 0; h < (BF16 ? 1 : 2); ++h) {
+            const uint4 a = src[h];
+            d.w[4 * h] = a.x, d.w[4 * h + 1] = a.y, d.w[4 * h + 2] = a.z, d.w[4 * h + 3] = a.w;
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < kPiece; ++e) {
-            if (k0 + e >= K)
-                v[e] = 0.0f;
-            else
-                v[e] = BF16 ? bf16_bits_to_float(static_cast<const uint16_t*>(x)[row_off + k0 + e])
-                            : static_cast<const float*>(x)[row_off + k0 + e];
+        for (int i = 0; i < (BF16 ? 4 : 8); ++i) {
+            if (BF16) {
+                const uint16_t* src = static_cast<const uint16_t*>(x) + row_off + k0 + 2 * i;
+                d.w[i] = (k0 + 2 * i < K ? (uint32_t)src[0] : 0u) |
+                         (k0 + 2 * i + 1 < K ? (uint32_t)src[1] << 16 : 0u);
+            } else {
+                d.w[i] = k0 + i < K ? static_cast<const uint32_t*>(x)[row_off + k0 + i] : 0u;
+            }
         }
     }
+    return d;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t piece_max(const Piece<BF16>& d, uint32_t amax)
+{
+    float v[kPiece];
+    d.floats(v);
+#pragma unroll
+    for (int e = 0; e < kPiece; ++e) amax = max(amax, __float_as_uint(v[e]) & 0x7fffffffu);
+    return amax;
+}
+
+// A piece's codes and their sum.
+template <bool BF16>
+__device__ __forceinline__ uint2 piece_codes(const Piece<BF16>& d, float s, float r, bool zero, int& sum)
+{
+    float v[kPiece], q[kPiece];
+    d.floats(v);
+    clipped_quotients(v, s, r, quotient_margin(128.0f), 127.0f, q);
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        // two codes at a time as the exact fp32 value (q0 + 128) + 256 (q1 + 128)
+        const float lo = fmaf(q[4 * h + 1], 256.0f, q[4 * h] + 32896.0f);
+        const float hi = fmaf(q[4 * h + 3], 256.0f, q[4 * h + 2] + 32896.0f);
+        w[h] = zero ? 0u : ((uint32_t)hi << 16 | (uint32_t)lo) ^ 0x80808080u;
+        sum = __builtin_amdgcn_sdot4((int)w[h], 0x01010101, sum, false);
+    }
+    return make_uint2(w[0], w[1]);
 }
 
 template <bool BF16>
@@ -68,17 +108,18 @@ __global__ __launch_bounds__(kTokenThreads) void quantize_tokens_kernel(
     const int64_t pieces = pitch / kPiece;
     const bool vec = (K * (BF16 ? 2 : 4)) % 16 == 0;
 
-    // pass 1: max |x| as an integer max over sign-cleared bit patterns
-    uint32_t amax = 0;
-    for (int64_t p = tid; p < pieces; p += kTokenThreads) {
-        float v[kPiece];
-        load_piece<BF16>(x, row_off, K, p, vec, v);
+    // max |x| as an integer max over sign-cleared bit patterns
+    Piece<BF16> held[kHeld];
 #pragma unroll
-        for (int e = 0; e < kPiece; ++e) {
-            const uint32_t a = __float_as_uint(v[e]) & 0x7fffffffu;
-            amax = a > amax ? a : amax;
-        }
-    }
+    for (int i = 0; i < kHeld; ++i)
+        if (tid + i * kTokenThreads < pieces)
+            held[i] = load_piece<BF16>(x, row_off, K, tid + i * kTokenThreads, vec);
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+        if (tid + i * kTokenThreads < pieces) amax = piece_max<BF16>(held[i], amax);
+    for (int64_t p = tid + kHeld * kTokenThreads; p < pieces; p += kTokenThreads)
+        amax = piece_max<BF16>(load_piece<BF16>(x, row_off, K, p, vec), amax);
     amax = wave_max_u32(amax);
     if ((tid & (kWave - 1)) == 0) red_max[tid / kWave] = amax;
     __syncthreads();
@@ -99,23 +140,16 @@ __global__ __launch_bounds__(kTokenThreads) void quantize_tokens_kernel(
         }
     }
     const float r = 1.0f / s;
-    const float margin = quotient_margin(128.0f);
 
-    // pass 2: codes and their sum (elements past K are 0, so is their code)
+    // codes and their sum (elements past K are 0, so is their code)
     int32_t sum = 0;
-    for (int64_t p = tid; p < pieces; p += kTokenThreads) {
-        float v[kPiece];
-        load_piece<BF16>(x, row_off, K, p, vec, v);
-        uint32_t w[2] = {0u, 0u};
+    uint2* out = reinterpret_cast<uint2*>(codes + m * pitch);
 #pragma unroll
-        for (int e = 0; e < kPiece; ++e) {
-            const float q = fminf(fmaxf(rounded_quotient(v[e], s, r, margin), -128.0f), 127.0f);
-            const int32_t c = zero_codes ? 0 : (int32_t)q;
-            sum += c;
-            w[e >> 2] |= (uint32_t)(c & 0xff) << (8 * (e & 3));
-        }
-        *reinterpret_cast<uint2*>(codes + m * pitch + p * kPiece) = make_uint2(w[0], w[1]);
-    }
+    for (int i = 0; i < kHeld; ++i)
+        if (tid + i * kTokenThreads < pieces)
+            out[tid + i * kTokenThreads] = piece_codes<BF16>(held[i], s, r, zero_codes, sum);
+    for (int64_t p = tid + kHeld * kTokenThreads; p < pieces; p += kTokenThreads)
+        out[p] = piece_codes<BF16>(load_piece<BF16>(x, row_off, K, p, vec), s, r, zero_codes, sum);
 #pragma unroll
     for (int o = kWave / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
     if ((tid & (kWave - 1)) == 0) red_sum[tid / kWave] = sum;
