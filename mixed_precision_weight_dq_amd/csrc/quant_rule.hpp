@@ -40,20 +40,23 @@ __host__ __device__ __forceinline__ float rounded_quotient(float w, float s, flo
 }
 
 // The clipped codes clip(rint(fl32(w / s)), -qmax - 1, qmax) of 8 elements of a
-// row or group whose |w| is at most fl32(s qmax)'s dividend, given r =
-// fl32(1 / s) and margin = quotient_margin(qmax + 1): one test for all of them.
-// For a normal s (r < 2^125) |w / s| <= qmax (1 + 2^-23), so rint needs no clip.
+// row or group whose largest |w| is a, s = fl32(a / qmax), given r = 1 / s within
+// a relative 2^-22 wherever it is in (2^-125, 2^125) and margin =
+// quotient_margin(qmax + 1): one test for all of them.  With such an r, s is
+// normal and |w / s| <= qmax (1 + 2^-23), so rint needs no clip.
 __host__ __device__ __forceinline__ void clipped_quotients(const float (&w)[8], float s, float r,
                                                            float margin, float qmax, float (&q)[8])
 {
-    float far = r < 0x1p125f ? 0.0f : 1.0f;
+    float far = r > 0x1p-125f && r < 0x1p125f ? 0.0f : 1.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const float t = w[e] * r;
         q[e] = rintf(t);
         far = fmaxf(far, fabsf(t - q[e]));
     }
+    // bf16 has many exact ties (w = a / 2 is one at qmax = 7): test each element again
     if (!(far < margin)) {
+        r = 1.0f / s;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             q[e] = fminf(fmaxf(rounded_quotient(w[e], s, r, margin), -qmax - 1.0f), qmax);
