@@ -195,10 +195,16 @@ __device__ __forceinline__ Rows rows_of(const AttnArgs& a, int64_t b)
 }
 
 // The work of a call as one line of steps: sequence by sequence, in it unit by
-// unit (a kv head's 16-row tile, tiles of a head next to each other), in that
-// the sequence's steps of kStride positions (at least one, which writes rows that
-// see nothing).  Workgroup w takes an equal stretch of the line, so lengths do
-// not have to be equal, nor known to the host, for the CUs to be.
+// unit (a kv head's tile of rows, tiles of a head next to each other), in that
+// the sequence's steps of positions (at least one, which writes rows that see
+// nothing).  Workgroup w takes an equal stretch of the line, so lengths do not
+// have to be equal, nor known to the host, for the CUs to be.  Cut: rows of a
+// tile, positions of a step, threads of the workgroup that lays the line out.
+template <int kTileRows, int kStepPos, int kGroupThreads>
+struct Cut {
+    static constexpr int kRows = kTileRows, kPos = kStepPos, kThreads = kGroupThreads;
+};
+using SmallCut = Cut<16, kStride, kThreads>;
 struct Line {
     int64_t total;   // steps of the call
     int64_t q, r;    // a workgroup's steps: q + 1 for the first r, else q
@@ -214,11 +220,20 @@ struct Line {
     }
 };
 
-__device__ __forceinline__ int steps_of(const Rows& rw) { return rw.len > 0 ? (rw.len - 1) / kStride + 1 : 1; }
-__device__ __forceinline__ int64_t tiles_of(const Rows& rw) { return (rw.rows() + 15) >> 4; }
+template <class C>
+__device__ __forceinline__ int steps_of(const Rows& rw)
+{
+    return rw.len > 0 ? (rw.len - 1) / C::kPos + 1 : 1;
+}
+template <class C>
+__device__ __forceinline__ int64_t tiles_of(const Rows& rw)
+{
+    return (rw.rows() + C::kRows - 1) / C::kRows;
+}
+template <class C>
 __device__ __forceinline__ int64_t line_steps(const AttnArgs& a, const Rows& rw)
 {
-    return tiles_of(rw) * a.c.heads * steps_of(rw);
+    return tiles_of<C>(rw) * a.c.heads * steps_of<C>(rw);
 }
 
 __device__ __forceinline__ int64_t lane64(int64_t v, int lane)
@@ -234,14 +249,14 @@ __device__ __forceinline__ int64_t lane64(int64_t v, int lane)
 // itself, one round of loads and no barrier (a launch's workgroups all start
 // here, so nothing else hides it).  More: each thread adds up a run of
 // sequences, and a scan over the workgroup joins the runs.
-template <bool kFind>
+template <class C, bool kFind>
 __device__ __forceinline__ Line lay_line_short(const AttnArgs& a, int64_t w, int b)
 {
     Line ln;
     const int lane = threadIdx.x & (kWave - 1);
     const bool in = lane < a.bt.count;
     const Rows mine = rows_of(a, in ? lane : 0);
-    const int64_t n = in ? line_steps(a, mine) : 0;
+    const int64_t n = in ? line_steps<C>(a, mine) : 0;
     int64_t upto = n;
     for (int o = 1; o < a.bt.count; o <<= 1) {
         const int64_t t = __shfl_up(upto, o, kWave);
@@ -267,21 +282,22 @@ __device__ __forceinline__ Line lay_line_short(const AttnArgs& a, int64_t w, int
     return ln;
 }
 
-template <bool kFind>
+template <class C, bool kFind>
 __device__ __forceinline__ Line lay_line_long(const AttnArgs& a, int64_t w, int b)
 {
-    __shared__ int64_t wave_sum[kWaves];
+    constexpr int kGroupWaves = C::kThreads / kWave;
+    __shared__ int64_t wave_sum[kGroupWaves];
     __shared__ int64_t found[2];
     Line ln;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
     const int64_t count = a.bt.count;
-    const int64_t run = (count + kThreads - 1) / kThreads;
+    const int64_t run = (count + C::kThreads - 1) / C::kThreads;
     const int64_t lo = run * tid < count ? run * tid : count;
     const int64_t hi = lo + run < count ? lo + run : count;
     int64_t mine = 0, to_b = 0;
     for (int64_t i = lo; i < hi; ++i) {
         if (!kFind && i == b) to_b = mine;
-        mine += line_steps(a, rows_of(a, i));
+        mine += line_steps<C>(a, rows_of(a, i));
     }
     int64_t upto = mine;  // inclusive scan over the wave
 #pragma unroll
@@ -295,7 +311,7 @@ __device__ __forceinline__ Line lay_line_long(const AttnArgs& a, int64_t w, int 
     int64_t base = 0;
     ln.total = 0;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
+    for (int i = 0; i < kGroupWaves; ++i) {
         if (i < wave) base += wave_sum[i];
         ln.total += wave_sum[i];
     }
@@ -306,7 +322,7 @@ __device__ __forceinline__ Line lay_line_long(const AttnArgs& a, int64_t w, int 
         const int64_t x = ln.first(w);
         if (x >= before && x < before + mine) {
             for (int64_t i = lo; i < hi; ++i) {
-                const int64_t n = line_steps(a, rows_of(a, i));
+                const int64_t n = line_steps<C>(a, rows_of(a, i));
                 if (x < before + n) {
                     found[0] = i;
                     found[1] = before;
@@ -326,10 +342,10 @@ __device__ __forceinline__ Line lay_line_long(const AttnArgs& a, int64_t w, int 
     return ln;
 }
 
-template <bool kFind>
+template <class C, bool kFind>
 __device__ __forceinline__ Line lay_line(const AttnArgs& a, int64_t w, int b)
 {
-    return a.bt.count <= kWave ? lay_line_short<kFind>(a, w, b) : lay_line_long<kFind>(a, w, b);
+    return a.bt.count <= kWave ? lay_line_short<C, kFind>(a, w, b) : lay_line_long<C, kFind>(a, w, b);
 }
 
 __device__ __forceinline__ int64_t uniform64(int64_t v)
@@ -410,7 +426,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 3 : 2)) void ca
     // consecutive stretches (which may read the same keys) on one XCD
     const int group = (a.groups & 7) == 0 ? (int)(blockIdx.x & 7) * (a.groups >> 3) + (int)(blockIdx.x >> 3)
                                           : (int)blockIdx.x;
-    const Line ln = lay_line<true>(a, group, 0);
+    const Line ln = lay_line<SmallCut, true>(a, group, 0);
     const int64_t x0 = uniform64(ln.first(group)), x1 = uniform64(ln.first(group + 1));
     int b = ln.b;
     int64_t before = uniform64(ln.before);
@@ -418,8 +434,8 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 3 : 2)) void ca
 
     Rows rw = ln.rw;
     for (int64_t x = x0; x < x1;) {
-        const int steps = steps_of(rw);
-        const int64_t tiles = tiles_of(rw);
+        const int steps = steps_of<SmallCut>(rw);
+        const int64_t tiles = tiles_of<SmallCut>(rw);
         if (x >= before + tiles * a.c.heads * steps) {
             before += tiles * a.c.heads * steps;
             ++b;
@@ -759,11 +775,11 @@ __global__ __launch_bounds__(kThreads) void cache4_join_kernel(AttnArgs a)
     const int tid = threadIdx.x;
     const int b = blockIdx.z;
     const int kvh = blockIdx.y;
-    const Line ln = lay_line<false>(a, 0, b);
+    const Line ln = lay_line<SmallCut, false>(a, 0, b);
     const Rows rw = ln.rw;
     if ((int64_t)blockIdx.x >= rw.rows()) return;
-    const int steps = steps_of(rw);
-    const int64_t tiles = tiles_of(rw);
+    const int steps = steps_of<SmallCut>(rw);
+    const int64_t tiles = tiles_of<SmallCut>(rw);
     const int d4 = tid % kPer;
 
     for (int64_t row = blockIdx.x; row < rw.rows(); row += gridDim.x) {
@@ -833,29 +849,29 @@ __global__ __launch_bounds__(kThreads) void cache4_join_kernel(AttnArgs a)
     }
 }
 
-template <int D>
+template <int D, class C>
 __global__ __launch_bounds__(kThreads) void cache4_join_edges_kernel(AttnArgs a)
 {
     constexpr int N = D / 16;  // dimensions of a thread
     const int64_t w = (int64_t)blockIdx.x + 1;
-    const Line ln = lay_line<true>(a, w, 0);
+    const Line ln = lay_line<Cut<C::kRows, C::kPos, kThreads>, true>(a, w, 0);
     if (ln.b < 0) return;
     const int64_t x = ln.first(w);
     const Rows rw = ln.rw;
-    const int steps = steps_of(rw);
+    const int steps = steps_of<C>(rw);
     const int64_t unit = udiv(x - ln.before, steps);
     const int64_t start = ln.before + unit * steps;
     // the unit's second stretch joins it
     if (x == start || x >= ln.total || ln.group_of(start) != w - 1) return;
     const int64_t n = ln.group_of(start + steps - 1) - w + 2;
-    const int64_t tiles = tiles_of(rw);
+    const int64_t tiles = tiles_of<C>(rw);
     const int kvh = (int)udiv(unit, tiles);
-    const int r16 = threadIdx.x >> 4;
-    const int64_t row = (unit - kvh * tiles) * 16 + r16;
+    const int r = (int)blockIdx.y * 16 + (threadIdx.x >> 4);  // of the tile
+    const int64_t row = (unit - kvh * tiles) * C::kRows + r;
     if (row >= rw.rows()) return;
     const int d = (threadIdx.x & 15) * N;
     const auto slot_of = [&](int64_t s) {
-        return ((w - 1 + s) * 2 + (s == 0 && ln.first(w - 1) != start)) * 16 + r16;
+        return ((w - 1 + s) * 2 + (s == 0 && ln.first(w - 1) != start)) * C::kRows + r;
     };
     float mx = -INFINITY;
     for (int64_t s = 0; s < n; ++s) mx = fmaxf(mx, a.part_ml[slot_of(s)].x);
@@ -920,11 +936,23 @@ __device__ __forceinline__ void lds_barrier()
     asm volatile("" ::: "memory");
 }
 
+// A piece by its LDS address.
+typedef __attribute__((address_space(3))) const void lds_void;
+__device__ __forceinline__ uint32_t lds_address(const uint4* p)
+{
+    return (uint32_t)(uintptr_t)(lds_void*)p;
+}
+__device__ __forceinline__ f16x8_t lds_piece(uint32_t address)
+{
+    return *(__attribute__((address_space(3))) const f16x8_t*)(uintptr_t)address;
+}
+
 template <int D, int G, int NW>
 struct PromptTile {
     static constexpr int kRows = 32 * NW;
     static constexpr int kTiles = NW / 2;      // of 32 positions per step
     static constexpr int kPos = 32 * kTiles;
+    static constexpr int kThreads = 64 * NW;
     static constexpr int kOcc = D == 256 ? 1 : 2;  // waves per SIMD
 };
 
@@ -951,19 +979,59 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
 
     // units (sequence, kv head, tile), a contiguous range of them per XCD, so that
     // the tiles of a kv head share an L2; a head's last tiles, the longest, first
-    const int64_t units = (int64_t)a.bt.count * a.c.heads * grid_tiles;
-    const int64_t u = (int64_t)(blockIdx.x & 7) * ((units + 7) >> 3) + (blockIdx.x >> 3);
-    if (u >= units) return;
-    const int64_t head_unit = udiv(u, grid_tiles);
-    const int tile_at = grid_tiles - 1 - (int)(u - head_unit * grid_tiles);
-    const int b = (int)udiv(head_unit, a.c.heads);
-    const int kvh = (int)(head_unit - (int64_t)b * a.c.heads);
-    const Rows rw = rows_of(a, b);
-    const int64_t rows = rw.rows();
-    const __attribute__((address_space(4))) int32_t* table =
-        (const __attribute__((address_space(4))) int32_t*)(a.bt.table + b * a.bt.width);
+    // Or, with grid_tiles = 0, an equal stretch of the line of steps, and the parts
+    // of a unit are joined by cache4_join_edges_kernel.
+    const bool split = grid_tiles == 0;
+    int b, kvh = 0, group = 0;
+    int64_t tile = 0, x = 0, x1 = 0, before = 0;
+    Rows rw;
+    if (split) {
+        group = (a.groups & 7) == 0 ? (int)(blockIdx.x & 7) * (a.groups >> 3) + (int)(blockIdx.x >> 3)
+                                    : (int)blockIdx.x;
+        const Line ln = lay_line<Tl, true>(a, group, 0);
+        if (ln.b < 0) return;
+        b = ln.b;
+        x = uniform64(ln.first(group));
+        x1 = uniform64(ln.first(group + 1));
+        before = uniform64(ln.before);
+        rw = ln.rw;
+    } else {
+        const int64_t units = (int64_t)a.bt.count * a.c.heads * grid_tiles;
+        const int64_t u = (int64_t)(blockIdx.x & 7) * ((units + 7) >> 3) + (blockIdx.x >> 3);
+        if (u >= units) return;
+        const int64_t head_unit = uniform64(udiv(u, grid_tiles));
+        tile = grid_tiles - 1 - (int)(u - head_unit * grid_tiles);
+        b = __builtin_amdgcn_readfirstlane((int)udiv(head_unit, a.c.heads));
+        kvh = (int)(head_unit - (int64_t)b * a.c.heads);
+        rw = rows_of(a, b);
+    }
+    const int64_t x0 = x;
 
-    for (int64_t tile = tile_at; tile * Tl::kRows < rows; tile += grid_tiles) {
+    for (;; tile += grid_tiles) {
+        const int64_t rows = rw.rows();
+        const int steps = steps_of<Tl>(rw);
+        int step0 = 0, take = steps, slot = 0;
+        if (split) {
+            if (x >= x1) break;
+            const int64_t tiles = tiles_of<Tl>(rw);
+            if (x >= before + tiles * a.c.heads * steps) {
+                before += tiles * a.c.heads * steps;
+                ++b;
+                rw = rows_of(a, b);
+                continue;
+            }
+            const int64_t unit = uniform64(udiv(x - before, steps));
+            step0 = (int)(x - before - unit * steps);
+            take = (int)(x1 - x < steps - step0 ? x1 - x : steps - step0);
+            slot = x == x0 ? 0 : 1;
+            kvh = __builtin_amdgcn_readfirstlane((int)udiv(unit, tiles));
+            tile = unit - kvh * tiles;
+            x += take;
+        } else if (tile * Tl::kRows >= rows) {
+            break;
+        }
+        const __attribute__((address_space(4))) int32_t* table =
+            (const __attribute__((address_space(4))) int32_t*)(a.bt.table + b * a.bt.width);
         const int64_t r0 = tile * Tl::kRows;
         const int64_t w0 = r0 + wave * 32;  // the wave's first row
         const bool live = w0 + r32 < rows;
@@ -971,10 +1039,12 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
         const int qi = (int)udiv(row, rw.per);
         const int head = kvh * rw.per + (int)(row - (int64_t)qi * rw.per);
         const int seen = live ? rw.seen(row) : 0;
-        const auto seen_at = [&](int64_t r) { return rw.seen(r < rows ? r : rows - 1); };
+        const auto seen_at = [&](int64_t r) { return __builtin_amdgcn_readfirstlane(rw.seen(r < rows ? r : rows - 1)); };
         const int end = seen_at(r0 + Tl::kRows - 1);                 // of the workgroup's rows
         const int wave_end = w0 < rows ? seen_at(w0 + 31) : 0;       // of the wave's
-        const int all_see = w0 < rows ? rw.seen(w0) : 0;             // by every live row of it
+        const int begin = step0 * kPos;
+        const int stop = end < begin + take * kPos ? end : begin + take * kPos;
+        const int all_see = w0 < rows ? seen_at(w0) : 0;             // by every live row of it
 
         // q rows: operand kk = 2 i + p holds dimensions 32 i + 8 (2 p + h) + (0 4 1 5 2 6 3 7)
         f16x8_t qf[2 * NC];
@@ -1069,6 +1139,9 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
         };
         // the loaded words -> fp16 pieces of buffer nb
         auto expand = [&](int pos0, int nb) __attribute__((always_inline)) {
+            int lane = (int)threadIdx.x & (kWave - 1);
+            pin(lane);  // what follows from it is worked out here, not kept
+            const int h = lane >> 5;
             const bool past = pos0 + 32 * part + 16 * h + (lane & 15) >= end;
             const int gpar = (lane >> 4) & 1;
             float top = 0.0f;
@@ -1173,6 +1246,18 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[j][e] = 0.0f;
 
+        // LDS addresses of this lane's operand pieces in the buffer to multiply next.
+        // Held as they are (pin): left to itself the compiler keeps far more derived
+        // ones over the loop than there are registers, and spills them.
+        uint32_t ka[2 * NC], va[2 * TT];
+#pragma unroll
+        for (int k = 0; k < 2 * NC; ++k)
+            ka[k] = lds_address(&Kt[0][r32 * (D / 8) + (((2 * (k & 1) + h) * NC + (k >> 1)) ^ swizzle<D / 8>(r32))]);
+#pragma unroll
+        for (int k = 0; k < 2 * TT; ++k)
+            va[k] = lds_address(&Vt[0][r32 * (kPos / 8) + ((2 * k + h) ^ swizzle<kPos / 8>(r32))]);
+        constexpr int kHop = sizeof(Kt[0]), vHop = sizeof(Vt[0]);  // to the other buffer
+
         // 64 positions of buffer cb, the tiles 2 hp and 2 hp + 1
         auto compute = [&](int pos, int cb, int hp) __attribute__((always_inline)) {
             f32x16_t s[2];
@@ -1181,13 +1266,10 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
             for (int t = 0; t < 2; ++t) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) s[t][e] = 0.0f;
-                const int at = 32 * (2 * hp + t) + r32;
 #pragma unroll
-                for (int k = 0; k < 2 * NC; ++k) {
-                    const int w = (2 * (k & 1) + h) * NC + (k >> 1);
+                for (int k = 0; k < 2 * NC; ++k)
                     s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                        __builtin_bit_cast(f16x8_t, Kt[cb][at * (D / 8) + (w ^ swizzle<D / 8>(r32))]), qf[k], s[t], 0, 0, 0);
-                }
+                        lds_piece(ka[k] + 32 * (2 * hp + t) * (2 * D)), qf[k], s[t], 0, 0, 0);
                 // (not 0, which a hidden position's -inf would make NaN)
                 f[t] = fmaxf(logit * pow2(kexp[cb][2 * hp + t] - 10), 0x1p-126f);
             }
@@ -1248,15 +1330,12 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
             }
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                const int d = 32 * j + r32;
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int q = (4 * (2 * hp + t) + 2 * k + h) ^ swizzle<kPos / 8>(r32);
+                    for (int k = 0; k < 2; ++k)
                         o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                            __builtin_bit_cast(f16x8_t, Vt[cb][d * (kPos / 8) + q]), p[t][k], o[j], 0, 0, 0);
-                    }
+                            lds_piece(va[2 * (2 * hp + t) + k] + 32 * j * (2 * kPos)), p[t][k], o[j], 0, 0, 0);
             }
             // a NaN value scale: NaN in its dimensions, in the rows that see it
 #pragma unroll
@@ -1274,18 +1353,18 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
             }
         };
 
-        if (end > 0) {
-            load(0);
-            expand(0, 0);
-            if (kPos < end) load(kPos);
-            for (int pos = 0, cb = 0; pos < end; pos += kPos, cb ^= 1) {
+        if (begin < stop) {
+            load(begin);
+            expand(begin, 0);
+            if (begin + kPos < stop) load(begin + kPos);
+            for (int pos = begin, cb = 0; pos < stop; pos += kPos, cb ^= 1) {
                 lds_barrier();  // buffer cb is whole, the other is read by no wave any more
                 // the waves of the keys expand before they multiply, those of the
                 // values after: a SIMD has one of each, and so both kinds of work
                 auto refill = [&]() __attribute__((always_inline)) {
-                    if (pos + kPos < end) {
+                    if (pos + kPos < stop) {
                         expand(pos + kPos, cb ^ 1);
-                        if (pos + 2 * kPos < end) load(pos + 2 * kPos);
+                        if (pos + 2 * kPos < stop) load(pos + 2 * kPos);
                     }
                 };
                 if (keys) refill();
@@ -1293,6 +1372,16 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
                 for (int hp = 0; hp < TT / 2; ++hp)
                     if (pos + 64 * hp < wave_end) compute(pos + 64 * hp, cb, hp);
                 if (!keys) refill();
+#pragma unroll
+                for (int k = 0; k < 2 * NC; ++k) {
+                    ka[k] += cb ? -kHop : kHop;
+                    pin(ka[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < 2 * TT; ++k) {
+                    va[k] += cb ? -vHop : vHop;
+                    pin(va[k]);
+                }
             }
         }
 
@@ -1301,7 +1390,17 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
         l = l0 + l1;
         float inv = l > 0.0f ? pow2(ve - 10) / l : (l == 0.0f ? 0.0f : l);  // NaN stays
         if (rw.bad) inv = __uint_as_float(0x7fc00000u);
-        if (live) {
+        if (live && take < steps) {
+            const int64_t at = ((int64_t)group * 2 + slot) * Tl::kRows + wave * 32 + r32;
+            float* pp = a.part + at * D + 4 * h;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    *reinterpret_cast<f32x4_t*>(pp + 32 * j + 8 * e) =
+                        (f32x4_t){o[j][4 * e], o[j][4 * e + 1], o[j][4 * e + 2], o[j][4 * e + 3]} * inv;
+            if (h == 0) a.part_ml[at] = make_float2(m, l);
+        } else if (live) {
             uint16_t* op = a.out + ((int64_t)(rw.first + qi) * a.q_heads + head) * D + 4 * h;
 #pragma unroll
             for (int j = 0; j < NT; ++j)
@@ -1320,6 +1419,13 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
 // are not that many steps.
 constexpr int64_t kFill = 512;
 constexpr int64_t kPromptUnits = 96;  // (sequence, kv head, row tile)s for the prompt kernel
+
+#ifndef SU
+#define SU 4
+#define SL 2
+#endif
+constexpr int64_t kSplitUnits = SU;
+constexpr int64_t kSplitLen = SL;
 
 struct Plan {
     int64_t rows, units, groups;
@@ -1341,6 +1447,12 @@ Plan plan_of(const Cache4& c, int64_t count, int64_t tokens, int q_heads, int64_
         if (p.rows >= 16 * waves && units >= kPromptUnits && units <= 0x7ffffff0LL) {
             p.prompt_waves = waves;
             p.prompt_tiles = tiles;
+            const int64_t fill = c.dim != 256 && waves == 4 ? 512 : 256;
+            if (units < kSplitUnits * fill && max_len >= kSplitLen * max_q) {
+                p.groups = fill;
+                p.part_bytes = (size_t)fill * 2 * 32 * waves * c.dim * sizeof(float);
+                p.ml_bytes = (size_t)fill * 2 * 32 * waves * sizeof(float2);
+            }
             return p;
         }
     }
@@ -1356,8 +1468,14 @@ Plan plan_of(const Cache4& c, int64_t count, int64_t tokens, int q_heads, int64_
 template <int D, int G, int NW>
 void launch_prompt(const AttnArgs& a, const Plan& p, hipStream_t stream)
 {
-    const int64_t units = a.bt.count * a.c.heads * p.prompt_tiles;
-    cache4_prompt_kernel<D, G, NW><<<(unsigned)((units + 7) & ~7LL), 64 * NW, 0, stream>>>(a, (int32_t)p.prompt_tiles);
+    if (p.groups) {
+        cache4_prompt_kernel<D, G, NW><<<(unsigned)p.groups, 64 * NW, 0, stream>>>(a, 0);
+        cache4_join_edges_kernel<D, PromptTile<D, G, NW>>
+            <<<dim3((unsigned)p.groups - 1, 2 * NW), kThreads, 0, stream>>>(a);
+    } else {
+        const int64_t units = a.bt.count * a.c.heads * p.prompt_tiles;
+        cache4_prompt_kernel<D, G, NW><<<(unsigned)((units + 7) & ~7LL), 64 * NW, 0, stream>>>(a, (int32_t)p.prompt_tiles);
+    }
 }
 
 template <int D, int G>
@@ -1371,7 +1489,7 @@ hipError_t launch_dg(const AttnArgs& a, const Plan& p, hipStream_t stream)
         cache4_attention_kernel<D, G><<<(unsigned)a.groups, kThreads, 0, stream>>>(a);
         if (a.groups > 1) {
             if (p.units * 2 > a.groups) {
-                cache4_join_edges_kernel<D><<<(unsigned)a.groups - 1, kThreads, 0, stream>>>(a);
+                cache4_join_edges_kernel<D, SmallCut><<<(unsigned)a.groups - 1, kThreads, 0, stream>>>(a);
             } else {
                 const dim3 jgrid((unsigned)p.rows, (unsigned)a.c.heads, (unsigned)a.bt.count);
                 cache4_join_kernel<D><<<jgrid, kThreads, 0, stream>>>(a);
