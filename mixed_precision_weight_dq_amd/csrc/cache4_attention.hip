@@ -1414,18 +1414,26 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
     }
 }
 
-// The launch's shape: as many workgroups as fill the 256 CUs four deep (two
-// for heads of 256, whose registers and LDS allow no more), fewer where there
-// are not that many steps.
+// The launch's shape.  Few new tokens: kFill stretches of the line, fewer where
+// there are not that many steps (half of it for heads of 256, whose LDS lets fewer
+// workgroups onto a CU).  Many: cache4_prompt_kernel from kPromptUnits units (sequence,
+// kv head, tile of rows) on, or kPromptRows rows per kv head and kPromptSteps steps
+// for each of its workgroups.  It splits units into stretches where whole ones would
+// leave CUs idle, and where the steps that the causal mask takes from a stretch are
+// few (len >= kSplitLen new).  Measured with 32 query and 8 kv heads of 128, one
+// sequence's new tokens over its length:
+//   100 over 20000 (400 rows, 12 steps): 110 us, cache4_attention_kernel 129 us;
+//    64 over 20000 (256 rows,  5 steps):  97 us, cache4_attention_kernel  91 us;
+//   2 x 100 over 6000 (400 rows, 6 steps): 76 us, cache4_attention_kernel 69 us;
+//   512 over 8000: split 144 us, whole units of 128 rows 338 us;
+//   3 x 3000 over 12000: split 1842 us, whole 2277 us; 4 x 2000 over 2000: split
+//   337 us, whole 254 us.
 constexpr int64_t kFill = 512;
-constexpr int64_t kPromptUnits = 96;  // (sequence, kv head, row tile)s for the prompt kernel
-
-#ifndef SU
-#define SU 4
-#define SL 2
-#endif
-constexpr int64_t kSplitUnits = SU;
-constexpr int64_t kSplitLen = SL;
+constexpr int64_t kPromptUnits = 96;
+constexpr int64_t kPromptRows = 320;
+constexpr int64_t kPromptSteps = 8;
+constexpr int64_t kSplitUnits = 4;
+constexpr int64_t kSplitLen = 2;
 
 struct Plan {
     int64_t rows, units, groups;
@@ -1444,17 +1452,19 @@ Plan plan_of(const Cache4& c, int64_t count, int64_t tokens, int q_heads, int64_
         if (waves == 8 && c.dim == 256) continue;  // the buffers would not fit in LDS
         const int64_t tiles = ceil_div(p.rows, 32 * waves);
         const int64_t units = count * c.heads * tiles;
-        if (p.rows >= 16 * waves && units >= kPromptUnits && units <= 0x7ffffff0LL) {
-            p.prompt_waves = waves;
-            p.prompt_tiles = tiles;
-            const int64_t fill = c.dim != 256 && waves == 4 ? 512 : 256;
-            if (units < kSplitUnits * fill && max_len >= kSplitLen * max_q) {
-                p.groups = fill;
-                p.part_bytes = (size_t)fill * 2 * 32 * waves * c.dim * sizeof(float);
-                p.ml_bytes = (size_t)fill * 2 * 32 * waves * sizeof(float2);
-            }
-            return p;
+        const int64_t fill = c.dim != 256 && waves == 4 ? 512 : 256;
+        const bool many = units >= kPromptUnits;
+        const bool deep = fill == 256 && p.rows >= kPromptRows &&
+                          units * ceil_div(max_len, 16 * waves) >= kPromptSteps * fill;
+        if (p.rows < 16 * waves || !(many || deep) || units > 0x7ffffff0LL) continue;
+        p.prompt_waves = waves;
+        p.prompt_tiles = tiles;
+        if (!many || (units < kSplitUnits * fill && max_len >= kSplitLen * max_q)) {
+            p.groups = fill;
+            p.part_bytes = (size_t)fill * 2 * 32 * waves * c.dim * sizeof(float);
+            p.ml_bytes = (size_t)fill * 2 * 32 * waves * sizeof(float2);
         }
+        return p;
     }
     p.units = count * c.heads * ceil_div(p.rows, 16);
     const int64_t fill = c.dim == 256 ? kFill / 2 : kFill;
