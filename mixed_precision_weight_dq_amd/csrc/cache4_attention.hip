@@ -15,6 +15,15 @@
 //   * p * (value scale) is rounded once, to fp16, after multiplication by a
 //     power of two that puts the largest value scale seen so far in [2^14,
 //     2^15): relative error 2^-11 down to 2^-29 of the largest.
+// This form (cache4_attention_kernel) is for few new tokens: bound by the cache's
+// bytes, and below them by the vector work of expanding the codes.  One token over
+// 65000 (8 kv heads of 128, 32 query heads, g = 32; 83 MB of cache) 30 us, of which
+// 15 are launch, first bytes and the join; 40 sequences of 3250 to 6000 (8 kv, 40
+// query heads; 240 MB) 62 us, 3.9 TB/s; 8 x 5 tokens over up to 1100 13 us.  Waves
+// of one workgroup take neighbouring steps and join through LDS; workgroups take
+// equal stretches of all sequences' steps (below) and join through the workspace: one
+// workgroup per sequence, head and 16 rows left the first case's long axis to 8 of
+// them, 4.7 ms.  For many new tokens see cache4_prompt_kernel.
 #include "cache4.hpp"
 #include "common.hpp"
 #include "gemm_tiles.hpp"
@@ -920,6 +929,14 @@ __global__ __launch_bounds__(kThreads) void cache4_join_edges_kernel(AttnArgs a)
 // transposed: the 8 positions that a lane's operand holds are a piece of
 // dimension d's row.  Piece p of a row lies at p ^ swizzle(row), which spreads the
 // rows of a pass over the banks (of rows of 8 pieces, two share all banks).
+//
+// 1000 new tokens over 6000 and 569 over 4083 (8 kv heads of 128, 32 query heads,
+// g = 32) 228 us: 126 GFLOP, 0.55 PFLOP/s.  The join is 14 us of it.  A step of 128
+// positions takes 6.5 us, about the sum of what its parts take alone: vector
+// work 2.9 (softmax, expansion), LDS reads 1.7, matrix instructions 1.7; two waves
+// per SIMD, which the registers of 32 rows by 128 dimensions allow, overlap little of
+// it.  Tiles of 128 rows (half as many codes shared) were slower, 294 against 254 us
+// before the stretches; whole units (200 for 256 CUs, 32 to 47 steps) 268 us.
 template <int kPieces>
 __device__ __forceinline__ int swizzle(int row)
 {
