@@ -334,7 +334,8 @@ typedef struct {
 
 typedef struct {
     const int32_t* starts; /* device, [count + 1], not decreasing, 4-byte aligned      */
-    const int32_t* lens;   /* device, [count] cached tokens, the call's own included   */
+    const int32_t* lens;   /* device, [count] cached tokens, the call's own included;
+                              for attention at most 2^31 - 2^16 (more: NaN)           */
     const int32_t* table;  /* device, [count, table_width] pages in order of position  */
     int64_t table_width;   /* pages per sequence, 1 .. 2^24 (unused entries: any value) */
     int64_t count;
@@ -364,7 +365,8 @@ dq_status dq_cache4_read(const dq_cache4* cache, const dq_cache4_batch* batch, v
  *   q       in   device, [tokens, q_heads, D] bf16 bits, 16-byte aligned; tokens lie
  *                q_stride elements apart (a multiple of 8, at least q_heads * D)
  *   q_heads      a multiple of kv_heads, at most DQ_CACHE4_MAX_HEADS
- *   scale        factor of the dot products, finite
+ *   scale        factor of the dot products; it and scale * q.k finite, with log2(e)
+ *                as a further factor, in fp32
  *   max_q, max_len  the most tokens of a sequence in this call and the most
  *                cached ones, at least 1: they size the launch (a larger sequence
  *                is served too, only slower)

@@ -434,7 +434,7 @@ dq_status dq_cache4_attention(const dq_cache4* cache, const dq_cache4_batch* bat
     if (!valid_heads(q_heads, c.heads) || !valid_stride(q_stride, (int64_t)q_heads * c.dim) ||
         max_q < 1 || max_len < 1)
         return DQ_ERR_SHAPE;
-    if (!std::isfinite(scale)) return DQ_ERR_VALUE;
+    if (!std::isfinite(scale * 1.44269504f)) return DQ_ERR_VALUE;  // exp2's argument is scaled
     const size_t need = dq::cache4_attention_workspace(c, bt.count, tokens, q_heads, max_q, max_len);
     if (need && !workspace) return DQ_ERR_NULL;
     if (need > workspace_bytes) return DQ_ERR_SHAPE;

@@ -139,13 +139,13 @@ __device__ __forceinline__ uint32_t quantize8(const Raw<BF16>& raw, int group_th
 template <int D, bool BF16>
 __global__ __launch_bounds__(kThreads) void cache4_append_kernel(
     Cache4 c, Cache4Batch bt, const void* __restrict__ k, const void* __restrict__ v,
-    int64_t tokens, int64_t k_stride, int64_t v_stride)
+    int64_t tokens, int64_t from_token, int64_t k_stride, int64_t v_stride)
 {
     constexpr int kParts = D / 8;
     constexpr int kPer = D / 16;               // value codes of a c (cache4.hpp)
     constexpr int kRun = kPer < 8 ? kPer : 8;  // of them in a word
     __shared__ __attribute__((aligned(16))) uint32_t turn[kThreads];
-    const int64_t t = (int64_t)blockIdx.x * (kThreads / kParts) + threadIdx.x / kParts;
+    const int64_t t = from_token + (int64_t)blockIdx.x * (kThreads / kParts) + threadIdx.x / kParts;
     const int part = threadIdx.x % kParts;
     const int head = blockIdx.y;
     const int64_t at = (int64_t)head * D + part * 8;
@@ -212,11 +212,12 @@ __device__ __forceinline__ void store8(void* dst, int64_t o, const float (&x)[8]
 template <int D, bool BF16>
 __global__ __launch_bounds__(kThreads) void cache4_read_kernel(Cache4 c, Cache4Batch bt,
                                                                void* __restrict__ k,
-                                                               void* __restrict__ v, int64_t tokens)
+                                                               void* __restrict__ v, int64_t tokens,
+                                                               int64_t from_token)
 {
     constexpr int kParts = D / 8;
     constexpr int kWords = D / 64 * 4;  // of the 8 c's of a thread's value dimensions
-    const int64_t t = (int64_t)blockIdx.x * (kThreads / kParts) + threadIdx.x / kParts;
+    const int64_t t = from_token + (int64_t)blockIdx.x * (kThreads / kParts) + threadIdx.x / kParts;
     const int part = threadIdx.x % kParts;
     const int head = blockIdx.y;
     const int64_t slot = find_slot<kParts>(c, bt, t, tokens);
@@ -257,9 +258,19 @@ __global__ __launch_bounds__(kThreads) void cache4_read_kernel(Cache4 c, Cache4B
     store8<BF16>(v, o, y);
 }
 
-dim3 token_grid(const Cache4& c, int64_t tokens)
+// Launches for the tokens from, from + kLaunchTokens, ... (a launch has at most
+// 2^32 - 1 threads a dimension).
+constexpr int64_t kLaunchTokens = 1LL << 26;
+template <class F>
+hipError_t by_tokens(const Cache4& c, int64_t tokens, F launch)
 {
-    return dim3((unsigned)ceil_div(tokens, kThreads / (c.dim / 8)), (unsigned)c.heads);
+    for (int64_t from = 0; from < tokens; from += kLaunchTokens) {
+        const int64_t n = tokens - from < kLaunchTokens ? tokens - from : kLaunchTokens;
+        launch(dim3((unsigned)ceil_div(n, kThreads / (c.dim / 8)), (unsigned)c.heads), from);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
 }
 
 }  // namespace
@@ -270,9 +281,10 @@ hipError_t launch_cache4_append(const Cache4& c, const Cache4Batch& bt, const vo
 {
 #define CALL(D) \
     (bf16 ? cache4_append_kernel<D, true> : cache4_append_kernel<D, false>)
-    (c.dim == 64 ? CALL(64) : (c.dim == 128 ? CALL(128) : CALL(256)))<<<
-        token_grid(c, tokens), kThreads, 0, stream>>>(c, bt, k, v, tokens, k_stride, v_stride);
-    return hipGetLastError();
+    const auto kernel = c.dim == 64 ? CALL(64) : (c.dim == 128 ? CALL(128) : CALL(256));
+    return by_tokens(c, tokens, [&](dim3 grid, int64_t from) {
+        kernel<<<grid, kThreads, 0, stream>>>(c, bt, k, v, tokens, from, k_stride, v_stride);
+    });
 #undef CALL
 }
 
@@ -281,9 +293,10 @@ hipError_t launch_cache4_read(const Cache4& c, const Cache4Batch& bt, void* k, v
 {
 #define CALL(D) \
     (bf16 ? cache4_read_kernel<D, true> : cache4_read_kernel<D, false>)
-    (c.dim == 64 ? CALL(64) : (c.dim == 128 ? CALL(128) : CALL(256)))<<<
-        token_grid(c, tokens), kThreads, 0, stream>>>(c, bt, k, v, tokens);
-    return hipGetLastError();
+    const auto kernel = c.dim == 64 ? CALL(64) : (c.dim == 128 ? CALL(128) : CALL(256));
+    return by_tokens(c, tokens, [&](dim3 grid, int64_t from) {
+        kernel<<<grid, kThreads, 0, stream>>>(c, bt, k, v, tokens, from);
+    });
 #undef CALL
 }
 

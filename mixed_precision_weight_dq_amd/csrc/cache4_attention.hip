@@ -174,6 +174,9 @@ __device__ __forceinline__ int64_t udiv(int64_t a, int64_t b)
     return a / b;
 }
 
+// Longest sequence: positions a few steps past its end are still below 2^31.
+constexpr int kMaxLen = 0x7fff0000;
+
 // What a workgroup knows of its sequence.  Token rows and positions are below 2^31.
 struct Rows {
     int first, nq, len;  // first token row, new tokens, cached tokens
@@ -197,7 +200,7 @@ __device__ __forceinline__ Rows rows_of(const AttnArgs& a, int64_t b)
     r.first = (int)first;
     r.nq = (int)nq;
     r.len = a.bt.lens[b];
-    r.bad = r.len > a.bt.width << a.c.page_shift;
+    r.bad = r.len > a.bt.width << a.c.page_shift || r.len > kMaxLen;
     if (r.len < 0 || r.bad) r.len = 0;
     r.per = a.q_heads / a.c.heads;
     return r;
@@ -1459,6 +1462,13 @@ struct Plan {
     size_t part_bytes, ml_bytes;
 };
 
+// heads * tiles, or kMaxUnits, which as a product with any length fits 64 bits
+constexpr int64_t kMaxUnits = 1LL << 23;
+int64_t units_of(int64_t heads, int64_t tiles)
+{
+    return tiles > kMaxUnits / heads ? kMaxUnits : heads * tiles;
+}
+
 Plan plan_of(const Cache4& c, int64_t count, int64_t tokens, int q_heads, int64_t max_q, int64_t max_len)
 {
     Plan p{};
@@ -1468,12 +1478,13 @@ Plan plan_of(const Cache4& c, int64_t count, int64_t tokens, int q_heads, int64_
     for (int waves = 8; waves >= 4; waves /= 2) {
         if (waves == 8 && c.dim == 256) continue;  // the buffers would not fit in LDS
         const int64_t tiles = ceil_div(p.rows, 32 * waves);
-        const int64_t units = count * c.heads * tiles;
+        const int64_t units = units_of(count * c.heads, tiles);
         const int64_t fill = c.dim != 256 && waves == 4 ? 512 : 256;
         const bool many = units >= kPromptUnits;
         const bool deep = fill == 256 && p.rows >= kPromptRows &&
                           units * ceil_div(max_len, 16 * waves) >= kPromptSteps * fill;
-        if (p.rows < 16 * waves || !(many || deep) || units > 0x7ffffff0LL) continue;
+        // (a launch has at most 2^32 - 1 threads)
+        if (p.rows < 16 * waves || !(many || deep) || units > kMaxUnits / 2) continue;
         p.prompt_waves = waves;
         p.prompt_tiles = tiles;
         if (!many || (units < kSplitUnits * fill && max_len >= kSplitLen * max_q)) {
@@ -1483,7 +1494,7 @@ Plan plan_of(const Cache4& c, int64_t count, int64_t tokens, int q_heads, int64_
         }
         return p;
     }
-    p.units = count * c.heads * ceil_div(p.rows, 16);
+    p.units = units_of(count * c.heads, ceil_div(p.rows, 16));
     const int64_t fill = c.dim == 256 ? kFill / 2 : kFill;
     p.groups = p.units > fill ? fill : p.units * ceil_div(max_len, kStride);
     if (p.groups > fill) p.groups = fill;

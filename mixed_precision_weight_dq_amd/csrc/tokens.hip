@@ -24,6 +24,7 @@ namespace {
 constexpr int kPiece = 8;
 constexpr int kTokenThreads = 256;
 constexpr int kHeld = 4;  // pieces per thread
+constexpr int64_t kLaunchTokens = 1LL << 23;  // (a multiple of 16 bytes of x for any K)
 
 // The 8 elements of a piece as they lie in memory.
 template <bool BF16>
@@ -171,12 +172,16 @@ hipError_t launch_quantize_tokens(const void* x, bool bf16, int64_t M, int64_t K
                                   float* scales, int32_t* sums, hipStream_t stream)
 {
     const int64_t pitch = token_row_bytes(K);
-    const dim3 grid((unsigned)M);
-    if (bf16)
-        quantize_tokens_kernel<true><<<grid, kTokenThreads, 0, stream>>>(x, K, pitch, codes, scales, sums);
-    else
-        quantize_tokens_kernel<false><<<grid, kTokenThreads, 0, stream>>>(x, K, pitch, codes, scales, sums);
-    return hipGetLastError();
+    // a launch has at most 2^32 - 1 threads
+    for (int64_t m = 0; m < M; m += kLaunchTokens) {
+        const dim3 grid((unsigned)(M - m < kLaunchTokens ? M - m : kLaunchTokens));
+        const void* row = static_cast<const char*>(x) + m * K * (bf16 ? 2 : 4);
+        (bf16 ? quantize_tokens_kernel<true> : quantize_tokens_kernel<false>)<<<grid, kTokenThreads, 0, stream>>>(
+            row, K, pitch, codes + m * pitch, scales + m, sums + m);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
 }
 
 }  // namespace dq

@@ -213,3 +213,28 @@ def test_cut_prompt_graphs():
         t.cuda.synchronize()
         for _, out, _ in graphs:
             assert t.equal(out, want), i
+
+
+def test_longest_sequence():
+    """2^31 - 2^16 positions, every one of them in the same page, are that page's softmax; one more
+    position is refused with NaN.  A lane adds up to 2^18 weights in fp32, each sum within 2^-24:
+    2^-6 of W at most, and the roundings of a short sequence beside it."""
+    t = torch()
+    D, g, page = 64, 64, 256
+    n = 2 ** 31 - 2 ** 16
+    x = head_vectors(1, page, 2, D)
+    cache = dq.Cache4.empty(1, 1, D, page, g)
+    one, st = gpu(np.zeros((1, 1), np.int32)), gpu(np.array([0, page], np.int32))
+    k, v = gpu(x)[:, :1], gpu(x)[:, 1:]
+    dq.cache4_append(cache, k, v, st, gpu(np.array([page], np.int32)), one)
+    q = t.randn(1, 2, D, device="cuda").bfloat16()
+    row = gpu(np.array([0, 1], np.int32))
+    table = t.zeros((1, 2 ** 31 // page), dtype=t.int32, device="cuda")
+    report("cache4_attention over 2^31 - 2^16 positions")
+    short = dq.cache4_attention(cache, q, row, gpu(np.array([page], np.int32)), one).float()
+    long = dq.cache4_attention(cache, q, row, gpu(np.array([n], np.int32)), table, max_q=1, max_len=n).float()
+    dq.cache4_append(cache, k, v.abs().contiguous(), st, gpu(np.array([page], np.int32)), one)
+    W = dq.cache4_attention(cache, q, row, gpu(np.array([page], np.int32)), one).float()
+    assert bool(((long - short).abs() <= 2.0 ** -7 * short.abs() + (2.0 ** -5 + 2.0 ** -9) * W).all())
+    over = dq.cache4_attention(cache, q, row, gpu(np.array([n + 1], np.int32)), table, max_q=1, max_len=n)
+    assert bool(t.isnan(over).all())
