@@ -37,40 +37,39 @@ struct I8Args {
 };
 
 // ---------------------------------------------------------------------------
-// Few tokens (M <= 64): bound by the packed weights.  A workgroup of four waves
-// has 16 R weight rows, all tokens (16 T, the last ones again past M) and all
-// of K: wave w takes the steps w, w + 4, ... of 256 codes, and the four sums
-// are added through LDS.  v_mfma_i32_16x16x64_i8 with the weights as its rows:
-// lane (r, g) holds, of weight row r, the chunks 2 g and 2 g + 1 of the step,
-// 2 B consecutive words, so codes go from memory to registers to the matrix
-// cores, a row's 256 codes with four lanes' neighbouring loads.  The tokens'
-// bytes of the same codes come from L1 / L2 likewise.  A step's loads are in
-// flight while the step before is multiplied.
+// Few tokens: bound by the packed weights.  A workgroup of W = 4 waves has 16 R
+// weight rows, all tokens (M <= 64: 16 T, the last ones again past M) and all of
+// K: wave w takes the steps w, w + W, ... of 256 codes, and the waves' sums are
+// added through LDS.  (W = 8 with 16 T of more tokens: few tiles, see launch_b.)
+// v_mfma_i32_16x16x64_i8 with the weights as its rows: lane (r, g) holds, of
+// weight row r, the chunks 2 g and 2 g + 1 of the step, 2 B consecutive words, so
+// codes go from memory to registers to the matrix cores, a row's 256 codes with
+// four lanes' neighbouring loads.  The tokens' bytes of the same codes come from L1
+// / L2 likewise.  A step's loads are in flight while the step before is multiplied.
 //
 // Rows per workgroup: the more, the less often the tokens' bytes are read and
 // the fewer rows are open at once, as long as every CU has a workgroup.  16 x
 // 28672 x 8192 at b = 6: 112 rows (256 workgroups) 39.5 us (4.5 TB/s of
 // weights), 64 rows 45.8, 32 rows 53.9, 16 rows 56; 1 x 4096 x 4096 at b = 4:
 // 16 rows (256 workgroups) 4.1 us, 32 rows 5.3, 64 rows 7.7.
-constexpr int kFewThreads = 256;
-constexpr int kFewWaves = kFewThreads / kWave;
-
-template <int B, int R, int T>
-__global__ __launch_bounds__(kFewThreads, R >= 7 || T == 4 ? 1 : (R == 1 ? 4 : 2)) void few_i8_kernel(I8Args a)
+template <int B, int R, int T, int W>
+__global__ __launch_bounds__(W * kWave, W == 8 ? 2 : (R >= 7 || T == 4 ? 1 : (R == 1 ? 4 : 2))) void few_i8_kernel(I8Args a)
 {
+    constexpr int kFewWaves = W, kFewThreads = W * kWave;
     __shared__ __attribute__((aligned(16))) int32_t part[kFewWaves][R * T * 4 * kWave];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int r = lane & 15;
     const int g = lane >> 4;
     const int64_t n0 = (int64_t)blockIdx.x * (16 * R);
+    const int64_t m0 = (int64_t)blockIdx.y * (16 * T);
+    const int64_t mrows = a.M - m0 < 16 * T ? a.M - m0 : 16 * T;
     const int64_t nrows = a.N - n0 < 16 * R ? a.N - n0 : 16 * R;
     const int steps = (int)((a.pitch + 255) >> 8);
 
     const uint32_t row_bytes = (uint32_t)a.row_words * 4;
     const BufRef wbuf = uniform_buf(a.packed + n0 * a.row_words, (uint32_t)nrows * row_bytes);
-    const uint32_t xbytes = (uint32_t)(a.M * a.pitch);
-    const BufRef xbuf = uniform_buf(a.x, xbytes);
+    const BufRef xbuf = uniform_buf(a.x + m0 * a.pitch, (uint32_t)(mrows * a.pitch));
     uint32_t woff[R], xoff[T];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -79,7 +78,7 @@ __global__ __launch_bounds__(kFewThreads, R >= 7 || T == 4 ? 1 : (R == 1 ? 4 : 2
     }
 #pragma unroll
     for (int t = 0; t < T; ++t) {
-        const int64_t m = 16 * t + r < a.M ? 16 * t + r : a.M - 1;
+        const int64_t m = 16 * t + r < mrows ? 16 * t + r : mrows - 1;
         xoff[t] = (uint32_t)(m * a.pitch) + g * 64;
     }
 
@@ -144,13 +143,13 @@ __global__ __launch_bounds__(kFewThreads, R >= 7 || T == 4 ? 1 : (R == 1 ? 4 : 2
             *reinterpret_cast<i32x4_t*>(&part[wave][((i * T + t) * kWave + lane) * 4]) = acc[i][t];
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < R * T; ++j) {
+    for (int j = 0; j < R * T * 4 / W; ++j) {
         const int o = j * kFewThreads + threadIdx.x;
         int32_t sum = part[0][o];
 #pragma unroll
         for (int v = 1; v < kFewWaves; ++v) sum += part[v][o];
         const int tl = o / (4 * kWave), l = (o >> 2) & (kWave - 1);
-        const int64_t m = 16 * (tl % T) + (l & 15);
+        const int64_t m = m0 + 16 * (tl % T) + (l & 15);
         const int64_t n = n0 + 16 * (tl / T) + 4 * (l >> 4) + (o & 3);
         if (m < a.M && n < a.N) {
             const float v = finish_i8(sum, code_shift<B>(a.zeros, n), a.x_sums[m], a.x_scales[m], a.scales[n]);
@@ -162,10 +161,11 @@ __global__ __launch_bounds__(kFewThreads, R >= 7 || T == 4 ? 1 : (R == 1 ? 4 : 2
     }
 }
 
-template <int B, int R, int T>
+template <int B, int R, int T, int W = 4>
 hipError_t launch_few(const I8Args& a, hipStream_t stream)
 {
-    few_i8_kernel<B, R, T><<<dim3((unsigned)ceil_div(a.N, 16 * R)), kFewThreads, 0, stream>>>(a);
+    few_i8_kernel<B, R, T, W>
+        <<<dim3((unsigned)ceil_div(a.N, 16 * R), (unsigned)ceil_div(a.M, 16 * T)), W * kWave, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -470,6 +470,15 @@ hipError_t launch_many(const I8Args& a, hipStream_t stream)
 template <int B>
 hipError_t launch_b(const I8Args& a, hipStream_t stream)
 {
+    // Too few tiles for the CUs: 32 weight rows by 32 or 64 tokens per workgroup, whose
+    // eight waves split K, in one round of workgroups.  100 x 2000 x 4096 at b = 4 / 7:
+    // 32 tokens 9.2 / 11.4 us, 64 tokens 13.2 / 15.4, 64 x 128 tiles 14.6 / 22.7; 200 x
+    // 1500 x 4096: 15.4 / 20.8, 13.6 / 15.7, 14.9 / 22.9; 128 x 6000 x 4096 (more than
+    // a round): 21.8 / 29.9, 25.2 / 29.9, 14.8 / 22.8
+    if (a.M > 32) {
+        if (ceil_div(a.N, 32) * ceil_div(a.M, 32) <= 256) return launch_few<B, 2, 2, 8>(a, stream);
+        if (ceil_div(a.N, 32) * ceil_div(a.M, 64) <= 256) return launch_few<B, 2, 4, 8>(a, stream);
+    }
     if (a.M <= 64) {
         if (a.M <= 16) return launch_few_rows<B, 1>(a, stream);
         if (a.M <= 32) return launch_few_rows<B, 2>(a, stream);

@@ -9,6 +9,7 @@ import pytest
 import mixed_precision_weight_dq_amd as dq
 from gpu_util import bf16_gpu, report, torch
 from serving_ref import Batch, bf16, group4, tokens_ref, values, widen
+from test_gpu_tokens_i8 import assert_product
 from test_gpu_cache4 import gpu, head_vectors, meta, run_attention
 
 pytestmark = pytest.mark.gpu
@@ -53,6 +54,16 @@ def test_long_token_rows(K):
         assert np.array_equal(codes.cpu().numpy()[:, :K], want)
         assert (codes.cpu().numpy()[:, K:] == 0).all()
         assert np.array_equal(sums.cpu().numpy(), wsum)
+
+
+@pytest.mark.parametrize("asym", [False, True])
+@pytest.mark.parametrize("bits", range(2, 9))
+def test_product_shapes(bits, asym):
+    """On either side of each choice of the products' kernels: 32 and 33 tokens, one round of
+    workgroups of 32 and of 64 tokens, tiles of 64 and of 128 rows, all ragged."""
+    for i, (M, N, K) in enumerate([(32, 70, 2200), (33, 70, 2200), (200, 1300, 517), (200, 1500, 517),
+                                   (130, 6100, 327), (260, 12000, 200)]):
+        assert_product("gemm", M, N, K, bits, asym, "bf16" if i % 2 else "f32", 7000 + 10 * bits + i)
 
 
 @pytest.mark.parametrize("D,g", [(64, 32), (128, 128), (256, 64)])
