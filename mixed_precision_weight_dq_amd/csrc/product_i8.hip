@@ -186,7 +186,7 @@ hipError_t launch_few_rows(const I8Args& a, hipStream_t stream)
 // workgroup's tile, as MT x NT tiles of v_mfma_i32_32x32x32_i8.
 //
 // A step is 128 codes.  Tokens and packed codes both go from memory to LDS
-// directly, as whole 128-byte lines of a row, in two stages of a step.  (Codes
+// directly, as whole 128-byte lines of a row, in two or four stages of a step.  (Codes
 // straight into the registers of their lanes touch 64 lines per load, eight
 // loads per line, and L1 looks up a line a cycle: 2048 x 8192 x 8192 at b = 8 took
 // 137 us so.)  Substep t (0 .. 3) multiplies, for lane half h, the bytes 64 h + 16 t ..
@@ -251,11 +251,11 @@ __device__ __forceinline__ void join_waves()
     asm volatile("" ::: "memory");
 }
 
-template <int B, int MT, int NT, int WM, int kOcc>
+template <int B, int MT, int NT, int WM, int kOcc, int S>
 __global__ __launch_bounds__(256 * WM, kOcc) void many_i8_kernel(I8Args a)
 {
     using Tl = ManyTile<MT, NT, WM>;
-    constexpr int S = 2;  // stages; three, for the codes they fit, were no faster
+    static_assert(S == 2 || S == 4, "stages");
     constexpr int kCopies = Tl::kCopies;
     constexpr int kWCopies = NT * B / (2 * WM);  // whole pieces of codes per thread and step
     constexpr bool kWHalf = (NT * B) % (2 * WM) != 0;  // and one more for half of the threads
@@ -264,13 +264,19 @@ __global__ __launch_bounds__(256 * WM, kOcc) void many_i8_kernel(I8Args a)
     // every copy, a whole memory latency per step)
     __shared__ __attribute__((aligned(16))) uint4 As0[Tl::BM * 8], As1[Tl::BM * 8];
     __shared__ __attribute__((aligned(16))) uint4 Ws0[Tl::BN * B], Ws1[Tl::BN * B];
+    __shared__ __attribute__((aligned(16))) uint4 As2[S > 2 ? Tl::BM * 8 : 1], As3[S > 2 ? Tl::BM * 8 : 1];
+    __shared__ __attribute__((aligned(16))) uint4 Ws2[S > 2 ? Tl::BN * B : 1], Ws3[S > 2 ? Tl::BN * B : 1];
     auto as = [&](auto St) __attribute__((always_inline)) -> uint4* {
         if constexpr (decltype(St)::value == 0) return As0;
-        else return As1;
+        else if constexpr (decltype(St)::value == 1) return As1;
+        else if constexpr (decltype(St)::value == 2) return As2;
+        else return As3;
     };
     auto ws = [&](auto St) __attribute__((always_inline)) -> uint4* {
         if constexpr (decltype(St)::value == 0) return Ws0;
-        else return Ws1;
+        else if constexpr (decltype(St)::value == 1) return Ws1;
+        else if constexpr (decltype(St)::value == 2) return Ws2;
+        else return Ws3;
     };
 
     const int tid = threadIdx.x;
@@ -457,13 +463,13 @@ __global__ __launch_bounds__(256 * WM, kOcc) void many_i8_kernel(I8Args a)
     }
 }
 
-template <int B, int MT, int NT, int WM, int kOcc>
+template <int B, int MT, int NT, int WM, int kOcc, int S = 2>
 hipError_t launch_many(const I8Args& a, hipStream_t stream)
 {
     using Tl = ManyTile<MT, NT, WM>;
     const int64_t tiles = ceil_div(a.M, Tl::BM) * ceil_div(a.N, Tl::BN);
     if (tiles > 0x7ffffff0LL) return hipErrorInvalidConfiguration;
-    many_i8_kernel<B, MT, NT, WM, kOcc><<<dim3((unsigned)((tiles + 7) & ~7LL)), dim3(Tl::kThreads), 0, stream>>>(a);
+    many_i8_kernel<B, MT, NT, WM, kOcc, S><<<dim3((unsigned)((tiles + 7) & ~7LL)), dim3(Tl::kThreads), 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -493,6 +499,10 @@ hipError_t launch_b(const I8Args& a, hipStream_t stream)
     // 128 x 128 tiles: 333 x 17408 x 5120 at b = 5 51 us (64 x 128 67 us, 192 x 128 59 us,
     // 128 x 256 55 us, 256 x 256 82 us); half as high while they leave CUs without one
     if (ceil_div(a.M, 128) * ceil_div(a.N, 128) >= 256) return launch_many<B, 4, 1, 1, B <= 5 ? 3 : 2>(a, stream);
+    // and with four stages while a CU has one workgroup at most, whose copies nothing
+    // else hides: 300 x 3000 x 8192 at b = 4 / 7 / 8 23.2 / 39.7 / 24.6 us, two stages
+    // 28.2 / 44.9 / 37.8 (the same within 2 % where the caches hold the operands)
+    if (ceil_div(a.M, 64) * ceil_div(a.N, 128) <= 256) return launch_many<B, 2, 1, 1, 1, 4>(a, stream);
     return launch_many<B, 2, 1, 1, 3>(a, stream);
 }
 
