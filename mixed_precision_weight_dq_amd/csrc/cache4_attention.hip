@@ -935,10 +935,10 @@ __global__ __launch_bounds__(kThreads) void cache4_join_edges_kernel(AttnArgs a)
 //
 // 1000 new tokens over 6000 and 569 over 4083 (8 kv heads of 128, 32 query heads,
 // g = 32) 228 us: 126 GFLOP, 0.55 PFLOP/s.  The join is 14 us of it.  A step of 128
-// positions takes 6.5 us, about the sum of what its parts take alone: vector
-// work 2.9 (softmax, expansion), LDS reads 1.7, matrix instructions 1.7; two waves
-// per SIMD, which the registers of 32 rows by 128 dimensions allow, overlap little of
-// it.  Tiles of 128 rows (half as many codes shared) were slower, 294 against 254 us
+// positions takes 6.5 us, about the sum of what its parts take alone (counted
+// instructions): vector work 2.4 (softmax, expansion), LDS reads 2.2, matrix
+// instructions 1.5; two waves per SIMD, which the registers of 32 rows by 128
+// dimensions allow, overlap little of it.  Tiles of 128 rows (half as many codes shared) were slower, 294 against 254 us
 // before the stretches; whole units (200 for 256 CUs, 32 to 47 steps) 268 us.
 template <int kPieces>
 __device__ __forceinline__ int swizzle(int row)
