@@ -249,3 +249,29 @@ def test_longest_sequence():
     assert bool(((long - short).abs() <= 2.0 ** -7 * short.abs() + (2.0 ** -5 + 2.0 ** -9) * W).all())
     over = dq.cache4_attention(cache, q, row, gpu(np.array([n + 1], np.int32)), table, max_q=1, max_len=n)
     assert bool(t.isnan(over).all())
+
+
+def test_long_cache_offsets_of_prompts():
+    """Many new tokens over pages past 4 GiB of codes: the bits of the same call on a cache that
+    holds those pages alone, units whole and cut."""
+    t = torch()
+    D, g, H, per, page, n, new = 128, 32, 8, 2, 64, 700, 200
+    pages = (1 << 32) // (H * page * D // 2) + 40  # 32 KiB of codes per page
+    c = dq.Cache4.empty(pages, H, D, page, g)
+    count = -(-n // page)
+    far = np.arange(count, dtype=np.int32)[None] * 3
+    far[0, 1::2] = pages - 1 - far[0, 1::2]
+    k, v = (t.randn(n, H, D, device="cuda") for _ in range(2))
+    st, lens = gpu(np.array([0, n], np.int32)), gpu(np.array([n], np.int32))
+    report("cache4 prompts beyond 4 GiB")
+    dq.cache4_append(c, k, v, st, lens, gpu(far))
+    small = dq.Cache4.empty(count, H, D, page, g)
+    for a, b in zip(small.tensors, c.tensors):
+        a.copy_(b[gpu(far)[0].long()])
+    near = gpu(np.arange(count, dtype=np.int32)[None])
+    q = t.randn(new, H * per, D, device="cuda").bfloat16()
+    rows = gpu(np.array([0, new], np.int32))
+    for max_q, max_len in ((new, 200000), (13 * new, 1)):
+        a = dq.cache4_attention(c, q, rows, lens, gpu(far), max_q=max_q, max_len=max_len)
+        b = dq.cache4_attention(small, q, rows, lens, near, max_q=max_q, max_len=max_len)
+        assert t.equal(a, b) and bool(t.isfinite(a).all())
