@@ -379,7 +379,7 @@ dq_status dq_cache4_read(const dq_cache4* cache, const dq_cache4_batch* batch, v
  * times its value's scale is rounded once to 11 significant bits.  Where a call
  * has many new tokens (by max_q, max_len, count and the heads), keys and values are
  * rounded too: a scale to 11 bits, and its product with the code again.
- * The work is cut into equal stretches over all sequences, and the parts of
+ * Long work is cut into equal stretches over all sequences, and the parts of
  * a row are added in a fixed order: a call repeated gives the same bits, a sequence
  * beside others of other lengths may differ in the last ones. */
 size_t dq_cache4_attention_workspace(const dq_cache4* cache, int64_t count, int64_t tokens,

@@ -159,6 +159,7 @@ struct AttnArgs {
     float* part;      // unfinished tiles: normalised outputs [workgroup, 2, 16, D]
     float2* part_ml;  // and their maxima and sums [workgroup, 2, 16]
     int32_t groups;   // workgroups of the attention kernel
+    int32_t step_shift;  // log2 of a step's positions; 31: a unit is one step
 };
 
 constexpr int kWaves = 4;
@@ -211,12 +212,12 @@ __device__ __forceinline__ Rows rows_of(const AttnArgs& a, int64_t b)
 // the sequence's steps of positions (at least one, which writes rows that see
 // nothing).  Workgroup w takes an equal stretch of the line, so lengths do not
 // have to be equal, nor known to the host, for the CUs to be.  Cut: rows of a
-// tile, positions of a step, threads of the workgroup that lays the line out.
-template <int kTileRows, int kStepPos, int kGroupThreads>
+// tile, threads of the workgroup that lays the line out.
+template <int kTileRows, int kGroupThreads>
 struct Cut {
-    static constexpr int kRows = kTileRows, kPos = kStepPos, kThreads = kGroupThreads;
+    static constexpr int kRows = kTileRows, kThreads = kGroupThreads;
 };
-using SmallCut = Cut<16, kStride, kThreads>;
+using SmallCut = Cut<16, kThreads>;
 struct Line {
     int64_t total;   // steps of the call
     int64_t q, r;    // a workgroup's steps: q + 1 for the first r, else q
@@ -232,10 +233,9 @@ struct Line {
     }
 };
 
-template <class C>
-__device__ __forceinline__ int steps_of(const Rows& rw)
+__device__ __forceinline__ int steps_of(const AttnArgs& a, const Rows& rw)
 {
-    return rw.len > 0 ? (rw.len - 1) / C::kPos + 1 : 1;
+    return rw.len > 0 ? ((rw.len - 1) >> a.step_shift) + 1 : 1;
 }
 template <class C>
 __device__ __forceinline__ int64_t tiles_of(const Rows& rw)
@@ -245,7 +245,7 @@ __device__ __forceinline__ int64_t tiles_of(const Rows& rw)
 template <class C>
 __device__ __forceinline__ int64_t line_steps(const AttnArgs& a, const Rows& rw)
 {
-    return tiles_of<C>(rw) * a.c.heads * steps_of<C>(rw);
+    return tiles_of<C>(rw) * a.c.heads * steps_of(a, rw);
 }
 
 __device__ __forceinline__ int64_t lane64(int64_t v, int lane)
@@ -446,7 +446,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 3 : 2)) void ca
 
     Rows rw = ln.rw;
     for (int64_t x = x0; x < x1;) {
-        const int steps = steps_of<SmallCut>(rw);
+        const int steps = steps_of(a, rw);
         const int64_t tiles = tiles_of<SmallCut>(rw);
         if (x >= before + tiles * a.c.heads * steps) {
             before += tiles * a.c.heads * steps;
@@ -470,7 +470,8 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 3 : 2)) void ca
         const int seen = live ? rw.seen(row) : 0;  // positions that the row sees
         const int end = rw.end(r0);
         const int begin = step0 * kStride;
-        const int stop = end < begin + take * kStride ? end : begin + take * kStride;
+        int stop = end;  // (a unit that is one step may have any length)
+        if (take < steps - step0 && begin + take * kStride < end) stop = begin + take * kStride;
         x += take;
         // constant address space: scalar loads, which leave the count of vector
         // loads in flight alone
@@ -790,7 +791,7 @@ __global__ __launch_bounds__(kThreads) void cache4_join_kernel(AttnArgs a)
     const Line ln = lay_line<SmallCut, false>(a, 0, b);
     const Rows rw = ln.rw;
     if ((int64_t)blockIdx.x >= rw.rows()) return;
-    const int steps = steps_of<SmallCut>(rw);
+    const int steps = steps_of(a, rw);
     const int64_t tiles = tiles_of<SmallCut>(rw);
     const int d4 = tid % kPer;
 
@@ -866,11 +867,11 @@ __global__ __launch_bounds__(kThreads) void cache4_join_edges_kernel(AttnArgs a)
 {
     constexpr int N = D / 16;  // dimensions of a thread
     const int64_t w = (int64_t)blockIdx.x + 1;
-    const Line ln = lay_line<Cut<C::kRows, C::kPos, kThreads>, true>(a, w, 0);
+    const Line ln = lay_line<Cut<C::kRows, kThreads>, true>(a, w, 0);
     if (ln.b < 0) return;
     const int64_t x = ln.first(w);
     const Rows rw = ln.rw;
-    const int steps = steps_of<C>(rw);
+    const int steps = steps_of(a, rw);
     const int64_t unit = udiv(x - ln.before, steps);
     const int64_t start = ln.before + unit * steps;
     // the unit's second stretch joins it
@@ -1029,7 +1030,7 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
 
     for (;; tile += grid_tiles) {
         const int64_t rows = rw.rows();
-        const int steps = steps_of<Tl>(rw);
+        const int steps = steps_of(a, rw);
         int step0 = 0, take = steps, slot = 0;
         if (split) {
             if (x >= x1) break;
@@ -1436,9 +1437,14 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
 
 // The launch's shape.  Few new tokens: kFill stretches of the line, fewer where
 // there are not that many steps (half of it for heads of 256, whose LDS lets fewer
-// workgroups onto a CU).  Many: cache4_prompt_kernel from kPromptUnits units (sequence,
-// kv head, tile of rows) on, or kPromptRows rows per kv head and kPromptSteps steps
-// for each of its workgroups.  It splits units into stretches where whole ones would
+// workgroups onto a CU); units are steps as they are, and nothing is joined, while
+// they are short or fill the CUs.  Decode with 8 kv heads of 128, whole / cut: 8
+// sequences of 400 10.3 / 11.2 us, of 800 14.0 / 12.8; 24 (192 units) of up to 1600
+// 22.5 / 23.2, of 2400 29.7 / 26.4; 64 (512) of 4000 63.7 / 64.7, of 7000 107 / 102;
+// 32 of 600 12.9 / 19.8.  Beyond 4096 one long sequence would outlast all others.
+// Many: cache4_prompt_kernel from kPromptUnits units (sequence, kv head, tile of
+// rows) on, or kPromptRows rows per kv head and kPromptSteps steps for each of its
+// workgroups.  It splits units into stretches where whole ones would
 // leave CUs idle, and where the steps that the causal mask takes from a stretch are
 // few (len >= kSplitLen new).  Measured with 32 query and 8 kv heads of 128, one
 // sequence's new tokens over its length:
@@ -1449,6 +1455,7 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
 //   3 x 3000 over 12000: split 1842 us, whole 2277 us; 4 x 2000 over 2000: split
 //   337 us, whole 254 us.
 constexpr int64_t kFill = 512;
+constexpr int64_t kWholeFill = 2048;
 constexpr int64_t kPromptUnits = 96;
 constexpr int64_t kPromptRows = 320;
 constexpr int64_t kPromptSteps = 8;
@@ -1457,6 +1464,7 @@ constexpr int64_t kSplitLen = 2;
 
 struct Plan {
     int64_t rows, units, groups;
+    int step_shift;
     int prompt_waves;      // 0: cache4_attention_kernel, else waves of cache4_prompt_kernel
     int64_t prompt_tiles;  // its row tiles per (sequence, kv head)
     size_t part_bytes, ml_bytes;
@@ -1486,6 +1494,7 @@ Plan plan_of(const Cache4& c, int64_t count, int64_t tokens, int q_heads, int64_
         // (a launch has at most 2^32 - 1 threads)
         if (p.rows < 16 * waves || !(many || deep) || units > kMaxUnits / 2) continue;
         p.prompt_waves = waves;
+        p.step_shift = waves == 8 ? 7 : 6;
         p.prompt_tiles = tiles;
         if (!many || (units < kSplitUnits * fill && max_len >= kSplitLen * max_q)) {
             p.groups = fill;
@@ -1496,6 +1505,12 @@ Plan plan_of(const Cache4& c, int64_t count, int64_t tokens, int q_heads, int64_
     }
     p.units = units_of(count * c.heads, ceil_div(p.rows, 16));
     const int64_t fill = c.dim == 256 ? kFill / 2 : kFill;
+    if (max_len <= 512 || (p.units >= 192 && max_len <= (p.units < 512 ? 8 * p.units : 4096))) {
+        p.groups = p.units < kWholeFill ? p.units : kWholeFill;
+        p.step_shift = 31;
+        return p;
+    }
+    p.step_shift = 7;
     p.groups = p.units > fill ? fill : p.units * ceil_div(max_len, kStride);
     if (p.groups > fill) p.groups = fill;
     p.part_bytes = (size_t)p.groups * 2 * 16 * c.dim * sizeof(float);
@@ -1525,7 +1540,7 @@ hipError_t launch_dg(const AttnArgs& a, const Plan& p, hipStream_t stream)
         launch_prompt<D, G, 4>(a, p, stream);
     } else {
         cache4_attention_kernel<D, G><<<(unsigned)a.groups, kThreads, 0, stream>>>(a);
-        if (a.groups > 1) {
+        if (a.groups > 1 && a.step_shift < 31) {
             if (p.units * 2 > a.groups) {
                 cache4_join_edges_kernel<D, SmallCut><<<(unsigned)a.groups - 1, kThreads, 0, stream>>>(a);
             } else {
@@ -1555,7 +1570,7 @@ hipError_t launch_cache4_attention(const Cache4& c, const Cache4Batch& bt, const
     const AttnArgs a{c, bt, q, q_stride, out, tokens, q_heads, scale * kLog2e,
                      static_cast<float*>(workspace),
                      reinterpret_cast<float2*>(static_cast<char*>(workspace) + p.part_bytes),
-                     (int32_t)p.groups};
+                     (int32_t)p.groups, p.step_shift};
     switch (c.dim * 1000 + c.group) {
     case 64032: return launch_dg<64, 32>(a, p, stream);
     case 64064: return launch_dg<64, 64>(a, p, stream);

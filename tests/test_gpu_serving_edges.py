@@ -122,9 +122,25 @@ def test_attention_many_sequences(count, D, g):
     lens = [int(n) for n in rng.integers(0, 150, count)]
     news = [int(n) for n in rng.integers(0, 3, count)]
     batch = Batch(count, lens, news, 16)
-    for hints in (dict(max_q=2, max_len=150), dict(max_q=1, max_len=1)):
+    for hints in (dict(max_q=2, max_len=150), dict(max_q=1, max_len=1), dict(max_q=2, max_len=200000)):
         report("cache4_attention count=%d D=%d g=%d %s" % (count, D, g, hints))
         run_attention(5, batch, 1, 4, D, g, **hints)
+
+
+@pytest.mark.parametrize("D,g", [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128), (256, 32),
+                                 (256, 64), (256, 128)])
+def test_attention_cut_decode(D, g):
+    """Few new tokens of short sequences, told of long ones, so that their units are cut: fewer steps
+    than workgroups, empty sequences, rows that see nothing, tiles that end inside a head's rows."""
+    for i, (lens, news, H, per, page) in enumerate([
+            ([1, 2, 15, 16, 17, 31, 32, 33], [1] * 8, 2, 4, 16), ([300, 7, 260], [1] * 3, 3, 8, 32),
+            ([513], [1], 2, 16, 256), ([30, 8, 5], [4, 8, 5], 2, 4, 16),
+            ([100, 40, 640, 9], [37, 0, 64, 7], 1, 3, 32), ([3, 50], [8, 3], 2, 2, 64),
+            ([0, 200], [2, 1], 1, 8, 16)]):
+        batch = Batch(i, lens, news, page)
+        for hints in (dict(max_q=max(news), max_len=200000), dict(max_q=1, max_len=1)):
+            report("cache4_attention cut decode D=%d g=%d lens=%s news=%s %s" % (D, g, lens, news, hints))
+            run_attention(i + 400, batch, H, per, D, g, **hints)
 
 
 # (lens, new tokens, kv heads, query heads of each, page); every call is told of sequences
