@@ -376,7 +376,8 @@ dq_status dq_cache4_read(const dq_cache4* cache, const dq_cache4_batch* batch, v
  *                again when the call's work is done: calls that may run at the
  *                same time need one each
  * Codes are exact, dot products and the softmax's statistics fp32; each weight
- * times its value's scale is rounded once to 11 significant bits.  Where a call
+ * times its value's scale is rounded once to 11 significant bits (or, far below
+ * them, to 2^-38 of the largest value of the head that its row sees).  Where a call
  * has many new tokens (by max_q, max_len, count and the heads), keys and values are
  * rounded too: a scale to 11 bits, and its product with the code again.
  * Long work is cut into equal stretches over all sequences, and the parts of

@@ -13,8 +13,11 @@
 //     largest element in [2^14, 2^15): exact for every element above 2^-28 of
 //     it.  A group's partial dot products are scaled in fp32.
 //   * p * (value scale) is rounded once, to fp16, after multiplication by a
-//     power of two that puts the largest value scale seen so far in [2^14,
-//     2^15): relative error 2^-11 down to 2^-29 of the largest.
+//     power of two that puts the largest scale of the group seen so far in [2^14,
+//     2^15): relative error 2^-11 down to 2^-29 of the largest.  Groups whose codes
+//     are all 0 (their stored scale says nothing) do not count for that, nor do
+//     positions that a row does not see: where the causal mask crosses a step with
+//     larger scales, every row takes a power of two of its own (finish_step).
 // This form (cache4_attention_kernel) is for few new tokens: bound by the cache's
 // bytes, and below them by the vector work of expanding the codes.  One token over
 // 65000 (8 kv heads of 128, 32 query heads, g = 32; 83 MB of cache) 30 us, of which
@@ -108,18 +111,21 @@ __device__ __forceinline__ float row_sum(float v)
     row_pair(x + y, false, x, y);
     return x + y;
 }
-// max over the wave of values that are not negative, NaN counting as 0; the
-// same in every lane (row_ror 8, 4, 2, 1 within 16 lanes, then across them)
+// max within 16 lanes (row_ror 8, 4, 2, 1), and over the wave of values that are
+// not negative, NaN counting as 0; the same in every lane
 template <int kRor>
 __device__ __forceinline__ uint32_t ror_max(uint32_t u)
 {
     const uint32_t t = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0x120 + kRor, 0xf, 0xf, false);
     return max(u, t);
 }
+__device__ __forceinline__ uint32_t row16_max(uint32_t u)
+{
+    return ror_max<1>(ror_max<2>(ror_max<4>(ror_max<8>(u))));
+}
 __device__ __forceinline__ float wave_max_abs(float v)
 {
-    uint32_t u = v >= 0.0f ? __float_as_uint(v) : 0u;
-    u = ror_max<1>(ror_max<2>(ror_max<4>(ror_max<8>(u))));
+    uint32_t u = row16_max(v >= 0.0f ? __float_as_uint(v) : 0u);
     float x, y;
     row_pair(__uint_as_float(u), true, x, y);
     u = max(__float_as_uint(x), __float_as_uint(y));
@@ -162,6 +168,9 @@ struct AttnArgs {
     int32_t step_shift;  // log2 of a step's positions; 31: a unit is one step
 };
 
+// The scale that the quantizer stores for a group whose codes are all 0: fl32(1 / 7).
+constexpr uint32_t kZeroScale = 0x3e124925u;
+
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * kWave;
 constexpr int kStep = 32;                // positions per wave and step
@@ -186,11 +195,6 @@ struct Rows {
     __device__ __forceinline__ int64_t rows() const { return (int64_t)nq * per; }
     // positions seen by row r (a new token's head)
     __device__ __forceinline__ int seen(int64_t r) const { return len - nq + (int)udiv(r, per) + 1; }
-    // positions seen by the last row of the tile that starts at row r0
-    __device__ __forceinline__ int end(int64_t r0) const
-    {
-        return seen(r0 + 15 < rows() ? r0 + 15 : rows() - 1);
-    }
 };
 
 __device__ __forceinline__ Rows rows_of(const AttnArgs& a, int64_t b)
@@ -417,7 +421,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 3 : 2)) void ca
     constexpr int NL = (NG + 3) / 4;               // scale loads per 16 positions
     constexpr int SC = 4 * NL * 16;                // floats of 16 positions' scales in LDS
     __shared__ __attribute__((aligned(16))) float scales[kWaves][2][2 * SC];  // keys, values
-    __shared__ __attribute__((aligned(16))) float join[kWaves / 2][(NT * 4 + 3) * kWave];
+    __shared__ __attribute__((aligned(16))) float join[kWaves / 2][(NT * 4 + 2) * kWave];
 
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -459,7 +463,9 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 3 : 2)) void ca
         const int take = (int)(x1 - x < steps - step0 ? x1 - x : steps - step0);
         const bool whole = take == steps;
         const int slot = x == x0 ? 0 : 1;
-        const int kvh = (int)udiv(unit, tiles);
+        // (readfirstlane: known to be the same in all lanes, so that page numbers and
+        // buffer bases stay in scalar registers)
+        const int kvh = __builtin_amdgcn_readfirstlane((int)udiv(unit, tiles));
         const int64_t tile = unit - kvh * tiles;
         const int64_t r0 = tile * 16;
         const int64_t rows = rw.rows();
@@ -467,21 +473,34 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 3 : 2)) void ca
         const int64_t row = live ? r0 + r16 : 0;
         const int qi = (int)udiv(row, rw.per);
         const int head = kvh * rw.per + (int)(row - (int64_t)qi * rw.per);
-        const int seen = live ? rw.seen(row) : 0;  // positions that the row sees
-        const int end = rw.end(r0);
-        const int begin = step0 * kStride;
+        const int seen = live ? rw.len - rw.nq + qi + 1 : 0;  // positions that the row sees
+        // positions that every live row of the tile sees, and the last one
+        const int all_see = __builtin_amdgcn_readfirstlane(seen);
+        const int end = __builtin_amdgcn_readlane(seen, rows - r0 < 16 ? (int)(rows - r0) - 1 : 15);
+        const int begin = __builtin_amdgcn_readfirstlane(step0) * kStride;
         int stop = end;  // (a unit that is one step may have any length)
-        if (take < steps - step0 && begin + take * kStride < end) stop = begin + take * kStride;
+        if (take < steps - step0 && begin + take * kStride < end)
+            stop = begin + __builtin_amdgcn_readfirstlane(take) * kStride;
+        stop = __builtin_amdgcn_readfirstlane(stop);
         x += take;
         // constant address space: scalar loads, which leave the count of vector
         // loads in flight alone
         const __attribute__((address_space(4))) int32_t* table =
-            (const __attribute__((address_space(4))) int32_t*)(a.bt.table + b * a.bt.width);
+            (const __attribute__((address_space(4))) int32_t*)(
+                a.bt.table + __builtin_amdgcn_readfirstlane(b) * a.bt.width);
 
         f16x8_t qf[NC];
         float logit = 1.0f;
         float m = -INFINITY, l = 0.0f;
-        int ve = -112;  // exponent that the value scales are measured against
+        // The scales of a group are measured in units of 2^(ve - 14), and so is o; lane
+        // (r16, kg) has ve for the groups 4 i + kg, as vtop = 65504 2^(ve - 14), what fp16
+        // holds of them.  It is raised to the exponent of a scale that passes vtop, so
+        // scales that grow by less than two or four times leave it (and o) as it is.
+        constexpr uint32_t kTopBits = 0x7fe000u;  // mantissa of 65504
+        uint32_t vtop[NL];
+#pragma unroll
+        for (int i = 0; i < NL; ++i) vtop[i] = (16u << 23) + kTopBits;  // ve = -112
+        bool finished = false;  // o and l are what the wave hands on (finish_step)
         f32x4_t o[NT];
 #pragma unroll
         for (int j = 0; j < NT; ++j) o[j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
@@ -537,26 +556,139 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 3 : 2)) void ca
         };
         float* const lk = &scales[wave][0][0];
         float* const lv = &scales[wave][1][0];
-        auto step = [&](int t0) __attribute__((always_inline)) {
-            // value scales: none past the end, measured by a common power of two
-            float vtop = 0.0f;
+        // 2^(ve - 14) of group g
+        const auto group_unit = [&](int g) {
+            return pow2((int)(__builtin_amdgcn_readlane(vtop[g / 4], 16 * (g % 4)) >> 23) - 142);
+        };
+        // Scales of groups whose codes are all 0 become 0.  Lanes (c, kg) hold the codes of
+        // the tokens 4 kg + e of both tiles, a group's in some of their bits.
+        auto drop_zero_groups = [&]() __attribute__((always_inline)) {
+            uint32_t zero[NG == 8 ? 2 : 1] = {};  // bit e * NG + g (of the 8 tokens, two words where NG is 8)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    constexpr int n = G / 16;  // codes of the group in a lane
+                    const uint32_t mask = (n == 8 ? ~0u : (1u << (4 * (n & 7))) - 1u) << (4 * (g * n % 8));
+                    const uint64_t lanes = __ballot(((vw[e][g * n / 8] ^ 0x88888888u) & mask) == 0);
+                    if (((lanes >> (16 * kg)) & 0xffffu) == 0xffffu)
+                        zero[NG == 8 ? e / 4 : 0] |= 1u << ((e * NG + g) & 31);
+                }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t z = (uint32_t)__shfl((int)zero[NG == 8 ? h : 0], (r16 & 12) << 2, kWave);
+#pragma unroll
+                for (int i = 0; i < NL; ++i) {
+                    const int g = 4 * i + kg < NG ? 4 * i + kg : NG - 1;
+                    const bool none = (z >> (((4 * h + (r16 & 3)) * NG + g) & 31)) & 1;
+                    if (none && vsl[h][i] == vsl[h][i]) vsl[h][i] = 0.0f;  // (a NaN stays)
+                }
+            }
+        };
+        // The reference of each group follows the step's largest scales.
+        auto raise = [&](bool first) __attribute__((always_inline)) {
+            int down[NL];
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t u = __float_as_uint(vsl[h][i]) & 0x7fffffffu;
+                    if (u < 0x7f800000u) top = max(top, u);
+                }
+                const uint32_t was = vtop[i] >> 23;
+                top = row16_max(top);
+                const uint32_t now = top >= vtop[i] ? (top >> 23) + 1 : was;
+                vtop[i] = (now << 23) + kTopBits;
+                down[i] = (int)was - (int)now;
+            }
+            if (first) return;  // o is 0
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const float f = pow2(__builtin_amdgcn_readlane(down[g / 4], 16 * (g % 4)));
+#pragma unroll
+                for (int j = g * G / 16; j < (g + 1) * G / 16; ++j) o[j] *= f;
+            }
+        };
+        // The products of a step that the causal mask crosses (the wave's last of the unit,
+        // for the rows of a tile are at most 15 positions apart), with a power of two per row
+        // and group that puts the row's own largest weight * scale in [2^14, 2^15): p the
+        // weights (0 where hidden), the scales in LDS as they are.  Leaves o and l as the
+        // wave hands them on.
+        auto finish_step = [&](const float (&p)[8]) __attribute__((always_inline)) {
+            l = row_sum(l);
+            const float inv = l > 0.0f ? 1.0f / l : l;  // (0 and NaN stay)
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                __builtin_amdgcn_sched_barrier(0);  // a group at a time
+                float t[8];
+                float top = 0.0f;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const f32x4_t vs = *reinterpret_cast<const f32x4_t*>(lv + h * SC + g * 16 + 4 * kg);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        t[4 * h + e] = mul_legacy(p[4 * h + e], vs[e]);
+                        top = fmaxf(top, fabsf(t[4 * h + e]));
+                    }
+                }
+                const int up = 14 - max(exponent(row_max(top)), -112);
+                const float f = pow2(up), unit = group_unit(g), back = pow2(-up) * inv;
+                f16x8_t pf;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) pf[e] = (_Float16)(t[e] * f);
+#pragma unroll
+                for (int w = g * G / 32; w < (g + 1) * G / 32; ++w) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    const uint32_t sel = 0x0c000c00u | ((uint32_t)(4 + w % 4) << 16) | (uint32_t)(w % 4);
+                    uint32_t lo[4], hi[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t v = __builtin_amdgcn_perm(vw[2 * e + 1][w / 4], vw[2 * e][w / 4], sel);
+                        lo[e] = low_codes(v);
+                        hi[e] = high_codes(v);
+                    }
+                    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+                    const f32x4_t x = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                        __builtin_bit_cast(f16x8_t, (u32x4_t){lo[0], lo[1], lo[2], lo[3]}), pf, zero, 0, 0, 0);
+                    const f32x4_t y = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                        __builtin_bit_cast(f16x8_t, (u32x4_t){hi[0], hi[1], hi[2], hi[3]}), pf, zero, 0, 0, 0);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        o[2 * w][e] = fmaf(x[e], back, o[2 * w][e] * inv * unit);
+                        o[2 * w + 1][e] = fmaf(y[e], back, o[2 * w + 1][e] * inv * unit);
+                    }
+                }
+            }
+        };
+        auto step = [&](auto Finish, int t0) __attribute__((always_inline)) {
+            constexpr bool kFinish = decltype(Finish)::value;
+            // value scales: none past the end, those of a group measured by a common power of two
+            bool larger = false;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int i = 0; i < NL; ++i) {
                     if (t0 + 16 * h + r16 >= end) vsl[h][i] = 0.0f;
-                    vtop = fmaxf(vtop, vsl[h][i]);
+                    larger |= !(fabsf(vsl[h][i]) < __uint_as_float(vtop[i]));
                 }
-            const int vx = exponent(__uint_as_float(
-                __builtin_amdgcn_readfirstlane(__float_as_uint(wave_max_abs(vtop)))));
-            const int vn = vx > ve ? vx : ve;
-            const float vfac = pow2(14 - vn);
+            if (kFinish || __builtin_expect(__any(larger), 0)) {
+                bool unsure = false;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < NL; ++i) unsure |= __float_as_uint(vsl[h][i]) == kZeroScale;
+                if (__builtin_expect(__any(unsure), 0)) drop_zero_groups();
+                if (!kFinish) raise(t0 == begin + wave * kStep);
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int i = 0; i < NL; ++i) {
+                    // times 2^(14 - ve), or as they are
+                    const float f = kFinish ? 1.0f : __uint_as_float((269u << 23) + kTopBits - vtop[i]);
                     lk[h * SC + i * 64 + lane] = __uint_as_float(__float_as_uint(ksl[h][i]) | bad[h]);
-                    lv[h * SC + i * 64 + lane] = vsl[h][i] * vfac;
+                    lv[h * SC + i * 64 + lane] = vsl[h][i] * f;
                 }
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");  // other lanes read them
             __builtin_amdgcn_wave_barrier();
@@ -595,7 +727,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 3 : 2)) void ca
 #pragma unroll
                 for (int g = 0; g < NG; ++g)
                     vs[h][g] = *reinterpret_cast<const f32x4_t*>(lv + h * SC + g * 16 + 4 * kg);
-            load_k(t0 + kStride);
+            if (!kFinish) load_k(t0 + kStride);
             __builtin_amdgcn_sched_barrier(0);
             // running maximum (of logits) and sum
             float mx = s[0];
@@ -605,9 +737,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 3 : 2)) void ca
             const float mn = fmaxf(m, mx * logit);
             const float base = mn == -INFINITY ? 0.0f : mn;
             const float alpha = __builtin_amdgcn_exp2f(m - base);
-            const float oscale = alpha * pow2(ve - vn);
             m = mn;
-            ve = vn;
             float p[8];
             float sum = 0.0f;
 #pragma unroll
@@ -618,9 +748,13 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 3 : 2)) void ca
             l = fmaf(l, alpha, sum);
 #pragma unroll
             for (int e = 0; e < 8; ++e) pin(p[e]);
-            if (__any(oscale != 1.0f)) {
+            if (__any(alpha != 1.0f)) {
 #pragma unroll
-                for (int j = 0; j < NT; ++j) o[j] *= oscale;
+                for (int j = 0; j < NT; ++j) o[j] *= alpha;
+            }
+            if constexpr (kFinish) {
+                finish_step(p);
+                return;
             }
             f16x8_t pf[NG];
 #pragma unroll
@@ -711,9 +845,27 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 3 : 2)) void ca
             }
         }
         if (t0 < stop) {
-            for (; t0 < stop; t0 += kStride) step(t0);
+            for (; min(t0 + kStep, stop) <= all_see && t0 < stop; t0 += kStride) step(std::false_type{}, t0);
+            if (t0 < stop) {
+                step(std::true_type{}, t0);
+                finished = true;
+            }
         }
 
+        int lane_e = (int)threadIdx.x & (kWave - 1);
+        pin(lane_e);  // what follows from it is worked out here, not kept over the steps
+        const int lane = lane_e, r16 = lane & 15, kg = lane >> 4;
+        // the wave's own result: sum p v / sum p, its maximum and its sum of weights
+        if (!finished) {
+            l = row_sum(l);
+            const float inv = l > 0.0f ? 1.0f / l : l;  // (0 and NaN stay)
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const float unit = group_unit(g);
+#pragma unroll
+                for (int j = g * G / 16; j < (g + 1) * G / 16; ++j) o[j] = o[j] * inv * unit;
+            }
+        }
         // join the waves: the upper half into the lower, and so on (the join buffers
         // are free again after the last barrier)
         auto put = [&](float* dst) {
@@ -721,26 +873,23 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 3 : 2)) void ca
             for (int j = 0; j < NT; ++j) *reinterpret_cast<f32x4_t*>(dst + (j * kWave + lane) * 4) = o[j];
             dst[NT * 4 * kWave + lane] = m;
             dst[(NT * 4 + 1) * kWave + lane] = l;
-            dst[(NT * 4 + 2) * kWave + lane] = __int_as_float(ve);
         };
         auto add = [&](const float* src) {
             const float m2 = src[NT * 4 * kWave + lane];
             const float l2 = src[(NT * 4 + 1) * kWave + lane];
-            const int v2 = __float_as_int(src[(NT * 4 + 2) * kWave + lane]);
             const float mn = fmaxf(m, m2);
             const float base = mn == -INFINITY ? 0.0f : mn;
-            const int vn = ve > v2 ? ve : v2;
-            const float w1 = __builtin_amdgcn_exp2f(m - base), w2 = __builtin_amdgcn_exp2f(m2 - base);
-            const float f1 = w1 * pow2(ve - vn), f2 = w2 * pow2(v2 - vn);
+            const float w1 = l * __builtin_amdgcn_exp2f(m - base), w2 = l2 * __builtin_amdgcn_exp2f(m2 - base);
+            l = w1 + w2;
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const float f1 = w1 * inv, f2 = w2 * inv;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 const f32x4_t x = *reinterpret_cast<const f32x4_t*>(src + (j * kWave + lane) * 4);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[j][e] = fmaf(x[e], f2, o[j][e] * f1);
             }
-            l = fmaf(l2, w2, l * w1);
             m = mn;
-            ve = vn;
         };
 #pragma unroll
         for (int n = kWaves / 2; n > 0; n >>= 1) {
@@ -750,22 +899,25 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 3 : 2)) void ca
             __syncthreads();
         }
         if (wave == 0) {
-            l = row_sum(l);
-            float inv = l > 0.0f ? pow2(ve - 14) / l : (l == 0.0f ? 0.0f : l);  // NaN stays
-            if (rw.bad) inv = __uint_as_float(0x7fc00000u);
+            if (rw.bad) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[j][e] = __uint_as_float(0x7fc00000u);
+            }
             if (whole) {
                 if (live) {
                     uint16_t* op = a.out + ((int64_t)(rw.first + qi) * a.q_heads + head) * D + 4 * kg;
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
                         *reinterpret_cast<uint2*>(op + 16 * j) =
-                            make_uint2(bf16x2(o[j][0] * inv, o[j][1] * inv), bf16x2(o[j][2] * inv, o[j][3] * inv));
+                            make_uint2(bf16x2(o[j][0], o[j][1]), bf16x2(o[j][2], o[j][3]));
                 }
             } else if (live) {
                 const int64_t at = ((int64_t)group * 2 + slot) * 16 + r16;
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
-                    *reinterpret_cast<f32x4_t*>(a.part + at * D + 16 * j + 4 * kg) = o[j] * inv;
+                    *reinterpret_cast<f32x4_t*>(a.part + at * D + 16 * j + 4 * kg) = o[j];
                 if (kg == 0) a.part_ml[at] = make_float2(m, l);
             }
         }
