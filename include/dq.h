@@ -361,7 +361,9 @@ dq_status dq_cache4_read(const dq_cache4* cache, const dq_cache4_batch* batch, v
 /* Causal attention of the call's tokens over the cache (append them first):
  *   out[t,h] = sum_p w_p v[p] / sum_p w_p,  w_p = exp(scale * q[t,h] . k[p] - max),
  * over the positions p up to t's own, k and v the dequantized vectors of kv
- * head h / (q_heads / kv_heads).  A token that sees no position gives zeros.
+ * head h / (q_heads / kv_heads).  A token that sees no position gives zeros; one that
+ * sees a key group with a NaN scale gives NaN, and a value group with one makes
+ * its dimensions NaN, however small its weight.
  *   q       in   device, [tokens, q_heads, D] bf16 bits, 16-byte aligned; tokens lie
  *                q_stride elements apart (a multiple of 8, at least q_heads * D)
  *   q_heads      a multiple of kv_heads, at most DQ_CACHE4_MAX_HEADS

@@ -56,14 +56,6 @@ __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t b
     return r;
 }
 
-// a * b, and 0 where either is 0 (a NaN or infinity beside it included)
-__device__ __forceinline__ float mul_legacy(float a, float b)
-{
-    float r;
-    asm("v_mul_legacy_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
-    return r;
-}
-
 // The codes in bits 0..3 and 16..19 of v as fp16 (u - 8), exact.
 __device__ __forceinline__ uint32_t low_codes(uint32_t v)
 {
@@ -581,7 +573,33 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 3 : 2)) void ca
                 for (int i = 0; i < NL; ++i) {
                     const int g = 4 * i + kg < NG ? 4 * i + kg : NG - 1;
                     const bool none = (z >> (((4 * h + (r16 & 3)) * NG + g) & 31)) & 1;
-                    if (none && vsl[h][i] == vsl[h][i]) vsl[h][i] = 0.0f;  // (a NaN stays)
+                    if (none) vsl[h][i] = 0.0f;
+                }
+            }
+        };
+        // A value scale that is not finite: NaN in its dimensions, in the rows that see it
+        // (whatever their weight), and 0 from here on.
+        auto mark_nan = [&](int t0) __attribute__((always_inline)) {
+            uint64_t lanes[2][NL];  // of a tile: bits 16 n + position, n + 4 i the group
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < NL; ++i) {
+                    const bool nan = !(fabsf(vsl[h][i]) < INFINITY);
+                    lanes[h][i] = __ballot(nan);
+                    if (nan) vsl[h][i] = 0.0f;
+                }
+            const int see = seen - t0;
+            const uint32_t mine = see >= 32 ? ~0u : (see <= 0 ? 0u : (1u << see) - 1u);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const uint32_t at = (uint32_t)(lanes[0][g / 4] >> (16 * (g % 4)) & 0xffffu) |
+                                    (uint32_t)(lanes[1][g / 4] >> (16 * (g % 4)) & 0xffffu) << 16;
+                if ((at & mine) != 0) {
+#pragma unroll
+                    for (int j = g * G / 16; j < (g + 1) * G / 16; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[j][e] = __uint_as_float(0x7fc00000u);
                 }
             }
         };
@@ -592,17 +610,14 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 3 : 2)) void ca
             for (int i = 0; i < NL; ++i) {
                 uint32_t top = 0;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t u = __float_as_uint(vsl[h][i]) & 0x7fffffffu;
-                    if (u < 0x7f800000u) top = max(top, u);
-                }
+                for (int h = 0; h < 2; ++h) top = max(top, __float_as_uint(vsl[h][i]) & 0x7fffffffu);
                 const uint32_t was = vtop[i] >> 23;
                 top = row16_max(top);
                 const uint32_t now = top >= vtop[i] ? (top >> 23) + 1 : was;
                 vtop[i] = (now << 23) + kTopBits;
                 down[i] = (int)was - (int)now;
             }
-            if (first) return;  // o is 0
+            if (first) return;  // o is 0 (or NaN)
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 const float f = pow2(__builtin_amdgcn_readlane(down[g / 4], 16 * (g % 4)));
@@ -628,7 +643,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 3 : 2)) void ca
                     const f32x4_t vs = *reinterpret_cast<const f32x4_t*>(lv + h * SC + g * 16 + 4 * kg);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        t[4 * h + e] = mul_legacy(p[4 * h + e], vs[e]);
+                        t[4 * h + e] = p[4 * h + e] * vs[e];
                         top = fmaxf(top, fabsf(t[4 * h + e]));
                     }
                 }
@@ -673,11 +688,15 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 3 : 2)) void ca
                     larger |= !(fabsf(vsl[h][i]) < __uint_as_float(vtop[i]));
                 }
             if (kFinish || __builtin_expect(__any(larger), 0)) {
-                bool unsure = false;
+                bool unsure = false, nan = false;
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int i = 0; i < NL; ++i) unsure |= __float_as_uint(vsl[h][i]) == kZeroScale;
+                    for (int i = 0; i < NL; ++i) {
+                        unsure |= __float_as_uint(vsl[h][i]) == kZeroScale;
+                        nan |= !(fabsf(vsl[h][i]) < INFINITY);
+                    }
+                if (__builtin_expect(__any(nan), 0)) mark_nan(t0);
                 if (__builtin_expect(__any(unsure), 0)) drop_zero_groups();
                 if (!kFinish) raise(t0 == begin + wave * kStep);
             }
@@ -762,11 +781,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 3 : 2)) void ca
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        // a weight of 0 takes nothing, of a NaN scale either: that
-                        // touches only the rows that see it
-                        pf[g][4 * h + e] = (_Float16)mul_legacy(p[4 * h + e], vs[h][g][e]);
-                    }
+                    for (int e = 0; e < 4; ++e) pf[g][4 * h + e] = (_Float16)(p[4 * h + e] * vs[h][g][e]);
                 }
             }
             // page numbers after the step's last LDS read: a wait for one waits for both
