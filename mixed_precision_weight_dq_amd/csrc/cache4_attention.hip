@@ -182,7 +182,8 @@ constexpr int kMaxLen = 0x7fff0000;
 // What a workgroup knows of its sequence.  Token rows and positions are below 2^31.
 struct Rows {
     int first, nq, len;  // first token row, new tokens, cached tokens
-    bool bad;            // a length past the table
+    int held;            // of them inside the table; rows that see more are NaN
+    bool bad;            // longer than kMaxLen
     int per;             // query heads of a kv head
     __device__ __forceinline__ int64_t rows() const { return (int64_t)nq * per; }
     // positions seen by row r (a new token's head)
@@ -197,8 +198,10 @@ __device__ __forceinline__ Rows rows_of(const AttnArgs& a, int64_t b)
     r.first = (int)first;
     r.nq = (int)nq;
     r.len = a.bt.lens[b];
-    r.bad = r.len > a.bt.width << a.c.page_shift || r.len > kMaxLen;
+    r.bad = r.len > kMaxLen;
     if (r.len < 0 || r.bad) r.len = 0;
+    const int64_t table = a.bt.width << a.c.page_shift;
+    r.held = r.len < table ? r.len : (int)table;
     r.per = a.q_heads / a.c.heads;
     return r;
 }
@@ -231,7 +234,7 @@ struct Line {
 
 __device__ __forceinline__ int steps_of(const AttnArgs& a, const Rows& rw)
 {
-    return rw.len > 0 ? ((rw.len - 1) >> a.step_shift) + 1 : 1;
+    return rw.held > 0 ? ((rw.held - 1) >> a.step_shift) + 1 : 1;
 }
 template <class C>
 __device__ __forceinline__ int64_t tiles_of(const Rows& rw)
@@ -285,6 +288,7 @@ __device__ __forceinline__ Line lay_line_short(const AttnArgs& a, int64_t w, int
     ln.rw.first = __builtin_amdgcn_readlane(mine.first, from);
     ln.rw.nq = __builtin_amdgcn_readlane(mine.nq, from);
     ln.rw.len = __builtin_amdgcn_readlane(mine.len, from);
+    ln.rw.held = __builtin_amdgcn_readlane(mine.held, from);
     ln.rw.bad = __builtin_amdgcn_readlane((int)mine.bad, from) != 0;
     ln.rw.per = mine.per;
     return ln;
@@ -466,9 +470,10 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 3 : 2)) void ca
         const int qi = (int)udiv(row, rw.per);
         const int head = kvh * rw.per + (int)(row - (int64_t)qi * rw.per);
         const int seen = live ? rw.len - rw.nq + qi + 1 : 0;  // positions that the row sees
-        // positions that every live row of the tile sees, and the last one
+        // positions that every live row of the tile sees, and the last one (in the table)
         const int all_see = __builtin_amdgcn_readfirstlane(seen);
-        const int end = __builtin_amdgcn_readlane(seen, rows - r0 < 16 ? (int)(rows - r0) - 1 : 15);
+        const int end = min(__builtin_amdgcn_readlane(seen, rows - r0 < 16 ? (int)(rows - r0) - 1 : 15),
+                            __builtin_amdgcn_readfirstlane(rw.held));
         const int begin = __builtin_amdgcn_readfirstlane(step0) * kStride;
         int stop = end;  // (a unit that is one step may have any length)
         if (take < steps - step0 && begin + take * kStride < end)
@@ -914,7 +919,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 3 : 2)) void ca
             __syncthreads();
         }
         if (wave == 0) {
-            if (rw.bad) {
+            if (rw.bad || seen > rw.held) {
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -1228,8 +1233,8 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
         const int head = kvh * rw.per + (int)(row - (int64_t)qi * rw.per);
         const int seen = live ? rw.seen(row) : 0;
         const auto seen_at = [&](int64_t r) { return __builtin_amdgcn_readfirstlane(rw.seen(r < rows ? r : rows - 1)); };
-        const int end = seen_at(r0 + Tl::kRows - 1);                 // of the workgroup's rows
-        const int wave_end = w0 < rows ? seen_at(w0 + 31) : 0;       // of the wave's
+        const int end = min(seen_at(r0 + Tl::kRows - 1), rw.held);   // of the workgroup's rows
+        const int wave_end = w0 < rows ? min(seen_at(w0 + 31), rw.held) : 0;  // of the wave's
         const int begin = step0 * kPos;
         const int stop = end < begin + take * kPos ? end : begin + take * kPos;
         const int all_see = w0 < rows ? seen_at(w0) : 0;             // by every live row of it
@@ -1577,7 +1582,7 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
         row_pair(l, true, l0, l1);
         l = l0 + l1;
         float inv = l > 0.0f ? pow2(ve - 10) / l : (l == 0.0f ? 0.0f : l);  // NaN stays
-        if (rw.bad) inv = __uint_as_float(0x7fc00000u);
+        if (rw.bad || seen > rw.held) inv = __uint_as_float(0x7fc00000u);
         if (live && take < steps) {
             const int64_t at = ((int64_t)group * 2 + slot) * Tl::kRows + wave * 32 + r32;
             float* pp = a.part + at * D + 4 * h;
