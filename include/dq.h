@@ -381,7 +381,10 @@ dq_status dq_cache4_read(const dq_cache4* cache, const dq_cache4_batch* batch, v
  * times its value's scale is rounded once to 11 significant bits (or, far below
  * them, to 2^-38 of the largest value of the head that its row sees).  Where a call
  * has many new tokens (by max_q, max_len, count and the heads), keys and values are
- * rounded too: a scale to 11 bits, and its product with the code again.
+ * rounded too: a scale to 11 bits, and its product with the code again (or, far below
+ * them, to 2^-22 of the largest value that the row sees; key scales below 2^-20 of
+ * the largest of 32 neighbouring positions have fewer bits).  A call with max_q *
+ * q_heads / kv_heads below 64 keeps the codes exact, whatever its sequences are.
  * Long work is cut into equal stretches over all sequences, and the parts of
  * a row are added in a fixed order: a call repeated gives the same bits, a sequence
  * beside others of other lengths may differ in the last ones. */

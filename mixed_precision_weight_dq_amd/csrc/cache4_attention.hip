@@ -1100,6 +1100,10 @@ __global__ __launch_bounds__(kThreads) void cache4_join_edges_kernel(AttnArgs a)
 // alternative, exact codes and a scale per group after the product, is 128 more
 // vector operations per 64 positions, a third of the step.  A value scale that is
 // NaN is taken as 0 and marked: its dimensions become NaN in the rows that see it.
+// The common power of two counts no group whose codes are all 0.  Where the causal
+// mask crosses the 32 and their scales lie far apart, each position takes a power of
+// two of its own instead, and a wave whose rows see less than its exponents stand
+// for scales its weights row by row and adds the products in fp32.
 //
 // LDS: 16-byte pieces.  Keys: word w of position t is piece w of row t; values,
 // transposed: the 8 positions that a lane's operand holds are a piece of
@@ -1113,6 +1117,7 @@ __global__ __launch_bounds__(kThreads) void cache4_join_edges_kernel(AttnArgs a)
 // instructions 1.5; two waves per SIMD, which the registers of 32 rows by 128
 // dimensions allow, overlap little of it.  Tiles of 128 rows (half as many codes shared) were slower, 294 against 254 us
 // before the stretches; whole units (200 for 256 CUs, 32 to 47 steps) 268 us.
+constexpr int kValueShift = 24;  // keeps a weight (up to 2^14) times a value's power of two in fp32
 template <int kPieces>
 __device__ __forceinline__ int swizzle(int row)
 {
@@ -1161,7 +1166,8 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
     __shared__ __attribute__((aligned(16))) uint4 Kt[2][kPos * (D / 8)];
     __shared__ __attribute__((aligned(16))) uint4 Vt[2][D * (kPos / 8)];
     __shared__ __attribute__((aligned(16))) _Float16 sc[NW][32 * NG];
-    __shared__ int kexp[2][TT], vexp[2][TT];
+    __shared__ int kexp[2][TT], vexp[2][TT];  // twice the exponent; odd: one per position
+    __shared__ __attribute__((aligned(16))) float kpow[2][TT][32], vpow[2][TT][32];
     __shared__ uint32_t vnan[2][TT][NG];
 
     const int lane = threadIdx.x & (kWave - 1);
@@ -1238,6 +1244,7 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
         const int begin = step0 * kPos;
         const int stop = end < begin + take * kPos ? end : begin + take * kPos;
         const int all_see = w0 < rows ? seen_at(w0) : 0;             // by every live row of it
+        const int tile_see = seen_at(r0);                            // and of the workgroup
 
         // q rows: operand kk = 2 i + p holds dimensions 32 i + 8 (2 p + h) + (0 4 1 5 2 6 3 7)
         f16x8_t qf[2 * NC];
@@ -1279,6 +1286,7 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
             }
         }
 
+        int vrun = -1000;  // the largest exponent of the values that this wave expanded
         // ---- a step's words: wave w < TT has the keys of 32 positions, w >= TT values
         const bool keys = wave < TT;
         const int part = keys ? wave : wave - TT;  // which 32 positions of the step
@@ -1330,6 +1338,43 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
                 sl[i] = sp[(int64_t)g << shift];
             }
         };
+        // Scales of groups whose codes are all 0 become 0 (a NaN stays NaN).
+        auto drop_zero_groups = [&](int lane) __attribute__((always_inline)) {
+            const int t = lane & 15, gpar = (lane >> 4) & 1;
+            uint32_t zero[2] = {0, 0};
+            if (keys) {
+                // two lanes have the words of a position, which say whether a group has others
+                uint32_t some = 0;
+#pragma unroll
+                for (int k = 0; k < KW; ++k)
+                    if (raw[k] != 0x88888888u) some |= 1u << (k % NC * 32 / G);
+                some |= (uint32_t)__shfl_xor((int)some, 1, kWave);
+                zero[0] = ~(uint32_t)__shfl((int)some, (lane & 32) + 2 * t, kWave);
+            } else {
+                // 16 lanes have those of 8 positions; bit e * NG + g, two words where NG is 8
+                uint32_t none[2] = {0, 0};
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        constexpr int n = G / 16;  // codes of the group in a lane
+                        const uint32_t mask = (n == 8 ? ~0u : (1u << (4 * (n & 7))) - 1u) << (4 * (g * n % 8));
+                        const uint64_t lanes = __ballot(((raw[e * VW + g * n / 8] ^ 0x88888888u) & mask) == 0);
+                        if (((lanes >> (lane & 48)) & 0xffffu) == 0xffffu)
+                            none[NG == 8 ? e / 4 : 0] |= 1u << ((e * NG + g) & 31);
+                    }
+                const int from = (lane & 32) + 4 * (t & 4);
+                zero[0] = (uint32_t)__shfl((int)none[0], from, kWave);
+                zero[1] = NG == 8 ? (uint32_t)__shfl((int)none[1], from, kWave) : 0u;
+                if (NG == 8 && t >= 8) zero[0] = zero[1];
+                zero[0] >>= ((t & 3) + (NG == 8 ? 0 : t >> 3 << 2)) * NG & 31;
+            }
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                const int g = 2 * i + gpar < NG ? 2 * i + gpar : NG - 1;
+                if ((zero[0] >> g & 1) && sl[i] == sl[i]) sl[i] = 0.0f;
+            }
+        };
         // the loaded words -> fp16 pieces of buffer nb
         auto expand = [&](int pos0, int nb) __attribute__((always_inline)) {
             int lane = (int)threadIdx.x & (kWave - 1);
@@ -1337,25 +1382,61 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
             const int h = lane >> 5;
             const bool past = pos0 + 32 * part + 16 * h + (lane & 15) >= end;
             const int gpar = (lane >> 4) & 1;
-            float top = 0.0f;
             uint64_t nan_at[NS];
+            bool unsure = false;
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
                 if (past) sl[i] = 0.0f;
                 nan_at[i] = 0;
                 if (!keys) {
-                    const bool nan = sl[i] != sl[i];
+                    const bool nan = !(fabsf(sl[i]) < INFINITY);
                     nan_at[i] = __ballot(nan);
                     if (nan) sl[i] = 0.0f;
                 }
-                top = fmaxf(top, sl[i]);
+                unsure |= __float_as_uint(sl[i]) == kZeroScale;
             }
-            int ex = exponent(__uint_as_float(
-                __builtin_amdgcn_readfirstlane(__float_as_uint(wave_max_abs(top)))));
-            if (ex < -104) ex = -104;
+            // the exponent of the largest scale of the 32 positions
+            const auto top_exponent = [&]() __attribute__((always_inline)) {
+                float top = 0.0f;
+#pragma unroll
+                for (int i = 0; i < NS; ++i) top = fmaxf(top, fabsf(sl[i]));
+                const int ex = exponent(__uint_as_float(
+                    __builtin_amdgcn_readfirstlane(__float_as_uint(wave_max_abs(top)))));
+                return ex < -104 ? -104 : ex;
+            };
+            int ex = top_exponent();
+            // Groups whose codes are all 0 must not raise it, nor positions that some row
+            // does not see those of the rows that do not: where the causal mask crosses the
+            // 32 and scales lie far apart, each position has an exponent of its own.
+            const bool crossed = pos0 + 32 * part + 32 > tile_see;
+            bool apart = false;
+            if (__builtin_expect(crossed || (keys ? __any(unsure) != 0 : ex > vrun), 0)) {
+                if (__any(unsure)) {
+                    drop_zero_groups(lane);
+                    ex = top_exponent();
+                }
+                uint32_t low = 0;  // of the smallest scale but 0, turned round
+#pragma unroll
+                for (int i = 0; i < NS; ++i)
+                    if (sl[i] != 0.0f) low = max(low, 0x7f800000u - (__float_as_uint(fabsf(sl[i])) & 0x7f800000u));
+                low = __float_as_uint(wave_max_abs(__uint_as_float(low)));
+                const int least = 128 - (int)(__builtin_amdgcn_readfirstlane(low) >> 23);
+                apart = ex - least > (keys ? 20 : 8) && (keys || crossed);
+                if (!crossed && ex > vrun) vrun = ex;
+            }
             // values: in steps of 8, so that the running exponent seldom moves
             if (!keys) ex |= 7;
-            const float fac = pow2(10 - ex);
+            int own = ex;
+            if (__builtin_expect(apart, 0)) {
+                float top = 0.0f;
+#pragma unroll
+                for (int i = 0; i < NS; ++i) top = fmaxf(top, fabsf(sl[i]));
+                top = fmaxf(top, __shfl_xor(top, 16, kWave));
+                if (top > 0.0f) own = max(exponent(top), -104);
+                float* const table = keys ? kpow[nb][part] : vpow[nb][part];
+                table[16 * h + (lane & 15)] = pow2(own - (keys ? 10 : kValueShift));
+            }
+            const float fac = pow2(10 - own);
             _Float16* const s16 = sc[wave];
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
@@ -1374,9 +1455,9 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
             }
             if (lane == 0) {
                 if (keys) {
-                    kexp[nb][part] = ex;
+                    kexp[nb][part] = 2 * ex + (apart ? 1 : 0);
                 } else {
-                    vexp[nb][part] = ex;
+                    vexp[nb][part] = 2 * ex + (apart ? 1 : 0);
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
                         // lanes 32 s + 16 (g & 1) + t: position 16 s + t
@@ -1432,7 +1513,7 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
         };
 
         float m = -INFINITY, l = 0.0f;
-        int ve = -97;  // exponent of the values in o
+        int ve = -97;  // exponent of the row's values in o
         f32x16_t o[NT];
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -1463,8 +1544,18 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
                 for (int k = 0; k < 2 * NC; ++k)
                     s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
                         lds_piece(ka[k] + 32 * (2 * hp + t) * (2 * D)), qf[k], s[t], 0, 0, 0);
+                const int kx = __builtin_amdgcn_readfirstlane(kexp[cb][2 * hp + t]);
                 // (not 0, which a hidden position's -inf would make NaN)
-                f[t] = fmaxf(logit * pow2(kexp[cb][2 * hp + t] - 10), 0x1p-126f);
+                f[t] = fmaxf(logit * pow2((kx >> 1) - 10), 0x1p-126f);
+                if (__builtin_expect(kx & 1, 0)) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f32x4_t w = *reinterpret_cast<const f32x4_t*>(&kpow[cb][2 * hp + t][8 * q + 4 * h]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[t][4 * q + e] *= logit * w[e];
+                    }
+                    f[t] = 1.0f;
+                }
             }
             if (pos + 64 > all_see) {
                 const int left = seen - pos - 4 * h;
@@ -1486,9 +1577,13 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
             const float top = fmaxf(x0, x1);
             // the reference only moves by more than 2^8 (weights stay below it), and
             // the values' exponent with the largest seen
-            const int v0 = vexp[cb][2 * hp], v1 = vexp[cb][2 * hp + 1];
-            const int vn = max(ve, max(v0, v1));
-            if (__any(top > m + 8.0f) || vn != ve) {
+            const int x0v = __builtin_amdgcn_readfirstlane(vexp[cb][2 * hp]);
+            const int x1v = __builtin_amdgcn_readfirstlane(vexp[cb][2 * hp + 1]);
+            const int v0 = x0v >> 1, v1 = x1v >> 1;
+            // a row may see less than the tiles' exponents stand for: a scale for each row
+            const bool alone = ((x0v | x1v) & 1) != 0 || (pos + 64 > all_see && __any(max(v0, v1) > ve));
+            const int vn = alone ? ve : max(ve, max(v0, v1));
+            if (__any(top > m + 8.0f || vn != ve)) {
                 const float mn = top > m + 8.0f ? top : m;
                 const float alpha = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
                 const float os = alpha * pow2(ve - vn);
@@ -1505,8 +1600,6 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
             f16x8_t p[2][2];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const int de = (t ? v1 : v0) - ve;
-                const float down = pow2(de);
                 float sum = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
@@ -1514,21 +1607,72 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
                     sum += s[t][e];
                 }
                 l += sum;
-                if (de != 0) {  // values of another exponent
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) s[t][e] *= down;
-                }
-#pragma unroll
-                for (int e = 0; e < 16; ++e) p[t][e >> 3][e & 7] = (_Float16)s[t][e];
             }
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
+            if (__builtin_expect(alone, 0)) {
+                // The weights times a power of two of each position's values, and of each row
+                // that puts the largest of it in [2^14, 2^15); the products are added to o
+                // in fp32, in units that follow what the row sees.
+                float top2 = 0.0f;
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                            lds_piece(va[2 * (2 * hp + t) + k] + 32 * j * (2 * kPos)), p[t][k], o[j], 0, 0, 0);
+                    for (int q = 0; q < 4; ++q) {
+                        const float all = pow2((t ? v1 : v0) - kValueShift);
+                        f32x4_t w = {all, all, all, all};
+                        if ((t ? x1v : x0v) & 1)
+                            w = *reinterpret_cast<const f32x4_t*>(&vpow[cb][2 * hp + t][8 * q + 4 * h]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            s[t][4 * q + e] *= w[e];
+                            top2 = fmaxf(top2, s[t][4 * q + e]);
+                        }
+                    }
+                float y0, y1;
+                row_pair(top2, true, y0, y1);
+                const int tx = max(exponent(fmaxf(y0, y1)), -112);
+                const int vm = max(ve, tx + kValueShift - 14);
+                const float os = pow2(ve - vm), up = pow2(14 - tx), back = pow2(tx - 14 + kValueShift - vm);
+                ve = vm;
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) p[t][e >> 3][e & 7] = (_Float16)(s[t][e] * up);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    f32x16_t x;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[e] = 0.0f;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            x = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                                lds_piece(va[2 * (2 * hp + t) + k] + 32 * j * (2 * kPos)), p[t][k], x, 0, 0, 0);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[j][e] = fmaf(x[e], back, o[j][e] * os);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            } else {
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const int de = (t ? v1 : v0) - ve;
+                    if (__any(de != 0)) {  // values of another exponent
+                        const float down = pow2(de);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) s[t][e] *= down;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) p[t][e >> 3][e & 7] = (_Float16)s[t][e];
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                                lds_piece(va[2 * (2 * hp + t) + k] + 32 * j * (2 * kPos)), p[t][k], o[j], 0, 0, 0);
+                }
             }
             // a NaN value scale: NaN in its dimensions, in the rows that see it
 #pragma unroll
@@ -1578,6 +1722,9 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
             }
         }
 
+        int lane_e = (int)threadIdx.x & (kWave - 1);
+        pin(lane_e);  // what follows from it is worked out here, not kept over the steps
+        const int r32 = lane_e & 31, h = lane_e >> 5;
         float l0, l1;
         row_pair(l, true, l0, l1);
         l = l0 + l1;

@@ -6,7 +6,7 @@ import numpy as np
 
 import mixed_precision_weight_dq_amd as dq
 from gpu_util import bf16_gpu, torch
-from serving_ref import Batch, attention_ref, attention_tolerance, bf16, widen
+from serving_ref import Batch, attention_tolerance, bf16, widen
 
 GEOMETRY = [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128), (256, 32), (256, 64), (256, 128)]
 FACTORS = [1e-5, 1e-9, 1e-13, 1e-25]
@@ -29,22 +29,36 @@ def with_zeros(x, n, g):
     return x.reshape(-1, *x.shape[2:])
 
 
-def visible_max(kv, batch, q_heads):
-    """[tokens, q_heads, 1]: the largest |v| of the positions and the kv head that a row sees."""
-    out = np.zeros((batch.tokens, q_heads, 1))
+def reference(q, kv, batch, q_heads, scale):
+    """serving_ref.attention_ref's (out, W, delta), a sequence's head at a time, and the largest |v| of
+    the positions and the kv head that a row sees, [tokens, q_heads, 1]."""
+    T, _, D = q.shape
+    out, W = np.zeros((T, q_heads, D)), np.zeros((T, q_heads, D))
+    delta, top = np.zeros((T, q_heads)), np.zeros((T, q_heads, 1))
     for b, new in enumerate(batch.news):
-        v = kv[b][1]
-        top = np.maximum.accumulate(np.abs(v).max(axis=-1), axis=0)  # [len, H]
-        per = q_heads // v.shape[1]
-        for i in range(new):
-            seen = int(batch.lens[b]) - new + i + 1
-            if seen > 0:
-                out[batch.starts[b] + i, :, 0] = np.repeat(top[seen - 1], per)
-    return out
+        k, v = kv[b]
+        n, first = int(batch.lens[b]), int(batch.starts[b])
+        seen = n - new + 1 + np.arange(new)
+        rows = np.flatnonzero(seen > 0)
+        if not rows.size:
+            continue
+        at, seen = first + rows, seen[rows]
+        hidden = np.arange(n)[None] >= seen[:, None]
+        largest = np.maximum.accumulate(np.abs(v).max(axis=-1), axis=0)
+        for h in range(q_heads):
+            kk, vv = k[:, h // (q_heads // k.shape[1])], v[:, h // (q_heads // k.shape[1])]
+            s = np.where(hidden, -np.inf, scale * (q[at, h] @ kk.T))
+            p = np.exp(s - s.max(axis=1, keepdims=True))
+            p /= p.sum(axis=1, keepdims=True)
+            out[at, h], W[at, h] = p @ vv, p @ np.abs(vv)
+            delta[at, h] = abs(scale) * np.where(hidden, 0, np.abs(q[at, h]) @ np.abs(kk).T).max(axis=1)
+            top[at, h, 0] = largest[seen - 1, h // (q_heads // k.shape[1])]
+    return out, W, delta, top
 
 
-def range_tolerance(kv, batch, ref, W, delta, D, prompt):
-    """attention_tolerance with the largest value that each row sees in place of the whole cache's.
+def range_tolerance(ref, W, delta, top, D, n, prompt):
+    """serving_ref.attention_tolerance with the largest value that each row sees (top) in place of the
+    whole cache's.
 
     A weight (times its value's scale) below fp16's normal range is off by half of its smallest
     step, 2^-25.  Few new tokens: that is 2^-25 of 2^14 of the largest scale seen, times |code| <= 8
@@ -52,9 +66,7 @@ def range_tolerance(kv, batch, ref, W, delta, D, prompt):
     reference is at least 2^6, a value in fp16 at most 2^14, and the largest value seen at least 7 *
     2^3, the exponents being multiples of 8: 2^-25 2^14 / (2^6 7 2^3) < 2^-22, which is 2^9 times the
     n 2^-38 (1 + 2^7) that attention_tolerance has for them."""
-    v = visible_max(kv, batch, ref.shape[1])
-    n = int(batch.lens.max())
-    return attention_tolerance(ref, W, delta, D, n, v * 2.0 ** 9 if prompt else v, prompt)
+    return attention_tolerance(ref, W, delta, D, n, top * 2.0 ** 9 if prompt else top, prompt)
 
 
 def check(batch, H, per, D, g, k, v, prompt, scale=None, q_mul=1.0, seed=3, hints=None):
@@ -74,9 +86,9 @@ def check(batch, H, per, D, g, k, v, prompt, scale=None, q_mul=1.0, seed=3, hint
     out = dq.cache4_attention(cache, bf16_gpu(qb), starts, lens, table, scale=scale, **hints)
     t.cuda.synchronize()
     got = out.double().cpu().numpy()
-    ref, W, delta = attention_ref(widen(qb).astype(np.float64), kv, batch, H * per,
-                                  D ** -0.5 if scale is None else scale)
-    tol = range_tolerance(kv, batch, ref, W, delta, D, prompt)
+    ref, W, delta, top = reference(widen(qb).astype(np.float64), kv, batch, H * per,
+                                   D ** -0.5 if scale is None else scale)
+    tol = range_tolerance(ref, W, delta, top, D, int(batch.lens.max()), prompt)
     bad = ~(np.abs(got - ref) <= tol)
     if bad.any():
         at = tuple(np.argwhere(bad)[0])
