@@ -992,17 +992,21 @@ __global__ __launch_bounds__(kThreads) void cache4_join_kernel(AttnArgs a)
 #pragma unroll
             for (int i = 0; i < 8; ++i) m8 = fmaxf(m8, ml[i].x);
             const float base = m8 == -INFINITY ? 0.0f : m8;
-            const float old = __builtin_amdgcn_exp2f(mx - base);
-            tot *= old;
-            acc *= old;
+            const float old = tot * __builtin_amdgcn_exp2f(mx - base);
+            tot = old;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 // nothing seen: no weight (and a NaN sum keeps its)
-                const float w = ml[i].y == 0.0f ? 0.0f : ml[i].y * __builtin_amdgcn_exp2f(ml[i].x - base);
-                tot += w;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[e] = fmaf(w, v[i][e], acc[e]);
+                ml[i].y = ml[i].y == 0.0f ? 0.0f : ml[i].y * __builtin_amdgcn_exp2f(ml[i].x - base);
+                tot += ml[i].y;
             }
+            // a weighted mean all along: sums of weights * values could pass fp32
+            const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
+            acc *= old * inv;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[e] = fmaf(ml[i].y * inv, v[i][e], acc[e]);
             mx = m8;
         }
         sums[tid] = acc;
@@ -1013,22 +1017,26 @@ __global__ __launch_bounds__(kThreads) void cache4_join_kernel(AttnArgs a)
 #pragma unroll
             for (int i = 0; i < kPar; ++i) top = fmaxf(top, ml_of[i].x);
             const float base = top == -INFINITY ? 0.0f : top;
+            float w[kPar];
             tot = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kPar; ++i) {
+                w[i] = ml_of[i].y * __builtin_amdgcn_exp2f(ml_of[i].x - base);
+                tot += w[i];
+            }
+            const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
             acc = (f32x4_t){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < kPar; ++i) {
-                const float w = __builtin_amdgcn_exp2f(ml_of[i].x - base);
-                tot = fmaf(ml_of[i].y, w, tot);
                 const f32x4_t v = sums[i * kPer + tid];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[e] = fmaf(v[e], w, acc[e]);
+                for (int e = 0; e < 4; ++e) acc[e] = fmaf(v[e], w[i] * inv, acc[e]);
             }
-            const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
             const int qi = (int)udiv(row, rw.per);
             const int head = kvh * rw.per + (int)(row - (int64_t)qi * rw.per);
             uint16_t* op = a.out + ((int64_t)(rw.first + qi) * a.q_heads + head) * D + 4 * d4;
             *reinterpret_cast<uint2*>(op) =
-                make_uint2(bf16x2(acc[0] * inv, acc[1] * inv), bf16x2(acc[2] * inv, acc[3] * inv));
+                make_uint2(bf16x2(acc[0], acc[1]), bf16x2(acc[2], acc[3]));
         }
         __syncthreads();
     }
@@ -1061,14 +1069,18 @@ __global__ __launch_bounds__(kThreads) void cache4_join_edges_kernel(AttnArgs a)
     float mx = -INFINITY;
     for (int64_t s = 0; s < n; ++s) mx = fmaxf(mx, a.part_ml[slot_of(s)].x);
     const float base = mx == -INFINITY ? 0.0f : mx;
+    const auto weight = [&](int64_t s) {
+        const float2 ml = a.part_ml[slot_of(s)];
+        return ml.y == 0.0f ? 0.0f : ml.y * __builtin_amdgcn_exp2f(ml.x - base);
+    };
     float tot = 0.0f;
+    for (int64_t s = 0; s < n; ++s) tot += weight(s);
+    const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
     float acc[N];
 #pragma unroll
     for (int e = 0; e < N; ++e) acc[e] = 0.0f;
     for (int64_t s = 0; s < n; ++s) {
-        const float2 ml = a.part_ml[slot_of(s)];
-        const float ws = ml.y == 0.0f ? 0.0f : ml.y * __builtin_amdgcn_exp2f(ml.x - base);
-        tot += ws;
+        const float ws = weight(s) * inv;  // (sums of weights * values could pass fp32)
 #pragma unroll
         for (int i = 0; i < N; i += 4) {
             const f32x4_t v = *reinterpret_cast<const f32x4_t*>(a.part + slot_of(s) * D + d + i);
@@ -1076,14 +1088,12 @@ __global__ __launch_bounds__(kThreads) void cache4_join_edges_kernel(AttnArgs a)
             for (int e = 0; e < 4; ++e) acc[i + e] = fmaf(ws, v[e], acc[i + e]);
         }
     }
-    const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
     const int qi = (int)udiv(row, rw.per);
     const int head = kvh * rw.per + (int)(row - (int64_t)qi * rw.per);
     uint16_t* op = a.out + ((int64_t)(rw.first + qi) * a.q_heads + head) * D + d;
 #pragma unroll
     for (int i = 0; i < N; i += 4)
-        *reinterpret_cast<uint2*>(op + i) = make_uint2(bf16x2(acc[i] * inv, acc[i + 1] * inv),
-                                                       bf16x2(acc[i + 2] * inv, acc[i + 3] * inv));
+        *reinterpret_cast<uint2*>(op + i) = make_uint2(bf16x2(acc[i], acc[i + 1]), bf16x2(acc[i + 2], acc[i + 3]));
 }
 
 // ---------------------------------------------------------------------------

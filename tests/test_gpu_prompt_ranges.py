@@ -33,12 +33,22 @@ def test_prompt_later_token_far_larger(D, g):
     n, H, per, count = 160, 4, 2, 13
     batch = prompt_batch(4, n)
     at = np.arange(count) * 12 + 3
-    for up in (2.0 ** 20, 2.0 ** 50, 2.0 ** 90):
+    for up in (2.0 ** 20, 2.0 ** 50, 2.0 ** 90, 2.0 ** 120):
         k, v = vectors(7, count * n, H, D), vectors(8, count * n, H, D)
         v[np.arange(count) * n + at] *= np.float32(up)
         for hints in (None, dict(max_q=n, max_len=200000)):
             report("prompts D=%d g=%d one token x %g %s" % (D, g, up, hints))
             check(batch, H, per, D, g, k, v, True, hints=hints)
+
+
+@pytest.mark.parametrize("D,g", GEOMETRY)
+def test_prompt_largest_values(D, g):
+    """Values up to 2^124, whole and in parts that are joined."""
+    n, H, per, count = 150, 4, 2, 13
+    k, v = vectors(16, count * n, H, D), vectors(17, count * n, H, D) * np.float32(2.0 ** 121)
+    for hints in (None, dict(max_q=n, max_len=200000)):
+        report("prompts D=%d g=%d values of 2^121 %s" % (D, g, hints))
+        check(prompt_batch(8, n), H, per, D, g, k, v, True, hints=hints)
 
 
 @pytest.mark.parametrize("D,g", [(64, 32), (128, 32), (128, 64), (256, 64)])

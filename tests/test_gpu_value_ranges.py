@@ -32,12 +32,26 @@ def test_draft_later_token_far_larger(D, g):
     H, per = 2, 2
     for n in (5, 20, 150, 133):
         batch = Batch(2, [n, 40], [5, 1], 16)
-        for up in (2.0 ** 20, 2.0 ** 45, 2.0 ** 90):
+        for up in (2.0 ** 20, 2.0 ** 45, 2.0 ** 90, 2.0 ** 120):
             k, v = vectors(3, n + 40, H, D), vectors(4, n + 40, H, D)
             v[n - 1] *= np.float32(up)
             v[n - 2] *= np.float32(up ** 0.5)
             report("draft D=%d g=%d n=%d last x %g" % (D, g, n, up))
             check(batch, H, per, D, g, k, v, False)
+
+
+@pytest.mark.parametrize("D,g", GEOMETRY)
+def test_decode_largest_values(D, g):
+    """Values up to 2^124, whole and in parts that are joined."""
+    H, per = 2, 4
+    batch = Batch(3, [1500, 40], [1, 3], 16)
+    many = Batch(4, [90] * 70, [1] * 70, 16)
+    for hints in (None, dict(max_q=3, max_len=200000)):
+        report("decode D=%d g=%d values of 2^121 %s" % (D, g, hints))
+        for b in (batch, many):
+            n = int(b.lens.sum())
+            v = np.abs(vectors(17, n, H, D)) * np.float32(2.0 ** 121)
+            check(b, H, per, D, g, vectors(16, n, H, D), v, False, scale=2.0 ** -9, hints=hints)
 
 
 def test_few_rows_keep_exact_codes():
