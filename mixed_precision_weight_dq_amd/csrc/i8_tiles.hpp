@@ -59,11 +59,22 @@ __device__ __forceinline__ int32_t code_shift(const int32_t* __restrict__ zeros,
     return (zeros ? zeros[n] : (1 << (B - 1))) - (B == 8 ? 128 : 0);
 }
 
-// acc - shift * sum is exact (unsigned arithmetic wraps; the result fits).
-__device__ __forceinline__ float finish_i8(int32_t acc, int32_t shift, int32_t sum, float sx, float sw)
+// A token's scale as two factors: the sum (below 2^31) times the scale itself would
+// pass fp32 from 2^97 on, where the weights' scale may bring the product back.
+struct TokenScale {
+    float s, up;
+};
+__device__ __forceinline__ TokenScale token_scale(float sx)
+{
+    return sx >= 0x1p96f ? TokenScale{sx * 0x1p-32f, 0x1p32f} : TokenScale{sx, 1.0f};
+}
+
+// acc - shift * sum is exact (unsigned arithmetic wraps; the result fits), so is
+// the last factor.
+__device__ __forceinline__ float finish_i8(int32_t acc, int32_t shift, int32_t sum, TokenScale sx, float sw)
 {
     const int32_t d = (int32_t)((uint32_t)acc - (uint32_t)shift * (uint32_t)sum);
-    return ((float)d * sx) * sw;
+    return ((float)d * sx.s) * sw * sx.up;
 }
 
 __device__ __forceinline__ uint16_t bf16_round(float v)

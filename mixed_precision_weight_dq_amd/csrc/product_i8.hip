@@ -152,7 +152,7 @@ __global__ __launch_bounds__(W * kWave, W == 8 ? 2 : (R >= 7 || T == 4 ? 1 : (R 
         const int64_t m = m0 + 16 * (tl % T) + (l & 15);
         const int64_t n = n0 + 16 * (tl / T) + 4 * (l >> 4) + (o & 3);
         if (m < a.M && n < a.N) {
-            const float v = finish_i8(sum, code_shift<B>(a.zeros, n), a.x_sums[m], a.x_scales[m], a.scales[n]);
+            const float v = finish_i8(sum, code_shift<B>(a.zeros, n), a.x_sums[m], token_scale(a.x_scales[m]), a.scales[n]);
             if (a.bf16)
                 store_y<true>(a.y, m * a.N + n, v);
             else
@@ -412,10 +412,13 @@ __global__ __launch_bounds__(256 * WM, kOcc) void many_i8_kernel(I8Args a)
     // serve for the tokens' scales and sums
     join_waves<0>();
     float* const sx = reinterpret_cast<float*>(As0);
-    int32_t* const ssum = reinterpret_cast<int32_t*>(sx + Tl::BM);
+    float* const sup = sx + Tl::BM;
+    int32_t* const ssum = reinterpret_cast<int32_t*>(sup + Tl::BM);
     if (tid < Tl::BM) {
         const int64_t m = m0 + tid < a.M ? m0 + tid : a.M - 1;
-        sx[tid] = a.x_scales[m];
+        const TokenScale ts = token_scale(a.x_scales[m]);
+        sx[tid] = ts.s;
+        sup[tid] = ts.up;
         ssum[tid] = a.x_sums[m];
     }
     __syncthreads();
@@ -438,8 +441,9 @@ __global__ __launch_bounds__(256 * WM, kOcc) void many_i8_kernel(I8Args a)
             for (int q = 0; q < 4; ++q) {
                 const int row = (wm * MT + i) * 32 + 8 * q + 4 * h;
                 const float4 s4 = *reinterpret_cast<const float4*>(sx + row);
+                const float4 u4 = *reinterpret_cast<const float4*>(sup + row);
                 const int4 t4 = *reinterpret_cast<const int4*>(ssum + row);
-                const float s[4] = {s4.x, s4.y, s4.z, s4.w};
+                const TokenScale s[4] = {{s4.x, u4.x}, {s4.y, u4.y}, {s4.z, u4.z}, {s4.w, u4.w}};
                 const int32_t t[4] = {t4.x, t4.y, t4.z, t4.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
