@@ -16,6 +16,7 @@
 #include "gemm_tiles.hpp"
 #include "i8_tiles.hpp"
 #include "launch_serving.hpp"
+#include "product_plan.hpp"
 
 namespace dq {
 
@@ -40,7 +41,7 @@ struct I8Args {
 // Few tokens: bound by the packed weights.  A workgroup of W = 4 waves has 16 R
 // weight rows, all tokens (M <= 64: 16 T, the last ones again past M) and all of
 // K: wave w takes the steps w, w + W, ... of 256 codes, and the waves' sums are
-// added through LDS.  (W = 8 with 16 T of more tokens: few tiles, see launch_b.)
+// added through LDS.  (W = 8 with 16 T of more tokens: few tiles, see product_plan.hpp.)
 // v_mfma_i32_16x16x64_i8 with the weights as its rows: lane (r, g) holds, of
 // weight row r, the chunks 2 g and 2 g + 1 of the step, 2 B consecutive words, so
 // codes go from memory to registers to the matrix cores, a row's 256 codes with
@@ -167,17 +168,6 @@ hipError_t launch_few(const I8Args& a, hipStream_t stream)
     few_i8_kernel<B, R, T, W>
         <<<dim3((unsigned)ceil_div(a.N, 16 * R), (unsigned)ceil_div(a.M, 16 * T)), W * kWave, 0, stream>>>(a);
     return hipGetLastError();
-}
-
-// The most rows per workgroup that leave 224 workgroups or more for the 256 CUs.
-template <int B, int T>
-hipError_t launch_few_rows(const I8Args& a, hipStream_t stream)
-{
-    constexpr int64_t kFill = 224;
-    if (a.N >= 16 * 7 * kFill) return launch_few<B, 7, T>(a, stream);
-    if (a.N >= 16 * 4 * kFill) return launch_few<B, 4, T>(a, stream);
-    if (a.N >= 16 * 2 * kFill) return launch_few<B, 2, T>(a, stream);
-    return launch_few<B, 1, T>(a, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -480,34 +470,26 @@ hipError_t launch_many(const I8Args& a, hipStream_t stream)
 template <int B>
 hipError_t launch_b(const I8Args& a, hipStream_t stream)
 {
-    // Too few tiles for the CUs: 32 weight rows by 32 or 64 tokens per workgroup, whose
-    // eight waves split K, in one round of workgroups.  100 x 2000 x 4096 at b = 4 / 7:
-    // 32 tokens 9.2 / 11.4 us, 64 tokens 13.2 / 15.4, 64 x 128 tiles 14.6 / 22.7; 200 x
-    // 1500 x 4096: 15.4 / 20.8, 13.6 / 15.7, 14.9 / 22.9; 128 x 6000 x 4096 (more than
-    // a round): 21.8 / 29.9, 25.2 / 29.9, 14.8 / 22.8
-    if (a.M > 32) {
-        if (ceil_div(a.N, 32) * ceil_div(a.M, 32) <= 256) return launch_few<B, 2, 2, 8>(a, stream);
-        if (ceil_div(a.N, 32) * ceil_div(a.M, 64) <= 256) return launch_few<B, 2, 4, 8>(a, stream);
+    switch (i8_kernel(a.M, a.N)) {
+    case I8Kernel::few_1_1: return launch_few<B, 1, 1>(a, stream);
+    case I8Kernel::few_2_1: return launch_few<B, 2, 1>(a, stream);
+    case I8Kernel::few_4_1: return launch_few<B, 4, 1>(a, stream);
+    case I8Kernel::few_7_1: return launch_few<B, 7, 1>(a, stream);
+    case I8Kernel::few_1_2: return launch_few<B, 1, 2>(a, stream);
+    case I8Kernel::few_2_2: return launch_few<B, 2, 2>(a, stream);
+    case I8Kernel::few_4_2: return launch_few<B, 4, 2>(a, stream);
+    case I8Kernel::few_7_2: return launch_few<B, 7, 2>(a, stream);
+    case I8Kernel::few_2_4: return launch_few<B, 2, 4>(a, stream);
+    case I8Kernel::few_4_4: return launch_few<B, 4, 4>(a, stream);
+    case I8Kernel::few_7_4: return launch_few<B, 7, 4>(a, stream);
+    case I8Kernel::split_2: return launch_few<B, 2, 2, 8>(a, stream);
+    case I8Kernel::split_4: return launch_few<B, 2, 4, 8>(a, stream);
+    case I8Kernel::tiles_256x256: return launch_many<B, 4, 2, 2, 2>(a, stream);
+    case I8Kernel::tiles_128x128: return launch_many<B, 4, 1, 1, B <= 5 ? 3 : 2>(a, stream);
+    case I8Kernel::tiles_64x128_deep: return launch_many<B, 2, 1, 1, 1, 4>(a, stream);
+    case I8Kernel::tiles_64x128: return launch_many<B, 2, 1, 1, 3>(a, stream);
+    default: return hipErrorInvalidValue;
     }
-    if (a.M <= 64) {
-        if (a.M <= 16) return launch_few_rows<B, 1>(a, stream);
-        if (a.M <= 32) return launch_few_rows<B, 2>(a, stream);
-        return launch_few_rows<B, 4>(a, stream);
-    }
-    // 256 x 256 tiles, eight waves, when they fill the 256 CUs in whole rounds (at
-    // least 80 % of the last round busy): 2048 x 8192 x 8192 at b = 8 122 us (2.25 POP/s)
-    // against 139 us for 128 x 128 tiles of four waves, two or three to a CU
-    const int64_t wide = ceil_div(a.M, 256) * ceil_div(a.N, 256);
-    if (a.M >= 256 && wide >= 256 && wide * 5 >= ceil_div(wide, 256) * 256 * 4)
-        return launch_many<B, 4, 2, 2, 2>(a, stream);
-    // 128 x 128 tiles: 333 x 17408 x 5120 at b = 5 51 us (64 x 128 67 us, 192 x 128 59 us,
-    // 128 x 256 55 us, 256 x 256 82 us); half as high while they leave CUs without one
-    if (ceil_div(a.M, 128) * ceil_div(a.N, 128) >= 256) return launch_many<B, 4, 1, 1, B <= 5 ? 3 : 2>(a, stream);
-    // and with four stages while a CU has one workgroup at most, whose copies nothing
-    // else hides: 300 x 3000 x 8192 at b = 4 / 7 / 8 23.2 / 39.7 / 24.6 us, two stages
-    // 28.2 / 44.9 / 37.8 (the same within 2 % where the caches hold the operands)
-    if (ceil_div(a.M, 64) * ceil_div(a.N, 128) <= 256) return launch_many<B, 2, 1, 1, 1, 4>(a, stream);
-    return launch_many<B, 2, 1, 1, 3>(a, stream);
 }
 
 }  // namespace
