@@ -35,3 +35,10 @@ def test_every_kernel_has_its_sizes(chosen):
     sides += [14400, 25100, 2 ** 31 - 1]
     count, kinds = chosen([(m, n) for m in sides for n in sides])
     assert set(kinds) == set(range(count))
+
+
+def test_gpu_cases_reach_every_kernel(chosen):
+    """The sizes that tests/test_gpu_product_kernels.py runs."""
+    from test_gpu_product_kernels import CASES
+    count, kinds = chosen([(m, n) for m, n, _ in CASES])
+    assert set(kinds) == set(range(count))
