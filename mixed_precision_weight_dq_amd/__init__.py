@@ -858,7 +858,9 @@ def gemm_i8(codes, x_scales, x_sums, packed, scales, K: int, bits: int, zeros=No
 class Cache4:
     """A paged key/value cache in 4 bits: k_codes, v_codes int32 [pages, kv_heads, P, D / 8]
     and k_scales, v_scales float32 [pages, kv_heads, D / g, P], contiguous GPU tensors that
-    the caller owns (``Cache4.empty`` allocates them).  The sequences of a call are given by
+    the caller owns (``Cache4.empty`` allocates them).  Its attributes cannot be set: other
+    tensors, a larger cache for instance, make another ``Cache4``, and a call on one whose
+    tensors were moved in place is refused.  The sequences of a call are given by
     ``starts`` int32 [count + 1] (token rows of each sequence), ``lens`` int32 [count] (cached
     tokens, the call's own included) and ``table`` int32 [count, width] (pages)."""
 
@@ -875,12 +877,25 @@ class Cache4:
                 or tuple(k_scales.shape) != (pages, heads, groups, P)
                 or groups < 1 or words * 8 % groups):
             raise ValueError("codes must be [pages, kv_heads, P, D / 8], scales [pages, kv_heads, D / g, P]")
-        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
-        self.pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, P, words * 8
-        self.group = words * 8 // groups
-        self.device_index = dev
-        self._c = DQCache4(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
-                           v_scales.data_ptr(), pages, heads, self.head_dim, P, self.group)
+        at = tuple(t.data_ptr() for t in (k_codes, v_codes, k_scales, v_scales))
+        D, g = words * 8, words * 8 // groups
+        self.__dict__.update(
+            k_codes=k_codes, v_codes=v_codes, k_scales=k_scales, v_scales=v_scales, pages=pages,
+            kv_heads=heads, page_size=P, head_dim=D, group=g, device_index=dev, _at=at,
+            _c=DQCache4(*at, pages, heads, D, P, g))
+
+    def __setattr__(self, name, value):
+        raise AttributeError("a Cache4's attributes are fixed: make another one (%s)" % name)
+
+    def __delattr__(self, name):
+        self.__setattr__(name, None)
+
+    def _struct(self):
+        """The C struct, if the tensors still lie where it says."""
+        if (self.k_codes.data_ptr(), self.v_codes.data_ptr(), self.k_scales.data_ptr(),
+                self.v_scales.data_ptr()) != self._at:
+            raise ValueError("the cache's tensors were moved: make another Cache4 of them")
+        return self._c
 
     @classmethod
     def empty(cls, pages: int, kv_heads: int, head_dim: int, page_size: int = 64, group: int = 32,
@@ -934,7 +949,7 @@ def cache4_append(cache: Cache4, k, v, starts, lens, table) -> None:
     if v.dtype != k.dtype or v.shape[0] != k.shape[0]:
         raise ValueError("k and v must have one dtype and one token count")
     batch = _batch4(starts, lens, table, dev)
-    _launch("dq_cache4_append", dev, load().dq_cache4_append, cache._c, batch, k.data_ptr(),
+    _launch("dq_cache4_append", dev, load().dq_cache4_append, cache._struct(), batch, k.data_ptr(),
             v.data_ptr(), kind, k.shape[0], ks, vs)
 
 
@@ -956,7 +971,7 @@ def cache4_read(cache: Cache4, tokens: int, starts, lens, table, dtype=None, k=N
                 raise ValueError("%s must be [tokens, kv_heads, D]" % name)
         out.append(t)
     batch = _batch4(starts, lens, table, dev)
-    _launch("dq_cache4_read", dev, load().dq_cache4_read, cache._c, batch, out[0].data_ptr(),
+    _launch("dq_cache4_read", dev, load().dq_cache4_read, cache._struct(), batch, out[0].data_ptr(),
             out[1].data_ptr(), code, tokens)
     return tuple(out)
 
@@ -989,14 +1004,15 @@ def cache4_attention(cache: Cache4, q, starts, lens, table, scale=None, max_q=No
     if scale is None:
         scale = D ** -0.5
     lib = load()
-    need = lib.dq_cache4_attention_workspace(cache._c, batch.count, tokens, heads, max_q, max_len)
+    c = cache._struct()
+    need = lib.dq_cache4_attention_workspace(c, batch.count, tokens, heads, max_q, max_len)
     if workspace is None:
         if need:
             workspace = q.new_empty((need,), dtype=torch.uint8)
     else:
         _fast_need(workspace, "workspace", torch.uint8, 1, dev)
         need = workspace.shape[0]
-    _launch("dq_cache4_attention", dev, lib.dq_cache4_attention, cache._c, batch, q.data_ptr(), tokens,
+    _launch("dq_cache4_attention", dev, lib.dq_cache4_attention, c, batch, q.data_ptr(), tokens,
             stride, heads, scale, max_q, max_len, out.data_ptr(),
             workspace.data_ptr() if workspace is not None else None, need)
     return out
