@@ -1442,7 +1442,7 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
 #pragma unroll
                 for (int i = 0; i < NS; ++i) top = fmaxf(top, fabsf(sl[i]));
                 top = fmaxf(top, __shfl_xor(top, 16, kWave));
-                if (top > 0.0f) own = max(exponent(top), -104);
+                own = max(exponent(top), -104);  // (a position without codes: the least)
                 float* const table = keys ? kpow[nb][part] : vpow[nb][part];
                 table[16 * h + (lane & 15)] = pow2(own - (keys ? 10 : kValueShift));
             }

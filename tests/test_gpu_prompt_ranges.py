@@ -51,6 +51,22 @@ def test_prompt_largest_values(D, g):
         check(prompt_batch(8, n), H, per, D, g, k, v, True, hints=hints)
 
 
+@pytest.mark.parametrize("D,g", GEOMETRY)
+def test_prompt_magnitudes_and_zeros(D, g):
+    """Every token's values of another magnitude, up to 2^60 either way, with zero groups and whole
+    zero tokens among them."""
+    n, H, per, count = 140, 4, 3, 13
+    rng = np.random.default_rng(D + g)
+    k, v = vectors(18, count * n, H, D), vectors(19, count * n, H, D)
+    v *= np.exp2(rng.integers(-60, 61, (count * n, 1, 1))).astype(np.float32)
+    zero = rng.random((count * n, H, D // g)) < 0.3
+    zero[::7] = True
+    v[np.repeat(zero, g, axis=2)] = 0
+    for hints in (None, dict(max_q=n, max_len=200000)):
+        report("prompts D=%d g=%d magnitudes and zeros %s" % (D, g, hints))
+        check(prompt_batch(9, n), H, per, D, g, k, v, True, hints=hints)
+
+
 @pytest.mark.parametrize("D,g", [(64, 32), (128, 32), (128, 64), (256, 64)])
 def test_prompt_groups_far_apart(D, g):
     """The groups of a head 2^18 apart, and each token's magnitude another: the bound is the head's."""

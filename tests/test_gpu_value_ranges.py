@@ -41,6 +41,24 @@ def test_draft_later_token_far_larger(D, g):
 
 
 @pytest.mark.parametrize("D,g", GEOMETRY)
+def test_draft_magnitudes_and_zeros(D, g):
+    """Every token's values of another magnitude, up to 2^60 either way, with zero groups and whole
+    zero tokens among them."""
+    H, per = 2, 3
+    rng = np.random.default_rng(D + g)
+    for batch in (Batch(5, [700, 40, 9], [6, 2, 9], 16), Batch(6, [60] * 70, [2] * 70, 32)):
+        n = int(batch.lens.sum())
+        k, v = vectors(18, n, H, D), vectors(19, n, H, D)
+        v *= np.exp2(rng.integers(-60, 61, (n, 1, 1))).astype(np.float32)
+        zero = rng.random((n, H, D // g)) < 0.3
+        zero[::7] = True
+        v[np.repeat(zero, g, axis=2)] = 0
+        for hints in (None, dict(max_q=9, max_len=200000)):
+            report("drafts D=%d g=%d magnitudes and zeros %s" % (D, g, hints))
+            check(batch, H, per, D, g, k, v, False, hints=hints)
+
+
+@pytest.mark.parametrize("D,g", GEOMETRY)
 def test_decode_largest_values(D, g):
     """Values up to 2^124, whole and in parts that are joined."""
     H, per = 2, 4
