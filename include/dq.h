@@ -377,12 +377,13 @@ dq_status dq_cache4_read(const dq_cache4* cache, const dq_cache4_batch* batch, v
  *                same arguments (may be NULL where that is 0); the caller's, free
  *                again when the call's work is done: calls that may run at the
  *                same time need one each
- * Codes are exact, dot products and the softmax's statistics fp32; each weight
+ * Codes are exact, dot products (of q in fp16 after a power of two: an element below
+ * 2^-28 of its row's largest has fewer bits) and the softmax's statistics fp32; each weight
  * times its value's scale is rounded once to 11 significant bits (or, far below
  * them, to 2^-38 of the largest value of the head that its row sees).  Where a call
  * has many new tokens (by max_q, max_len, count and the heads), keys and values are
  * rounded too: a scale to 11 bits, and its product with the code again (or, far below
- * them, to 2^-22 of the largest value that the row sees; key scales below 2^-20 of
+ * them, to 2^-22 of the largest value that the row sees; key scales below 2^-24 of
  * the largest of 32 neighbouring positions have fewer bits).  A call with max_q *
  * q_heads / kv_heads below 64 keeps the codes exact, whatever its sequences are.
  * Long work is cut into equal stretches over all sequences, and the parts of

@@ -15,6 +15,8 @@
 // reverse) 10.0 us, 3.2 TB/s; 32 tokens 4.8 and 3.5 us.  (A workgroup per two tokens, all
 // heads: 15.8 and 11.6 us, for a page's lines are then written two tokens at a
 // time; 32 tokens 4.1 and 3.7.)  About half of the append's time is vector work.
+// The read of heads of 256 picks a word by a lane's bit, for which the compiler keeps
+// the words in 16 KB of LDS; not measured against a select.
 #include "cache4.hpp"
 #include "common.hpp"
 #include "launch_serving.hpp"

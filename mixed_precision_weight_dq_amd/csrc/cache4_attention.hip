@@ -20,9 +20,9 @@
 //     larger scales, every row takes a power of two of its own (finish_step).
 // This form (cache4_attention_kernel) is for few new tokens: bound by the cache's
 // bytes, and below them by the vector work of expanding the codes.  One token over
-// 65000 (8 kv heads of 128, 32 query heads, g = 32; 83 MB of cache) 30 us, of which
+// 65000 (8 kv heads of 128, 32 query heads, g = 32; 83 MB of cache) 29 us, of which
 // 15 are launch, first bytes and the join; 40 sequences of 3250 to 6000 (8 kv, 40
-// query heads; 240 MB) 62 us, 3.9 TB/s; 8 x 5 tokens over up to 1100 13 us.  Waves
+// query heads; 240 MB) 60 us, 4.0 TB/s; 8 x 5 tokens over up to 1100 13 us.  Waves
 // of one workgroup take neighbouring steps and join through LDS; workgroups take
 // equal stretches of all sequences' steps (below) and join through the workspace: one
 // workgroup per sequence, head and 16 rows left the first case's long axis to 8 of
@@ -1121,12 +1121,16 @@ __global__ __launch_bounds__(kThreads) void cache4_join_edges_kernel(AttnArgs a)
 // rows of a pass over the banks (of rows of 8 pieces, two share all banks).
 //
 // 1000 new tokens over 6000 and 569 over 4083 (8 kv heads of 128, 32 query heads,
-// g = 32) 228 us: 126 GFLOP, 0.55 PFLOP/s.  The join is 14 us of it.  A step of 128
-// positions takes 6.5 us, about the sum of what its parts take alone (counted
+// g = 32) 215 us: 126 GFLOP, 0.59 PFLOP/s.  The join is 14 us of it.  A step of 128
+// positions takes 6.2 us, about the sum of what its parts take alone (counted
 // instructions): vector work 2.4 (softmax, expansion), LDS reads 2.2, matrix
 // instructions 1.5; two waves per SIMD, which the registers of 32 rows by 128
-// dimensions allow, overlap little of it.  Tiles of 128 rows (half as many codes shared) were slower, 294 against 254 us
-// before the stretches; whole units (200 for 256 CUs, 32 to 47 steps) 268 us.
+// dimensions allow, overlap little of it.  The registers do not suffice either: heads
+// of 128 spill 71 to 110 of them (260 bytes of scratch a lane at g = 32), nearly all
+// outside the steps; a dozen scratch accesses are in the loop.  Tiles of 128 rows
+// (half as many codes shared) were slower, 294 against 254 us before the stretches;
+// whole units (200 for 256 CUs, 32 to 47 steps) 268 us.
+
 constexpr int kValueShift = 24;  // keeps a weight (up to 2^14) times a value's power of two in fp32
 template <int kPieces>
 __device__ __forceinline__ int swizzle(int row)
@@ -1773,16 +1777,20 @@ __global__ __launch_bounds__(64 * NW, (PromptTile<D, G, NW>::kOcc)) void cache4_
 // 32 of 600 12.9 / 19.8.  Beyond 4096 one long sequence would outlast all others.
 // Many: cache4_prompt_kernel from kPromptUnits units (sequence, kv head, tile of
 // rows) on, or kPromptRows rows per kv head and kPromptSteps steps for each of its
-// workgroups.  It splits units into stretches where whole ones would
-// leave CUs idle, and where the steps that the causal mask takes from a stretch are
-// few (len >= kSplitLen new).  Measured with 32 query and 8 kv heads of 128, one
-// sequence's new tokens over its length:
+// workgroups.  It splits units into stretches below kSplitUnits units for each
+// workgroup, if the steps that the causal mask takes from a stretch are
+// few (len >= kSplitLen new).  Both limits are rough: a stretch counts a unit's steps
+// as if its rows saw the whole sequence, so first prompts stay whole though few
+// units leave CUs idle (1 x 1000 over 1000, 128 units, 54 us; 1 x 2000 over 2000 99
+// us), and the last but one line below has 1128 units and takes the slower form.
+// Measured with 32 query and 8 kv heads of 128, one sequence's new tokens over its
+// length:
 //   100 over 20000 (400 rows, 12 steps): 110 us, cache4_attention_kernel 129 us;
 //    64 over 20000 (256 rows,  5 steps):  97 us, cache4_attention_kernel  91 us;
 //   2 x 100 over 6000 (400 rows, 6 steps): 76 us, cache4_attention_kernel 69 us;
 //   512 over 8000: split 144 us, whole units of 128 rows 338 us;
-//   3 x 3000 over 12000: split 1842 us, whole 2277 us; 4 x 2000 over 2000: split
-//   337 us, whole 254 us.
+//   3 x 3000 over 12000: split 1842 us, whole 2100 us;
+//   4 x 2000 over 2000: split 337 us, whole 242 us.
 constexpr int64_t kFill = 512;
 constexpr int64_t kWholeFill = 2048;
 constexpr int64_t kPromptUnits = 96;
