@@ -981,7 +981,8 @@ def cache4_attention(cache: Cache4, q, starts, lens, table, scale=None, max_q=No
     """Causal attention of q [tokens, q_heads, D] (bfloat16; tokens may be strided) over the
     cache, its tokens' keys and values already appended.  scale: D ** -0.5 unless given.
     max_q / max_len: the most new / cached tokens of a sequence, for sizing the launch
-    (default: an even share of the call's tokens / the whole table).  out bfloat16 [tokens,
+    (default: an even share of the call's tokens / the whole table); max_q = 1 (max_q * q_heads /
+    kv_heads < 64) keeps the codes exact for prompts too, only slower.  out bfloat16 [tokens,
     q_heads, D]; workspace: uint8 tensor to use instead of a new one."""
     torch = _torch()
     dev = cache.device_index

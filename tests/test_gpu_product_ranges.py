@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 import mixed_precision_weight_dq_amd as dq
-from gpu_util import bf16_gpu, report, torch
+from gpu_util import report, torch
 from serving_ref import EPS32, EPS_BF16, bf16, pad128, product_ref, tokens_ref, widen
 from test_gpu_tokens_i8 import gpu_weights, weights_i8
 
