@@ -396,6 +396,121 @@ dq_status dq_cache4_attention(const dq_cache4* cache, const dq_cache4_batch* bat
                               float scale, int64_t max_q, int64_t max_len, uint16_t* out,
                               void* workspace, size_t workspace_bytes, void* stream);
 
+/* Rotary positions.  Pair i of a head's first `dims` dimensions, (i, i + dims / 2) or,
+ * interleaved, (2 i, 2 i + 1), at position p turns by the angle 2 pi p turns[i]:
+ *   a' = factor (a cos - b sin),  b' = factor (b cos + a sin);
+ * the other dimensions stay.  Every scaling of the frequencies for long contexts is a
+ * choice of turns and factor (the torch layer's Rope makes them).
+ *   turns        device, [dims / 2] fp64, 8-byte aligned
+ *   dims         even, 2 .. DQ_MAX_ROTATED
+ *   interleaved  0 or 1
+ *   factor       finite (else DQ_ERR_VALUE) */
+#define DQ_MAX_ROTATED 4096
+typedef struct {
+    const double* turns;
+    int32_t dims;
+    int32_t interleaved;
+    double factor;
+} dq_rope;
+
+/* Rotate tokens: angles in fp64, sines, cosines and products in fp32, rounded once.
+ *   x, out     device, [tokens, heads, head_dim] of dtype (DQ_F32 or DQ_BF16), strides in
+ *              elements: a head's dimensions are contiguous, heads at least head_dim
+ *              apart, tokens at least a token's extent (slices of a projection's
+ *              output serve as they are).  out may be x with x's strides; else
+ *              the two do not overlap.  Fastest where both are 16-byte aligned, strides
+ *              multiples of 16 bytes, dims of 16 and head_dim of 8.
+ *   positions  device, [tokens] int32, any values, 4-byte aligned
+ *   tokens 1 .. 2^31-1, heads 1 .. DQ_CACHE4_MAX_HEADS, head_dim dims .. DQ_MAX_ROTATED */
+dq_status dq_rotate(const dq_rope* rope, const void* x, int32_t dtype, int64_t tokens, int32_t heads,
+                    int32_t head_dim, int64_t x_token_stride, int64_t x_head_stride,
+                    const int32_t* positions, void* out, int64_t out_token_stride,
+                    int64_t out_head_stride, void* stream);
+
+/* dq_cache4_append with the keys rotated on the way: in fp64, rounded once to fp32 (never
+ * to bf16 in between), then quantized.  A value that passes fp32 makes its group NaN.
+ *   rope       dims a multiple of 16, at most head_dim
+ *   positions  device, [tokens] int32, 4-byte aligned; NULL: each token's position in
+ *              its sequence (the drafts of a tree need dq_draft_tree's) */
+dq_status dq_cache4_append_rope(const dq_cache4* cache, const dq_cache4_batch* batch, const void* k,
+                                const void* v, int32_t dtype, int64_t tokens, int64_t k_stride,
+                                int64_t v_stride, const dq_rope* rope, const int32_t* positions,
+                                void* stream);
+
+/* Drafted tokens.  A sequence's rows of a call are a tree: parents[t] is the row, counted
+ * within the sequence, of token t's parent, an earlier one; -1 (any other value) is a
+ * root.  Its root, row 0, is the last token known, the others are drafted behind it.
+ *
+ * dq_draft_tree: what the attention and the rotation of such a tree need.
+ *   mask       out  device, [tokens, words] int32: bit j % 32 of word j / 32 says that the row
+ *                   sees its sequence's row j: itself and its ancestors (rows from 32
+ *                   words on have no bit and are seen by none)
+ *   positions  out  device, [tokens] int32, may be NULL: lens[b] less the sequence's rows,
+ *                   plus the row's depth
+ *   words           1 .. DQ_MAX_MASK_WORDS
+ * Rows of no sequence are left as they were. */
+#define DQ_MAX_MASK_WORDS 65536
+dq_status dq_draft_tree(const int32_t* parents, const int32_t* starts, const int32_t* lens, int64_t count,
+                        int64_t tokens, int64_t words, int32_t* mask, int32_t* positions, void* stream);
+
+/* dq_cache4_attention with a mask in place of causality: token t sees the cached positions
+ * before the call's own, and of those its sequence's rows whose bits are set in
+ * mask[t] (any bits, not only a tree's; bits past the sequence's rows say nothing).  A token
+ * that sees nothing gives zeros, and what it does not see has no part in it, NaN scales
+ * and positions that the cache does not hold among it.  A length past the table, or past
+ * what dq_cache4_attention takes, makes all of a sequence's rows NaN.
+ *   mask        device, [tokens, mask_words] int32, 4-byte aligned
+ *   mask_words  1 .. DQ_MAX_MASK_WORDS
+ * Everything else as there. */
+size_t dq_cache4_tree_attention_workspace(const dq_cache4* cache, int64_t count, int64_t tokens,
+                                          int32_t q_heads, int64_t max_q, int64_t max_len);
+dq_status dq_cache4_tree_attention(const dq_cache4* cache, const dq_cache4_batch* batch, const uint16_t* q,
+                                   int64_t tokens, int64_t q_stride, int32_t q_heads, const int32_t* mask,
+                                   int64_t mask_words, float scale, int64_t max_q, int64_t max_len,
+                                   uint16_t* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Verify drafted tokens against the target's probabilities, from given random numbers.  From
+ * the root on, the children of the row reached, cur, are tried in order of their rows:
+ *   without draft_probs, child c is taken if u[c] * rest < p[cur][id[c]], rest being 1 less
+ *     the probabilities of the children tried before it (an id that comes again counts as
+ *     0); one that is not taken has its id's probability set to 0;
+ *   with them, the first child alone, whose id was drawn from q[cur]: it is taken if
+ *     u[c] * q[cur][id[c]] < p[cur][id[c]], else p becomes max(p - q, 0).
+ * A child taken is the new cur.  Then `next` is drawn from what p[cur] has become: the first
+ * id whose running sum passes u[root] times the whole sum.  So the tokens that come out
+ * are distributed as the target's own, whatever the drafts.  Products and sums are fp64.
+ *   probs        device, [tokens, vocab] fp32, rows probs_stride elements apart: row t is the
+ *                target's distribution of the token behind row t (not negative, sum 1)
+ *   draft_probs  the same of the drafts, or NULL
+ *   ids          device, [tokens] int32: the rows' tokens (one outside the vocabulary is
+ *                never taken)
+ *   uniforms     device, [tokens] fp32 in [0, 1)
+ *   path         out  device, [tokens] int32: of sequence b, from starts[b] on, the rows taken,
+ *                     the root first, then -1
+ *   accepted     out  device, [count] int32: how many (a sequence without rows: 0)
+ *   next         out  device, [count] int32 (a sequence without rows: -1).  Where nothing is
+ *                     left (p is nowhere above q) it is drawn from p as it is; -1 where p
+ *                     has nothing either.
+ *   workspace    device, 16-byte aligned, dq_verify_drafts_workspace bytes; one for each call
+ *                that may run at the same time
+ * 1 <= vocab <= DQ_MAX_VOCAB; everything else 4-byte aligned.  Entries of path of no sequence
+ * are left as they were. */
+#define DQ_MAX_VOCAB (1LL << 24)
+size_t dq_verify_drafts_workspace(int64_t count, int64_t vocab);
+dq_status dq_verify_drafts(const float* probs, int64_t probs_stride, const float* draft_probs,
+                           int64_t draft_stride, const int32_t* ids, const int32_t* parents,
+                           const int32_t* starts, const float* uniforms, int64_t tokens, int64_t count,
+                           int64_t vocab, int32_t* path, int32_t* accepted, int32_t* next,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Move the accepted rows' entries of the cache to the front of the call's own: position
+ * lens[b] - n + j, n the sequence's rows, gets the entry of lens[b] - n + path[starts[b] + j]
+ * for j < accepted[b], every head's codes and scales; path and accepted as
+ * dq_verify_drafts gives them.  The sequence then has lens[b] - n + accepted[b] tokens.
+ * An entry whose path[j] is below j or not a row, or that the cache does not hold, is left. */
+dq_status dq_cache4_keep(const dq_cache4* cache, const dq_cache4_batch* batch, const int32_t* path,
+                         const int32_t* accepted, int64_t tokens, void* stream);
+
 /* Not a step of the method: a plain streaming read of `bytes` bytes, the
  * yardstick for the bandwidth-bound entry points above (the rate a kernel
  * that only reads the same bytes reaches at the same size).  `nparts`

@@ -22,6 +22,11 @@ kernels behind the C ABI declared in ``include/dq.h``):
   per token) and their integer products with packed weights of at most 8 bits.
 * ``Cache4``, ``cache4_append``, ``cache4_read``, ``cache4_attention`` -- a paged
   key/value cache held in 4 bits: fill it, read it back, attend over it.
+* ``Rope``, ``rotate`` -- rotary positions (halves or neighbours, part of a head, scaled for long
+  contexts); ``cache4_append(..., rope=)`` rotates keys on their way into the cache.
+* ``draft_tree``, ``cache4_tree_attention``, ``verify_drafts``, ``cache4_keep`` -- a step of drafted
+  tokens: the masks of a tree of them, its attention over the cache, their verification
+  against the target's probabilities, and the accepted ones' entries moved together.
 * ``sensitivity``, ``allocate_bits`` -- the host-side allocation calls on
   numpy arrays (the recipe: one bit width per matrix).
 * ``write_packed_file``, ``PackedFile`` -- the on-disk packed-weight format
@@ -53,7 +58,10 @@ __all__ = [
     "dq_quantize_tokens", "dq_gemv_i8", "dq_gemm_i8", "quantize_tokens", "gemv_i8", "gemm_i8",
     "DQCache4", "DQCache4Batch", "dq_cache4_append", "dq_cache4_read",
     "dq_cache4_attention_workspace", "dq_cache4_attention", "Cache4", "cache4_append",
-    "cache4_read", "cache4_attention",
+    "cache4_read", "cache4_attention", "DQRope", "dq_rotate", "dq_cache4_append_rope", "dq_draft_tree",
+    "dq_cache4_tree_attention_workspace", "dq_cache4_tree_attention", "dq_verify_drafts_workspace",
+    "dq_verify_drafts", "dq_cache4_keep", "Rope", "rotate", "draft_tree", "cache4_tree_attention",
+    "verify_drafts", "cache4_keep",
 ]
 
 (DQ_OK, DQ_ERR_NULL, DQ_ERR_BITS, DQ_ERR_SHAPE, DQ_ERR_ALIGN, DQ_ERR_DTYPE, DQ_ERR_HIP,
@@ -98,6 +106,12 @@ class DQCache4Batch(ctypes.Structure):
     """``dq_cache4_batch`` of include/dq.h."""
     _fields_ = [("starts", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("table", ctypes.c_void_p),
                 ("table_width", ctypes.c_int64), ("count", ctypes.c_int64)]
+
+
+class DQRope(ctypes.Structure):
+    """``dq_rope`` of include/dq.h."""
+    _fields_ = [("turns", ctypes.c_void_p), ("dims", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("factor", ctypes.c_double)]
 
 
 class DQError(RuntimeError):
@@ -168,6 +182,24 @@ def load():
     lib.dq_cache4_attention.argtypes = [c4, c4b, vp, i64, i64, i32, ctypes.c_float, i64, i64, vp,
                                         vp, ctypes.c_size_t, vp]
     lib.dq_cache4_attention.restype = st
+    rp, sz = ctypes.POINTER(DQRope), ctypes.c_size_t
+    lib.dq_rotate.argtypes = [rp, vp, i32, i64, i32, i32, i64, i64, vp, vp, i64, i64, vp]
+    lib.dq_rotate.restype = st
+    lib.dq_cache4_append_rope.argtypes = [c4, c4b, vp, vp, i32, i64, i64, i64, rp, vp, vp]
+    lib.dq_cache4_append_rope.restype = st
+    lib.dq_draft_tree.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, vp]
+    lib.dq_draft_tree.restype = st
+    lib.dq_cache4_tree_attention_workspace.argtypes = [c4, i64, i64, i32, i64, i64]
+    lib.dq_cache4_tree_attention_workspace.restype = sz
+    lib.dq_cache4_tree_attention.argtypes = [c4, c4b, vp, i64, i64, i32, vp, i64, ctypes.c_float, i64, i64,
+                                             vp, vp, sz, vp]
+    lib.dq_cache4_tree_attention.restype = st
+    lib.dq_verify_drafts_workspace.argtypes = [i64, i64]
+    lib.dq_verify_drafts_workspace.restype = sz
+    lib.dq_verify_drafts.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, i64, i64, i64, vp, vp, vp, vp, sz, vp]
+    lib.dq_verify_drafts.restype = st
+    lib.dq_cache4_keep.argtypes = [c4, c4b, vp, vp, i64, vp]
+    lib.dq_cache4_keep.restype = st
     fp = ctypes.POINTER(DQFileMatrix)
     lib.dq_file_write.argtypes = [ctypes.c_char_p, fp, i64]
     lib.dq_file_write.restype = st
@@ -333,6 +365,57 @@ def dq_cache4_attention(cache: DQCache4, batch: DQCache4Batch, q: int, tokens: i
                         workspace: int, workspace_bytes: int, stream: int = 0) -> int:
     return int(load().dq_cache4_attention(cache, batch, q, tokens, q_stride, q_heads, scale, max_q,
                                           max_len, out, workspace, workspace_bytes, stream))
+
+
+def dq_rotate(rope: DQRope, x: int, dtype: int, tokens: int, heads: int, head_dim: int,
+              x_token_stride: int, x_head_stride: int, positions: int, out: int,
+              out_token_stride: int, out_head_stride: int, stream: int = 0) -> int:
+    return int(load().dq_rotate(rope, x, dtype, tokens, heads, head_dim, x_token_stride, x_head_stride,
+                                positions, out, out_token_stride, out_head_stride, stream))
+
+
+def dq_cache4_append_rope(cache: DQCache4, batch: DQCache4Batch, k: int, v: int, dtype: int,
+                          tokens: int, k_stride: int, v_stride: int, rope: DQRope, positions: int,
+                          stream: int = 0) -> int:
+    return int(load().dq_cache4_append_rope(cache, batch, k, v, dtype, tokens, k_stride, v_stride, rope,
+                                            positions, stream))
+
+
+def dq_draft_tree(parents: int, starts: int, lens: int, count: int, tokens: int, words: int, mask: int,
+                  positions: int, stream: int = 0) -> int:
+    return int(load().dq_draft_tree(parents, starts, lens, count, tokens, words, mask, positions, stream))
+
+
+def dq_cache4_tree_attention_workspace(cache: DQCache4, count: int, tokens: int, q_heads: int,
+                                       max_q: int, max_len: int) -> int:
+    return int(load().dq_cache4_tree_attention_workspace(cache, count, tokens, q_heads, max_q, max_len))
+
+
+def dq_cache4_tree_attention(cache: DQCache4, batch: DQCache4Batch, q: int, tokens: int, q_stride: int,
+                             q_heads: int, mask: int, mask_words: int, scale: float, max_q: int,
+                             max_len: int, out: int, workspace: int, workspace_bytes: int,
+                             stream: int = 0) -> int:
+    return int(load().dq_cache4_tree_attention(cache, batch, q, tokens, q_stride, q_heads, mask,
+                                               mask_words, scale, max_q, max_len, out, workspace,
+                                               workspace_bytes, stream))
+
+
+def dq_verify_drafts_workspace(count: int, vocab: int) -> int:
+    return int(load().dq_verify_drafts_workspace(count, vocab))
+
+
+def dq_verify_drafts(probs: int, probs_stride: int, draft_probs: int, draft_stride: int, ids: int,
+                     parents: int, starts: int, uniforms: int, tokens: int, count: int, vocab: int,
+                     path: int, accepted: int, next: int, workspace: int, workspace_bytes: int,
+                     stream: int = 0) -> int:
+    return int(load().dq_verify_drafts(probs, probs_stride, draft_probs, draft_stride, ids, parents, starts,
+                                       uniforms, tokens, count, vocab, path, accepted, next, workspace,
+                                       workspace_bytes, stream))
+
+
+def dq_cache4_keep(cache: DQCache4, batch: DQCache4Batch, path: int, accepted: int, tokens: int,
+                   stream: int = 0) -> int:
+    return int(load().dq_cache4_keep(cache, batch, path, accepted, tokens, stream))
 
 
 def dq_stream_read(buf: int, nbytes: int, partial: int, nparts: int, stream: int = 0) -> int:
@@ -939,9 +1022,160 @@ def _token_rows(t, name, heads, D, dev):
     return token if shape[0] > 1 else heads * D
 
 
-def cache4_append(cache: Cache4, k, v, starts, lens, table) -> None:
+class Rope:
+    """Rotary positions: pairs of a head's first ``dims`` dimensions, (i, i + dims / 2) or,
+    ``interleaved``, (2 i, 2 i + 1), turn by ``base ** (-2 i / dims)`` radians a position.
+
+    ``scaling`` stretches them for contexts longer than those of training, by ``factor`` s > 0:
+    ``dict(kind="linear", factor=s)``, every frequency divided by s;
+    ``dict(kind="ntk", factor=s)``, base times s ** (dims / (dims - 2));
+    ``dict(kind="yarn", factor=s, length=L, fast=32, slow=1)``, a ramp over the pairs from the one that
+    turns ``fast`` times over the trained length L (as it was) to the one that turns ``slow`` times
+    (divided by s), and vectors times 0.1 ln s + 1 (``amplitude=`` sets another factor);
+    ``dict(kind="bands", factor=s, length=L, low=1, high=4)``, wavelengths below L / high as they were, above
+    L / low divided by s, between them mixed;
+    ``dict(kind="list", divisors=[...], amplitude=1.0)``, a divisor for each pair.
+    Attributes (fixed): turns (float64 GPU tensor [dims / 2], turns a position), dims, interleaved,
+    factor (of the rotated vector)."""
+
+    def __init__(self, dims: int, base: float = 10000.0, interleaved: bool = False, scaling=None,
+                 device="cuda"):
+        torch = _torch()
+        turns, factor = _rope_turns(dims, base, scaling)
+        turns = torch.tensor(turns, dtype=torch.float64).to(device)
+        dev = _gpu_index(turns, "device")
+        self.__dict__.update(turns=turns, dims=dims, interleaved=bool(interleaved), factor=factor,
+                             device_index=dev, _at=turns.data_ptr(),
+                             _c=DQRope(turns.data_ptr(), dims, bool(interleaved), factor))
+
+    def __setattr__(self, name, value):
+        raise AttributeError("a Rope's attributes are fixed: make another one (%s)" % name)
+
+    def __delattr__(self, name):
+        self.__setattr__(name, None)
+
+    def _struct(self, dev):
+        """The C struct, for a call on GPU ``dev``."""
+        if dev != self.device_index:
+            raise ValueError("the rope is on cuda:%d, the call on cuda:%d" % (self.device_index, dev))
+        if self.turns.data_ptr() != self._at:
+            raise ValueError("the rope's tensor was moved: make another Rope")
+        return self._c
+
+
+def _rope_turns(dims, base, scaling):
+    """(turns a position of each pair, factor of the rotated vector), on the host in float64."""
+    import math
+    if not 2 <= dims <= 4096 or dims % 2:
+        raise DQError(DQ_ERR_SHAPE, "Rope")
+    if not (math.isfinite(base) and base > 1):
+        raise ValueError("base must be finite and above 1")
+    given = dict(scaling or {})
+    kind = given.pop("kind", None)
+    allowed = {None: (), "linear": ("factor",), "ntk": ("factor",),
+               "yarn": ("factor", "length", "fast", "slow", "amplitude"),
+               "bands": ("factor", "length", "low", "high"), "list": ("divisors", "amplitude")}
+    if kind not in allowed:
+        raise ValueError("scaling kind must be linear, ntk, yarn, bands or list (got %r)" % (kind,))
+    if kind in ("linear", "ntk"):
+        given = {k: v for k, v in given.items() if k != "length"}  # (they need none)
+    unknown = set(given) - set(allowed[kind])
+    if unknown:
+        raise ValueError("scaling %s does not take %s" % (kind, ", ".join(sorted(map(str, unknown)))))
+
+    def number(name, default=None):
+        value = given.get(name, default)
+        if isinstance(value, bool) or not isinstance(value, (int, float)) or not math.isfinite(value) or value <= 0:
+            raise ValueError("scaling %s: %s must be a positive number (got %r)" % (kind, name, value))
+        return float(value)
+
+    pairs = range(dims // 2)
+    factor = 1.0
+    s = number("factor") if "factor" in allowed[kind] else 1.0
+    if kind == "ntk":
+        if dims == 2:
+            raise ValueError("scaling ntk needs more than one pair")
+        base = base * s ** (dims / (dims - 2))
+    rate = [base ** (-2 * i / dims) for i in pairs]
+    if kind == "linear":
+        rate = [r / s for r in rate]
+    elif kind == "yarn":
+        length, fast, slow = number("length"), number("fast", 32), number("slow", 1)
+        if fast < slow:
+            raise ValueError("scaling yarn: fast must be at least slow")
+        # the pair that turns n times over the length
+        at = [dims * math.log(length / (2 * math.pi * n)) / (2 * math.log(base)) for n in (fast, slow)]
+        low, high = max(math.floor(at[0]), 0), min(math.ceil(at[1]), dims - 1)
+        ramp = [min(max((i - low) / max(high - low, 0.001), 0.0), 1.0) for i in pairs]
+        rate = [r / s * w + r * (1 - w) for r, w in zip(rate, ramp)]
+        factor = number("amplitude", 0.1 * math.log(s) + 1 if s > 1 else 1.0)
+    elif kind == "bands":
+        length, low, high = number("length"), number("low", 1), number("high", 4)
+        if high <= low:
+            raise ValueError("scaling bands: high must be above low")
+        mix = [min(max((length * r / (2 * math.pi) - low) / (high - low), 0.0), 1.0) for r in rate]
+        rate = [r / s * (1 - w) + r * w for r, w in zip(rate, mix)]
+    elif kind == "list":
+        divisors = [float(d) for d in given.get("divisors", ())]
+        if len(divisors) != dims // 2 or not all(math.isfinite(d) and d > 0 for d in divisors):
+            raise ValueError("scaling list: divisors must be dims / 2 positive numbers")
+        rate = [r / d for r, d in zip(rate, divisors)]
+        factor = number("amplitude", 1.0)
+    return [r / (2 * math.pi) for r in rate], factor
+
+
+def _head_rows(t, name, shape, dev):
+    """Checks t [tokens, heads, D] with contiguous dimensions on GPU ``dev``; returns its token and
+    head strides."""
+    if _gpu_index(t, name) != dev:
+        raise ValueError("%s: all tensors must be on one GPU (cuda:%d and %s)" % (name, dev, t.device))
+    if t.dim() != 3 or (shape is not None and t.shape != shape):
+        raise ValueError("%s must be [tokens, heads, D]" % name)
+    tokens, heads, D = t.shape
+    token, head, dim = t.stride()
+    if dim != 1 and D > 1:
+        raise ValueError("%s: a head's dimensions must be contiguous" % name)
+    if heads == 1:
+        head = D
+    if tokens == 1:
+        token = heads * head
+    return token, head
+
+
+def _positions(positions, tokens, dev):
+    torch = _torch()
+    _fast_need(positions, "positions", torch.int32, 1, dev)
+    if positions.shape[0] != tokens:
+        raise ValueError("positions must be [tokens]")
+    return positions.data_ptr()
+
+
+def rotate(rope: Rope, x, positions, out=None):
+    """x [tokens, heads, D] (float32 or bfloat16; tokens and heads may be strided) with its first
+    ``rope.dims`` dimensions rotated at positions int32 [tokens].  out: a tensor of x's shape
+    and type, x itself among them (a new contiguous one unless given)."""
+    dev = _gpu_index(x, "x")
+    kind = _dtype_code(x.dtype, "x")
+    token, head = _head_rows(x, "x", None, dev)
+    tokens, heads, D = x.shape
+    at = _positions(positions, tokens, dev)
+    if out is None:
+        out = x.new_empty((tokens, heads, D))
+        out_token, out_head = heads * D, D
+    else:
+        out_token, out_head = _head_rows(out, "out", x.shape, dev)
+        if out.dtype != x.dtype:
+            raise ValueError("out must have x's type")
+    _launch("dq_rotate", dev, load().dq_rotate, rope._struct(dev), x.data_ptr(), kind, tokens, heads, D,
+            token, head, at, out.data_ptr(), out_token, out_head)
+    return out
+
+
+def cache4_append(cache: Cache4, k, v, starts, lens, table, rope=None, positions=None) -> None:
     """Quantize k, v [tokens, kv_heads, D] (float32 or bfloat16; tokens may be strided) into
-    the pages of their positions."""
+    the pages of their positions.  rope: a ``Rope`` (dims a multiple of 16, at most D) that
+    rotates the keys on the way, at ``positions`` int32 [tokens] or, without them, at each token's
+    position in its sequence."""
     dev = cache.device_index
     ks = _token_rows(k, "k", cache.kv_heads, cache.head_dim, dev)
     vs = _token_rows(v, "v", cache.kv_heads, cache.head_dim, dev)
@@ -949,8 +1183,16 @@ def cache4_append(cache: Cache4, k, v, starts, lens, table) -> None:
     if v.dtype != k.dtype or v.shape[0] != k.shape[0]:
         raise ValueError("k and v must have one dtype and one token count")
     batch = _batch4(starts, lens, table, dev)
-    _launch("dq_cache4_append", dev, load().dq_cache4_append, cache._struct(), batch, k.data_ptr(),
-            v.data_ptr(), kind, k.shape[0], ks, vs)
+    if rope is None:
+        if positions is not None:
+            raise ValueError("positions are the rope's: give one")
+        _launch("dq_cache4_append", dev, load().dq_cache4_append, cache._struct(), batch, k.data_ptr(),
+                v.data_ptr(), kind, k.shape[0], ks, vs)
+        return
+    if positions is not None:
+        positions = _positions(positions, k.shape[0], dev)
+    _launch("dq_cache4_append_rope", dev, load().dq_cache4_append_rope, cache._struct(), batch,
+            k.data_ptr(), v.data_ptr(), kind, k.shape[0], ks, vs, rope._struct(dev), positions)
 
 
 def cache4_read(cache: Cache4, tokens: int, starts, lens, table, dtype=None, k=None, v=None):
@@ -1017,6 +1259,149 @@ def cache4_attention(cache: Cache4, q, starts, lens, table, scale=None, max_q=No
             stride, heads, scale, max_q, max_len, out.data_ptr(),
             workspace.data_ptr() if workspace is not None else None, need)
     return out
+
+
+def draft_tree(parents, starts, lens=None, words=None):
+    """What a tree of drafted tokens needs: (mask int32 [tokens, words], positions int32 [tokens]).
+    parents int32 [tokens]: each token's parent, counted within its sequence's rows (starts int32
+    [count + 1]), an earlier row, -1 for a root.  Bit j % 32 of mask word j / 32 says that the token
+    sees its sequence's row j: itself or an ancestor.  words: the most rows of a sequence / 32,
+    rounded up (default: enough for any sequence, tokens / 32).  positions: with ``lens`` (cached tokens, the rows
+    included), where to rotate each: the context's length plus the row's depth; else None.  Rows of no
+    sequence are left as allocated: zeros."""
+    torch = _torch()
+    dev = _gpu_index(parents, "parents")
+    _fast_need(parents, "parents", torch.int32, 1, dev)
+    _fast_need(starts, "starts", torch.int32, 1, dev)
+    tokens, count = parents.shape[0], starts.shape[0] - 1
+    if words is None:
+        words = -(-tokens // 32)
+    if not 1 <= words <= 65536:
+        raise DQError(DQ_ERR_SHAPE, "draft_tree")
+    mask = parents.new_zeros((tokens, words))
+    positions = None
+    if lens is not None:
+        _fast_need(lens, "lens", torch.int32, 1, dev)
+        if lens.shape[0] != count:
+            raise ValueError("starts must be [count + 1], lens [count]")
+        positions = parents.new_zeros((tokens,))
+    _launch("dq_draft_tree", dev, load().dq_draft_tree, parents.data_ptr(), starts.data_ptr(),
+            lens.data_ptr() if lens is not None else None, count, tokens, words, mask.data_ptr(),
+            positions.data_ptr() if positions is not None else None)
+    return mask, positions
+
+
+def cache4_tree_attention(cache: Cache4, q, starts, lens, table, mask, scale=None, max_q=None,
+                          max_len=None, out=None, workspace=None):
+    """``cache4_attention`` for trees of drafted tokens: a token sees the cached positions before
+    the call's own and, of its sequence's rows, those with a bit in mask int32 [tokens, words]
+    (``draft_tree`` makes it; any bits will do).  The other arguments as there."""
+    torch = _torch()
+    dev = cache.device_index
+    _gpu_index(q, "q")
+    if q.dtype is not torch.bfloat16 or q.dim() != 3:
+        raise TypeError("q must be a bfloat16 [tokens, q_heads, D] tensor")
+    tokens, heads, D = q.shape
+    stride = _token_rows(q, "q", heads, cache.head_dim, dev)
+    batch = _batch4(starts, lens, table, dev)
+    _fast_need(mask, "mask", torch.int32, 2, dev)
+    if mask.shape[0] != tokens:
+        raise ValueError("mask must be [tokens, words]")
+    if out is None:
+        out = q.new_empty((tokens, heads, D))
+    else:
+        _fast_need(out, "out", torch.bfloat16, 3, dev)
+        if tuple(out.shape) != (tokens, heads, D):
+            raise ValueError("out must be [tokens, q_heads, D]")
+    if max_q is None:
+        max_q = -(-tokens // max(batch.count, 1))
+    if max_len is None:
+        max_len = batch.table_width * cache.page_size
+    if scale is None:
+        scale = D ** -0.5
+    lib = load()
+    c = cache._struct()
+    need = lib.dq_cache4_tree_attention_workspace(c, batch.count, tokens, heads, max_q, max_len)
+    if workspace is None:
+        if need:
+            workspace = q.new_empty((need,), dtype=torch.uint8)
+    else:
+        _fast_need(workspace, "workspace", torch.uint8, 1, dev)
+        need = workspace.shape[0]
+    _launch("dq_cache4_tree_attention", dev, lib.dq_cache4_tree_attention, c, batch, q.data_ptr(), tokens,
+            stride, heads, mask.data_ptr(), mask.shape[1], scale, max_q, max_len, out.data_ptr(),
+            workspace.data_ptr() if workspace is not None else None, need)
+    return out
+
+
+def _prob_rows(t, name, tokens, vocab, dev):
+    """Checks t float32 [tokens, vocab] (rows may be strided) on GPU ``dev``; returns its row stride."""
+    torch = _torch()
+    if _gpu_index(t, name) != dev:
+        raise ValueError("%s: all tensors must be on one GPU (cuda:%d and %s)" % (name, dev, t.device))
+    if t.dtype is not torch.float32:
+        raise TypeError("%s must be float32 (got %s)" % (name, t.dtype))
+    if t.dim() != 2 or t.shape[0] != tokens or (vocab is not None and t.shape[1] != vocab):
+        raise ValueError("%s must be [tokens, vocab]" % name)
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("%s: a row must be contiguous" % name)
+    return t.stride(0) if tokens > 1 else t.shape[1]
+
+
+def verify_drafts(probs, ids, parents, starts, uniforms, draft_probs=None, workspace=None):
+    """Verify drafted tokens against the target's probabilities: (path int32 [tokens], accepted int32
+    [count], next int32 [count]).
+
+    probs float32 [tokens, vocab]: the target's distribution of the token behind each row; ids,
+    parents int32 [tokens]: the rows' tokens, and their parents as for ``draft_tree`` (row 0 of a sequence
+    is its root, the last token known); starts int32 [count + 1]; uniforms float32 [tokens] in [0, 1).
+    Without draft_probs a row's children are candidates of any origin, tried in order; with them
+    (float32 [tokens, vocab]) a row's first child, drawn from its draft_probs, is tried alone.  The tokens
+    that come out are distributed as the target's (the rule: ``dq_verify_drafts`` in include/dq.h).
+    path: from starts[b] on, the accepted[b] rows of sequence b, its root first, then -1; next: the token
+    drawn behind the last of them.  workspace: uint8 tensor to use instead of a new one."""
+    torch = _torch()
+    dev = _gpu_index(probs, "probs")
+    _fast_need(ids, "ids", torch.int32, 1, dev)
+    _fast_need(parents, "parents", torch.int32, 1, dev)
+    _fast_need(starts, "starts", torch.int32, 1, dev)
+    _fast_need(uniforms, "uniforms", torch.float32, 1, dev)
+    tokens, count = ids.shape[0], starts.shape[0] - 1
+    if parents.shape[0] != tokens or uniforms.shape[0] != tokens:
+        raise ValueError("ids, parents and uniforms must be [tokens]")
+    stride = _prob_rows(probs, "probs", tokens, None, dev)
+    vocab = probs.shape[1]
+    draft_stride = 0
+    if draft_probs is not None:
+        draft_stride = _prob_rows(draft_probs, "draft_probs", tokens, vocab, dev)
+        draft_probs = draft_probs.data_ptr()
+    lib = load()
+    need = lib.dq_verify_drafts_workspace(count, vocab)
+    if workspace is None:
+        workspace = ids.new_empty((need,), dtype=torch.uint8)
+    else:
+        _fast_need(workspace, "workspace", torch.uint8, 1, dev)
+        need = workspace.shape[0]
+    path, accepted, drawn = ids.new_empty((tokens,)), ids.new_empty((count,)), ids.new_empty((count,))
+    _launch("dq_verify_drafts", dev, lib.dq_verify_drafts, probs.data_ptr(), stride, draft_probs,
+            draft_stride, ids.data_ptr(), parents.data_ptr(), starts.data_ptr(), uniforms.data_ptr(), tokens,
+            count, vocab, path.data_ptr(), accepted.data_ptr(), drawn.data_ptr(), workspace.data_ptr(), need)
+    return path, accepted, drawn
+
+
+def cache4_keep(cache: Cache4, starts, lens, table, path, accepted) -> None:
+    """Move the accepted rows' keys and values to the front of the call's own positions: of each
+    sequence the rows path[starts[b]], path[starts[b] + 1], ... (``verify_drafts``' path int32 [tokens] and
+    accepted int32 [count]).  It then has lens - rows + accepted tokens."""
+    torch = _torch()
+    dev = cache.device_index
+    batch = _batch4(starts, lens, table, dev)
+    _fast_need(path, "path", torch.int32, 1, dev)
+    _fast_need(accepted, "accepted", torch.int32, 1, dev)
+    if accepted.shape[0] != batch.count:
+        raise ValueError("accepted must be [count]")
+    _launch("dq_cache4_keep", dev, load().dq_cache4_keep, cache._struct(), batch, path.data_ptr(),
+            accepted.data_ptr(), path.shape[0])
 
 
 def stream_read(buf, nparts: int, partial=None):

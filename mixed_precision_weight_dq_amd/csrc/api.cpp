@@ -96,6 +96,27 @@ bool valid_heads(int32_t q_heads, int32_t kv_heads)
     return q_heads >= 1 && q_heads <= DQ_CACHE4_MAX_HEADS && q_heads % kv_heads == 0;
 }
 
+dq_status check_rope(const dq_rope* rope, dq::Rope* r)
+{
+    if (!rope || !rope->turns) return DQ_ERR_NULL;
+    if (rope->dims < 2 || rope->dims > DQ_MAX_ROTATED || rope->dims % 2 != 0) return DQ_ERR_SHAPE;
+    if (!std::isfinite((float)rope->factor)) return DQ_ERR_VALUE;
+    if (!aligned(rope->turns, 8)) return DQ_ERR_ALIGN;
+    *r = dq::Rope{rope->turns, rope->dims, rope->interleaved != 0, rope->factor};
+    return DQ_OK;
+}
+
+// strides of [tokens, heads, dim] whose rows do not overlap
+bool valid_rows(int64_t token, int64_t head, int32_t heads, int32_t dim)
+{
+    return head >= dim && head <= (1LL << 32) && token <= (1LL << 32) && token >= (heads - 1) * head + dim;
+}
+
+bool valid_batch(int64_t count, int64_t tokens)
+{
+    return count >= 1 && count <= DQ_CACHE4_MAX_COUNT && tokens >= 1 && tokens <= 0x7fffffffLL;
+}
+
 }  // namespace
 
 int32_t dq::record_hip_error(hipError_t e) { return hip_status(e); }
@@ -444,6 +465,135 @@ dq_status dq_cache4_attention(const dq_cache4* cache, const dq_cache4_batch* bat
                                                   static_cast<hipStream_t>(stream)));
 }
 
+dq_status dq_rotate(const dq_rope* rope, const void* x, int32_t dtype, int64_t tokens, int32_t heads,
+                    int32_t head_dim, int64_t x_token_stride, int64_t x_head_stride,
+                    const int32_t* positions, void* out, int64_t out_token_stride,
+                    int64_t out_head_stride, void* stream)
+{
+    if (!x || !positions || !out) return DQ_ERR_NULL;
+    dq::Rope r;
+    const dq_status st = check_rope(rope, &r);
+    if (st != DQ_OK) return st;
+    if (tokens < 1 || tokens > 0x7fffffffLL || heads < 1 || heads > DQ_CACHE4_MAX_HEADS ||
+        head_dim < r.dims || head_dim > DQ_MAX_ROTATED ||
+        !valid_rows(x_token_stride, x_head_stride, heads, head_dim) ||
+        !valid_rows(out_token_stride, out_head_stride, heads, head_dim))
+        return DQ_ERR_SHAPE;
+    if (dtype != DQ_F32 && dtype != DQ_BF16) return DQ_ERR_DTYPE;
+    const uintptr_t size = dtype == DQ_BF16 ? 2 : 4;
+    if (!aligned(x, size) || !aligned(out, size) || !aligned(positions, 4)) return DQ_ERR_ALIGN;
+    return hip_status(dq::launch_rotate(r, x, dtype == DQ_BF16, tokens, heads, head_dim, x_token_stride,
+                                        x_head_stride, positions, out, out_token_stride, out_head_stride,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+dq_status dq_cache4_append_rope(const dq_cache4* cache, const dq_cache4_batch* batch, const void* k,
+                                const void* v, int32_t dtype, int64_t tokens, int64_t k_stride,
+                                int64_t v_stride, const dq_rope* rope, const int32_t* positions,
+                                void* stream)
+{
+    if (!k || !v) return DQ_ERR_NULL;
+    dq::Cache4 c;
+    dq::Cache4Batch bt;
+    dq_status st = check_cache4(cache, batch, tokens, &c, &bt);
+    if (st != DQ_OK) return st;
+    dq::Rope r;
+    st = check_rope(rope, &r);
+    if (st != DQ_OK) return st;
+    const int64_t row = (int64_t)c.heads * c.dim;
+    if (!valid_stride(k_stride, row) || !valid_stride(v_stride, row) || r.dims % 16 != 0 || r.dims > c.dim)
+        return DQ_ERR_SHAPE;
+    if (dtype != DQ_F32 && dtype != DQ_BF16) return DQ_ERR_DTYPE;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(positions, 4)) return DQ_ERR_ALIGN;
+    return hip_status(dq::launch_cache4_append_rope(c, bt, k, v, dtype == DQ_BF16, tokens, k_stride, v_stride, r,
+                                                    positions, static_cast<hipStream_t>(stream)));
+}
+
+dq_status dq_cache4_keep(const dq_cache4* cache, const dq_cache4_batch* batch, const int32_t* path,
+                         const int32_t* accepted, int64_t tokens, void* stream)
+{
+    if (!path || !accepted) return DQ_ERR_NULL;
+    dq::Cache4 c;
+    dq::Cache4Batch bt;
+    const dq_status st = check_cache4(cache, batch, tokens, &c, &bt);
+    if (st != DQ_OK) return st;
+    if (!aligned(path, 4) || !aligned(accepted, 4)) return DQ_ERR_ALIGN;
+    return hip_status(dq::launch_cache4_keep(c, bt, path, accepted, tokens, static_cast<hipStream_t>(stream)));
+}
+
+size_t dq_cache4_tree_attention_workspace(const dq_cache4* cache, int64_t count, int64_t tokens,
+                                          int32_t q_heads, int64_t max_q, int64_t max_len)
+{
+    dq::Cache4 c;
+    if (!cache || cache4_geometry(cache, &c) != DQ_OK || !valid_batch(count, tokens) ||
+        !valid_heads(q_heads, c.heads) || max_q < 1 || max_len < 1)
+        return 0;
+    return dq::cache4_tree_workspace(c, count, tokens, q_heads, max_q, max_len);
+}
+
+dq_status dq_cache4_tree_attention(const dq_cache4* cache, const dq_cache4_batch* batch, const uint16_t* q,
+                                   int64_t tokens, int64_t q_stride, int32_t q_heads, const int32_t* mask,
+                                   int64_t mask_words, float scale, int64_t max_q, int64_t max_len,
+                                   uint16_t* out, void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (!q || !out || !mask) return DQ_ERR_NULL;
+    dq::Cache4 c;
+    dq::Cache4Batch bt;
+    const dq_status st = check_cache4(cache, batch, tokens, &c, &bt);
+    if (st != DQ_OK) return st;
+    if (!valid_heads(q_heads, c.heads) || !valid_stride(q_stride, (int64_t)q_heads * c.dim) ||
+        mask_words < 1 || mask_words > DQ_MAX_MASK_WORDS || max_q < 1 || max_len < 1)
+        return DQ_ERR_SHAPE;
+    if (!std::isfinite(scale * 1.44269504f)) return DQ_ERR_VALUE;  // exp2's argument is scaled
+    const size_t need = dq::cache4_tree_workspace(c, bt.count, tokens, q_heads, max_q, max_len);
+    if (need && !workspace) return DQ_ERR_NULL;
+    if (need > workspace_bytes) return DQ_ERR_SHAPE;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(mask, 4) || !aligned(workspace, 16))
+        return DQ_ERR_ALIGN;
+    return hip_status(dq::launch_cache4_tree(c, bt, q, tokens, q_stride, q_heads, mask, mask_words, scale, max_q,
+                                             max_len, out, workspace, static_cast<hipStream_t>(stream)));
+}
+
+dq_status dq_draft_tree(const int32_t* parents, const int32_t* starts, const int32_t* lens, int64_t count,
+                        int64_t tokens, int64_t words, int32_t* mask, int32_t* positions, void* stream)
+{
+    if (!parents || !starts || !mask || (positions && !lens)) return DQ_ERR_NULL;
+    if (!valid_batch(count, tokens) || words < 1 || words > DQ_MAX_MASK_WORDS) return DQ_ERR_SHAPE;
+    if (!aligned(parents, 4) || !aligned(starts, 4) || !aligned(lens, 4) || !aligned(mask, 4) ||
+        !aligned(positions, 4))
+        return DQ_ERR_ALIGN;
+    return hip_status(dq::launch_draft_tree(parents, starts, lens, count, tokens, words, mask, positions,
+                                            static_cast<hipStream_t>(stream)));
+}
+
+size_t dq_verify_drafts_workspace(int64_t count, int64_t vocab)
+{
+    if (!valid_batch(count, 1) || vocab < 1 || vocab > DQ_MAX_VOCAB) return 0;
+    return dq::verify_workspace(count, vocab);
+}
+
+dq_status dq_verify_drafts(const float* probs, int64_t probs_stride, const float* draft_probs,
+                           int64_t draft_stride, const int32_t* ids, const int32_t* parents,
+                           const int32_t* starts, const float* uniforms, int64_t tokens, int64_t count,
+                           int64_t vocab, int32_t* path, int32_t* accepted, int32_t* next,
+                           void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (!probs || !ids || !parents || !starts || !uniforms || !path || !accepted || !next || !workspace)
+        return DQ_ERR_NULL;
+    if (!valid_batch(count, tokens) || vocab < 1 || vocab > DQ_MAX_VOCAB || probs_stride < vocab ||
+        probs_stride > (1LL << 32) ||
+        (draft_probs && (draft_stride < vocab || draft_stride > (1LL << 32))) ||
+        workspace_bytes < dq::verify_workspace(count, vocab))
+        return DQ_ERR_SHAPE;
+    const void* words[] = {probs, draft_probs, ids, parents, starts, uniforms, path, accepted, next};
+    for (const void* p : words)
+        if (!aligned(p, 4)) return DQ_ERR_ALIGN;
+    if (!aligned(workspace, 16)) return DQ_ERR_ALIGN;
+    const dq::VerifyArgs a{probs, probs_stride, draft_probs, draft_stride, ids, parents, starts, uniforms,
+                           tokens, count, vocab, path, accepted, next, nullptr, 0, nullptr};
+    return hip_status(dq::launch_verify(a, workspace, static_cast<hipStream_t>(stream)));
+}
+
 dq_status dq_stream_read(const void* buf, int64_t bytes, uint32_t* partial, int64_t nparts,
                          void* stream)
 {
@@ -461,7 +611,7 @@ const char* dq_status_string(dq_status status)
     case DQ_OK: return "ok";
     case DQ_ERR_NULL: return "a required pointer is NULL";
     case DQ_ERR_BITS: return "bits must be in [2, 15] (integer products: [2, 8]; allocation levels: increasing, in [2, 16])";
-    case DQ_ERR_SHAPE: return "N, K, M, or a cache's sizes, heads, strides or workspace out of range";
+    case DQ_ERR_SHAPE: return "N, K, M, or a cache's, rotation's, mask's or vocabulary's sizes, heads, strides or workspace out of range";
     case DQ_ERR_ALIGN:
         return "pointer not aligned (W, packed, x, token codes, cache, q, k, v: 16 bytes; fp64 sums: 8; others: their elements)";
     case DQ_ERR_DTYPE: return "a dtype must be DQ_F32 or DQ_BF16";

@@ -27,6 +27,7 @@ namespace dq {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int64_t kFillGroups = 1024;
 
 // The place of token row t: -2 for one of no sequence, -1 for one that the cache
 // does not hold.  All threads of the wave take part, kParts neighbours with the same
@@ -34,7 +35,8 @@ constexpr int kThreads = 256;
 // at the start of one, so the search is one load (the 32 tokens of a decode step,
 // searched by halving: 5.4 us instead of 4.8).
 template <int kParts>
-__device__ __forceinline__ int64_t find_slot(const Cache4& c, const Cache4Batch& bt, int64_t t, int64_t tokens)
+__device__ __forceinline__ int64_t find_slot(const Cache4& c, const Cache4Batch& bt, int64_t t, int64_t tokens,
+                                             int64_t* position = nullptr)
 {
     int64_t b = 0;
     if (bt.count <= kWave) {
@@ -52,7 +54,9 @@ __device__ __forceinline__ int64_t find_slot(const Cache4& c, const Cache4Batch&
     int64_t first, n;
     cache4_rows(bt, b, tokens, first, n);
     if (t < first || t >= first + n) return -2;
-    return cache4_slot(c, bt, b, (int64_t)bt.lens[b] - n + (t - first));
+    const int64_t pos = (int64_t)bt.lens[b] - n + (t - first);
+    if (position) *position = pos;
+    return cache4_slot(c, bt, b, pos);
 }
 
 // Where the parts of (page, head, token) begin: its code row, and the scale of its
@@ -103,11 +107,9 @@ __device__ __forceinline__ Raw<BF16> load8(const void* p, int64_t off)
 }
 
 // The 8 codes of a thread (LSB first) and its group's scale.
-template <bool BF16>
-__device__ __forceinline__ uint32_t quantize8(const Raw<BF16>& raw, int group_threads, float* scale)
+__device__ __forceinline__ uint32_t quantize8(const float (&x)[8], int group_threads, float* scale)
 {
-    float x[8], q[8];
-    raw.floats(x);
+    float q[8];
     uint32_t amax = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(x[e]) & 0x7fffffffu);
@@ -137,6 +139,40 @@ __device__ __forceinline__ uint32_t quantize8(const Raw<BF16>& raw, int group_th
     }
     return zero ? 0x88888888u : (uint32_t)hi << 16 | (uint32_t)lo;
 }
+template <bool BF16>
+__device__ __forceinline__ uint32_t quantize8(const Raw<BF16>& raw, int group_threads, float* scale)
+{
+    float x[8];
+    raw.floats(x);
+    return quantize8(x, group_threads, scale);
+}
+
+// The value codes of a thread (8 dimensions of a vector, LSB first) turned into
+// the word that it stores, by way of LDS (mine: the vector's D/8 words).
+template <int D>
+__device__ __forceinline__ uint32_t turn_values(uint32_t wv, int part, uint32_t* mine)
+{
+    constexpr int kPer = D / 16;               // value codes of a c (cache4.hpp)
+    constexpr int kRun = kPer < 8 ? kPer : 8;  // of them in a word
+    // dimension 8 part + e is 16 j + c with j = part / 2, c = 8 (part & 1) + e, and
+    // word w holds codes 8 w + n = c (D/16) + j: the words of one half of the c's lie
+    // next to each other (a vector is within a wave, whose LDS accesses are in order)
+    mine[(part & 1) * kPer + (part >> 1)] = wv;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const int c0 = part * 8 / kPer;
+    const uint4* from = reinterpret_cast<const uint4*>(mine + (c0 >> 3) * kPer + part * 8 % kPer);
+    uint32_t x8[kRun];
+#pragma unroll
+    for (int e = 0; e < kRun; e += 4) {
+        const uint4 d = from[e / 4];
+        x8[e] = d.x, x8[e + 1] = d.y, x8[e + 2] = d.z, x8[e + 3] = d.w;
+    }
+    uint32_t w = 0;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) w |= ((x8[n % kRun] >> (4 * ((c0 + n / kRun) & 7))) & 15u) << (4 * n);
+    return w;
+}
 
 template <int D, bool BF16>
 __global__ __launch_bounds__(kThreads) void cache4_append_kernel(
@@ -144,8 +180,6 @@ __global__ __launch_bounds__(kThreads) void cache4_append_kernel(
     int64_t tokens, int64_t from_token, int64_t k_stride, int64_t v_stride)
 {
     constexpr int kParts = D / 8;
-    constexpr int kPer = D / 16;               // value codes of a c (cache4.hpp)
-    constexpr int kRun = kPer < 8 ? kPer : 8;  // of them in a word
     __shared__ __attribute__((aligned(16))) uint32_t turn[kThreads];
     const int64_t t = from_token + (int64_t)blockIdx.x * (kThreads / kParts) + threadIdx.x / kParts;
     const int part = threadIdx.x % kParts;
@@ -161,35 +195,173 @@ __global__ __launch_bounds__(kThreads) void cache4_append_kernel(
     const uint32_t wk = quantize8<BF16>(rk, group_threads, &sk);
     const uint32_t wv = quantize8<BF16>(rv, group_threads, &sv);
 
-    // keys: dimensions 8 part .. = 32 i + 8 r are word r (D/32) + i.
-    // values: dimension 8 part + e is 16 j + c with j = part / 2, c = 8 (part & 1)
-    // + e, and word w holds codes 8 w + n = c (D/16) + j: the words of a vector
-    // change hands through LDS, those of one half of the c's next to each other (a
-    // vector is within a wave, whose LDS accesses are in order)
-    uint32_t* const mine = turn + (threadIdx.x - part);
-    mine[(part & 1) * kPer + (part >> 1)] = wv;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    const int c0 = part * 8 / kPer;
-    const uint4* from = reinterpret_cast<const uint4*>(mine + (c0 >> 3) * kPer + part * 8 % kPer);
-    uint32_t x8[kRun];
-#pragma unroll
-    for (int e = 0; e < kRun; e += 4) {
-        const uint4 d = from[e / 4];
-        x8[e] = d.x, x8[e + 1] = d.y, x8[e + 2] = d.z, x8[e + 3] = d.w;
-    }
-    uint32_t w = 0;
-#pragma unroll
-    for (int n = 0; n < 8; ++n) w |= ((x8[n % kRun] >> (4 * ((c0 + n / kRun) & 7))) & 15u) << (4 * n);
+    const uint32_t w = turn_values<D>(wv, part, turn + (threadIdx.x - part));
 
     if (slot < 0) return;
     const Place p = place_of<D>(c, slot, head, group_shift);
+    // (keys: dimensions 8 part .. = 32 i + 8 r are word r (D/32) + i)
     c.k_codes[p.row + (part & 3) * (D / 32) + (part >> 2)] = wk;
     c.v_codes[p.row + part] = w;
     if ((part & (group_threads - 1)) == 0) {
         const int64_t o = p.scale + ((int64_t)((part * 8) >> group_shift) << c.page_shift);
         c.k_scales[o] = sk;
         c.v_scales[o] = sv;
+    }
+}
+
+// The same with the keys rotated (rope.hpp) on the way.  Angles, sines, cosines and
+// products are fp64 and the rotated key is rounded once, to fp32: next to a border
+// between codes fp32 angles would decide by their own error.
+//
+// A workgroup keeps the 1024 or fewer cosines and sines of its tokens in LDS (16 KB) and
+// walks its heads with those of a thread's 8 dimensions in registers, so that they
+// are worked out once for all heads.  The partner of a dimension is in the same
+// thread (interleaved) or comes from the thread dims / 16 away, by a shuffle.
+template <int D, bool BF16>
+__global__ __launch_bounds__(kThreads) void cache4_append_rope_kernel(
+    Cache4 c, Cache4Batch bt, const void* __restrict__ k, const void* __restrict__ v,
+    int64_t tokens, int64_t from_token, int64_t k_stride, int64_t v_stride, Rope rope,
+    const int32_t* __restrict__ positions)
+{
+    constexpr int kParts = D / 8;
+    constexpr int kTokens = kThreads / kParts;
+    constexpr int kPairs = D / 2;
+    __shared__ __attribute__((aligned(16))) uint32_t turn[kThreads];
+    __shared__ __attribute__((aligned(16))) double2 turns[kTokens * kPairs];
+    __shared__ int32_t at_position[kTokens];
+    const int64_t t = from_token + (int64_t)blockIdx.x * kTokens + threadIdx.x / kParts;
+    const int part = threadIdx.x % kParts;
+    const int per = (c.heads + (int)gridDim.y - 1) / (int)gridDim.y;
+    const int head0 = (int)blockIdx.y * per;
+    const int head1 = head0 + per < c.heads ? head0 + per : c.heads;
+    const int64_t row = t < tokens ? t : tokens - 1;
+    int64_t pos = 0;
+    const int64_t slot = find_slot<kParts>(c, bt, t, tokens, &pos);
+    if (part == 0) at_position[threadIdx.x / kParts] = positions ? positions[row] : (int32_t)pos;
+    __syncthreads();
+    const int pairs = rope.dims / 2;
+    for (int i = threadIdx.x; i < kTokens * kPairs; i += kThreads) {
+        const int pair = i % kPairs;
+        if (pair < pairs) {
+            double s, co;
+            sincospi(2.0 * rope_fraction(rope, at_position[i / kPairs], pair), &s, &co);
+            turns[i] = make_double2(co * rope.factor, s * rope.factor);
+        }
+    }
+    __syncthreads();
+    const bool inter = rope.interleaved;
+    const int d0 = part * 8;
+    const bool turned = d0 < rope.dims;
+    const bool upper = !inter && d0 >= pairs;   // the second of a pair
+    const int shift = pairs / 8;                // threads to the partner
+    const int partner = (int)(threadIdx.x & (kWave - 1)) + (turned && !inter ? (upper ? -shift : shift) : 0);
+    double2 cs[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int pair = inter ? (d0 + e) / 2 : (upper ? d0 + e - pairs : d0 + e);
+        cs[e] = turned ? turns[(threadIdx.x / kParts) * kPairs + pair] : make_double2(1.0, 0.0);
+        if (!inter && !upper) cs[e].y = -cs[e].y;
+    }
+
+    const int group_shift = 31 - __builtin_clz(c.group);
+    const int group_threads = c.group >> 3;
+    for (int head = head0; head < head1; ++head) {
+        const int64_t at = (int64_t)head * D + d0;
+        const Raw<BF16> rk = load8<BF16>(k, row * k_stride + at), rv = load8<BF16>(v, row * v_stride + at);
+        Raw<BF16> other = rk;
+        if (!inter) {
+#pragma unroll
+            for (int i = 0; i < (BF16 ? 1 : 2); ++i) {
+                other.d[i].x = (uint32_t)__shfl((int)rk.d[i].x, partner, kWave);
+                other.d[i].y = (uint32_t)__shfl((int)rk.d[i].y, partner, kWave);
+                other.d[i].z = (uint32_t)__shfl((int)rk.d[i].z, partner, kWave);
+                other.d[i].w = (uint32_t)__shfl((int)rk.d[i].w, partner, kWave);
+            }
+        }
+        float x[8], y[8], z[8];
+        rk.floats(x);
+        other.floats(y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const double partner_of = inter ? (e & 1 ? (double)x[e ^ 1] : -(double)x[e ^ 1]) : (double)y[e];
+            z[e] = turned ? (float)fma(partner_of, cs[e].y, (double)x[e] * cs[e].x) : x[e];
+        }
+        float sk, sv;
+        const uint32_t wk = quantize8(z, group_threads, &sk);
+        const uint32_t wv = quantize8<BF16>(rv, group_threads, &sv);
+        const uint32_t w = turn_values<D>(wv, part, turn + (threadIdx.x - part));
+        if (slot < 0) continue;
+        const Place p = place_of<D>(c, slot, head, group_shift);
+        c.k_codes[p.row + (part & 3) * (D / 32) + (part >> 2)] = wk;
+        c.v_codes[p.row + part] = w;
+        if ((part & (group_threads - 1)) == 0) {
+            const int64_t o = p.scale + ((int64_t)((part * 8) >> group_shift) << c.page_shift);
+            c.k_scales[o] = sk;
+            c.v_scales[o] = sv;
+        }
+    }
+}
+
+// Moves the entries of accepted tokens to the front of a call's tokens: row path[j] of
+// a sequence's new ones goes to row j.  A thread has 16 bytes of the codes or a scale
+// of one head, in every token, so it reads what it overwrites itself: no barrier, and
+// with path[j] >= j no source is overwritten before it is read.
+template <int D>
+__global__ __launch_bounds__(kThreads) void cache4_keep_kernel(Cache4 c, Cache4Batch bt,
+                                                               const int32_t* __restrict__ path,
+                                                               const int32_t* __restrict__ accepted,
+                                                               int64_t tokens)
+{
+    constexpr int kPieces = D / 32;  // of a code row
+    constexpr int kDeep = 8;         // tokens in flight
+    const int64_t b = blockIdx.y;
+    const int groups = D / c.group;
+    const int columns = 2 * kPieces + 2 * groups;
+    const int i = (int)blockIdx.x * kThreads + threadIdx.x;
+    const int head = i / columns, column = i - head * columns;
+    if (head >= c.heads) return;
+    int64_t first, n;
+    cache4_rows(bt, b, tokens, first, n);
+    const int64_t base = (int64_t)bt.lens[b] - n;
+    int64_t count = accepted[b];
+    count = count < n ? count : n;
+    const int group_shift = 31 - __builtin_clz(c.group);
+    const bool code = column < 2 * kPieces;
+    const bool key = code ? column < kPieces : column < 2 * kPieces + groups;
+    const int at = code ? (key ? column : column - kPieces) : column - 2 * kPieces - (key ? 0 : groups);
+    uint32_t* const codes = key ? c.k_codes : c.v_codes;
+    float* const scales = key ? c.k_scales : c.v_scales;
+    const auto place = [&](int64_t slot) {
+        const Place p = place_of<D>(c, slot, head, group_shift);
+        return code ? p.row + 4 * at : p.scale + ((int64_t)at << c.page_shift);
+    };
+    for (int64_t j0 = 0; j0 < count; j0 += kDeep) {
+        int64_t from[kDeep], to[kDeep];
+#pragma unroll
+        for (int e = 0; e < kDeep; ++e) {
+            const int64_t j = j0 + e;
+            const int64_t r = j < count ? path[first + j] : -1;
+            const bool moves = r > j && r < n;
+            from[e] = moves ? cache4_slot(c, bt, b, base + r) : -1;
+            to[e] = moves ? cache4_slot(c, bt, b, base + j) : -1;
+        }
+        uint4 v[kDeep];
+#pragma unroll
+        for (int e = 0; e < kDeep; ++e) {
+            if (from[e] < 0 || to[e] < 0) continue;
+            if (code)
+                v[e] = *reinterpret_cast<const uint4*>(codes + place(from[e]));
+            else
+                v[e].x = __float_as_uint(scales[place(from[e])]);
+        }
+#pragma unroll
+        for (int e = 0; e < kDeep; ++e) {
+            if (from[e] < 0 || to[e] < 0) continue;
+            if (code)
+                *reinterpret_cast<uint4*>(codes + place(to[e])) = v[e];
+            else
+                scales[place(to[e])] = __uint_as_float(v[e].x);
+        }
     }
 }
 
@@ -288,6 +460,33 @@ hipError_t launch_cache4_append(const Cache4& c, const Cache4Batch& bt, const vo
         kernel<<<grid, kThreads, 0, stream>>>(c, bt, k, v, tokens, from, k_stride, v_stride);
     });
 #undef CALL
+}
+
+hipError_t launch_cache4_append_rope(const Cache4& c, const Cache4Batch& bt, const void* k, const void* v,
+                                     bool bf16, int64_t tokens, int64_t k_stride, int64_t v_stride,
+                                     const Rope& rope, const int32_t* positions, hipStream_t stream)
+{
+#define CALL(D) \
+    (bf16 ? cache4_append_rope_kernel<D, true> : cache4_append_rope_kernel<D, false>)
+    const auto kernel = c.dim == 64 ? CALL(64) : (c.dim == 128 ? CALL(128) : CALL(256));
+    return by_tokens(c, tokens, [&](dim3 grid, int64_t from) {
+        // heads of a workgroup: all, unless that leaves CUs without one
+        const int64_t split = kFillGroups / grid.x;
+        grid.y = (unsigned)(split < 1 ? 1 : (split > c.heads ? c.heads : split));
+        kernel<<<grid, kThreads, 0, stream>>>(c, bt, k, v, tokens, from, k_stride, v_stride, rope, positions);
+    });
+#undef CALL
+}
+
+hipError_t launch_cache4_keep(const Cache4& c, const Cache4Batch& bt, const int32_t* path,
+                              const int32_t* accepted, int64_t tokens, hipStream_t stream)
+{
+    const auto kernel = c.dim == 64 ? cache4_keep_kernel<64>
+                                    : (c.dim == 128 ? cache4_keep_kernel<128> : cache4_keep_kernel<256>);
+    const int columns = 2 * (c.dim / 32) + 2 * (c.dim / c.group);
+    const dim3 grid((unsigned)ceil_div((int64_t)c.heads * columns, kThreads), (unsigned)bt.count);
+    kernel<<<grid, kThreads, 0, stream>>>(c, bt, path, accepted, tokens);
+    return hipGetLastError();
 }
 
 hipError_t launch_cache4_read(const Cache4& c, const Cache4Batch& bt, void* k, void* v, bool bf16,
