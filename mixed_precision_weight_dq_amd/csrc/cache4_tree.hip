@@ -1,9 +1,36 @@
-// Attention of drafted tokens over the paged 4-bit cache: every token sees the cached
-// context, and of the call's own tokens those whose bits its mask has.
+// Attention of drafted tokens over the paged 4-bit cache (cache4.hpp): every token sees the
+// cached context, and of the call's own tokens those whose bits its mask has.
+//   o[i,h] = sum_t p_t vhat[t] / sum_t p_t,  p_t = exp(scale q[i,h] . khat[t] - max).
 //
-// One wave per token and query head; a lane has the dot product of one of 64
-// positions, then the wave's lanes the dimensions of the output.
+// A tree has 8 to 64 tokens, so a kv head has some 32 to 500 rows (token, query head),
+// between the one tile of 16 that cache4_attention_kernel is made for and the
+// thousands of a prompt.  Here a wave expands the codes of 32 positions in registers, once,
+// for T tiles of 32 rows (T = 1 or 2: 64 rows by 128 dimensions of output are 128
+// registers), and the four waves of a workgroup take neighbouring positions, each with a
+// softmax of its own; they meet only at the end of a unit.  Both products run on
+// v_mfma_f32_32x32x16_f16 in transposed form, S^T = K Q^T and O^T = V^T P^T: lane & 31 is a
+// row throughout, and S^T comes out in the lane and order in which P^T goes in.  Rows of q
+// lie in LDS as operands (registers for them would halve the waves of a SIMD).
+//
+// Expansion.  A code u in bits 0..3 (or 4..7) of a half is the fp16 subnormal u 2^-24 (u
+// 2^-20), so (u - 8) * scale is one packed fma, u 2^-24 * S - 8 2^-24 * S, with S the scale
+// times a power of two that puts it below 65504.  Two roundings to 11 bits: of S and of
+// the result.
+//   * Keys: the power of two is each position's own, by the largest of its groups (not
+//     those whose codes are all 0: their stored scale says nothing), and comes back as a
+//     factor of the position's logits.  An element of a much smaller group is off by up to
+//     2^-24, 2^-17 of the position's largest.
+//   * Values: the power of two is a group's, common to the positions that all rows see, and
+//     follows the largest scale so far.  An element far below it is off by 2^-20 of that.
+// Steps of 32 positions that touch the call's own tokens (the last ones) are different:
+// masked weights, codes expanded exactly, the weight times the value's scale rounded after
+// a power of two of each row and group, and sums as weighted means, so that what a row does not
+// see has no part in its rounding either.
+//
+// Weights are fp16 up to 2^14 (a row's reference moves only when passed by 2^8): 11 bits
+// down to 2^-20 of the largest, then to 2^-31 of it.
 #include "cache4.hpp"
+#include "cache4_line.hpp"
 #include "common.hpp"
 #include "launch_serving.hpp"
 
@@ -11,116 +38,772 @@ namespace dq {
 
 namespace {
 
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kMaxLen = 0x7fff0000;
-
 struct TreeArgs {
-    Cache4 c;
-    Cache4Batch bt;
-    const uint16_t* q;
-    int64_t q_stride;
-    uint16_t* out;
-    int64_t tokens;
-    int32_t q_heads;
-    float scale_log2;
-    const int32_t* mask;
+    AttnArgs a;
+    const int32_t* mask;  // [tokens, words]
     int64_t words;
 };
 
-template <int D>
-__global__ __launch_bounds__(kWave) void cache4_tree_kernel(TreeArgs a)
+constexpr uint32_t kTopBits = 0x7fe000u;  // mantissa of 65504, fp16's largest
+
+__device__ __forceinline__ f16x2_t twice(float v)
 {
-    __shared__ float qs[D];
-    __shared__ float ps[kWave];
-    __shared__ int64_t at[kWave];
-    const int lane = threadIdx.x;
-    const int head = blockIdx.y, kvh = head / (a.q_heads / a.c.heads);
-    const int gshift = 31 - __builtin_clz(a.c.group);
-    const int64_t P = 1LL << a.c.page_shift;
-    for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-        const int64_t b = cache4_sequence(a.bt, t);
-        int64_t first, n;
-        cache4_rows(a.bt, b, a.tokens, first, n);
-        if (t < first || t >= first + n) continue;
-        int64_t len = a.bt.lens[b];
-        const bool bad = len > kMaxLen || len > a.bt.width * P;
-        if (len < 0 || bad) len = 0;
-        const int64_t context = len - n;
-        __syncthreads();
-        for (int d = lane; d < D; d += kWave)
-            qs[d] = bf16_bits_to_float(a.q[t * a.q_stride + (int64_t)head * D + d]) * a.scale_log2;
-        __syncthreads();
-        float m = -INFINITY, l = 0.0f, o[D / kWave];
+    const _Float16 h = (_Float16)v;
+    return (f16x2_t){h, h};
+}
+__device__ __forceinline__ f16x8_t operand(const uint32_t (&w)[4])
+{
+    return __builtin_bit_cast(f16x8_t, (u32x4_t){w[0], w[1], w[2], w[3]});
+}
+__device__ __forceinline__ uint32_t scaled(uint32_t codes, f16x2_t s, f16x2_t b)
+{
+    return u32_of(__builtin_elementwise_fma(f16x2_of(codes), s, b));
+}
+
+// max over the 32 lanes of a half of the wave
+__device__ __forceinline__ uint32_t half_max(uint32_t u)
+{
+    float x, y;
+    row_pair(__uint_as_float(row16_max(u)), false, x, y);
+    return max(__float_as_uint(x), __float_as_uint(y));
+}
+
+// The 32 mask bits of positions from (bit `at` of the row's words) on; bits before 0 are 1.
+__device__ __forceinline__ uint32_t mask_window(const int32_t* row, int64_t words, int at)
+{
+    if (at < 0) return (uint32_t)row[0] << -at | ((1u << -at) - 1);
+    const int w = at >> 5, s = at & 31;
+    uint32_t v = w < words ? (uint32_t)row[w] >> s : 0u;
+    if (s != 0 && w + 1 < words) v |= (uint32_t)row[w + 1] << (32 - s);
+    return v;
+}
+
+template <int D, int G, int T>
+__global__ __launch_bounds__(kThreads, 2) void cache4_tree_kernel(TreeArgs args)
+{
+    using C = Cut<32 * T, kThreads>;
+    constexpr int NC = D / 32;    // 32-dimension steps of a dot product, and tiles of the output
+    constexpr int NG = D / G;     // groups of a head
+    constexpr int NL = (NG + 1) / 2;               // value scales of a lane
+    constexpr int VW = D / 128 > 0 ? D / 128 : 1;  // value words of a lane and position
+    constexpr int kPieces = D / 8;                 // of a row of q in LDS
+    constexpr int kPartFloats = (NC * 16 + 2) * T * kWave;
+    constexpr int kShared = kWaves / 2 * kPartFloats * 4 > C::kRows * D * 2 ? kWaves / 2 * kPartFloats * 4
+                                                                           : C::kRows * D * 2;
+    // the rows of q, and, at the end of a unit, the waves' results
+    __shared__ __attribute__((aligned(16))) char shared[kShared];
+    __shared__ float logits[C::kRows];
+    __shared__ __attribute__((aligned(16))) float kpow[kWaves][32];
+    __shared__ __attribute__((aligned(16))) _Float16 vs16[kWaves][NG][32];
+    __shared__ __attribute__((aligned(16))) float vs32[kWaves][NG][32];
+    uint4* const qs = reinterpret_cast<uint4*>(shared);
+
+    const AttnArgs& a = args.a;
+    const int tid = threadIdx.x;
+    const int lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int r32 = lane & 31;
+    const int h = lane >> 5;
+    const int shift = a.c.page_shift;
+    const int nibble = (lane >> 4) & 1 ? 0 : 4;  // shift that puts a lane's value codes in bits 4..7
+
+    // consecutive stretches (which may read the same keys) on one XCD
+    const int group = (a.groups & 7) == 0 ? (int)(blockIdx.x & 7) * (a.groups >> 3) + (int)(blockIdx.x >> 3)
+                                          : (int)blockIdx.x;
+    const Line ln = lay_line<C, true>(a, group, 0);
+    const int64_t x0 = uniform64(ln.first(group)), x1 = uniform64(ln.first(group + 1));
+    int b = ln.b;
+    int64_t before = uniform64(ln.before);
+    if (b < 0) return;
+
+    Rows rw = ln.rw;
+    for (int64_t x = x0; x < x1;) {
+        const int steps = steps_of(a, rw);
+        const int64_t tiles = tiles_of<C>(rw);
+        if (x >= before + tiles * a.c.heads * steps) {
+            before += tiles * a.c.heads * steps;
+            ++b;
+            rw = rows_of(a, b);
+            continue;
+        }
+        const int64_t unit = udiv(x - before, steps);
+        const int step0 = (int)(x - before - unit * steps);
+        const int take = (int)(x1 - x < steps - step0 ? x1 - x : steps - step0);
+        const bool whole = take == steps;
+        const int slot = x == x0 ? 0 : 1;
+        const int kvh = __builtin_amdgcn_readfirstlane((int)udiv(unit, tiles));
+        const int64_t tile = unit - kvh * tiles;
+        const int64_t r0 = tile * C::kRows;
+        const int64_t rows = rw.rows();
+        const int len = __builtin_amdgcn_readfirstlane(rw.held);
+        const int context = __builtin_amdgcn_readfirstlane(rw.len - rw.nq);
+        const bool nothing = rw.bad || rw.len > rw.held;  // all rows NaN
+        const int begin = __builtin_amdgcn_readfirstlane(step0) * kStride;
+        int stop = len;  // (a unit that is one step may have any length)
+        if (take < steps - step0 && begin + take * kStride < len)
+            stop = begin + __builtin_amdgcn_readfirstlane(take) * kStride;
+        stop = __builtin_amdgcn_readfirstlane(stop);
+        x += take;
+        const __attribute__((address_space(4))) int32_t* table =
+            (const __attribute__((address_space(4))) int32_t*)(
+                a.bt.table + __builtin_amdgcn_readfirstlane(b) * a.bt.width);
+        // token row and query head of row r of the unit (of the first where there is none)
+        const auto row_at = [&](int r, int64_t& token, int& head) {
+            const int64_t row = r0 + r < rows ? r0 + r : 0;
+            const int qi = (int)udiv(row, rw.per);
+            token = rw.first + qi;
+            head = kvh * rw.per + (int)(row - (int64_t)qi * rw.per);
+        };
+
+        // ---- a step's loads: keys' and values' words, scales
+        u32x4_t kw[NC / 4 > 0 ? NC / 4 * 2 : 2];  // words (h NC + i), then ((2 + h) NC + i); D = 64: two of each
+        uint32_t vw[16][VW];
+        float ksl[NG], vsl[NL];
+        uint32_t bad = 0;  // a NaN's bits where this lane's position lies in no page
+        int pg[2];
+        int64_t block[2];
+        const auto tile_at = [&](int t) { return t < stop ? t : (stop - 1) & ~15; };
+        const auto load_pages = [&](int t0) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < D / kWave; ++i) o[i] = 0.0f;
-        for (int64_t t0 = 0; t0 < len; t0 += kWave) {
-            const int64_t pos = t0 + lane, j = pos - context;
-            bool sees = pos < len;
-            if (sees && j >= 0) sees = (j >> 5) < a.words && (a.mask[t * a.words + (j >> 5)] >> (j & 31) & 1);
-            float s = -INFINITY;
-            int64_t slot = -1;
-            if (sees) {
-                slot = cache4_slot(a.c, a.bt, b, pos);
-                s = __uint_as_float(0x7fc00000u);
-                if (slot >= 0) {
-                    const int64_t block = (slot >> a.c.page_shift) * a.c.heads + kvh, off = slot & (P - 1);
-                    const uint32_t* k = a.c.k_codes + (block * P + off) * (D / 8);
-                    s = 0.0f;
-                    for (int w = 0; w < D / 8; ++w) {
-                        const int d0 = (w % (D / 32)) * 32 + w / (D / 32) * 8;
-                        const float sc = a.c.k_scales[((block * D >> gshift) + (d0 >> gshift)) * P + off];
-                        float dot = 0.0f;
-                        for (int e = 0; e < 8; ++e) dot += ((int)(k[w] >> (4 * e) & 15) - 8) * qs[d0 + e];
-                        s += dot * sc;
+            for (int i = 0; i < 2; ++i) pg[i] = table[tile_at(t0 + 16 * i) >> shift];
+        };
+        const auto load_k = [&](int t0) __attribute__((always_inline)) {
+            bool ok[2];
+            int off[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                ok[i] = (unsigned)pg[i] < (unsigned)a.c.pages;
+                block[i] = (int64_t)(ok[i] ? pg[i] : 0) * a.c.heads + kvh;
+                off[i] = tile_at(t0 + 16 * i) & ((1 << shift) - 1);
+            }
+            const bool second = (lane & 16) != 0;
+            bad = (second ? ok[1] : ok[0]) ? 0u : 0x7fc00000u;
+            const int64_t bl = second ? block[1] : block[0];
+            const int o = (second ? off[1] : off[0]) + (lane & 15);
+            const uint32_t* kp = a.c.k_codes + ((bl << shift) + o) * (D / 8) + h * NC;
+            if constexpr (D == 64) {
+                typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+                const u32x2_t u = *reinterpret_cast<const u32x2_t*>(kp);
+                const u32x2_t w = *reinterpret_cast<const u32x2_t*>(kp + 2 * NC);
+                kw[0] = (u32x4_t){u.x, u.y, 0u, 0u};
+                kw[1] = (u32x4_t){w.x, w.y, 0u, 0u};
+            } else {
+#pragma unroll
+                for (int i = 0; i < NC / 4; ++i) {
+                    kw[i] = reinterpret_cast<const u32x4_t*>(kp)[i];
+                    kw[NC / 4 + i] = reinterpret_cast<const u32x4_t*>(kp + 2 * NC)[i];
+                }
+            }
+            const int64_t sb = ((bl * NG) << shift) + o;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) ksl[g] = a.c.k_scales[sb + ((int64_t)g << shift)];
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const int g = 2 * i + h < NG ? 2 * i + h : NG - 1;
+                vsl[i] = a.c.v_scales[sb + ((int64_t)g << shift)];
+            }
+        };
+        // values: positions 16 i + 8 (j >> 2) + 4 h + (j & 3), codes of the dimensions that are
+        // lane & 15 modulo 16
+        const auto load_v = [&](int t0) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int off = tile_at(t0 + 16 * i) & ((1 << shift) - 1);
+                const uint32_t* vp = a.c.v_codes + ((block[i] << shift) + off + 4 * h) * (D / 8);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t* p = vp + (8 * (j >> 2) + (j & 3)) * (D / 8);
+                    if constexpr (D == 64) {
+                        vw[8 * i + j][0] = reinterpret_cast<const uint16_t*>(p)[lane & 15];
+                    } else {
+#pragma unroll
+                        for (int w = 0; w < VW; ++w) vw[8 * i + j][w] = p[(lane & 15) * VW + w];
                     }
                 }
             }
-            float mx = s;
-            for (int x = kWave / 2; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor(mx, x, kWave));
-            const float mn = fmaxf(m, mx), base = mn == -INFINITY ? 0.0f : mn;
-            const float p = exp2f(s - base), alpha = exp2f(m - base);
-            float sum = p;
-            for (int x = kWave / 2; x > 0; x >>= 1) sum += __shfl_xor(sum, x, kWave);
-            l = l * alpha + sum;
-            m = mn;
-            ps[lane] = p;
-            at[lane] = sees ? slot : -2;
-            __syncthreads();
+        };
+        int t0 = begin + wave * kStep;
+        if (t0 < stop) {
+            load_pages(t0);
+            load_k(t0);
+            load_v(t0);
+            load_pages(t0 + kStride);
+        }
+
+        // ---- rows of q -> fp16 operands in LDS, each times a power of two (and the sign of the softmax's
+        // scale, so that larger is always larger)
+        {
+            constexpr int kPer = kThreads / C::kRows;  // threads of a row
+            constexpr int kMine = kPieces / kPer;      // pieces of a thread
+            const int r = tid / kPer, sub = tid % kPer;
+            int64_t token;
+            int head;
+            row_at(r, token, head);
+            const uint16_t* qp = a.q + token * a.q_stride + (int64_t)head * D + sub * kMine * 8;
+            uint4 qr[kMine];
+            uint32_t qmax = 0;
 #pragma unroll
-            for (int i = 0; i < D / kWave; ++i) {
-                const int d = i * kWave + lane, place = (d % 16) * (D / 16) + d / 16;
-                o[i] *= alpha;
-                for (int e = 0; e < kWave; ++e) {
-                    if (at[e] < 0) continue;
-                    const int64_t block = (at[e] >> a.c.page_shift) * a.c.heads + kvh, off = at[e] & (P - 1);
-                    const uint32_t w = a.c.v_codes[(block * P + off) * (D / 8) + place / 8];
-                    const float sc = a.c.v_scales[((block * D >> gshift) + (d >> gshift)) * P + off];
-                    o[i] += ps[e] * (((int)(w >> (4 * (place % 8)) & 15) - 8) * sc);
+            for (int i = 0; i < kMine; ++i) {
+                qr[i] = reinterpret_cast<const uint4*>(qp)[i];
+                const uint32_t u[4] = {qr[i].x, qr[i].y, qr[i].z, qr[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)  // as integers: a NaN is the largest
+                    qmax = max(qmax, max((u[e] << 16) & 0x7fffffffu, u[e] & 0x7fff0000u));
+            }
+#pragma unroll
+            for (int o = 1; o < kPer; o <<= 1) qmax = max(qmax, (uint32_t)__shfl_xor((int)qmax, o, kWave));
+            const int ue = min(14 - exponent(__uint_as_float(qmax)), 126);
+            float up = a.scale_log2 < 0.0f ? -pow2(ue) : pow2(ue);
+            float logit = fabsf(a.scale_log2) * pow2(-ue);
+            if (logit == 0.0f) {  // logits of 0 (and no 0 * -inf where positions are hidden)
+                up = 0.0f;
+                logit = 1.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const uint32_t u[4] = {qr[i].x, qr[i].y, qr[i].z, qr[i].w};
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    f[2 * e] = __uint_as_float(u[e] << 16) * up;
+                    f[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u) * up;
+                }
+                uint32_t w[4];  // the order in which a word's codes come: 0 4 1 5 2 6 3 7
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = u32_of((f16x2_t){(_Float16)f[e], (_Float16)f[e + 4]});
+                qs[r * kPieces + ((sub * kMine + i) ^ swizzle<kPieces>(r))] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            // (a key is its codes times 2^(9 + the position's exponent) less than it is)
+            if (sub == 0) logits[r] = logit * 512.0f;
+        }
+        __syncthreads();
+
+        // this lane's first operand: piece h of row r32 (its row is a multiple of 2 kPieces pieces
+        // from the start, so piece 2 k + h is an exclusive or away)
+        const uint32_t q_lane = lds_address(&qs[r32 * kPieces + (h ^ swizzle<kPieces>(r32))]);
+        float logit[T], m[T], l[T];
+        f32x16_t o[T][NC];
+#pragma unroll
+        for (int n = 0; n < T; ++n) {
+            logit[n] = logits[32 * n + r32];
+            m[n] = -INFINITY;
+            l[n] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NC; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[n][j][e] = 0.0f;
+        }
+        // The scales of a group are measured in units of 2^(ve - 15) (and o in as many of 2^(5 + ve));
+        // lanes of half h have ve for the groups 2 i + h, as vtop = 65504 2^(ve - 15), what fp16
+        // then holds of them.  It is raised past the exponent of a scale that passes vtop.
+        uint32_t vtop[NL];
+#pragma unroll
+        for (int i = 0; i < NL; ++i) vtop[i] = (16u << 23) + kTopBits;  // ve = -111
+        bool means = false;  // o is sum p v / sum p as it is, l the whole row's (masked steps)
+        const auto group_unit = [&](int g) {
+            return pow2((int)(__builtin_amdgcn_readlane(vtop[g / 2], 32 * (g & 1)) >> 23) - 127);
+        };
+
+        // Key scales of groups whose codes are all 0 become 0 (the words of a position lie in two lanes).
+        const auto drop_zero_keys = [&]() __attribute__((always_inline)) {
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                uint32_t some = 0;
+#pragma unroll
+                for (int i = g * G / 32; i < (g + 1) * G / 32; ++i)
+                    some |= (kw[i / 4][i % 4] ^ 0x88888888u) |
+                            (kw[(NC / 4 > 0 ? NC / 4 : 1) + i / 4][i % 4] ^ 0x88888888u);
+                some |= (uint32_t)__shfl_xor((int)some, 32, kWave);
+                if (some == 0 && ksl[g] == ksl[g]) ksl[g] = 0.0f;
+            }
+        };
+        // The same of values: 16 lanes have the codes of 16 positions (register r of half i: position
+        // 16 (r >> 3) + 8 (r >> 2 & 1) + 4 i + (r & 3)).
+        const auto drop_zero_values = [&]() __attribute__((always_inline)) {
+            const int r = (r32 >> 4) * 8 + ((r32 >> 3) & 1) * 4 + (r32 & 3);  // where position r32 is
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                uint32_t none = 0;
+                constexpr int n = G / 16;  // codes of the group in a lane
+                const uint32_t mask = (n == 8 ? ~0u : (1u << (4 * (n & 7))) - 1u) << (4 * (g * n % 8));
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const uint64_t lanes = __ballot(((vw[e][g * n / 8] ^ 0x88888888u) & mask) == 0);
+                    if (((lanes >> (32 * h)) & 0xffffu) == 0xffffu) none |= 1u << e;
+                }
+                const uint32_t z0 = __builtin_amdgcn_readlane(none, 0), z1 = __builtin_amdgcn_readlane(none, 32);
+                const bool zero = (((r32 >> 2) & 1 ? z1 : z0) >> r & 1) != 0;
+                if ((g & 1) == h && zero) vsl[g / 2] = 0.0f;
+                if (NG == 1 && zero) vsl[0] = 0.0f;
+            }
+        };
+        // A value scale that is not finite: NaN in its dimensions, in the rows that see it (vis[n]: the
+        // positions that a lane's row of tile n sees), whatever their weight, and 0 from here on.
+        const auto mark_nan = [&](const uint32_t (&vis)[T]) __attribute__((always_inline)) {
+            uint64_t lanes[NL];  // bits 32 h + position: group 2 i + h
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const bool nan = !(fabsf(vsl[i]) < INFINITY);
+                lanes[i] = __ballot(nan);
+                if (nan) vsl[i] = 0.0f;
+            }
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const uint32_t at = (uint32_t)(lanes[g / 2] >> (32 * (g & 1)));
+#pragma unroll
+                for (int n = 0; n < T; ++n)
+                    if ((at & vis[n]) != 0) {
+#pragma unroll
+                        for (int j = g * G / 32; j < (g + 1) * G / 32; ++j)
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[n][j][e] = __uint_as_float(0x7fc00000u);
+                    }
+            }
+        };
+        // The reference of each group follows the step's largest scales.
+        const auto raise = [&]() __attribute__((always_inline)) {
+            int down[NL];
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const uint32_t top = half_max(__float_as_uint(vsl[i]) & 0x7fffffffu), was = vtop[i] >> 23;
+                const uint32_t now = top >= vtop[i] ? (top >> 23) + 1 : was;
+                vtop[i] = (now << 23) + kTopBits;
+                down[i] = (int)was - (int)now;
+            }
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const float f = pow2(__builtin_amdgcn_readlane(down[g / 2], 32 * (g & 1)));
+#pragma unroll
+                for (int n = 0; n < T; ++n)
+#pragma unroll
+                    for (int j = g * G / 32; j < (g + 1) * G / 32; ++j) o[n][j] *= f;
+            }
+        };
+        // Value codes of tile j, positions of half i: an operand, times 2^-20 S + B.
+        const auto value_operand = [&](int i, int j, const f16x2_t (&s)[4], const f16x2_t (&bias)[4])
+                                       __attribute__((always_inline)) {
+            constexpr uint32_t kBytes = 0x0c000c00u;
+            const uint32_t sel = kBytes | (uint32_t)(4 + j % 4) << 16 | (uint32_t)(j % 4);
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[e] = scaled(__builtin_amdgcn_perm(vw[8 * i + 2 * e + 1][j / 4], vw[8 * i + 2 * e][j / 4], sel), s[e],
+                              bias[e]);
+            return operand(w);
+        };
+
+        const auto step = [&](auto Masked, int t0) __attribute__((always_inline)) {
+            constexpr bool kMasked = decltype(Masked)::value;
+            uint32_t q_at = q_lane;
+            pin(q_at);  // (its pieces' addresses are worked out as they are needed, not kept)
+            uint32_t vis[T];
+#pragma unroll
+            for (int n = 0; n < T; ++n) {
+                vis[n] = ~0u;
+                if (kMasked) {
+                    int64_t token;
+                    int head;
+                    row_at(32 * n + r32, token, head);
+                    vis[n] = mask_window(args.mask + token * args.words, args.words, t0 - context);
+                    if (len - t0 < 32) vis[n] &= (1u << (len - t0)) - 1;
                 }
             }
+            // scales
+            bool unsure = false, larger = false;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                unsure |= __float_as_uint(ksl[g]) == kZeroScale;
+                ksl[g] = __uint_as_float(__float_as_uint(ksl[g]) | bad);
+            }
+            if (__builtin_expect(__any(unsure), 0)) drop_zero_keys();
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                if (kMasked && t0 + r32 >= len) vsl[i] = 0.0f;
+                larger |= !(fabsf(vsl[i]) < __uint_as_float(vtop[i]));
+            }
+            if (kMasked || __builtin_expect(__any(larger), 0)) {
+                bool zero = false, nan = false;
+#pragma unroll
+                for (int i = 0; i < NL; ++i) {
+                    zero |= __float_as_uint(vsl[i]) == kZeroScale;
+                    nan |= !(fabsf(vsl[i]) < INFINITY);
+                }
+                if (__builtin_expect(__any(nan), 0)) mark_nan(vis);
+                if (!kMasked) {
+                    if (__any(zero)) drop_zero_values();
+                    raise();
+                }
+            }
+            float top = 0.0f;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) top = fmaxf(top, fabsf(ksl[g]));
+            // the exponent that leaves the largest at most 65504 2^-15
+            int ex = (int)((__float_as_uint(top) + 0x1fffu) >> 23) - 127;
+            ex = ex < -104 ? -104 : (ex > 127 ? 127 : ex);
+            const float down = pow2(15 - ex);
+            kpow[wave][r32] = pow2(ex);
+            f16x2_t ks[NG], kh[NG], kb[NG];
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                ks[g] = twice(ksl[g] * down);
+                kh[g] = ks[g] * (f16x2_t){(_Float16)0.0625f, (_Float16)0.0625f};
+                kb[g] = ks[g] * (f16x2_t){(_Float16)-0x1p-21f, (_Float16)-0x1p-21f};
+            }
+            // (where position r32 is in the order of value_operand's halves)
+            const int at = (r32 & 16) + ((r32 >> 2) & 1) * 8 + ((r32 >> 3) & 1) * 4 + (r32 & 3);
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const int g = 2 * i + h;
+                if (g < NG) {
+                    if (kMasked)
+                        vs32[wave][g][r32] = vsl[i];
+                    else  // times 2^(15 - ve)
+                        vs16[wave][g][at] = (_Float16)(vsl[i] * __uint_as_float((269u << 23) + kTopBits - vtop[i]));
+                }
+            }
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");  // other lanes read them
+            __builtin_amdgcn_wave_barrier();
+
+            // S^T = K Q^T
+            f32x16_t s[T];
+#pragma unroll
+            for (int n = 0; n < T; ++n)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) s[n][e] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 2 * NC; ++k) {
+                const int i = k >> 1, g = 32 * i / G;
+                const uint32_t w = kw[(k & 1) * (NC / 4 > 0 ? NC / 4 : 1) + i / 4][i % 4], y = w >> 8;
+                const uint32_t c[4] = {scaled(w & 0x000f000fu, ks[g], kb[g]), scaled(w & 0x00f000f0u, kh[g], kb[g]),
+                                       scaled(y & 0x000f000fu, ks[g], kb[g]), scaled(y & 0x00f000f0u, kh[g], kb[g])};
+                const f16x8_t key = operand(c);
+#pragma unroll
+                for (int n = 0; n < T; ++n)
+                    s[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                        key, lds_piece((q_at ^ (32 * k)) + 32 * n * kPieces * 16), s[n], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);  // else all keys are expanded ahead, and spill
+            }
+            f32x4_t kf[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) kf[i] = *reinterpret_cast<const f32x4_t*>(&kpow[wave][8 * i + 4 * h]);
+            if (t0 + kStride < stop) load_k(t0 + kStride);
+
+            // weights
+            f16x8_t p[T][2];
+            float carry[T], inv[T];  // masked steps: what is left of the mean so far, 1 / the new sum
+#pragma unroll
+            for (int n = 0; n < T; ++n) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    s[n][e] *= kf[e >> 2][e & 3] * logit[n];
+                    if (kMasked && !(vis[n] >> (8 * (e >> 2) + 4 * h + (e & 3)) & 1)) s[n][e] = -INFINITY;
+                    mx = fmaxf(mx, s[n][e]);
+                }
+                float y0, y1;
+                row_pair(mx, true, y0, y1);
+                mx = fmaxf(y0, y1);
+                float alpha = 1.0f;
+                if (__any(mx > m[n] + 8.0f)) {
+                    const float mn = mx > m[n] + 8.0f ? mx : m[n];
+                    alpha = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m[n] - mn);
+                    m[n] = mn;
+                    if (!kMasked) {
+                        l[n] *= alpha;
+#pragma unroll
+                        for (int j = 0; j < NC; ++j) o[n][j] *= alpha;
+                    }
+                }
+                // weights up to 2^14: fp16's normal range then reaches 2^-20 of the largest
+                const float base = m[n] == -INFINITY ? 0.0f : m[n] - 6.0f;
+                float sum = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    s[n][e] = __builtin_amdgcn_exp2f(s[n][e] - base);
+                    sum += s[n][e];
+                }
+                if constexpr (kMasked) {
+                    row_pair(sum, true, y0, y1);
+                    const float old = l[n] * alpha;
+                    l[n] = old + (y0 + y1);
+                    inv[n] = l[n] > 0.0f ? 1.0f / l[n] : l[n];  // (0 and NaN stay)
+                    carry[n] = l[n] == 0.0f ? 1.0f : old * inv[n];
+                } else {
+                    l[n] += sum;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) p[n][e >> 3][e & 7] = (_Float16)s[n][e];
+                }
+            }
+            // O^T = V^T P^T
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+#pragma unroll
+                for (int w = 0; w < VW; ++w) vw[e][w] = (vw[e][w] << nibble) & 0xf0f0f0f0u;
+            if constexpr (!kMasked) {
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 sv = *reinterpret_cast<const uint4*>(&vs16[wave][g][16 * i + 8 * h]);
+                        const f16x2_t sc[4] = {f16x2_of(sv.x), f16x2_of(sv.y), f16x2_of(sv.z), f16x2_of(sv.w)};
+                        f16x2_t bias[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            bias[e] = sc[e] * (f16x2_t){(_Float16)-0x1p-17f, (_Float16)-0x1p-17f};
+#pragma unroll
+                        for (int j = g * G / 32; j < (g + 1) * G / 32; ++j) {
+                            const f16x8_t v = value_operand(i, j, sc, bias);
+#pragma unroll
+                            for (int n = 0; n < T; ++n)
+                                o[n][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[n][i], o[n][j], 0, 0, 0);
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                    }
+                }
+            } else {
+                const f16x2_t one = twice(0x1p15f), eight = twice(-0x1p-2f);  // (u - 8) 2^-5
+                const f16x2_t sc[4] = {one, one, one, one}, bias[4] = {eight, eight, eight, eight};
+#pragma unroll
+                for (int n = 0; n < T; ++n) {
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        __builtin_amdgcn_sched_barrier(0);  // a group at a time, its codes expanded again for
+#pragma unroll                                              // each tile of rows
+                        for (int e = 0; e < 16; ++e)
+#pragma unroll
+                            for (int w = 0; w < VW; ++w) pin(vw[e][w]);
+                        float t[16], high = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const f32x4_t v = *reinterpret_cast<const f32x4_t*>(&vs32[wave][g][8 * i + 4 * h]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                t[4 * i + e] = s[n][4 * i + e] * 0x1p-14f * v[e];
+                                high = fmaxf(high, fabsf(t[4 * i + e]));
+                            }
+                        }
+                        float y0, y1;
+                        row_pair(high, true, y0, y1);
+                        const int tx = max(exponent(fmaxf(y0, y1)), -112);
+                        const float up = pow2(14 - tx), back = pow2(tx), part = inv[n] * 32.0f;
+                        f16x8_t pf[2];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) pf[e >> 3][e & 7] = (_Float16)(t[e] * up);
+#pragma unroll
+                        for (int j = g * G / 32; j < (g + 1) * G / 32; ++j) {
+                            f32x16_t z;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) z[e] = 0.0f;
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                z = __builtin_amdgcn_mfma_f32_32x32x16_f16(value_operand(i, j, sc, bias), pf[i], z, 0,
+                                                                           0, 0);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                o[n][j][e] = fmaf(z[e] * part, back, o[n][j][e] * carry[n]);
+                        }
+                    }
+                }
+            }
+            if (t0 + kStride < stop) {
+                load_v(t0 + kStride);
+                load_pages(t0 + 2 * kStride);
+            }
+        };
+        // from sums of weights and values in units of the groups to means
+        const auto to_means = [&]() __attribute__((always_inline)) {
+#pragma unroll
+            for (int n = 0; n < T; ++n) {
+                float y0, y1;
+                row_pair(l[n], true, y0, y1);
+                l[n] = y0 + y1;
+                const float inv = l[n] > 0.0f ? 1.0f / l[n] : l[n];  // (0 and NaN stay)
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const float unit = group_unit(g);
+#pragma unroll
+                    for (int j = g * G / 32; j < (g + 1) * G / 32; ++j) o[n][j] = o[n][j] * (inv * 32.0f) * unit;
+                }
+            }
+            means = true;
+        };
+
+        for (; t0 < stop && t0 + kStep <= context; t0 += kStride) step(std::false_type{}, t0);
+        to_means();
+        for (; t0 < stop; t0 += kStride) step(std::true_type{}, t0);
+
+        // join the waves: the upper half into the lower, and so on
+        float* const join = reinterpret_cast<float*>(shared);
+        const auto put = [&](float* dst) {
+#pragma unroll
+            for (int n = 0; n < T; ++n) {
+#pragma unroll
+                for (int j = 0; j < NC; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<f32x4_t*>(dst + (((n * NC + j) * 4 + e) * kWave + lane) * 4) =
+                            (f32x4_t){o[n][j][4 * e], o[n][j][4 * e + 1], o[n][j][4 * e + 2], o[n][j][4 * e + 3]};
+                dst[(T * NC * 16 + 2 * n) * kWave + lane] = m[n];
+                dst[(T * NC * 16 + 2 * n + 1) * kWave + lane] = l[n];
+            }
+        };
+        const auto add = [&](const float* src) {
+#pragma unroll
+            for (int n = 0; n < T; ++n) {
+                const float m2 = src[(T * NC * 16 + 2 * n) * kWave + lane];
+                const float l2 = src[(T * NC * 16 + 2 * n + 1) * kWave + lane];
+                const float mn = fmaxf(m[n], m2);
+                const float base = mn == -INFINITY ? 0.0f : mn;
+                const float w1 = l[n] * __builtin_amdgcn_exp2f(m[n] - base), w2 = l2 * __builtin_amdgcn_exp2f(m2 - base);
+                l[n] = w1 + w2;
+                const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];
+                const float f1 = w1 * inv, f2 = w2 * inv;
+#pragma unroll
+                for (int j = 0; j < NC; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const f32x4_t v =
+                            *reinterpret_cast<const f32x4_t*>(src + (((n * NC + j) * 4 + e) * kWave + lane) * 4);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[n][j][4 * e + i] = fmaf(v[i], f2, o[n][j][4 * e + i] * f1);
+                    }
+                m[n] = mn;
+            }
+        };
+        __syncthreads();  // q is read no more
+#pragma unroll
+        for (int n = kWaves / 2; n > 0; n >>= 1) {
+            if (wave >= n && wave < 2 * n) put(join + (wave - n) * kPartFloats);
+            __syncthreads();
+            if (wave < n) add(join + wave * kPartFloats);
             __syncthreads();
         }
+        if (wave == 0) {
 #pragma unroll
-        for (int i = 0; i < D / kWave; ++i) {
-            const float v = bad ? __uint_as_float(0x7fc00000u) : (l == 0.0f ? 0.0f : o[i] / l);
-            a.out[(t * a.q_heads + head) * D + i * kWave + lane] = __builtin_bit_cast(uint16_t, (__bf16)v);
+            for (int n = 0; n < T; ++n) {
+                if (r0 + 32 * n + r32 >= rows) continue;
+                if (nothing) {
+#pragma unroll
+                    for (int j = 0; j < NC; ++j)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[n][j][e] = __uint_as_float(0x7fc00000u);
+                }
+                if (whole) {
+                    int64_t token;
+                    int head;
+                    row_at(32 * n + r32, token, head);
+                    uint16_t* op = a.out + (token * a.q_heads + head) * D + 4 * h;
+#pragma unroll
+                    for (int j = 0; j < NC; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            *reinterpret_cast<uint2*>(op + 32 * j + 8 * e) =
+                                make_uint2(bf16x2(o[n][j][4 * e], o[n][j][4 * e + 1]),
+                                           bf16x2(o[n][j][4 * e + 2], o[n][j][4 * e + 3]));
+                } else {
+                    const int64_t at = ((int64_t)group * 2 + slot) * C::kRows + 32 * n + r32;
+                    float* pp = a.part + at * D + 4 * h;
+#pragma unroll
+                    for (int j = 0; j < NC; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            *reinterpret_cast<f32x4_t*>(pp + 32 * j + 8 * e) =
+                                (f32x4_t){o[n][j][4 * e], o[n][j][4 * e + 1], o[n][j][4 * e + 2], o[n][j][4 * e + 3]};
+                    if (h == 0) a.part_ml[at] = make_float2(m[n], l[n]);
+                }
+            }
         }
     }
 }
 
+constexpr int64_t kFill = 512;  // workgroups of a launch: two for each CU
+constexpr int64_t kMaxUnits = 1LL << 23;
+
+struct TreePlan {
+    int64_t rows, units, groups;
+    int tiles;  // T
+    int step_shift;
+    size_t part_bytes, ml_bytes;
+};
+
+TreePlan plan_of(const Cache4& c, int64_t count, int64_t tokens, int q_heads, int64_t max_q, int64_t max_len)
+{
+    TreePlan p{};
+    if (max_q > tokens) max_q = tokens;
+    if (max_len > 0x7fffffffLL) max_len = 0x7fffffffLL;
+    p.rows = max_q * (q_heads / c.heads);
+    p.tiles = c.dim == 256 || p.rows <= 32 ? 1 : 2;
+    const int64_t tiles = ceil_div(p.rows, 32 * p.tiles), heads = count * c.heads;
+    p.units = tiles > kMaxUnits / heads ? kMaxUnits : heads * tiles;
+    if (max_len <= 512 || (p.units >= kFill / 2 && max_len <= 4096)) {
+        p.groups = p.units < 4 * kFill ? p.units : 4 * kFill;
+        p.step_shift = 31;
+        return p;
+    }
+    p.step_shift = 7;
+    p.groups = p.units > kFill ? kFill : p.units * ceil_div(max_len, kStride);
+    if (p.groups > kFill) p.groups = kFill;
+    p.part_bytes = (size_t)p.groups * 2 * 32 * p.tiles * c.dim * sizeof(float);
+    p.ml_bytes = (size_t)p.groups * 2 * 32 * p.tiles * sizeof(float2);
+    return p;
+}
+
+template <int D, int G, int T>
+hipError_t launch_tiles(const TreeArgs& t, const TreePlan& p, hipStream_t stream)
+{
+    using C = Cut<32 * T, kThreads>;
+    const AttnArgs& a = t.a;
+    cache4_tree_kernel<D, G, T><<<(unsigned)a.groups, kThreads, 0, stream>>>(t);
+    if (a.groups > 1 && a.step_shift < 31) {
+        if (p.units * 2 > a.groups) {
+            cache4_join_edges_kernel<D, C><<<dim3((unsigned)a.groups - 1, 2 * T), kThreads, 0, stream>>>(a);
+        } else {
+            const dim3 grid((unsigned)p.rows, (unsigned)a.c.heads, (unsigned)a.bt.count);
+            cache4_join_kernel<D, C><<<grid, kThreads, 0, stream>>>(a);
+        }
+    }
+    return hipGetLastError();
+}
+
+template <int D, int G>
+hipError_t launch_dg(const TreeArgs& t, const TreePlan& p, hipStream_t stream)
+{
+    if constexpr (D != 256)
+        if (p.tiles == 2) return launch_tiles<D, G, 2>(t, p, stream);
+    return launch_tiles<D, G, 1>(t, p, stream);
+}
+
 }  // namespace
 
-size_t cache4_tree_workspace(const Cache4&, int64_t, int64_t, int, int64_t, int64_t) { return 0; }
+size_t cache4_tree_workspace(const Cache4& c, int64_t count, int64_t tokens, int q_heads, int64_t max_q,
+                             int64_t max_len)
+{
+    const TreePlan p = plan_of(c, count, tokens, q_heads, max_q, max_len);
+    return p.part_bytes + p.ml_bytes;
+}
 
 hipError_t launch_cache4_tree(const Cache4& c, const Cache4Batch& bt, const uint16_t* q, int64_t tokens,
                               int64_t q_stride, int q_heads, const int32_t* mask, int64_t words,
-                              float scale, int64_t, int64_t, uint16_t* out, void*, hipStream_t stream)
+                              float scale, int64_t max_q, int64_t max_len, uint16_t* out,
+                              void* workspace, hipStream_t stream)
 {
-    const TreeArgs a{c, bt, q, q_stride, out, tokens, q_heads, scale * kLog2e, mask, words};
-    const dim3 grid((unsigned)(tokens < 65536 ? tokens : 65536), (unsigned)q_heads);
-    (c.dim == 64 ? cache4_tree_kernel<64> : (c.dim == 128 ? cache4_tree_kernel<128> : cache4_tree_kernel<256>))
-        <<<grid, kWave, 0, stream>>>(a);
-    return hipGetLastError();
+    const TreePlan p = plan_of(c, bt.count, tokens, q_heads, max_q, max_len);
+    const TreeArgs t{{c, bt, q, q_stride, out, tokens, q_heads, scale * kLog2e,
+                      static_cast<float*>(workspace),
+                      reinterpret_cast<float2*>(static_cast<char*>(workspace) + p.part_bytes),
+                      (int32_t)p.groups, p.step_shift},
+                     mask, words};
+    switch (c.dim * 1000 + c.group) {
+    case 64032: return launch_dg<64, 32>(t, p, stream);
+    case 64064: return launch_dg<64, 64>(t, p, stream);
+    case 128032: return launch_dg<128, 32>(t, p, stream);
+    case 128064: return launch_dg<128, 64>(t, p, stream);
+    case 128128: return launch_dg<128, 128>(t, p, stream);
+    case 256032: return launch_dg<256, 32>(t, p, stream);
+    case 256064: return launch_dg<256, 64>(t, p, stream);
+    case 256128: return launch_dg<256, 128>(t, p, stream);
+    default: return hipErrorInvalidValue;
+    }
 }
 
 }  // namespace dq
