@@ -32,6 +32,7 @@
 #include "cache4.hpp"
 #include "cache4_line.hpp"
 #include "common.hpp"
+#include "gemm_tiles.hpp"
 #include "launch_serving.hpp"
 
 namespace dq {
@@ -78,24 +79,135 @@ __device__ __forceinline__ uint32_t mask_window(const int32_t* row, int64_t word
     return v;
 }
 
+// A wave's ring of steps in LDS: the codes and scales of 32 positions, copied straight from memory
+// (buffer loads to LDS), two tiles of 16 positions each.  Tiles of codes are rows of D / 16
+// 16-byte pieces; piece j of row r lies at j ^ turn(r), which spreads what a pass of lanes reads over
+// the banks (the copy's lanes pick their pieces accordingly).  Scales lie four groups of a position next
+// to each other, keys' in order, values' the even ones first.
+template <int D, int G>
+struct Ring {
+    static constexpr int kPieces = D / 32;               // of a row of codes (D / 2 bytes)
+    static constexpr int kCodes = 16 * kPieces * 16;     // bytes of a tile's codes
+    static constexpr int kCopies = (kCodes + 1023) / 1024;
+    static constexpr int kQuads = (D / G + 3) / 4;       // groups by four
+    static constexpr int kKeys = 0, kValues = 2 * kCodes, kKeyScales = 4 * kCodes;
+    static constexpr int kValueScales = kKeyScales + 2 * kQuads * 256;
+    static constexpr int kBytes = kValueScales + 2 * kQuads * 256;
+    static constexpr int kLoads = 4 * kCopies + 4 * kQuads;  // of a step
+    static __device__ __forceinline__ int turn(int r)
+    {
+        return D == 64 ? (r >> 2) & 1 : (D == 128 ? (r >> 1) & 3 : r & 7);
+    }
+};
+
+// Waits until at most N of the wave's loads are in flight (and for no LDS operation).
+template <int N>
+__device__ __forceinline__ void wait_loads()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+    asm volatile("" ::: "memory");
+}
+
+// Reads of the ring, by LDS address, each block with its own wait: reads that the compiler knew of
+// would wait for every copy in flight, those of later steps among them.
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+template <int D, int kQuads>
+__device__ __forceinline__ void read_keys(uint32_t k0, uint32_t k1, uint32_t ks, uint32_t vs, u32x4_t (&kw)[D == 256 ? 4 : 2],
+                                          u32x4_t (&kscale)[kQuads], u32x2_t (&vscale)[kQuads])
+{
+    if constexpr (D == 64) {
+        u32x2_t a, b;
+        asm volatile(
+            "ds_read_b64 %0, %4\n\tds_read_b64 %1, %5\n\tds_read_b128 %2, %6\n\tds_read_b64 %3, %7\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(a), "=&v"(b), "=&v"(kscale[0]), "=&v"(vscale[0])
+            : "v"(k0), "v"(k1), "v"(ks), "v"(vs)
+            : "memory");
+        kw[0] = (u32x4_t){a.x, a.y, 0u, 0u};
+        kw[1] = (u32x4_t){b.x, b.y, 0u, 0u};
+    } else if constexpr (D == 128) {
+        asm volatile(
+            "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %6\n\tds_read_b64 %3, %7\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(kw[0]), "=&v"(kw[1]), "=&v"(kscale[0]), "=&v"(vscale[0])
+            : "v"(k0), "v"(k1), "v"(ks), "v"(vs)
+            : "memory");
+    } else {
+        // pieces 2 h, 2 h + 1, 4 + 2 h, 5 + 2 h: a lane's are an exclusive or of 16 or 64 bytes away
+        asm volatile(
+            "ds_read_b128 %0, %6\n\tds_read_b128 %1, %7\n\tds_read_b128 %2, %8\n\tds_read_b128 %3, %9\n\t"
+            "ds_read_b128 %4, %10\n\tds_read_b64 %5, %11\n\ts_waitcnt lgkmcnt(0)"
+            : "=&v"(kw[0]), "=&v"(kw[1]), "=&v"(kw[2]), "=&v"(kw[3]), "=&v"(kscale[0]), "=&v"(vscale[0])
+            : "v"(k0), "v"(k0 ^ 16u), "v"(k1), "v"(k1 ^ 16u), "v"(ks), "v"(vs)
+            : "memory");
+        if constexpr (kQuads == 2)
+            asm volatile("ds_read_b128 %0, %2 offset:512\n\tds_read_b64 %1, %3 offset:512\n\ts_waitcnt lgkmcnt(0)"
+                         : "=&v"(kscale[1]), "=&v"(vscale[1])
+                         : "v"(ks), "v"(vs)
+                         : "memory");
+    }
+}
+
+// The value words of 16 positions: register 8 i + 4 q + j is row 8 q + 4 h + j of tile i; v[j] the address of
+// row 4 h + j of tile 0.
+template <int D>
+__device__ __forceinline__ void read_values(const uint32_t (&v)[4], uint32_t (&w)[16][D == 256 ? 2 : 1])
+{
+    constexpr int kTile = Ring<D, D == 64 ? 64 : 128>::kCodes, kHalf = kTile / 2;
+#define READ8(OP, C, W, T)                                                                                   \
+    asm volatile(OP " %0, %8 offset:%12\n\t" OP " %1, %9 offset:%12\n\t" OP " %2, %10 offset:%12\n\t" OP    \
+                    " %3, %11 offset:%12\n\t" OP " %4, %8 offset:%13\n\t" OP " %5, %9 offset:%13\n\t" OP      \
+                    " %6, %10 offset:%13\n\t" OP " %7, %11 offset:%13\n\ts_waitcnt lgkmcnt(0)"               \
+                 : "=&v"(W[0] C), "=&v"(W[1] C), "=&v"(W[2] C), "=&v"(W[3] C), "=&v"(W[4] C), "=&v"(W[5] C), \
+                   "=&v"(W[6] C), "=&v"(W[7] C)                                                              \
+                 : "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "n"(T), "n"(T + kHalf)                        \
+                 : "memory")
+    if constexpr (D == 256) {
+        u32x2_t t[2][8];
+        READ8("ds_read_b64", , t[0], 0);
+        READ8("ds_read_b64", , t[1], kTile);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            w[e][0] = t[e >> 3][e & 7].x;
+            w[e][1] = t[e >> 3][e & 7].y;
+        }
+    } else {
+        uint32_t t[2][8];
+        if constexpr (D == 64) {
+            READ8("ds_read_u16", , t[0], 0);
+            READ8("ds_read_u16", , t[1], kTile);
+        } else {
+            READ8("ds_read_b32", , t[0], 0);
+            READ8("ds_read_b32", , t[1], kTile);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w[e][0] = t[e >> 3][e & 7];
+    }
+#undef READ8
+}
+
 template <int D, int G, int T>
-__global__ __launch_bounds__(kThreads, 2) void cache4_tree_kernel(TreeArgs args)
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel(TreeArgs args)
 {
     using C = Cut<32 * T, kThreads>;
+    using R = Ring<D, G>;
+    constexpr int S = D != 256 && T == 1 ? 3 : 2;  // steps of the ring
     constexpr int NC = D / 32;    // 32-dimension steps of a dot product, and tiles of the output
     constexpr int NG = D / G;     // groups of a head
     constexpr int NL = (NG + 1) / 2;               // value scales of a lane
     constexpr int VW = D / 128 > 0 ? D / 128 : 1;  // value words of a lane and position
     constexpr int kPieces = D / 8;                 // of a row of q in LDS
-    constexpr int kPartFloats = (NC * 16 + 2) * T * kWave;
+    constexpr int kCols = NC / 2;                       // tiles of the output that the waves join at a time
+    constexpr int kPartFloats = (kCols * 16 + 2) * kWave;  // a wave's result for them and a tile of rows
     constexpr int kShared = kWaves / 2 * kPartFloats * 4 > C::kRows * D * 2 ? kWaves / 2 * kPartFloats * 4
                                                                            : C::kRows * D * 2;
     // the rows of q, and, at the end of a unit, the waves' results
     __shared__ __attribute__((aligned(16))) char shared[kShared];
     __shared__ float logits[C::kRows];
     __shared__ __attribute__((aligned(16))) float kpow[kWaves][32];
-    __shared__ __attribute__((aligned(16))) _Float16 vs16[kWaves][NG][32];
-    __shared__ __attribute__((aligned(16))) float vs32[kWaves][NG][32];
+    __shared__ __attribute__((aligned(16))) float vscale[kWaves][NG][32];  // (or halves, unless masked)
+    __shared__ __attribute__((aligned(128))) char ring[kWaves][S][R::kBytes];
     uint4* const qs = reinterpret_cast<uint4*>(shared);
 
     const AttnArgs& a = args.a;
@@ -106,6 +218,37 @@ __global__ __launch_bounds__(kThreads, 2) void cache4_tree_kernel(TreeArgs args)
     const int h = lane >> 5;
     const int shift = a.c.page_shift;
     const int nibble = (lane >> 4) & 1 ? 0 : 4;  // shift that puts a lane's value codes in bits 4..7
+
+    // byte offsets of a lane's piece in a tile of codes (the copy's lane i fills piece i, that of rows of
+    // the next copy lie 1024 bytes on), and of its scale in those of a tile
+    uint32_t code_lane, ks_lane[R::kQuads], vs_lane[R::kQuads];
+    {
+        const int r = lane / R::kPieces % 16, j = lane % R::kPieces;
+        code_lane = r * (D / 2) + (j ^ R::turn(r)) * 16;
+#pragma unroll
+        for (int n = 0; n < R::kQuads; ++n) {
+            const int i = lane & 3, kg = 4 * n + i, vg = 4 * n + (i & 1) * 2 + (i >> 1);
+            ks_lane[n] = (uint32_t)(((kg < NG ? kg : NG - 1) << shift) + (lane >> 2)) * 4;
+            vs_lane[n] = (uint32_t)(((vg < NG ? vg : NG - 1) << shift) + (lane >> 2)) * 4;
+        }
+    }
+    // where a lane reads in a step of the ring
+    uint32_t k_read[2], v_read[4], s_read;
+    {
+        const int t = lane & 15, tile = (lane >> 4) & 1;  // position r32: row t of a tile
+        const uint32_t at = lds_address(reinterpret_cast<const uint4*>(ring[wave][0]));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // words (2 i + h) NC on
+            const int byte = (2 * i + h) * NC * 4;
+            k_read[i] = at + R::kKeys + tile * R::kCodes + t * (D / 2) + ((byte >> 4) ^ R::turn(t)) * 16 + (byte & 15);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // the codes of the dimensions that are t modulo 16, of row 4 h + j
+            const int r = 4 * h + j, byte = t * (D / 32);
+            v_read[j] = at + R::kValues + r * (D / 2) + ((byte >> 4) ^ R::turn(r)) * 16 + (byte & 15);
+        }
+        s_read = at + R::kKeyScales + tile * 256 + t * 16;
+    }
 
     // consecutive stretches (which may read the same keys) on one XCD
     const int group = (a.groups & 7) == 0 ? (int)(blockIdx.x & 7) * (a.groups >> 3) + (int)(blockIdx.x >> 3)
@@ -155,80 +298,57 @@ __global__ __launch_bounds__(kThreads, 2) void cache4_tree_kernel(TreeArgs args)
             head = kvh * rw.per + (int)(row - (int64_t)qi * rw.per);
         };
 
-        // ---- a step's loads: keys' and values' words, scales
-        u32x4_t kw[NC / 4 > 0 ? NC / 4 * 2 : 2];  // words (h NC + i), then ((2 + h) NC + i); D = 64: two of each
-        uint32_t vw[16][VW];
-        float ksl[NG], vsl[NL];
-        uint32_t bad = 0;  // a NaN's bits where this lane's position lies in no page
+        // ---- a step's copies into the ring
+        uint32_t bad_tiles = 0;  // two bits for each step in flight: a tile whose page is outside the cache
         int pg[2];
-        int64_t block[2];
         const auto tile_at = [&](int t) { return t < stop ? t : (stop - 1) & ~15; };
         const auto load_pages = [&](int t0) __attribute__((always_inline)) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) pg[i] = table[tile_at(t0 + 16 * i) >> shift];
         };
-        const auto load_k = [&](int t0) __attribute__((always_inline)) {
-            bool ok[2];
-            int off[2];
+        const auto copy = [&](int t0, char* to, int ahead) __attribute__((always_inline)) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                ok[i] = (unsigned)pg[i] < (unsigned)a.c.pages;
-                block[i] = (int64_t)(ok[i] ? pg[i] : 0) * a.c.heads + kvh;
-                off[i] = tile_at(t0 + 16 * i) & ((1 << shift) - 1);
-            }
-            const bool second = (lane & 16) != 0;
-            bad = (second ? ok[1] : ok[0]) ? 0u : 0x7fc00000u;
-            const int64_t bl = second ? block[1] : block[0];
-            const int o = (second ? off[1] : off[0]) + (lane & 15);
-            const uint32_t* kp = a.c.k_codes + ((bl << shift) + o) * (D / 8) + h * NC;
-            if constexpr (D == 64) {
-                typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-                const u32x2_t u = *reinterpret_cast<const u32x2_t*>(kp);
-                const u32x2_t w = *reinterpret_cast<const u32x2_t*>(kp + 2 * NC);
-                kw[0] = (u32x4_t){u.x, u.y, 0u, 0u};
-                kw[1] = (u32x4_t){w.x, w.y, 0u, 0u};
-            } else {
-#pragma unroll
-                for (int i = 0; i < NC / 4; ++i) {
-                    kw[i] = reinterpret_cast<const u32x4_t*>(kp)[i];
-                    kw[NC / 4 + i] = reinterpret_cast<const u32x4_t*>(kp + 2 * NC)[i];
-                }
-            }
-            const int64_t sb = ((bl * NG) << shift) + o;
-#pragma unroll
-            for (int g = 0; g < NG; ++g) ksl[g] = a.c.k_scales[sb + ((int64_t)g << shift)];
-#pragma unroll
-            for (int i = 0; i < NL; ++i) {
-                const int g = 2 * i + h < NG ? 2 * i + h : NG - 1;
-                vsl[i] = a.c.v_scales[sb + ((int64_t)g << shift)];
-            }
-        };
-        // values: positions 16 i + 8 (j >> 2) + 4 h + (j & 3), codes of the dimensions that are
-        // lane & 15 modulo 16
-        const auto load_v = [&](int t0) __attribute__((always_inline)) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
+                const bool ok = (unsigned)pg[i] < (unsigned)a.c.pages;
+                bad_tiles |= (ok ? 0u : 1u) << (2 * ahead + i);
+                const int64_t block = (int64_t)(ok ? pg[i] : 0) * a.c.heads + kvh;
                 const int off = tile_at(t0 + 16 * i) & ((1 << shift) - 1);
-                const uint32_t* vp = a.c.v_codes + ((block[i] << shift) + off + 4 * h) * (D / 8);
+                const BufRef kb{a.c.k_codes + ((block << shift) + off) * (D / 8), R::kCodes};
+                const BufRef vb{a.c.v_codes + ((block << shift) + off) * (D / 8), R::kCodes};
+                const int64_t sb = ((block * NG) << shift) + off;
+                const uint32_t bytes = (((NG - 1) << shift) + 16) * 4;
+                const BufRef ks{a.c.k_scales + sb, bytes}, vs{a.c.v_scales + sb, bytes};
+                if (D != 64 || lane < 32) {  // (heads of 64: a tile is 32 pieces)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t* p = vp + (8 * (j >> 2) + (j & 3)) * (D / 8);
-                    if constexpr (D == 64) {
-                        vw[8 * i + j][0] = reinterpret_cast<const uint16_t*>(p)[lane & 15];
-                    } else {
-#pragma unroll
-                        for (int w = 0; w < VW; ++w) vw[8 * i + j][w] = p[(lane & 15) * VW + w];
+                    for (int n = 0; n < R::kCopies; ++n) {
+                        buf_load_lds16(kb, to + R::kKeys + i * R::kCodes + n * 1024, code_lane, n * 1024);
+                        buf_load_lds16(vb, to + R::kValues + i * R::kCodes + n * 1024, code_lane, n * 1024);
                     }
                 }
+#pragma unroll
+                for (int n = 0; n < R::kQuads; ++n) {
+                    buf_load_lds4(ks, to + R::kKeyScales + n * 512 + i * 256, ks_lane[n], 0);
+                    buf_load_lds4(vs, to + R::kValueScales + n * 512 + i * 256, vs_lane[n], 0);
+                }
             }
         };
+        char* const mine = ring[wave][0];
         int t0 = begin + wave * kStep;
         if (t0 < stop) {
             load_pages(t0);
-            load_k(t0);
-            load_v(t0);
+            copy(t0, mine, 0);
             load_pages(t0 + kStride);
+            if (S > 2 && t0 + kStride < stop) {
+                copy(t0 + kStride, mine + R::kBytes, 1);
+                load_pages(t0 + 2 * kStride);
+            }
         }
+        // what the step at hand has in registers
+        u32x4_t kw[D == 256 ? 4 : 2];  // words (h NC + i), then ((2 + h) NC + i)
+        uint32_t vw[16][VW];
+        float ksl[NG], vsl[NL];
+        constexpr int kHalf = D == 256 ? 2 : 1;  // of them
+        int stage = 0;  // of the step at hand
 
         // ---- rows of q -> fp16 operands in LDS, each times a power of two (and the sign of the softmax's
         // scale, so that larger is always larger)
@@ -280,7 +400,7 @@ __global__ __launch_bounds__(kThreads, 2) void cache4_tree_kernel(TreeArgs args)
 
         // this lane's first operand: piece h of row r32 (its row is a multiple of 2 kPieces pieces
         // from the start, so piece 2 k + h is an exclusive or away)
-        const uint32_t q_lane = lds_address(&qs[r32 * kPieces + (h ^ swizzle<kPieces>(r32))]);
+        const uint32_t q_lane = (uint32_t)(r32 * kPieces + (h ^ swizzle<kPieces>(r32))) * 16;
         float logit[T], m[T], l[T];
         f32x16_t o[T][NC];
 #pragma unroll
@@ -304,6 +424,10 @@ __global__ __launch_bounds__(kThreads, 2) void cache4_tree_kernel(TreeArgs args)
             return pow2((int)(__builtin_amdgcn_readlane(vtop[g / 2], 32 * (g & 1)) >> 23) - 127);
         };
 
+        const auto read_words = [&](uint32_t here) __attribute__((always_inline)) {
+            const uint32_t at[4] = {v_read[0] + here, v_read[1] + here, v_read[2] + here, v_read[3] + here};
+            read_values<D>(at, vw);
+        };
         // Key scales of groups whose codes are all 0 become 0 (the words of a position lie in two lanes).
         const auto drop_zero_keys = [&]() __attribute__((always_inline)) {
 #pragma unroll
@@ -311,15 +435,15 @@ __global__ __launch_bounds__(kThreads, 2) void cache4_tree_kernel(TreeArgs args)
                 uint32_t some = 0;
 #pragma unroll
                 for (int i = g * G / 32; i < (g + 1) * G / 32; ++i)
-                    some |= (kw[i / 4][i % 4] ^ 0x88888888u) |
-                            (kw[(NC / 4 > 0 ? NC / 4 : 1) + i / 4][i % 4] ^ 0x88888888u);
+                    some |= (kw[i / 4][i % 4] ^ 0x88888888u) | (kw[kHalf + i / 4][i % 4] ^ 0x88888888u);
                 some |= (uint32_t)__shfl_xor((int)some, 32, kWave);
                 if (some == 0 && ksl[g] == ksl[g]) ksl[g] = 0.0f;
             }
         };
         // The same of values: 16 lanes have the codes of 16 positions (register r of half i: position
         // 16 (r >> 3) + 8 (r >> 2 & 1) + 4 i + (r & 3)).
-        const auto drop_zero_values = [&]() __attribute__((always_inline)) {
+        const auto drop_zero_values = [&](uint32_t here) __attribute__((always_inline)) {
+            read_words(here);
             const int r = (r32 >> 4) * 8 + ((r32 >> 3) & 1) * 4 + (r32 & 3);  // where position r32 is
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
@@ -394,6 +518,31 @@ __global__ __launch_bounds__(kThreads, 2) void cache4_tree_kernel(TreeArgs args)
 
         const auto step = [&](auto Masked, int t0) __attribute__((always_inline)) {
             constexpr bool kMasked = decltype(Masked)::value;
+            // the copies of a step to come go out, then those of this one are waited for
+            const int free = stage == 0 ? S - 1 : stage - 1;
+            if (t0 + (S - 1) * kStride < stop) {
+                copy(t0 + (S - 1) * kStride, mine + free * R::kBytes, S - 1);
+                load_pages(t0 + S * kStride);
+                wait_loads<(S - 1) * R::kLoads>();
+            } else if (S > 2 && t0 + kStride < stop) {
+                wait_loads<R::kLoads>();
+            } else {
+                wait_loads<0>();
+            }
+            const uint32_t here = stage * R::kBytes;
+            stage = stage == S - 1 ? 0 : stage + 1;
+            {
+                u32x4_t ks[R::kQuads];
+                u32x2_t vs[R::kQuads];
+                read_keys<D, R::kQuads>(k_read[0] + here, k_read[1] + here, s_read + here,
+                                        s_read + here + (R::kValueScales - R::kKeyScales) + 8 * h, kw, ks, vs);
+                const uint32_t bad = (bad_tiles >> ((lane >> 4) & 1) & 1) ? 0x7fc00000u : 0u;
+                bad_tiles >>= 2;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) ksl[g] = __uint_as_float(ks[g / 4][g % 4] | bad);
+#pragma unroll
+                for (int i = 0; i < NL; ++i) vsl[i] = __uint_as_float(vs[i / 2][i % 2]);
+            }
             uint32_t q_at = q_lane;
             pin(q_at);  // (its pieces' addresses are worked out as they are needed, not kept)
             uint32_t vis[T];
@@ -413,7 +562,6 @@ __global__ __launch_bounds__(kThreads, 2) void cache4_tree_kernel(TreeArgs args)
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 unsure |= __float_as_uint(ksl[g]) == kZeroScale;
-                ksl[g] = __uint_as_float(__float_as_uint(ksl[g]) | bad);
             }
             if (__builtin_expect(__any(unsure), 0)) drop_zero_keys();
 #pragma unroll
@@ -430,7 +578,7 @@ __global__ __launch_bounds__(kThreads, 2) void cache4_tree_kernel(TreeArgs args)
                 }
                 if (__builtin_expect(__any(nan), 0)) mark_nan(vis);
                 if (!kMasked) {
-                    if (__any(zero)) drop_zero_values();
+                    if (__any(zero)) drop_zero_values(here);
                     raise();
                 }
             }
@@ -456,9 +604,9 @@ __global__ __launch_bounds__(kThreads, 2) void cache4_tree_kernel(TreeArgs args)
                 const int g = 2 * i + h;
                 if (g < NG) {
                     if (kMasked)
-                        vs32[wave][g][r32] = vsl[i];
+                        vscale[wave][g][r32] = vsl[i];
                     else  // times 2^(15 - ve)
-                        vs16[wave][g][at] = (_Float16)(vsl[i] * __uint_as_float((269u << 23) + kTopBits - vtop[i]));
+                        reinterpret_cast<_Float16*>(vscale[wave][g])[at] = (_Float16)(vsl[i] * __uint_as_float((269u << 23) + kTopBits - vtop[i]));
                 }
             }
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");  // other lanes read them
@@ -473,20 +621,25 @@ __global__ __launch_bounds__(kThreads, 2) void cache4_tree_kernel(TreeArgs args)
 #pragma unroll
             for (int k = 0; k < 2 * NC; ++k) {
                 const int i = k >> 1, g = 32 * i / G;
-                const uint32_t w = kw[(k & 1) * (NC / 4 > 0 ? NC / 4 : 1) + i / 4][i % 4], y = w >> 8;
+                // (pins: else all keys are expanded ahead of the matrix instructions, and spill)
+                uint32_t w = kw[(k & 1) * kHalf + i / 4][i % 4];
+                pin(w);
+                const uint32_t y = w >> 8;
                 const uint32_t c[4] = {scaled(w & 0x000f000fu, ks[g], kb[g]), scaled(w & 0x00f000f0u, kh[g], kb[g]),
                                        scaled(y & 0x000f000fu, ks[g], kb[g]), scaled(y & 0x00f000f0u, kh[g], kb[g])};
                 const f16x8_t key = operand(c);
 #pragma unroll
-                for (int n = 0; n < T; ++n)
+                for (int n = 0; n < T; ++n) {
                     s[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                        key, lds_piece((q_at ^ (32 * k)) + 32 * n * kPieces * 16), s[n], 0, 0, 0);
-                __builtin_amdgcn_sched_barrier(0);  // else all keys are expanded ahead, and spill
+                        key,
+                        *reinterpret_cast<const f16x8_t*>(shared + (q_at ^ (32 * k)) + 32 * n * kPieces * 16), s[n], 0,
+                        0, 0);
+                    pin(s[n]);
+                }
             }
             f32x4_t kf[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) kf[i] = *reinterpret_cast<const f32x4_t*>(&kpow[wave][8 * i + 4 * h]);
-            if (t0 + kStride < stop) load_k(t0 + kStride);
 
             // weights
             f16x8_t p[T][2];
@@ -496,13 +649,13 @@ __global__ __launch_bounds__(kThreads, 2) void cache4_tree_kernel(TreeArgs args)
                 float mx = -INFINITY;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    s[n][e] *= kf[e >> 2][e & 3] * logit[n];
+                    s[n][e] *= kf[e >> 2][e & 3];
                     if (kMasked && !(vis[n] >> (8 * (e >> 2) + 4 * h + (e & 3)) & 1)) s[n][e] = -INFINITY;
                     mx = fmaxf(mx, s[n][e]);
                 }
                 float y0, y1;
                 row_pair(mx, true, y0, y1);
-                mx = fmaxf(y0, y1);
+                mx = fmaxf(y0, y1) * logit[n];
                 float alpha = 1.0f;
                 if (__any(mx > m[n] + 8.0f)) {
                     const float mn = mx > m[n] + 8.0f ? mx : m[n];
@@ -519,7 +672,7 @@ __global__ __launch_bounds__(kThreads, 2) void cache4_tree_kernel(TreeArgs args)
                 float sum = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    s[n][e] = __builtin_amdgcn_exp2f(s[n][e] - base);
+                    s[n][e] = __builtin_amdgcn_exp2f(fmaf(s[n][e], logit[n], -base));
                     sum += s[n][e];
                 }
                 if constexpr (kMasked) {
@@ -535,6 +688,7 @@ __global__ __launch_bounds__(kThreads, 2) void cache4_tree_kernel(TreeArgs args)
                 }
             }
             // O^T = V^T P^T
+            read_words(here);
 #pragma unroll
             for (int e = 0; e < 16; ++e)
 #pragma unroll
@@ -544,7 +698,7 @@ __global__ __launch_bounds__(kThreads, 2) void cache4_tree_kernel(TreeArgs args)
                 for (int g = 0; g < NG; ++g) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const uint4 sv = *reinterpret_cast<const uint4*>(&vs16[wave][g][16 * i + 8 * h]);
+                        const uint4 sv = *reinterpret_cast<const uint4*>(&vscale[wave][g][8 * i + 4 * h]);
                         const f16x2_t sc[4] = {f16x2_of(sv.x), f16x2_of(sv.y), f16x2_of(sv.z), f16x2_of(sv.w)};
                         f16x2_t bias[4];
 #pragma unroll
@@ -575,7 +729,7 @@ __global__ __launch_bounds__(kThreads, 2) void cache4_tree_kernel(TreeArgs args)
                         float t[16], high = 0.0f;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const f32x4_t v = *reinterpret_cast<const f32x4_t*>(&vs32[wave][g][8 * i + 4 * h]);
+                            const f32x4_t v = *reinterpret_cast<const f32x4_t*>(&vscale[wave][g][8 * i + 4 * h]);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 t[4 * i + e] = s[n][4 * i + e] * 0x1p-14f * v[e];
@@ -605,10 +759,6 @@ __global__ __launch_bounds__(kThreads, 2) void cache4_tree_kernel(TreeArgs args)
                     }
                 }
             }
-            if (t0 + kStride < stop) {
-                load_v(t0 + kStride);
-                load_pages(t0 + 2 * kStride);
-            }
         };
         // from sums of weights and values in units of the groups to means
         const auto to_means = [&]() __attribute__((always_inline)) {
@@ -632,51 +782,55 @@ __global__ __launch_bounds__(kThreads, 2) void cache4_tree_kernel(TreeArgs args)
         to_means();
         for (; t0 < stop; t0 += kStride) step(std::true_type{}, t0);
 
-        // join the waves: the upper half into the lower, and so on
+        // join the waves, a tile of rows at a time: the upper half into the lower, and so on
         float* const join = reinterpret_cast<float*>(shared);
-        const auto put = [&](float* dst) {
+        const auto put = [&](int n, int j0, float m1, float l1, float* dst) {
 #pragma unroll
-            for (int n = 0; n < T; ++n) {
+            for (int j = 0; j < kCols; ++j)
 #pragma unroll
-                for (int j = 0; j < NC; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        *reinterpret_cast<f32x4_t*>(dst + (((n * NC + j) * 4 + e) * kWave + lane) * 4) =
-                            (f32x4_t){o[n][j][4 * e], o[n][j][4 * e + 1], o[n][j][4 * e + 2], o[n][j][4 * e + 3]};
-                dst[(T * NC * 16 + 2 * n) * kWave + lane] = m[n];
-                dst[(T * NC * 16 + 2 * n + 1) * kWave + lane] = l[n];
-            }
+                for (int e = 0; e < 4; ++e)
+                    *reinterpret_cast<f32x4_t*>(dst + ((j * 4 + e) * kWave + lane) * 4) =
+                        (f32x4_t){o[n][j0 + j][4 * e], o[n][j0 + j][4 * e + 1], o[n][j0 + j][4 * e + 2],
+                                  o[n][j0 + j][4 * e + 3]};
+            dst[kCols * 16 * kWave + lane] = m1;
+            dst[(kCols * 16 + 1) * kWave + lane] = l1;
         };
-        const auto add = [&](const float* src) {
+        const auto add = [&](int n, int j0, const float* src, float& m1, float& l1) {
+            const float m2 = src[kCols * 16 * kWave + lane];
+            const float l2 = src[(kCols * 16 + 1) * kWave + lane];
+            const float mn = fmaxf(m1, m2);
+            const float base = mn == -INFINITY ? 0.0f : mn;
+            const float w1 = l1 * __builtin_amdgcn_exp2f(m1 - base), w2 = l2 * __builtin_amdgcn_exp2f(m2 - base);
+            l1 = w1 + w2;
+            m1 = mn;
+            const float inv = l1 == 0.0f ? 0.0f : 1.0f / l1;
+            const float f1 = w1 * inv, f2 = w2 * inv;
 #pragma unroll
-            for (int n = 0; n < T; ++n) {
-                const float m2 = src[(T * NC * 16 + 2 * n) * kWave + lane];
-                const float l2 = src[(T * NC * 16 + 2 * n + 1) * kWave + lane];
-                const float mn = fmaxf(m[n], m2);
-                const float base = mn == -INFINITY ? 0.0f : mn;
-                const float w1 = l[n] * __builtin_amdgcn_exp2f(m[n] - base), w2 = l2 * __builtin_amdgcn_exp2f(m2 - base);
-                l[n] = w1 + w2;
-                const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];
-                const float f1 = w1 * inv, f2 = w2 * inv;
+            for (int j = 0; j < kCols; ++j)
 #pragma unroll
-                for (int j = 0; j < NC; ++j)
+                for (int e = 0; e < 4; ++e) {
+                    const f32x4_t v = *reinterpret_cast<const f32x4_t*>(src + ((j * 4 + e) * kWave + lane) * 4);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const f32x4_t v =
-                            *reinterpret_cast<const f32x4_t*>(src + (((n * NC + j) * 4 + e) * kWave + lane) * 4);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[n][j][4 * e + i] = fmaf(v[i], f2, o[n][j][4 * e + i] * f1);
-                    }
-                m[n] = mn;
-            }
+                    for (int i = 0; i < 4; ++i)
+                        o[n][j0 + j][4 * e + i] = fmaf(v[i], f2, o[n][j0 + j][4 * e + i] * f1);
+                }
         };
         __syncthreads();  // q is read no more
 #pragma unroll
-        for (int n = kWaves / 2; n > 0; n >>= 1) {
-            if (wave >= n && wave < 2 * n) put(join + (wave - n) * kPartFloats);
-            __syncthreads();
-            if (wave < n) add(join + wave * kPartFloats);
-            __syncthreads();
+        for (int n = 0; n < T; ++n) {
+            float m1 = m[n], l1 = l[n];
+#pragma unroll
+            for (int j0 = 0; j0 < NC; j0 += kCols) {
+                m1 = m[n], l1 = l[n];
+#pragma unroll
+                for (int k = kWaves / 2; k > 0; k >>= 1) {
+                    if (wave >= k && wave < 2 * k) put(n, j0, m1, l1, join + (wave - k) * kPartFloats);
+                    __syncthreads();
+                    if (wave < k) add(n, j0, join + wave * kPartFloats, m1, l1);
+                    __syncthreads();
+                }
+            }
+            m[n] = m1, l[n] = l1;
         }
         if (wave == 0) {
 #pragma unroll
