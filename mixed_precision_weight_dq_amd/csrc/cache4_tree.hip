@@ -198,15 +198,15 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
     constexpr int NL = (NG + 1) / 2;               // value scales of a lane
     constexpr int VW = D / 128 > 0 ? D / 128 : 1;  // value words of a lane and position
     constexpr int kPieces = D / 8;                 // of a row of q in LDS
-    constexpr int kCols = NC / 2;                       // tiles of the output that the waves join at a time
-    constexpr int kPartFloats = (kCols * 16 + 2) * kWave;  // a wave's result for them and a tile of rows
-    constexpr int kShared = kWaves / 2 * kPartFloats * 4 > C::kRows * D * 2 ? kWaves / 2 * kPartFloats * 4
-                                                                           : C::kRows * D * 2;
+    constexpr int kCols = T == 1 && D != 256 ? 1 : 2;  // tiles of the output that the waves join at a time
+    constexpr int kJoin = kWaves * kCols * 4096;
+    constexpr int kShared = kJoin > C::kRows * D * 2 ? kJoin : C::kRows * D * 2;
     // the rows of q, and, at the end of a unit, the waves' results
     __shared__ __attribute__((aligned(16))) char shared[kShared];
     __shared__ float logits[C::kRows];
     __shared__ __attribute__((aligned(16))) float kpow[kWaves][32];
-    __shared__ __attribute__((aligned(16))) float vscale[kWaves][NG][32];  // (or halves, unless masked)
+    __shared__ __attribute__((aligned(16))) float vscale[kWaves][NG][32];  // (masked), or halves: scales, biases
+    __shared__ float2 sums[kWaves][T][32];
     __shared__ __attribute__((aligned(128))) char ring[kWaves][S][R::kBytes];
     uint4* const qs = reinterpret_cast<uint4*>(shared);
 
@@ -419,7 +419,6 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
         uint32_t vtop[NL];
 #pragma unroll
         for (int i = 0; i < NL; ++i) vtop[i] = (16u << 23) + kTopBits;  // ve = -111
-        bool means = false;  // o is sum p v / sum p as it is, l the whole row's (masked steps)
         const auto group_unit = [&](int g) {
             return pow2((int)(__builtin_amdgcn_readlane(vtop[g / 2], 32 * (g & 1)) >> 23) - 127);
         };
@@ -603,10 +602,14 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
             for (int i = 0; i < NL; ++i) {
                 const int g = 2 * i + h;
                 if (g < NG) {
-                    if (kMasked)
+                    if (kMasked) {
                         vscale[wave][g][r32] = vsl[i];
-                    else  // times 2^(15 - ve)
-                        reinterpret_cast<_Float16*>(vscale[wave][g])[at] = (_Float16)(vsl[i] * __uint_as_float((269u << 23) + kTopBits - vtop[i]));
+                    } else {  // times 2^(15 - ve)
+                        _Float16* const to = reinterpret_cast<_Float16*>(vscale[wave][g]) + at;
+                        const _Float16 v = (_Float16)(vsl[i] * __uint_as_float((269u << 23) + kTopBits - vtop[i]));
+                        to[0] = v;
+                        to[32] = v * (_Float16)-0x1p-17f;
+                    }
                 }
             }
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");  // other lanes read them
@@ -618,9 +621,21 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
             for (int n = 0; n < T; ++n)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) s[n][e] = 0.0f;
+            // (a step's first operands of q are read ahead, each pair's next ones before its matrix
+            // instructions: their latency is not waited for)
+            f16x8_t qf[2][T];
+            const auto read_q = [&](int k) __attribute__((always_inline)) {
+#pragma unroll
+                for (int n = 0; n < T; ++n)
+                    qf[k & 1][n] =
+                        *reinterpret_cast<const f16x8_t*>(shared + (q_at ^ (32 * k)) + 32 * n * kPieces * 16);
+            };
+            read_q(0);
 #pragma unroll
             for (int k = 0; k < 2 * NC; ++k) {
                 const int i = k >> 1, g = 32 * i / G;
+                if (k + 1 < 2 * NC) read_q(k + 1);
+                __builtin_amdgcn_sched_barrier(0);
                 // (pins: else all keys are expanded ahead of the matrix instructions, and spill)
                 uint32_t w = kw[(k & 1) * kHalf + i / 4][i % 4];
                 pin(w);
@@ -630,10 +645,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
                 const f16x8_t key = operand(c);
 #pragma unroll
                 for (int n = 0; n < T; ++n) {
-                    s[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                        key,
-                        *reinterpret_cast<const f16x8_t*>(shared + (q_at ^ (32 * k)) + 32 * n * kPieces * 16), s[n], 0,
-                        0, 0);
+                    s[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(key, qf[k & 1][n], s[n], 0, 0, 0);
                     pin(s[n]);
                 }
             }
@@ -668,7 +680,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
                     }
                 }
                 // weights up to 2^14: fp16's normal range then reaches 2^-20 of the largest
-                const float base = m[n] == -INFINITY ? 0.0f : m[n] - 6.0f;
+                // (masked steps, whose weights meet fp32 scales first, 2^-14 of that)
+                const float base = m[n] == -INFINITY ? 0.0f : m[n] - (kMasked ? -8.0f : 6.0f);
                 float sum = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
@@ -678,7 +691,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
                 if constexpr (kMasked) {
                     row_pair(sum, true, y0, y1);
                     const float old = l[n] * alpha;
-                    l[n] = old + (y0 + y1);
+                    l[n] = fmaf(y0 + y1, 0x1p14f, old);
                     inv[n] = l[n] > 0.0f ? 1.0f / l[n] : l[n];  // (0 and NaN stay)
                     carry[n] = l[n] == 0.0f ? 1.0f : old * inv[n];
                 } else {
@@ -699,11 +712,9 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const uint4 sv = *reinterpret_cast<const uint4*>(&vscale[wave][g][8 * i + 4 * h]);
+                        const uint4 bv = *reinterpret_cast<const uint4*>(&vscale[wave][g][16 + 8 * i + 4 * h]);
                         const f16x2_t sc[4] = {f16x2_of(sv.x), f16x2_of(sv.y), f16x2_of(sv.z), f16x2_of(sv.w)};
-                        f16x2_t bias[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            bias[e] = sc[e] * (f16x2_t){(_Float16)-0x1p-17f, (_Float16)-0x1p-17f};
+                        const f16x2_t bias[4] = {f16x2_of(bv.x), f16x2_of(bv.y), f16x2_of(bv.z), f16x2_of(bv.w)};
 #pragma unroll
                         for (int j = g * G / 32; j < (g + 1) * G / 32; ++j) {
                             const f16x8_t v = value_operand(i, j, sc, bias);
@@ -732,14 +743,14 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
                             const f32x4_t v = *reinterpret_cast<const f32x4_t*>(&vscale[wave][g][8 * i + 4 * h]);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                t[4 * i + e] = s[n][4 * i + e] * 0x1p-14f * v[e];
+                                t[4 * i + e] = s[n][4 * i + e] * v[e];
                                 high = fmaxf(high, fabsf(t[4 * i + e]));
                             }
                         }
                         float y0, y1;
                         row_pair(high, true, y0, y1);
                         const int tx = max(exponent(fmaxf(y0, y1)), -112);
-                        const float up = pow2(14 - tx), back = pow2(tx), part = inv[n] * 32.0f;
+                        const float up = pow2(14 - tx), back = pow2(tx) * (inv[n] * 32.0f);
                         f16x8_t pf[2];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) pf[e >> 3][e & 7] = (_Float16)(t[e] * up);
@@ -754,7 +765,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
                                                                            0, 0);
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
-                                o[n][j][e] = fmaf(z[e] * part, back, o[n][j][e] * carry[n]);
+                                o[n][j][e] = fmaf(z[e], back, o[n][j][e] * carry[n]);
                         }
                     }
                 }
@@ -775,96 +786,74 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
                     for (int j = g * G / 32; j < (g + 1) * G / 32; ++j) o[n][j] = o[n][j] * (inv * 32.0f) * unit;
                 }
             }
-            means = true;
         };
 
-        for (; t0 < stop && t0 + kStep <= context; t0 += kStride) step(std::false_type{}, t0);
-        to_means();
+        if (t0 < stop && t0 + kStep <= context) {
+            do {
+                step(std::false_type{}, t0);
+                t0 += kStride;
+            } while (t0 < stop && t0 + kStep <= context);
+            to_means();
+        }
         for (; t0 < stop; t0 += kStride) step(std::true_type{}, t0);
 
-        // join the waves, a tile of rows at a time: the upper half into the lower, and so on
-        float* const join = reinterpret_cast<float*>(shared);
-        const auto put = [&](int n, int j0, float m1, float l1, float* dst) {
+        // Join the waves, kCols tiles of the output at a time: each wave takes the rows of four dimensions in
+        // 16 from all of them.
+        f32x4_t* const join = reinterpret_cast<f32x4_t*>(shared);
+        if (h == 0) {
 #pragma unroll
-            for (int j = 0; j < kCols; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    *reinterpret_cast<f32x4_t*>(dst + ((j * 4 + e) * kWave + lane) * 4) =
-                        (f32x4_t){o[n][j0 + j][4 * e], o[n][j0 + j][4 * e + 1], o[n][j0 + j][4 * e + 2],
-                                  o[n][j0 + j][4 * e + 3]};
-            dst[kCols * 16 * kWave + lane] = m1;
-            dst[(kCols * 16 + 1) * kWave + lane] = l1;
-        };
-        const auto add = [&](int n, int j0, const float* src, float& m1, float& l1) {
-            const float m2 = src[kCols * 16 * kWave + lane];
-            const float l2 = src[(kCols * 16 + 1) * kWave + lane];
-            const float mn = fmaxf(m1, m2);
-            const float base = mn == -INFINITY ? 0.0f : mn;
-            const float w1 = l1 * __builtin_amdgcn_exp2f(m1 - base), w2 = l2 * __builtin_amdgcn_exp2f(m2 - base);
-            l1 = w1 + w2;
-            m1 = mn;
-            const float inv = l1 == 0.0f ? 0.0f : 1.0f / l1;
-            const float f1 = w1 * inv, f2 = w2 * inv;
-#pragma unroll
-            for (int j = 0; j < kCols; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const f32x4_t v = *reinterpret_cast<const f32x4_t*>(src + ((j * 4 + e) * kWave + lane) * 4);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        o[n][j0 + j][4 * e + i] = fmaf(v[i], f2, o[n][j0 + j][4 * e + i] * f1);
-                }
-        };
+            for (int n = 0; n < T; ++n) sums[wave][n][r32] = make_float2(m[n], l[n]);
+        }
         __syncthreads();  // q is read no more
 #pragma unroll
         for (int n = 0; n < T; ++n) {
-            float m1 = m[n], l1 = l[n];
+            float top = -INFINITY, tot = 0.0f, f[kWaves];
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) top = fmaxf(top, sums[w][n][r32].x);
+            const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                const float2 ml = sums[w][n][r32];
+                f[w] = ml.y * __builtin_amdgcn_exp2f(ml.x - base);
+                tot += f[w];
+            }
+            const float inv = nothing ? __uint_as_float(0x7fc00000u) : (tot == 0.0f ? 0.0f : 1.0f / tot);
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) f[w] *= inv;
+            int64_t token;
+            int head;
+            row_at(32 * n + r32, token, head);
+            const bool live = r0 + 32 * n + r32 < rows;
+            const int64_t at = ((int64_t)group * 2 + slot) * C::kRows + 32 * n + r32;
+            if (!whole && live && wave == 0 && h == 0) a.part_ml[at] = make_float2(top, tot);
+            const int64_t place = (whole ? token * a.q_heads + head : at) * D + 8 * wave + 4 * h;
 #pragma unroll
             for (int j0 = 0; j0 < NC; j0 += kCols) {
-                m1 = m[n], l1 = l[n];
 #pragma unroll
-                for (int k = kWaves / 2; k > 0; k >>= 1) {
-                    if (wave >= k && wave < 2 * k) put(n, j0, m1, l1, join + (wave - k) * kPartFloats);
-                    __syncthreads();
-                    if (wave < k) add(n, j0, join + wave * kPartFloats, m1, l1);
-                    __syncthreads();
+                for (int j = 0; j < kCols; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        join[((wave * kCols + j) * 4 + e) * kWave + lane] =
+                            (f32x4_t){o[n][j0 + j][4 * e], o[n][j0 + j][4 * e + 1], o[n][j0 + j][4 * e + 2],
+                                      o[n][j0 + j][4 * e + 3]};
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < kCols; ++j) {
+                    f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int w = 0; w < kWaves; ++w) {
+                        const f32x4_t x = join[((w * kCols + j) * 4 + wave) * kWave + lane];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] = fmaf(x[e], f[w], v[e]);
+                    }
+                    if (!live) continue;
+                    if (whole)
+                        *reinterpret_cast<uint2*>(a.out + place + 32 * (j0 + j)) =
+                            make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+                    else
+                        *reinterpret_cast<f32x4_t*>(a.part + place + 32 * (j0 + j)) = v;
                 }
-            }
-            m[n] = m1, l[n] = l1;
-        }
-        if (wave == 0) {
-#pragma unroll
-            for (int n = 0; n < T; ++n) {
-                if (r0 + 32 * n + r32 >= rows) continue;
-                if (nothing) {
-#pragma unroll
-                    for (int j = 0; j < NC; ++j)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o[n][j][e] = __uint_as_float(0x7fc00000u);
-                }
-                if (whole) {
-                    int64_t token;
-                    int head;
-                    row_at(32 * n + r32, token, head);
-                    uint16_t* op = a.out + (token * a.q_heads + head) * D + 4 * h;
-#pragma unroll
-                    for (int j = 0; j < NC; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            *reinterpret_cast<uint2*>(op + 32 * j + 8 * e) =
-                                make_uint2(bf16x2(o[n][j][4 * e], o[n][j][4 * e + 1]),
-                                           bf16x2(o[n][j][4 * e + 2], o[n][j][4 * e + 3]));
-                } else {
-                    const int64_t at = ((int64_t)group * 2 + slot) * C::kRows + 32 * n + r32;
-                    float* pp = a.part + at * D + 4 * h;
-#pragma unroll
-                    for (int j = 0; j < NC; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            *reinterpret_cast<f32x4_t*>(pp + 32 * j + 8 * e) =
-                                (f32x4_t){o[n][j][4 * e], o[n][j][4 * e + 1], o[n][j][4 * e + 2], o[n][j][4 * e + 3]};
-                    if (h == 0) a.part_ml[at] = make_float2(m[n], l[n]);
-                }
+                __syncthreads();
             }
         }
     }
