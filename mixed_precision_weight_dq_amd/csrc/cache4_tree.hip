@@ -155,36 +155,36 @@ template <int D>
 __device__ __forceinline__ void read_values(const uint32_t (&v)[4], uint32_t (&w)[16][D == 256 ? 2 : 1])
 {
     constexpr int kTile = Ring<D, D == 64 ? 64 : 128>::kCodes, kHalf = kTile / 2;
-#define READ8(OP, C, W, T)                                                                                   \
-    asm volatile(OP " %0, %8 offset:%12\n\t" OP " %1, %9 offset:%12\n\t" OP " %2, %10 offset:%12\n\t" OP    \
-                    " %3, %11 offset:%12\n\t" OP " %4, %8 offset:%13\n\t" OP " %5, %9 offset:%13\n\t" OP      \
-                    " %6, %10 offset:%13\n\t" OP " %7, %11 offset:%13\n\ts_waitcnt lgkmcnt(0)"               \
-                 : "=&v"(W[0] C), "=&v"(W[1] C), "=&v"(W[2] C), "=&v"(W[3] C), "=&v"(W[4] C), "=&v"(W[5] C), \
-                   "=&v"(W[6] C), "=&v"(W[7] C)                                                              \
-                 : "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "n"(T), "n"(T + kHalf)                        \
+#define READ16(OP, W)                                                                                        \
+    asm volatile(OP " %0, %16\n\t" OP " %1, %17\n\t" OP " %2, %18\n\t" OP " %3, %19\n\t" OP                   \
+                    " %4, %16 offset:%20\n\t" OP " %5, %17 offset:%20\n\t" OP " %6, %18 offset:%20\n\t" OP   \
+                    " %7, %19 offset:%20\n\t" OP " %8, %16 offset:%21\n\t" OP " %9, %17 offset:%21\n\t" OP   \
+                    " %10, %18 offset:%21\n\t" OP " %11, %19 offset:%21\n\t" OP " %12, %16 offset:%22\n\t" OP \
+                    " %13, %17 offset:%22\n\t" OP " %14, %18 offset:%22\n\t" OP " %15, %19 offset:%22\n\t"   \
+                    "s_waitcnt lgkmcnt(0)"                                                                   \
+                 : "=&v"(W[0]), "=&v"(W[1]), "=&v"(W[2]), "=&v"(W[3]), "=&v"(W[4]), "=&v"(W[5]),             \
+                   "=&v"(W[6]), "=&v"(W[7]), "=&v"(W[8]), "=&v"(W[9]), "=&v"(W[10]), "=&v"(W[11]),           \
+                   "=&v"(W[12]), "=&v"(W[13]), "=&v"(W[14]), "=&v"(W[15])                                    \
+                 : "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "n"(kHalf), "n"(kTile), "n"(kTile + kHalf)    \
                  : "memory")
     if constexpr (D == 256) {
-        u32x2_t t[2][8];
-        READ8("ds_read_b64", , t[0], 0);
-        READ8("ds_read_b64", , t[1], kTile);
+        u32x2_t t[16];
+        READ16("ds_read_b64", t);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-            w[e][0] = t[e >> 3][e & 7].x;
-            w[e][1] = t[e >> 3][e & 7].y;
+            w[e][0] = t[e].x;
+            w[e][1] = t[e].y;
         }
     } else {
-        uint32_t t[2][8];
-        if constexpr (D == 64) {
-            READ8("ds_read_u16", , t[0], 0);
-            READ8("ds_read_u16", , t[1], kTile);
-        } else {
-            READ8("ds_read_b32", , t[0], 0);
-            READ8("ds_read_b32", , t[1], kTile);
-        }
+        uint32_t t[16];
+        if constexpr (D == 64)
+            READ16("ds_read_u16", t);
+        else
+            READ16("ds_read_b32", t);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) w[e][0] = t[e >> 3][e & 7];
+        for (int e = 0; e < 16; ++e) w[e][0] = t[e];
     }
-#undef READ8
+#undef READ16
 }
 
 template <int D, int G, int T>
@@ -652,6 +652,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
             f32x4_t kf[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) kf[i] = *reinterpret_cast<const f32x4_t*>(&kpow[wave][8 * i + 4 * h]);
+            __builtin_amdgcn_sched_barrier(0);
+            read_words(here);  // (their latency runs beside the matrix instructions')
 
             // weights
             f16x8_t p[T][2];
@@ -701,28 +703,34 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
                 }
             }
             // O^T = V^T P^T
-            read_words(here);
 #pragma unroll
             for (int e = 0; e < 16; ++e)
 #pragma unroll
                 for (int w = 0; w < VW; ++w) vw[e][w] = (vw[e][w] << nibble) & 0xf0f0f0f0u;
             if constexpr (!kMasked) {
+                // scales and biases of half i of group g, read a pair ahead
+                uint4 sv[2], bv[2];
+                const auto read_scales = [&](int k) __attribute__((always_inline)) {
+                    const float* at = &vscale[wave][k >> 1][8 * (k & 1) + 4 * h];
+                    sv[k & 1] = *reinterpret_cast<const uint4*>(at);
+                    bv[k & 1] = *reinterpret_cast<const uint4*>(at + 16);
+                };
+                read_scales(0);
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
+                for (int k = 0; k < 2 * NG; ++k) {
+                    const int g = k >> 1, i = k & 1;
+                    if (k + 1 < 2 * NG) read_scales(k + 1);
+                    __builtin_amdgcn_sched_barrier(0);
+                    const f16x2_t sc[4] = {f16x2_of(sv[i].x), f16x2_of(sv[i].y), f16x2_of(sv[i].z), f16x2_of(sv[i].w)};
+                    const f16x2_t bias[4] = {f16x2_of(bv[i].x), f16x2_of(bv[i].y), f16x2_of(bv[i].z),
+                                             f16x2_of(bv[i].w)};
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint4 sv = *reinterpret_cast<const uint4*>(&vscale[wave][g][8 * i + 4 * h]);
-                        const uint4 bv = *reinterpret_cast<const uint4*>(&vscale[wave][g][16 + 8 * i + 4 * h]);
-                        const f16x2_t sc[4] = {f16x2_of(sv.x), f16x2_of(sv.y), f16x2_of(sv.z), f16x2_of(sv.w)};
-                        const f16x2_t bias[4] = {f16x2_of(bv.x), f16x2_of(bv.y), f16x2_of(bv.z), f16x2_of(bv.w)};
+                    for (int j = g * G / 32; j < (g + 1) * G / 32; ++j) {
+                        const f16x8_t v = value_operand(i, j, sc, bias);
 #pragma unroll
-                        for (int j = g * G / 32; j < (g + 1) * G / 32; ++j) {
-                            const f16x8_t v = value_operand(i, j, sc, bias);
-#pragma unroll
-                            for (int n = 0; n < T; ++n)
-                                o[n][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[n][i], o[n][j], 0, 0, 0);
-                            __builtin_amdgcn_sched_barrier(0);
-                        }
+                        for (int n = 0; n < T; ++n)
+                            o[n][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[n][i], o[n][j], 0, 0, 0);
+                        __builtin_amdgcn_sched_barrier(0);
                     }
                 }
             } else {
