@@ -685,15 +685,6 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : (D == 128 ? 3 : 2)) void ca
 // whole units (200 for 256 CUs, 32 to 47 steps) 268 us.
 
 constexpr int kValueShift = 24;  // keeps a weight (up to 2^14) times a value's power of two in fp32
-// every wave's LDS operations done, then the barrier (loads stay in flight)
-__device__ __forceinline__ void lds_barrier()
-{
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));  // lgkmcnt(0)
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
-
 template <int D, int G, int NW>
 struct PromptTile {
     static constexpr int kRows = 32 * NW;

@@ -314,6 +314,15 @@ __device__ __forceinline__ int swizzle(int row)
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 
+// every wave's LDS operations done, then the barrier (loads stay in flight)
+__device__ __forceinline__ void lds_barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));  // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // A piece by its LDS address.
 typedef __attribute__((address_space(3))) const void lds_void;
 __device__ __forceinline__ uint32_t lds_address(const uint4* p)

@@ -287,9 +287,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
             stop = begin + __builtin_amdgcn_readfirstlane(take) * kStride;
         stop = __builtin_amdgcn_readfirstlane(stop);
         x += take;
-        const __attribute__((address_space(4))) int32_t* table =
-            (const __attribute__((address_space(4))) int32_t*)(
-                a.bt.table + __builtin_amdgcn_readfirstlane(b) * a.bt.width);
+        const int32_t* table = a.bt.table + __builtin_amdgcn_readfirstlane(b) * a.bt.width;
         // token row and query head of row r of the unit (of the first where there is none)
         const auto row_at = [&](int r, int64_t& token, int& head) {
             const int64_t row = r0 + r < rows ? r0 + r : 0;
@@ -298,20 +296,38 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
             head = kvh * rw.per + (int)(row - (int64_t)qi * rw.per);
         };
 
+        // the rows of q that the unit's threads have, asked for first: loads come back in order
+        constexpr int kPer = kThreads / C::kRows;  // threads of a row
+        constexpr int kMine = kPieces / kPer;      // pieces of a thread
+        uint4 qr[kMine];
+        {
+            int64_t token;
+            int head;
+            row_at(tid / kPer, token, head);
+            const uint16_t* qp = a.q + token * a.q_stride + (int64_t)head * D + tid % kPer * kMine * 8;
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) qr[i] = reinterpret_cast<const uint4*>(qp)[i];
+        }
+
         // ---- a step's copies into the ring
         uint32_t bad_tiles = 0;  // two bits for each step in flight: a tile whose page is outside the cache
-        int pg[2];
+        // Page numbers of 32 of the wave's steps, a tile's in each lane (scalar loads would count with the LDS
+        // operations, and a wait for those would wait for memory in every step).
+        int pages = 0, pages_from = 0;
         const auto tile_at = [&](int t) { return t < stop ? t : (stop - 1) & ~15; };
         const auto load_pages = [&](int t0) __attribute__((always_inline)) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) pg[i] = table[tile_at(t0 + 16 * i) >> shift];
+            pages = table[tile_at(t0 + (lane >> 1) * kStride + (lane & 1) * 16) >> shift];
+            pages_from = t0;
         };
         const auto copy = [&](int t0, char* to, int ahead) __attribute__((always_inline)) {
+            if (t0 - pages_from >= 32 * kStride) load_pages(t0);
+            const int at = (t0 - pages_from) / kStride * 2;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const bool ok = (unsigned)pg[i] < (unsigned)a.c.pages;
+                const int page = __builtin_amdgcn_readlane(pages, at + i);
+                const bool ok = (unsigned)page < (unsigned)a.c.pages;
                 bad_tiles |= (ok ? 0u : 1u) << (2 * ahead + i);
-                const int64_t block = (int64_t)(ok ? pg[i] : 0) * a.c.heads + kvh;
+                const int64_t block = (int64_t)(ok ? page : 0) * a.c.heads + kvh;
                 const int off = tile_at(t0 + 16 * i) & ((1 << shift) - 1);
                 const BufRef kb{a.c.k_codes + ((block << shift) + off) * (D / 8), R::kCodes};
                 const BufRef vb{a.c.v_codes + ((block << shift) + off) * (D / 8), R::kCodes};
@@ -337,11 +353,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
         if (t0 < stop) {
             load_pages(t0);
             copy(t0, mine, 0);
-            load_pages(t0 + kStride);
-            if (S > 2 && t0 + kStride < stop) {
-                copy(t0 + kStride, mine + R::kBytes, 1);
-                load_pages(t0 + 2 * kStride);
-            }
+            if (S > 2 && t0 + kStride < stop) copy(t0 + kStride, mine + R::kBytes, 1);
         }
         // what the step at hand has in registers
         u32x4_t kw[D == 256 ? 4 : 2];  // words (h NC + i), then ((2 + h) NC + i)
@@ -353,18 +365,10 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
         // ---- rows of q -> fp16 operands in LDS, each times a power of two (and the sign of the softmax's
         // scale, so that larger is always larger)
         {
-            constexpr int kPer = kThreads / C::kRows;  // threads of a row
-            constexpr int kMine = kPieces / kPer;      // pieces of a thread
             const int r = tid / kPer, sub = tid % kPer;
-            int64_t token;
-            int head;
-            row_at(r, token, head);
-            const uint16_t* qp = a.q + token * a.q_stride + (int64_t)head * D + sub * kMine * 8;
-            uint4 qr[kMine];
             uint32_t qmax = 0;
 #pragma unroll
             for (int i = 0; i < kMine; ++i) {
-                qr[i] = reinterpret_cast<const uint4*>(qp)[i];
                 const uint32_t u[4] = {qr[i].x, qr[i].y, qr[i].z, qr[i].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e)  // as integers: a NaN is the largest
@@ -396,7 +400,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
             // (a key is its codes times 2^(9 + the position's exponent) less than it is)
             if (sub == 0) logits[r] = logit * 512.0f;
         }
-        __syncthreads();
+        lds_barrier();
 
         // this lane's first operand: piece h of row r32 (its row is a multiple of 2 kPieces pieces
         // from the start, so piece 2 k + h is an exclusive or away)
@@ -521,7 +525,6 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
             const int free = stage == 0 ? S - 1 : stage - 1;
             if (t0 + (S - 1) * kStride < stop) {
                 copy(t0 + (S - 1) * kStride, mine + free * R::kBytes, S - 1);
-                load_pages(t0 + S * kStride);
                 wait_loads<(S - 1) * R::kLoads>();
             } else if (S > 2 && t0 + kStride < stop) {
                 wait_loads<R::kLoads>();
@@ -812,7 +815,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
 #pragma unroll
             for (int n = 0; n < T; ++n) sums[wave][n][r32] = make_float2(m[n], l[n]);
         }
-        __syncthreads();  // q is read no more
+        lds_barrier();  // q is read no more
 #pragma unroll
         for (int n = 0; n < T; ++n) {
             float top = -INFINITY, tot = 0.0f, f[kWaves];
@@ -844,7 +847,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
                         join[((wave * kCols + j) * 4 + e) * kWave + lane] =
                             (f32x4_t){o[n][j0 + j][4 * e], o[n][j0 + j][4 * e + 1], o[n][j0 + j][4 * e + 2],
                                       o[n][j0 + j][4 * e + 3]};
-                __syncthreads();
+                lds_barrier();
 #pragma unroll
                 for (int j = 0; j < kCols; ++j) {
                     f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -861,7 +864,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
                     else
                         *reinterpret_cast<f32x4_t*>(a.part + place + 32 * (j0 + j)) = v;
                 }
-                __syncthreads();
+                lds_barrier();
             }
         }
     }
