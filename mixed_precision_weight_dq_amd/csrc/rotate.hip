@@ -96,49 +96,61 @@ struct Piece {
     }
 };
 
-template <bool BF16>
+template <bool BF16, bool kInter>
 __global__ __launch_bounds__(kThreads) void rotate_kernel(RotateArgs a)
 {
+    constexpr int kDeep = 4;  // heads whose pieces are in flight
     uint32_t slot, lane;
     int64_t token;
     if (!rotate_place(a, slot, lane, token)) return;
     const int groups = a.rope.dims / 16;
     const bool turned = (int)slot < groups;
-    const bool inter = a.rope.interleaved;
     // the slot's pieces: rotated, or the ones behind them, two by two
-    const int d0 = turned ? (inter ? 16 : 8) * (int)slot : a.rope.dims + 16 * ((int)slot - groups);
-    const int d1 = turned && !inter ? d0 + a.rope.dims / 2 : d0 + 8;
+    const int d0 = turned ? (kInter ? 16 : 8) * (int)slot : a.rope.dims + 16 * ((int)slot - groups);
+    const int d1 = turned && !kInter ? d0 + a.rope.dims / 2 : d0 + 8;
     const bool second = d1 < a.dim;
+    const int64_t from = token * a.x_token, to = token * a.out_token;
+    Piece<BF16> p0[kDeep], p1[kDeep];
+    const auto load = [&](int h) __attribute__((always_inline)) {
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) {
+            const int64_t n = h + k * (int)a.lanes < a.heads ? h + k * (int)a.lanes : h;  // (the first again)
+            p0[k].load(a.x, from + n * a.x_head + d0);
+            p1[k].load(a.x, from + n * a.x_head + (second ? d1 : d0));
+        }
+    };
+    load(lane);
     float c[8], s[8];
     if (turned) {
         const int32_t pos = a.positions[token];
 #pragma unroll
         for (int i = 0; i < 8; ++i) rotate_turn(a.rope, pos, 8 * (int)slot + i, c[i], s[i]);
     }
-    for (int h = lane; h < a.heads; h += a.lanes) {
-        const int64_t from = token * a.x_token + h * a.x_head;
-        const int64_t to = token * a.out_token + h * a.out_head;
-        Piece<BF16> p0, p1;
-        p0.load(a.x, from + d0);
-        if (second) p1.load(a.x, from + d1);
-        if (turned) {
-            float x[8], y[8];
-            p0.floats(x);
-            p1.floats(y);
+    for (int h = lane; h < a.heads; h += kDeep * a.lanes) {
+        if (h != (int)lane) load(h);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                // pair i: an element of each piece, or two neighbours
-                float& u = inter ? (i < 4 ? x[2 * (i & 3)] : y[2 * (i & 3)]) : x[i];
-                float& v = inter ? (i < 4 ? x[2 * (i & 3) + 1] : y[2 * (i & 3) + 1]) : y[i];
-                const float p = u, q = v;
-                u = fmaf(p, c[i], -q * s[i]);
-                v = fmaf(q, c[i], p * s[i]);
+        for (int k = 0; k < kDeep; ++k) {
+            const int64_t n = h + k * (int)a.lanes;
+            if (n >= a.heads) break;
+            if (turned) {
+                float x[8], y[8];
+                p0[k].floats(x);
+                p1[k].floats(y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    // pair i: an element of each piece, or two neighbours
+                    float& u = !kInter ? x[i] : (i < 4 ? x[2 * (i & 3)] : y[2 * (i & 3)]);
+                    float& v = !kInter ? y[i] : (i < 4 ? x[2 * (i & 3) + 1] : y[2 * (i & 3) + 1]);
+                    const float p = u, q = v;
+                    u = fmaf(p, c[i], -q * s[i]);
+                    v = fmaf(q, c[i], p * s[i]);
+                }
+                p0[k].set(x);
+                p1[k].set(y);
             }
-            p0.set(x);
-            p1.set(y);
+            p0[k].store(a.out, to + n * a.out_head + d0);
+            if (second) p1[k].store(a.out, to + n * a.out_head + d1);
         }
-        p0.store(a.out, to + d0);
-        if (second) p1.store(a.out, to + d1);
     }
 }
 
@@ -208,7 +220,9 @@ hipError_t launch_rotate(const Rope& rope, const void* x, bool bf16, int64_t tok
         a.tokens = (uint32_t)(tokens - from < step ? tokens - from : step);
         const dim3 grid((unsigned)ceil_div(a.tokens * token_threads, kThreads));
         if (pieces)
-            (bf16 ? rotate_kernel<true> : rotate_kernel<false>)<<<grid, kThreads, 0, stream>>>(a);
+            (rope.interleaved ? (bf16 ? rotate_kernel<true, true> : rotate_kernel<false, true>)
+                              : (bf16 ? rotate_kernel<true, false> : rotate_kernel<false, false>))
+                <<<grid, kThreads, 0, stream>>>(a);
         else
             (bf16 ? rotate_any_kernel<true> : rotate_any_kernel<false>)<<<grid, kThreads, 0, stream>>>(a);
         const hipError_t err = hipGetLastError();
