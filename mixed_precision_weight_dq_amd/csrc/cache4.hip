@@ -235,6 +235,11 @@ __global__ __launch_bounds__(kThreads) void cache4_append_rope_kernel(
     const int head0 = (int)blockIdx.y * per;
     const int head1 = head0 + per < c.heads ? head0 + per : c.heads;
     const int64_t row = t < tokens ? t : tokens - 1;
+    const int d0 = part * 8;
+    // (a head's vectors are asked for a head ahead)
+    const auto load_k = [&](int head) { return load8<BF16>(k, row * k_stride + (int64_t)head * D + d0); };
+    const auto load_v = [&](int head) { return load8<BF16>(v, row * v_stride + (int64_t)head * D + d0); };
+    Raw<BF16> rk = load_k(head0 < head1 ? head0 : 0), rv = load_v(head0 < head1 ? head0 : 0);
     int64_t pos = 0;
     const int64_t slot = find_slot<kParts>(c, bt, t, tokens, &pos);
     if (part == 0) at_position[threadIdx.x / kParts] = positions ? positions[row] : (int32_t)pos;
@@ -250,7 +255,6 @@ __global__ __launch_bounds__(kThreads) void cache4_append_rope_kernel(
     }
     __syncthreads();
     const bool inter = rope.interleaved;
-    const int d0 = part * 8;
     const bool turned = d0 < rope.dims;
     const bool upper = !inter && d0 >= pairs;   // the second of a pair
     const int shift = pairs / 8;                // threads to the partner
@@ -266,8 +270,8 @@ __global__ __launch_bounds__(kThreads) void cache4_append_rope_kernel(
     const int group_shift = 31 - __builtin_clz(c.group);
     const int group_threads = c.group >> 3;
     for (int head = head0; head < head1; ++head) {
-        const int64_t at = (int64_t)head * D + d0;
-        const Raw<BF16> rk = load8<BF16>(k, row * k_stride + at), rv = load8<BF16>(v, row * v_stride + at);
+        const int ahead = head + 1 < head1 ? head + 1 : head;
+        const Raw<BF16> next_k = load_k(ahead), next_v = load_v(ahead);
         Raw<BF16> other = rk;
         if (!inter) {
 #pragma unroll
@@ -290,6 +294,8 @@ __global__ __launch_bounds__(kThreads) void cache4_append_rope_kernel(
         const uint32_t wk = quantize8(z, group_threads, &sk);
         const uint32_t wv = quantize8<BF16>(rv, group_threads, &sv);
         const uint32_t w = turn_values<D>(wv, part, turn + (threadIdx.x - part));
+        rk = next_k;
+        rv = next_v;
         if (slot < 0) continue;
         const Place p = place_of<D>(c, slot, head, group_shift);
         c.k_codes[p.row + (part & 3) * (D / 32) + (part >> 2)] = wk;
@@ -303,9 +309,10 @@ __global__ __launch_bounds__(kThreads) void cache4_append_rope_kernel(
 }
 
 // Moves the entries of accepted tokens to the front of a call's tokens: row path[j] of
-// a sequence's new ones goes to row j.  A thread has 16 bytes of the codes or a scale
-// of one head, in every token, so it reads what it overwrites itself: no barrier, and
-// with path[j] >= j no source is overwritten before it is read.
+// a sequence's new ones goes to row j.  A workgroup has one kv head of a sequence; a thread
+// 16 bytes of the codes or a scale of one token, as many tokens side by side as fit.  All
+// of them are read before any is written, and with path[j] >= j what is written is never a
+// later one's source.  Bound by the chain of loads to a token's place and its data.
 template <int D>
 __global__ __launch_bounds__(kThreads) void cache4_keep_kernel(Cache4 c, Cache4Batch bt,
                                                                const int32_t* __restrict__ path,
@@ -313,13 +320,12 @@ __global__ __launch_bounds__(kThreads) void cache4_keep_kernel(Cache4 c, Cache4B
                                                                int64_t tokens)
 {
     constexpr int kPieces = D / 32;  // of a code row
-    constexpr int kDeep = 8;         // tokens in flight
     const int64_t b = blockIdx.y;
+    const int head = blockIdx.x;
     const int groups = D / c.group;
     const int columns = 2 * kPieces + 2 * groups;
-    const int i = (int)blockIdx.x * kThreads + threadIdx.x;
-    const int head = i / columns, column = i - head * columns;
-    if (head >= c.heads) return;
+    const int side = kThreads / columns;  // tokens side by side
+    const int mine = (int)threadIdx.x / columns, column = (int)threadIdx.x - mine * columns;
     int64_t first, n;
     cache4_rows(bt, b, tokens, first, n);
     const int64_t base = (int64_t)bt.lens[b] - n;
@@ -335,33 +341,27 @@ __global__ __launch_bounds__(kThreads) void cache4_keep_kernel(Cache4 c, Cache4B
         const Place p = place_of<D>(c, slot, head, group_shift);
         return code ? p.row + 4 * at : p.scale + ((int64_t)at << c.page_shift);
     };
-    for (int64_t j0 = 0; j0 < count; j0 += kDeep) {
-        int64_t from[kDeep], to[kDeep];
-#pragma unroll
-        for (int e = 0; e < kDeep; ++e) {
-            const int64_t j = j0 + e;
-            const int64_t r = j < count ? path[first + j] : -1;
-            const bool moves = r > j && r < n;
-            from[e] = moves ? cache4_slot(c, bt, b, base + r) : -1;
-            to[e] = moves ? cache4_slot(c, bt, b, base + j) : -1;
-        }
-        uint4 v[kDeep];
-#pragma unroll
-        for (int e = 0; e < kDeep; ++e) {
-            if (from[e] < 0 || to[e] < 0) continue;
+    for (int64_t j0 = 0; j0 < count; j0 += side) {
+        const int64_t j = j0 + mine;
+        const int64_t r = mine < side && j < count ? path[first + j] : -1;
+        const bool moves = r > j && r < n;
+        const int64_t from = moves ? cache4_slot(c, bt, b, base + r) : -1;
+        const int64_t to = moves ? cache4_slot(c, bt, b, base + j) : -1;
+        uint4 v = {0, 0, 0, 0};
+        if (from >= 0 && to >= 0) {
             if (code)
-                v[e] = *reinterpret_cast<const uint4*>(codes + place(from[e]));
+                v = *reinterpret_cast<const uint4*>(codes + place(from));
             else
-                v[e].x = __float_as_uint(scales[place(from[e])]);
+                v.x = __float_as_uint(scales[place(from)]);
         }
-#pragma unroll
-        for (int e = 0; e < kDeep; ++e) {
-            if (from[e] < 0 || to[e] < 0) continue;
+        __syncthreads();
+        if (from >= 0 && to >= 0) {
             if (code)
-                *reinterpret_cast<uint4*>(codes + place(to[e])) = v[e];
+                *reinterpret_cast<uint4*>(codes + place(to)) = v;
             else
-                scales[place(to[e])] = __uint_as_float(v[e].x);
+                scales[place(to)] = __uint_as_float(v.x);
         }
+        __syncthreads();
     }
 }
 
@@ -483,9 +483,7 @@ hipError_t launch_cache4_keep(const Cache4& c, const Cache4Batch& bt, const int3
 {
     const auto kernel = c.dim == 64 ? cache4_keep_kernel<64>
                                     : (c.dim == 128 ? cache4_keep_kernel<128> : cache4_keep_kernel<256>);
-    const int columns = 2 * (c.dim / 32) + 2 * (c.dim / c.group);
-    const dim3 grid((unsigned)ceil_div((int64_t)c.heads * columns, kThreads), (unsigned)bt.count);
-    kernel<<<grid, kThreads, 0, stream>>>(c, bt, path, accepted, tokens);
+    kernel<<<dim3((unsigned)c.heads, (unsigned)bt.count), kThreads, 0, stream>>>(c, bt, path, accepted, tokens);
     return hipGetLastError();
 }
 

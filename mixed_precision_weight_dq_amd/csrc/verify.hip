@@ -23,7 +23,7 @@
 // their parents, so a walk is one pass over a sequence's rows, 64 of them in a wave's
 // lanes.  verify_sums_kernel: every wave walks for itself (no barrier, and the loads of
 // all waves of a sequence are the same) and sums one stretch of kStretch tokens;
-// verify_draw_kernel: a wave per sequence finds the stretch, and the token in it.
+// verify_draw_kernel: a workgroup per sequence finds the stretch, and the token in it.
 #include "common.hpp"
 #include "launch_serving.hpp"
 
@@ -187,20 +187,24 @@ __global__ __launch_bounds__(kThreads) void verify_sums_kernel(VerifyArgs a)
     }
     const int64_t x0 = wave * kStretch;
     const float* p = a.probs + (first + w.cur) * a.probs_stride;
+    // (past the vocabulary: the last token again, which counts as 0)
     float v[kEach];
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) {
+    const auto place = [&](int e) {
         const int64_t x = x0 + e * kWave + lane;
-        v[e] = x < a.vocab ? p[x] : 0.0f;
-    }
+        return x < a.vocab ? x : a.vocab - 1;
+    };
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) v[e] = p[place(e)];
     double sum = 0.0;
     if (kDraft && w.less) {
         const float* q = a.draft + (first + w.cur) * a.draft_stride;
+        float d[kEach];
 #pragma unroll
-        for (int e = 0; e < kEach; ++e) {
-            const int64_t x = x0 + e * kWave + lane;
-            sum += left_of(positive(v[e]), x < a.vocab ? q[x] : 0.0f);
-        }
+        for (int e = 0; e < kEach; ++e) d[e] = q[place(e)];
+        __builtin_amdgcn_sched_barrier(0);  // both rows in flight
+#pragma unroll
+        for (int e = 0; e < kEach; ++e)
+            sum += x0 + e * kWave + lane < a.vocab ? left_of(positive(v[e]), d[e]) : 0.0;
     } else {
         if (!kDraft)
             each_child(a, first, n, w.cur, n, [&](int token) {
@@ -211,121 +215,141 @@ __global__ __launch_bounds__(kThreads) void verify_sums_kernel(VerifyArgs a)
                     if (at == e * kWave + lane) v[e] = 0.0f;
             });
 #pragma unroll
-        for (int e = 0; e < kEach; ++e) sum += positive(v[e]);
+        for (int e = 0; e < kEach; ++e) sum += x0 + e * kWave + lane < a.vocab ? positive(v[e]) : 0.0f;
     }
     sum = wave_sum(sum);
     if (lane == 0) a.sums[b * a.chunks + wave] = sum;
 }
 
-// The first token of stretch c whose running sum passes target, else the last that has
-// any probability, else -1.  A lane has kEach neighbours.
-template <bool kDraft>
-__device__ __forceinline__ int64_t find_token(const VerifyArgs& a, int64_t first, int64_t n, int64_t cur, bool less,
-                                              bool plain, int64_t c, double target)
+__device__ __forceinline__ double wave_scan(double v)
 {
     const int lane = threadIdx.x & (kWave - 1);
-    const int64_t x0 = c * kStretch + lane * kEach;
-    const float* p = a.probs + (first + cur) * a.probs_stride;
-    double v[kEach];
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) v[e] = x0 + e < a.vocab ? positive(p[x0 + e]) : 0.0f;
+    for (int o = 1; o < kWave; o <<= 1) {
+        const double t = __shfl_up(v, o, kWave);
+        if (lane >= o) v += t;
+    }
+    return v;
+}
+
+// The first stretch (of sums that sum_of gives) whose running sum passes u times the whole,
+// or the last with any probability, or -1; before: the running sum before it.  A wave's work.
+template <class F>
+__device__ __forceinline__ int64_t find_stretch(int64_t chunks, float u, F sum_of, double& before, double& target)
+{
+    const int lane = threadIdx.x & (kWave - 1);
+    const double own = lane < chunks ? sum_of(lane) : 0.0;  // of the first 64
+    double total = own;
+    for (int64_t c = kWave + lane; c < chunks; c += kWave) total += sum_of(c);
+    total = wave_sum(total);
+    target = (double)u * total;
+    before = 0.0;
+    int64_t last = -1;
+    for (int64_t c0 = 0; c0 < chunks; c0 += kWave) {
+        const double mine = c0 == 0 ? own : (c0 + lane < chunks ? sum_of(c0 + lane) : 0.0);
+        const double upto = wave_scan(mine);
+        const uint64_t passes = __ballot(mine > 0.0 && before + upto > target), some = __ballot(mine > 0.0);
+        if (passes) {
+            const int l = __builtin_ctzll(passes);
+            before += __shfl(upto - mine, l, kWave);
+            return c0 + l;
+        }
+        if (some) last = c0 + 63 - __builtin_clzll(some);
+        before += __shfl(upto, kWave - 1, kWave);
+    }
+    target = __builtin_huge_val();  // (a random number of 1 or more, a sum that is not finite)
+    return last;
+}
+
+// Four waves per sequence: each finds the stretch for itself, a thread has 8 of its tokens.
+template <bool kDraft>
+__global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a)
+{
+    constexpr int kMine = kStretch / kThreads;
+    __shared__ double wave_total[kThreads / kWave];
+    __shared__ int wave_pass[kThreads / kWave], wave_last[kThreads / kWave];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int64_t b = blockIdx.x;
+    const double* sums = a.sums + b * a.chunks;
+    const int64_t cur = a.state[2 * b];
+    const bool less = a.state[2 * b + 1] != 0;
+    int64_t first, n;
+    rows_of(a.starts, b, a.tokens, first, n);
+    if (n == 0) return;
+    const float u = a.uniforms[first];
+    const float* p = a.probs + (first + cur) * a.probs_stride;
+    double before, target;
+    int64_t c = find_stretch(a.chunks, u, [&](int64_t i) { return sums[i]; }, before, target);
+    // nothing left, as where p and q are the same: of p as it is
+    const bool plain = c < 0;
+    if (plain)
+        c = find_stretch(
+            a.chunks, u,
+            [&](int64_t i) {
+                double sum = 0.0;
+                for (int64_t x = i * kStretch; x < (i + 1) * kStretch && x < a.vocab; ++x) sum += positive(p[x]);
+                return sum;
+            },
+            before, target);
+    if (c < 0) {
+        if (threadIdx.x == 0) a.next[b] = -1;
+        return;
+    }
+    const int64_t x0 = c * kStretch + threadIdx.x * kMine;
+    const auto place = [&](int e) { return x0 + e < a.vocab ? x0 + e : a.vocab - 1; };
+    double v[kMine];
+#pragma unroll
+    for (int e = 0; e < kMine; ++e) v[e] = positive(p[place(e)]);
     if (!plain) {
         if (kDraft && less) {
             const float* q = a.draft + (first + cur) * a.draft_stride;
 #pragma unroll
-            for (int e = 0; e < kEach; ++e)
-                if (x0 + e < a.vocab) v[e] = left_of(v[e], q[x0 + e]);
+            for (int e = 0; e < kMine; ++e) v[e] = left_of(v[e], q[place(e)]);
         } else if (!kDraft) {
             each_child(a, first, n, cur, n, [&](int token) {
-                const int64_t at = token - x0;
-                if (at < 0 || at >= kEach) return;
 #pragma unroll
-                for (int e = 0; e < kEach; ++e)
-                    if (at == e) v[e] = 0.0;
+                for (int e = 0; e < kMine; ++e)
+                    if (token == x0 + e) v[e] = 0.0;
             });
         }
     }
     double mine = 0.0;
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) mine += v[e];
-    double upto = mine;
-#pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-        const double t = __shfl_up(upto, o, kWave);
-        if (lane >= o) upto += t;
+    for (int e = 0; e < kMine; ++e) {
+        if (x0 + e >= a.vocab) v[e] = 0.0;
+        mine += v[e];
     }
-    // the lane's own first token that passes, or its last with any probability
-    int64_t pass = -1, last = -1;
-    double run = upto - mine;
+    const double upto = wave_scan(mine);
+    if (lane == kWave - 1) wave_total[wave] = upto;
+    __syncthreads();
+    double run = before + (upto - mine);
+    for (int w = 0; w < wave; ++w) run += wave_total[w];
+    // the thread's own first token that passes, or its last with any probability
+    int pass = -1, last = -1;
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) {
+    for (int e = 0; e < kMine; ++e) {
         run += v[e];
         if (v[e] > 0.0) {
-            last = x0 + e;
-            if (pass < 0 && run > target) pass = x0 + e;
+            last = (int)(x0 + e);
+            if (pass < 0 && run > target) pass = (int)(x0 + e);
         }
     }
     const uint64_t passes = __ballot(pass >= 0), some = __ballot(last >= 0);
-    if (passes) return __shfl((int)pass, __builtin_ctzll(passes), kWave);
-    return some ? __shfl((int)last, 63 - __builtin_clzll(some), kWave) : -1;
-}
-
-// A wave per sequence.
-template <bool kDraft>
-__global__ __launch_bounds__(kWave) void verify_draw_kernel(VerifyArgs a)
-{
-    const int lane = threadIdx.x;
-    const int64_t b = blockIdx.x;
-    int64_t first, n;
-    rows_of(a.starts, b, a.tokens, first, n);
-    if (n == 0) return;
-    const int64_t cur = a.state[2 * b];
-    const bool less = a.state[2 * b + 1] != 0;
-    const double* sums = a.sums + b * a.chunks;
-    double total = 0.0;
-    for (int64_t c = lane; c < a.chunks; c += kWave) total += sums[c];
-    total = wave_sum(total);
-    // nothing left, as where p and q are the same: of p as it is
-    const bool plain = !(total > 0.0);
-    const auto sum_of = [&](int64_t c) {
-        if (!plain) return c < a.chunks ? sums[c] : 0.0;
-        double s = 0.0;
-        const float* p = a.probs + (first + cur) * a.probs_stride;
-        for (int64_t x = c * kStretch; x < (c + 1) * kStretch && x < a.vocab; ++x) s += positive(p[x]);
-        return s;
-    };
-    if (plain) {
-        total = 0.0;
-        for (int64_t c = lane; c < a.chunks; c += kWave) total += sum_of(c);
-        total = wave_sum(total);
+    if (lane == 0) {
+        wave_pass[wave] = -1;
+        wave_last[wave] = -1;
     }
-    const double target = (double)a.uniforms[first] * total;
-    double before = 0.0;
-    int64_t found = -1, last = -1;
-    for (int64_t c0 = 0; c0 < a.chunks && found < 0; c0 += kWave) {
-        const double mine = c0 + lane < a.chunks ? sum_of(c0 + lane) : 0.0;
-        double upto = mine;
-#pragma unroll
-        for (int o = 1; o < kWave; o <<= 1) {
-            const double t = __shfl_up(upto, o, kWave);
-            if (lane >= o) upto += t;
-        }
-        const uint64_t passes = __ballot(mine > 0.0 && before + upto > target), some = __ballot(mine > 0.0);
-        if (passes) {
-            const int l = __builtin_ctzll(passes);
-            found = c0 + l;
-            before += __shfl(upto - mine, l, kWave);
-        } else {
-            if (some) last = c0 + 63 - __builtin_clzll(some);
-            before += __shfl(upto, kWave - 1, kWave);
-        }
+    if (passes && lane == (int)__builtin_ctzll(passes)) wave_pass[wave] = pass;
+    if (some && lane == 63 - (int)__builtin_clzll(some)) wave_last[wave] = last;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int token = -1;
+        for (int w = kThreads / kWave - 1; w >= 0; --w)
+            if (token < 0) token = wave_last[w];
+        for (int w = kThreads / kWave - 1; w >= 0; --w)
+            if (wave_pass[w] >= 0) token = wave_pass[w];
+        a.next[b] = token;
     }
-    int64_t token = -1;
-    if (found >= 0)
-        token = find_token<kDraft>(a, first, n, cur, less, plain, found, target - before);
-    else if (last >= 0)  // (a random number of 1 or more, a sum that is not finite)
-        token = find_token<kDraft>(a, first, n, cur, less, plain, last, __builtin_huge_val());
-    if (lane == 0) a.next[b] = (int32_t)token;
 }
 
 // Mask and position of every drafted row: the bits of itself and its ancestors, and the cached
@@ -382,7 +406,7 @@ hipError_t launch_verify(VerifyArgs a, void* workspace, hipStream_t stream)
     (a.draft ? verify_sums_kernel<true> : verify_sums_kernel<false>)<<<grid, kThreads, 0, stream>>>(a);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    (a.draft ? verify_draw_kernel<true> : verify_draw_kernel<false>)<<<(unsigned)a.count, kWave, 0, stream>>>(a);
+    (a.draft ? verify_draw_kernel<true> : verify_draw_kernel<false>)<<<(unsigned)a.count, kThreads, 0, stream>>>(a);
     return hipGetLastError();
 }
 
