@@ -15,8 +15,8 @@
 // reverse) 10.0 us, 3.2 TB/s; 32 tokens 4.8 and 3.5 us.  (A workgroup per two tokens, all
 // heads: 15.8 and 11.6 us, for a page's lines are then written two tokens at a
 // time; 32 tokens 4.1 and 3.7.)  About half of the append's time is vector work.
-// The read of heads of 256 picks a word by a lane's bit, for which the compiler keeps
-// the words in 16 KB of LDS; not measured against a select.
+// (The read of heads of 256 takes a code out of 64 bits: a word picked by a lane's bit
+// went through LDS, whose address needs the dispatch packet, some 14 us away in host memory.)
 #include "cache4.hpp"
 #include "common.hpp"
 #include "launch_serving.hpp"
@@ -240,17 +240,20 @@ __global__ __launch_bounds__(kThreads) void cache4_append_rope_kernel(
     const auto load_k = [&](int head) { return load8<BF16>(k, row * k_stride + (int64_t)head * D + d0); };
     const auto load_v = [&](int head) { return load8<BF16>(v, row * v_stride + (int64_t)head * D + d0); };
     Raw<BF16> rk = load_k(head0 < head1 ? head0 : 0), rv = load_v(head0 < head1 ? head0 : 0);
+    // (a thread works out one pair's angles, of every so many tokens)
+    const int pairs = rope.dims / 2, pair = threadIdx.x % kPairs;
+    const double pair_turn = rope.turns[pair < pairs ? pair : 0];
     int64_t pos = 0;
     const int64_t slot = find_slot<kParts>(c, bt, t, tokens, &pos);
     if (part == 0) at_position[threadIdx.x / kParts] = positions ? positions[row] : (int32_t)pos;
     __syncthreads();
-    const int pairs = rope.dims / 2;
-    for (int i = threadIdx.x; i < kTokens * kPairs; i += kThreads) {
-        const int pair = i % kPairs;
+#pragma unroll
+    for (int i = 0; i < kTokens * kPairs / kThreads; ++i) {
+        const int at = i * kThreads + threadIdx.x;
         if (pair < pairs) {
             double s, co;
-            sincospi(2.0 * rope_fraction(rope, at_position[i / kPairs], pair), &s, &co);
-            turns[i] = make_double2(co * rope.factor, s * rope.factor);
+            sincos_turn(turn_fraction(at_position[at / kPairs], pair_turn), s, co);
+            turns[at] = make_double2(co * rope.factor, s * rope.factor);
         }
     }
     __syncthreads();
@@ -313,8 +316,10 @@ __global__ __launch_bounds__(kThreads) void cache4_append_rope_kernel(
 // 16 bytes of the codes or a scale of one token, as many tokens side by side as fit.  All
 // of them are read before any is written, and with path[j] >= j what is written is never a
 // later one's source.  Bound by the chain of loads to a token's place and its data.
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+constexpr int kKeepThreads = 512;
 template <int D>
-__global__ __launch_bounds__(kThreads) void cache4_keep_kernel(Cache4 c, Cache4Batch bt,
+__global__ __launch_bounds__(kKeepThreads) void cache4_keep_kernel(Cache4 c, Cache4Batch bt,
                                                                const int32_t* __restrict__ path,
                                                                const int32_t* __restrict__ accepted,
                                                                int64_t tokens)
@@ -324,7 +329,7 @@ __global__ __launch_bounds__(kThreads) void cache4_keep_kernel(Cache4 c, Cache4B
     const int head = blockIdx.x;
     const int groups = D / c.group;
     const int columns = 2 * kPieces + 2 * groups;
-    const int side = kThreads / columns;  // tokens side by side
+    const int side = kKeepThreads / columns;  // tokens side by side
     const int mine = (int)threadIdx.x / columns, column = (int)threadIdx.x - mine * columns;
     int64_t first, n;
     cache4_rows(bt, b, tokens, first, n);
@@ -347,17 +352,15 @@ __global__ __launch_bounds__(kThreads) void cache4_keep_kernel(Cache4 c, Cache4B
         const bool moves = r > j && r < n;
         const int64_t from = moves ? cache4_slot(c, bt, b, base + r) : -1;
         const int64_t to = moves ? cache4_slot(c, bt, b, base + j) : -1;
-        uint4 v = {0, 0, 0, 0};
-        if (from >= 0 && to >= 0) {
-            if (code)
-                v = *reinterpret_cast<const uint4*>(codes + place(from));
-            else
-                v.x = __float_as_uint(scales[place(from)]);
-        }
+        // (a vector type: the compiler would keep a struct that is set in two ways in LDS)
+        u32x4_t v = {0, 0, 0, 0};
+        if (from >= 0 && to >= 0)
+            v = code ? *reinterpret_cast<const u32x4_t*>(codes + place(from))
+                     : (u32x4_t){__float_as_uint(scales[place(from)]), 0, 0, 0};
         __syncthreads();
         if (from >= 0 && to >= 0) {
             if (code)
-                *reinterpret_cast<uint4*>(codes + place(to)) = v;
+                *reinterpret_cast<u32x4_t*>(codes + place(to)) = v;
             else
                 scales[place(to)] = __uint_as_float(v.x);
         }
@@ -423,7 +426,7 @@ __global__ __launch_bounds__(kThreads) void cache4_read_kernel(Cache4 c, Cache4B
             else if constexpr (D == 128)
                 u = w[e] >> (4 * j);
             else
-                u = (j & 8 ? w[2 * e + 1] : w[2 * e]) >> (4 * (j & 7));
+                u = (uint32_t)(((uint64_t)w[2 * e + 1] << 32 | w[2 * e]) >> (4 * j));
             x[e] = (float)((int32_t)((wk >> (4 * e)) & 15u) - 8) * sk;
             y[e] = (float)((int32_t)(u & 15u) - 8) * sv;
         }
@@ -483,7 +486,7 @@ hipError_t launch_cache4_keep(const Cache4& c, const Cache4Batch& bt, const int3
 {
     const auto kernel = c.dim == 64 ? cache4_keep_kernel<64>
                                     : (c.dim == 128 ? cache4_keep_kernel<128> : cache4_keep_kernel<256>);
-    kernel<<<dim3((unsigned)c.heads, (unsigned)bt.count), kThreads, 0, stream>>>(c, bt, path, accepted, tokens);
+    kernel<<<dim3((unsigned)c.heads, (unsigned)bt.count), kKeepThreads, 0, stream>>>(c, bt, path, accepted, tokens);
     return hipGetLastError();
 }
 

@@ -43,7 +43,7 @@ __device__ __forceinline__ bool rotate_place(const RotateArgs& a, uint32_t& slot
 
 __device__ __forceinline__ void rotate_turn(const Rope& r, int32_t pos, int i, float& c, float& s)
 {
-    sincospif(2.0f * (float)rope_fraction(r, pos, i), &s, &c);
+    sincospif(2.0f * (float)turn_fraction(pos, r.turns[i]), &s, &c);
     c *= (float)r.factor;
     s *= (float)r.factor;
 }
