@@ -192,17 +192,15 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
 {
     using C = Cut<32 * T, kThreads>;
     using R = Ring<D, G>;
-    constexpr int S = D != 256 && T == 1 ? 3 : 2;  // steps of the ring
+    constexpr int S = 2;  // steps of the ring
     constexpr int NC = D / 32;    // 32-dimension steps of a dot product, and tiles of the output
     constexpr int NG = D / G;     // groups of a head
     constexpr int NL = (NG + 1) / 2;               // value scales of a lane
     constexpr int VW = D / 128 > 0 ? D / 128 : 1;  // value words of a lane and position
     constexpr int kPieces = D / 8;                 // of a row of q in LDS
-    constexpr int kCols = T == 1 && D != 256 ? 1 : 2;  // tiles of the output that the waves join at a time
-    constexpr int kJoin = kWaves * kCols * 4096;
-    constexpr int kShared = kJoin > C::kRows * D * 2 ? kJoin : C::kRows * D * 2;
-    // the rows of q, and, at the end of a unit, the waves' results
-    __shared__ __attribute__((aligned(16))) char shared[kShared];
+    constexpr int kCols = D == 64 ? 1 : 2;  // tiles of the output that the waves join at a time (in the ring)
+    static_assert(kWaves * S * R::kBytes >= kWaves * kCols * 4096, "the ring holds them");
+    __shared__ __attribute__((aligned(16))) char shared[C::kRows * D * 2];  // the rows of q
     __shared__ float logits[C::kRows];
     __shared__ __attribute__((aligned(16))) float kpow[kWaves][32];
     __shared__ __attribute__((aligned(16))) float vscale[kWaves][NG][32];  // (masked), or halves: scales, biases
@@ -296,7 +294,19 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
             head = kvh * rw.per + (int)(row - (int64_t)qi * rw.per);
         };
 
-        // the rows of q that the unit's threads have, asked for first: loads come back in order
+        // ---- a step's copies into the ring
+        uint32_t bad_tiles = 0;  // two bits for each step in flight: a tile whose page is outside the cache
+        // Page numbers of 32 of the wave's steps, a tile's in each lane (scalar loads would count with the LDS
+        // operations, and a wait for those would wait for memory in every step).
+        int pages = 0, pages_from = 0;
+        const auto tile_at = [&](int t) { return t < stop ? t : (stop - 1) & ~15; };
+        const auto load_pages = [&](int t0) __attribute__((always_inline)) {
+            pages = table[tile_at(t0 + (lane >> 1) * kStride + (lane & 1) * 16) >> shift];
+            pages_from = t0;
+        };
+        int t0 = begin + wave * kStep;
+        if (t0 < stop) load_pages(t0);
+        // the rows of q that the unit's threads have, asked for before the copies: loads come back in order
         constexpr int kPer = kThreads / C::kRows;  // threads of a row
         constexpr int kMine = kPieces / kPer;      // pieces of a thread
         uint4 qr[kMine];
@@ -308,17 +318,6 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
 #pragma unroll
             for (int i = 0; i < kMine; ++i) qr[i] = reinterpret_cast<const uint4*>(qp)[i];
         }
-
-        // ---- a step's copies into the ring
-        uint32_t bad_tiles = 0;  // two bits for each step in flight: a tile whose page is outside the cache
-        // Page numbers of 32 of the wave's steps, a tile's in each lane (scalar loads would count with the LDS
-        // operations, and a wait for those would wait for memory in every step).
-        int pages = 0, pages_from = 0;
-        const auto tile_at = [&](int t) { return t < stop ? t : (stop - 1) & ~15; };
-        const auto load_pages = [&](int t0) __attribute__((always_inline)) {
-            pages = table[tile_at(t0 + (lane >> 1) * kStride + (lane & 1) * 16) >> shift];
-            pages_from = t0;
-        };
         const auto copy = [&](int t0, char* to, int ahead) __attribute__((always_inline)) {
             if (t0 - pages_from >= 32 * kStride) load_pages(t0);
             const int at = (t0 - pages_from) / kStride * 2;
@@ -349,9 +348,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
             }
         };
         char* const mine = ring[wave][0];
-        int t0 = begin + wave * kStep;
         if (t0 < stop) {
-            load_pages(t0);
             copy(t0, mine, 0);
             if (S > 2 && t0 + kStride < stop) copy(t0 + kStride, mine + R::kBytes, 1);
         }
@@ -590,6 +587,18 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
             // the exponent that leaves the largest at most 65504 2^-15
             int ex = (int)((__float_as_uint(top) + 0x1fffu) >> 23) - 127;
             ex = ex < -104 ? -104 : (ex > 127 ? 127 : ex);
+            // In steps that all rows see whole the 32 positions share the largest, if all are within 2^6 of it
+            // (fp16 then has 11 bits of all of them): one factor of the logits in place of one each.
+            bool each = true;
+            float unit = 1.0f;
+            if (!kMasked) {
+                const int most = (int)__builtin_amdgcn_readfirstlane(half_max((uint32_t)(ex + 104))) - 104;
+                each = __any(ex < most - 6);
+                if (!each) {
+                    ex = most;
+                    unit = pow2(most);
+                }
+            }
             const float down = pow2(15 - ex);
             kpow[wave][r32] = pow2(ex);
             f16x2_t ks[NG], kh[NG], kb[NG];
@@ -652,9 +661,6 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
                     pin(s[n]);
                 }
             }
-            f32x4_t kf[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) kf[i] = *reinterpret_cast<const f32x4_t*>(&kpow[wave][8 * i + 4 * h]);
             __builtin_amdgcn_sched_barrier(0);
             read_words(here);  // (their latency runs beside the matrix instructions')
 
@@ -664,15 +670,22 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
 #pragma unroll
             for (int n = 0; n < T; ++n) {
                 float mx = -INFINITY;
+                if (each) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const f32x4_t kf = *reinterpret_cast<const f32x4_t*>(&kpow[wave][8 * i + 4 * h]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[n][4 * i + e] *= kf[e];
+                    }
+                }
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    s[n][e] *= kf[e >> 2][e & 3];
                     if (kMasked && !(vis[n] >> (8 * (e >> 2) + 4 * h + (e & 3)) & 1)) s[n][e] = -INFINITY;
                     mx = fmaxf(mx, s[n][e]);
                 }
                 float y0, y1;
                 row_pair(mx, true, y0, y1);
-                mx = fmaxf(y0, y1) * logit[n];
+                mx = fmaxf(y0, y1) * (logit[n] * unit);
                 float alpha = 1.0f;
                 if (__any(mx > m[n] + 8.0f)) {
                     const float mn = mx > m[n] + 8.0f ? mx : m[n];
@@ -687,22 +700,26 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
                 // weights up to 2^14: fp16's normal range then reaches 2^-20 of the largest
                 // (masked steps, whose weights meet fp32 scales first, 2^-14 of that)
                 const float base = m[n] == -INFINITY ? 0.0f : m[n] - (kMasked ? -8.0f : 6.0f);
-                float sum = 0.0f;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    s[n][e] = __builtin_amdgcn_exp2f(fmaf(s[n][e], logit[n], -base));
-                    sum += s[n][e];
-                }
+                for (int e = 0; e < 16; ++e) s[n][e] = __builtin_amdgcn_exp2f(fmaf(s[n][e], logit[n] * unit, -base));
                 if constexpr (kMasked) {
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) sum += s[n][e];
                     row_pair(sum, true, y0, y1);
                     const float old = l[n] * alpha;
                     l[n] = fmaf(y0 + y1, 0x1p14f, old);
                     inv[n] = l[n] > 0.0f ? 1.0f / l[n] : l[n];  // (0 and NaN stay)
                     carry[n] = l[n] == 0.0f ? 1.0f : old * inv[n];
                 } else {
-                    l[n] += sum;
+                    // (the sum of the weights as they are rounded, two at a time)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) p[n][e >> 3][e & 7] = (_Float16)s[n][e];
+                    for (int e = 0; e < 16; e += 2) {
+                        const f16x2_t w = {(_Float16)s[n][e], (_Float16)s[n][e + 1]};
+                        l[n] = __builtin_amdgcn_fdot2(w, (f16x2_t){(_Float16)1.0f, (_Float16)1.0f}, l[n], false);
+                        p[n][e >> 3][e & 7] = w.x;
+                        p[n][e >> 3][(e & 7) + 1] = w.y;
+                    }
                 }
             }
             // O^T = V^T P^T
@@ -810,12 +827,12 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
 
         // Join the waves, kCols tiles of the output at a time: each wave takes the rows of four dimensions in
         // 16 from all of them.
-        f32x4_t* const join = reinterpret_cast<f32x4_t*>(shared);
+        f32x4_t* const join = reinterpret_cast<f32x4_t*>(ring[0][0]);
         if (h == 0) {
 #pragma unroll
             for (int n = 0; n < T; ++n) sums[wave][n][r32] = make_float2(m[n], l[n]);
         }
-        lds_barrier();  // q is read no more
+        lds_barrier();  // q and the ring are read no more
 #pragma unroll
         for (int n = 0; n < T; ++n) {
             float top = -INFINITY, tot = 0.0f, f[kWaves];
@@ -870,33 +887,42 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
     }
 }
 
-constexpr int64_t kFill = 512;  // workgroups of a launch: two for each CU
-constexpr int64_t kMaxUnits = 1LL << 23;
-
+// The launch's shape; a step is 128 positions, a stretch what one workgroup takes of the line.
 struct TreePlan {
     int64_t rows, units, groups;
-    int tiles;  // T
-    int step_shift;
+    int tiles;       // T
+    int step_shift;  // 31: a unit is one step, and nothing is joined
     size_t part_bytes, ml_bytes;
 };
+constexpr int64_t kMaxUnits = 1LL << 23;
+constexpr int64_t kWholeSteps = 16;
+constexpr int64_t kLongSteps = 96;
 
 TreePlan plan_of(const Cache4& c, int64_t count, int64_t tokens, int q_heads, int64_t max_q, int64_t max_len)
 {
+    const int64_t fill = c.dim == 256 ? 256 : 512;  // workgroups that run at a time
     TreePlan p{};
     if (max_q > tokens) max_q = tokens;
     if (max_len > 0x7fffffffLL) max_len = 0x7fffffffLL;
     p.rows = max_q * (q_heads / c.heads);
-    p.tiles = c.dim == 256 || p.rows <= 32 ? 1 : 2;
-    const int64_t tiles = ceil_div(p.rows, 32 * p.tiles), heads = count * c.heads;
-    p.units = tiles > kMaxUnits / heads ? kMaxUnits : heads * tiles;
-    if (max_len <= 512 || (p.units >= kFill / 2 && max_len <= 4096)) {
-        p.groups = p.units < 4 * kFill ? p.units : 4 * kFill;
+    const int64_t heads = count * c.heads, steps = ceil_div(max_len, kStride);
+    const auto units_of = [&](int64_t rows) {
+        const int64_t tiles = ceil_div(p.rows, rows);
+        return tiles > kMaxUnits / heads ? kMaxUnits : heads * tiles;
+    };
+    p.tiles = c.dim != 256 && p.rows > 32 && steps >= kLongSteps && units_of(64) * steps >= 16 * fill ? 2 : 1;
+    p.units = units_of(32 * p.tiles);
+    const int64_t total = p.units * steps;  // (below 2^48)
+    const bool whole = p.units > fill ? steps <= kWholeSteps
+                                      : steps <= 4 || (4 * p.units >= fill && steps - total / fill <= kWholeSteps);
+    if (whole) {
+        p.groups = p.units < 4 * fill ? p.units : 4 * fill;
         p.step_shift = 31;
         return p;
     }
     p.step_shift = 7;
-    p.groups = p.units > kFill ? kFill : p.units * ceil_div(max_len, kStride);
-    if (p.groups > kFill) p.groups = kFill;
+    p.groups = total / 4 < fill ? total / 4 : fill;
+    if (p.groups < 256) p.groups = total < 256 ? total : 256;
     p.part_bytes = (size_t)p.groups * 2 * 32 * p.tiles * c.dim * sizeof(float);
     p.ml_bytes = (size_t)p.groups * 2 * 32 * p.tiles * sizeof(float2);
     return p;
