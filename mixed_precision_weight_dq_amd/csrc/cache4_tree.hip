@@ -576,10 +576,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
                     nan |= !(fabsf(vsl[i]) < INFINITY);
                 }
                 if (__builtin_expect(__any(nan), 0)) mark_nan(vis);
-                if (!kMasked) {
-                    if (__any(zero)) drop_zero_values(here);
-                    raise();
-                }
+                if (__builtin_expect(__any(zero), 0)) drop_zero_values(here);
+                if (!kMasked) raise();
             }
             float top = 0.0f;
 #pragma unroll

@@ -325,6 +325,30 @@ def test_verify_odd_inputs(draft):
     check_verify(one, q, ids, parents, starts, u, draft)
 
 
+@pytest.mark.parametrize("draft", [False, True])
+def test_verify_many_stretches(draft):
+    """A vocabulary of more stretches than a wave has lanes, the drawn token in the first, the last and between."""
+    V = 2048 * 66 + 5
+    probs, q, ids, parents, starts, u = drafts(3, [3, 2, 2, 1], V, not draft)
+    u[starts[:-1]] = [0.0, 0.999999, 0.97, 0.5]
+    last = check_verify(probs, q, ids, parents, starts, u, draft)[2]
+    assert last[1] > 2048 * 60
+
+
+def test_verify_rows_far_apart():
+    """Rows 2^29 elements apart: offsets past 32 bits."""
+    t = torch()
+    probs, q, ids, parents, starts, u = drafts(3, [5, 4], 777, True)
+    far = t.empty((8 << 29) + 777, device="cuda")
+    rows = far.as_strided((9, 777), (1 << 29, 1))
+    rows.copy_(gpu(probs))
+    for draft in (None, gpu(q)):
+        got = dq.verify_drafts(rows, ints(ids), ints(parents), ints(starts), gpu(u), draft_probs=draft)
+        want = verify_ref(probs, ids, parents, starts, u, None if draft is None else q)
+        for a, b in zip(got, want):
+            assert np.array_equal(a.cpu().numpy(), b)
+
+
 def test_verify_not_finite_ends():
     """Probabilities that are not finite give some token or none, and touch nothing else."""
     probs, q, ids, parents, starts, u = drafts(3, [6, 3], 5000, True)

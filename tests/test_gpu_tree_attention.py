@@ -260,6 +260,7 @@ def test_a_whole_step():
     """Rotated queries and keys, the tree's attention, verification and kept entries, together; then the next
     token's attention over the kept cache is that over one filled with the accepted tokens alone."""
     t = torch()
+    t.manual_seed(5)
     g, contexts, batch, parents = step_inputs()
     H, per, D, V = 2, 4, 128, 500
     rope = dq.Rope(D)
@@ -367,3 +368,88 @@ def test_streams_and_graphs():
         t.cuda.synchronize()
         for a, b in zip(eager, want):
             assert t.equal(a, b)
+
+
+@pytest.mark.parametrize("D,g", GEOMETRY)
+@pytest.mark.parametrize("hints", [dict(max_q=64, max_len=200000), dict(max_q=8, max_len=300), dict(max_q=20, max_len=4000)])
+def test_every_shape_of_the_launch(D, g, hints):
+    """Tiles of 64 rows, whole units and stretches (what the hints ask for), on lengths that are none of those:
+    several tiles, several masked steps of a wave, units that end inside a stretch."""
+    batch = Batch(3, [700, 333, 150], [290, 21, 150], 32)
+    cache, kv = filled(11, batch, 2, D, g)
+    sees = masks(np.random.default_rng(6), batch, "any")
+    report("tree attention D=%d g=%d %s" % (D, g, hints))
+    check(*attend(cache, kv, batch, 2, 3, sees, seed=5, **hints))
+
+
+def test_repeated_calls_give_the_same_bits():
+    batch = Batch(3, [5000, 900], [30, 12], 64)
+    cache, _ = filled(11, batch, 4, 128, 32)
+    sees = masks(np.random.default_rng(6), batch, "tree")
+    mask = gpu(np.concatenate([mask_words(s, 1) for s in sees]))
+    q = torch().randn(batch.tokens, 16, 128, device="cuda").bfloat16()
+    call = lambda: dq.cache4_tree_attention(cache, q, *meta(batch), mask, max_q=30, max_len=5000)
+    first = call()
+    for _ in range(5):
+        assert torch().equal(call(), first)
+
+
+@pytest.mark.parametrize("D,g", [(64, 64), (128, 32), (256, 128)])
+@pytest.mark.parametrize("f", [1e-5, 1e-9, 1e-25])
+def test_a_row_keeps_its_bits_beside_larger_drafts(D, g, f):
+    """Drafts (and their zero groups) far larger than what other rows see: the bound is relative to what a row
+    sees.  Context far smaller than the drafts, none at all, and drafts apart from each other."""
+    from serving_ranges import with_zeros
+    for lens, news in (([90, 40], [60, 40]), ([300, 33], [20, 2])):
+        batch = Batch(7, lens, news, 16)
+        H, n = 2, sum(lens)
+        cache = dq.Cache4.empty(batch.pages, H, D, 16, g)
+        full = gpu(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32))
+        x = head_vectors(3, n, 2 * H, D)
+        at = 0
+        for length, new in zip(lens, news):
+            x[at:at + length] *= f
+            x[at + length - new:at + length:3] /= f
+            x[at:at + length] = with_zeros(x[at:at + length], length, g)
+            at += length
+        dq.cache4_append(cache, gpu(x[:, :H]), gpu(x[:, H:]), full, gpu(batch.lens), gpu(batch.table))
+        k, v = dq.cache4_read(cache, n, full, gpu(batch.lens), gpu(batch.table))
+        cuts = np.cumsum(lens)[:-1]
+        kv = list(zip(np.split(k.double().cpu().numpy(), cuts), np.split(v.double().cpu().numpy(), cuts)))
+        sees = []
+        for new in news:  # rows see their own kind of drafts: the larger or the smaller ones
+            i = np.arange(new)
+            sees.append((i[:, None] % 3 == 0) == (i[None] % 3 == 0))
+            sees[-1] &= i[None] <= i[:, None]
+        report("tree attention, larger drafts D=%d f=%g %s" % (D, f, lens))
+        check(*attend(cache, kv, batch, H, 3, sees))
+
+
+def test_pages_past_4_gib():
+    """Codes, scales and kept entries at offsets past 32 bits."""
+    t = torch()
+    pages, H, D, P, g = 150000, 8, 128, 64, 32
+    codes = lambda: t.empty(pages, H, P, D // 8, dtype=t.int32, device="cuda")
+    scales = lambda: t.empty(pages, H, D // g, P, device="cuda")
+    big = dq.Cache4(codes(), codes(), scales(), scales())
+    batch = Batch(3, [300, 70], [30, 9], P)
+    small = dq.Cache4.empty(batch.pages, H, D, P, g)
+    move = pages - 1 - batch.table  # the same pages from the far end
+    rope = dq.Rope(D)
+    T = int(batch.lens.sum())
+    full = gpu(np.concatenate([[0], np.cumsum(batch.lens)]).astype(np.int32))
+    x = t.randn(T, 2 * H, D, device="cuda").bfloat16()
+    starts, lens, table = meta(batch)
+    far = gpu(move.astype(np.int32))
+    q = t.randn(batch.tokens, 4 * H, D, device="cuda").bfloat16()
+    sees = masks(np.random.default_rng(6), batch, "tree")
+    mask = gpu(np.concatenate([mask_words(s, 1) for s in sees]))
+    path = gpu(np.array([0, 3, 5, 7] + [-1] * 26 + [0, 8] + [-1] * 7, np.int32))
+    outs = []
+    for cache, tab in ((small, table), (big, far)):
+        dq.cache4_append(cache, x[:, :H], x[:, H:], full, lens, tab, rope=rope)
+        out = dq.cache4_tree_attention(cache, q, starts, lens, tab, mask)
+        dq.cache4_keep(cache, starts, lens, tab, path, gpu(np.array([4, 2], np.int32)))
+        outs.append((out, *dq.cache4_read(cache, T, full, lens, tab)))
+    for a, b in zip(*outs):
+        assert t.equal(a, b)
