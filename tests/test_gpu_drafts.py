@@ -291,6 +291,16 @@ def test_verify(V, draft):
 
 
 @pytest.mark.parametrize("draft", [False, True])
+@pytest.mark.parametrize("V", [255, 256, 257, 1023, 1024, 1025, 1281])
+def test_verify_ends_of_stretches(V, draft):
+    """The last ids of a stretch, of a wave's and of a thread's part of it: drawn with random numbers near 1."""
+    for seed in range(3):
+        probs, q, ids, parents, starts, u = drafts(100 * seed + V, [1, 3, 4, 1, 2], V, True)
+        u[starts[:-1]] = [1 - 2.0 ** -24, 0.9999, 0.75, 0.25, 0.0]
+        check_verify(probs, q, ids, parents, starts, u, draft)
+
+
+@pytest.mark.parametrize("draft", [False, True])
 def test_verify_everything_taken_or_refused(draft):
     probs, q, ids, parents, starts, u = drafts(7, [40, 70, 6], 300, True)
     assert list(check_verify(probs, probs if draft else q, ids, parents, starts, u * 0, draft)[1]) == [40, 70, 6]
