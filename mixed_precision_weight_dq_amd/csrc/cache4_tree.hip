@@ -10,7 +10,19 @@
 // softmax of its own; they meet only at the end of a unit.  Both products run on
 // v_mfma_f32_32x32x16_f16 in transposed form, S^T = K Q^T and O^T = V^T P^T: lane & 31 is a
 // row throughout, and S^T comes out in the lane and order in which P^T goes in.  Rows of q
-// lie in LDS as operands (registers for them would halve the waves of a SIMD).
+// lie in LDS as operands (registers for them would halve the waves of a SIMD).  Codes and scales
+// come by buffer loads straight into a wave's ring of two steps in LDS: no register holds
+// a load in flight (registers instead of the ring: 245 us for the first case below, the ring 146).
+//
+// Bound by vector work and matrix work in turn.  A step of 32 positions and 32 rows of 128 is 16
+// matrix instructions (512 cycles) and, counted over a call, 380 vector ones (T = 2: 238), of
+// which 181 expand codes and 100 are the softmax: 151 k cycles of vector and 47 k of matrix
+// instructions in the 218 k that a wave lives (second case below), so two waves hardly overlap; a third
+// (168 registers, 3 x 52 KB of LDS) changed nothing.  T = 2 of heads of 128 spills 48 to 58 registers
+// outside the loop, T = 4 312.  With 8 kv heads of 128, g = 32: 64 tokens of 32 heads over 65000
+// positions 126 us and their join 10 (68 GFLOP, 0.51 PFLOP/s), 24 sequences of 24 tokens of 40 heads
+// over up to 6000 116 us and 7 (42 GFLOP, 0.34 PFLOP/s; 1.2 TB/s of cache), 8 of 6 tokens over 1100
+// (16 / 4 heads of 64) 8.3 us and 5.
 //
 // Expansion.  A code u in bits 0..3 (or 4..7) of a half is the fp16 subnormal u 2^-24 (u
 // 2^-20), so (u - 8) * scale is one packed fma, u 2^-24 * S - 8 2^-24 * S, with S the scale
@@ -18,8 +30,9 @@
 // the result.
 //   * Keys: the power of two is each position's own, by the largest of its groups (not
 //     those whose codes are all 0: their stored scale says nothing), and comes back as a
-//     factor of the position's logits.  An element of a much smaller group is off by up to
-//     2^-24, 2^-17 of the position's largest.
+//     factor of the position's logits; where the exponents of 32 positions lie within 2^6 they
+//     share the largest.  An element below fp16's normal range is off by up to 2^-25, where
+//     the largest of the position (of the 32) is 7 2^-9 or more: by 2^-18 of that.
 //   * Values: the power of two is a group's, common to the positions that all rows see, and
 //     follows the largest scale so far.  An element far below it is off by 2^-20 of that.
 // Steps of 32 positions that touch the call's own tokens (the last ones) are different:
@@ -585,8 +598,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
             // the exponent that leaves the largest at most 65504 2^-15
             int ex = (int)((__float_as_uint(top) + 0x1fffu) >> 23) - 127;
             ex = ex < -104 ? -104 : (ex > 127 ? 127 : ex);
-            // In steps that all rows see whole the 32 positions share the largest, if all are within 2^6 of it
-            // (fp16 then has 11 bits of all of them): one factor of the logits in place of one each.
+            // In steps that all rows see whole the 32 positions share the largest, if all are within 2^6 of it:
+            // one factor of the logits in place of one each.
             bool each = true;
             float unit = 1.0f;
             if (!kMasked) {
@@ -899,12 +912,28 @@ struct TreePlan {
     size_t part_bytes, ml_bytes;
 };
 constexpr int64_t kMaxUnits = 1LL << 23;
+// The choices, in us, 32 query / 8 kv heads of 128, g = 32, sequences x tokens over positions:
+//
+// Two tiles of rows a wave where units are long: T = 2 reads and expands a position once for 64 rows, but
+// has the longer way into a unit and out of it (14 us against 8).
+//     T = 1, T = 2:  8 x 32 over 16000 94, 107;  4 x 64 over 16000 102, 105;  1 x 64 over 16000 57, 64;
+//                    4 x 64 over 24000 141, 138;  8 x 32 over 24000 142, 153;  4 x 64 over 32000 191, 182;
+//                    16 x 16 over 32000 225, 189;  1 x 64 over 65000 144, 132
+// so from 192 steps (24576 positions) on, given 16 steps for each of the CUs' workgroups.
+constexpr int64_t kLongSteps = 192;
+// Units that are cut into stretches need a second launch, and memory for the parts; whole ones leave CUs idle
+// at the end.
+//     whole, 512 stretches:  16 x 16 over 1000 20, 46;  64 x 8 over 1500 35, 52;  4 x 32 over 2000 30, 35;
+//                            1 x 64 over 2000 29, 26 (256: 23);  8 x 64 over 3000 59, 55;
+//                            8 x 8 over 4000 50, 31;  32 x 8 over 4000 56, 67;  32 x 8 over 8000 101, 92;
+//                            12 x 60 over 2500 (40 heads) 90, 71;  24 x 24 over 6000 (40 heads) 145, 125
+// so whole up to 16 steps if there are more units than run at a time, up to 4 always, and between them where a
+// quarter of the workgroups have a unit and stretches would save no more than 16 steps.
 constexpr int64_t kWholeSteps = 16;
-constexpr int64_t kLongSteps = 96;
 
 TreePlan plan_of(const Cache4& c, int64_t count, int64_t tokens, int q_heads, int64_t max_q, int64_t max_len)
 {
-    const int64_t fill = c.dim == 256 ? 256 : 512;  // workgroups that run at a time
+    const int64_t fill = c.dim == 256 ? 256 : 512;  // workgroups that run at a time (registers: 512 a lane, or 256)
     TreePlan p{};
     if (max_q > tokens) max_q = tokens;
     if (max_len > 0x7fffffffLL) max_len = 0x7fffffffLL;
@@ -925,7 +954,7 @@ TreePlan plan_of(const Cache4& c, int64_t count, int64_t tokens, int q_heads, in
         return p;
     }
     p.step_shift = 7;
-    p.groups = total / 4 < fill ? total / 4 : fill;
+    p.groups = total / 4 < fill ? total / 4 : fill;  // (a stretch of fewer than 4 steps is mostly its ends)
     if (p.groups < 256) p.groups = total < 256 ? total : 256;
     p.part_bytes = (size_t)p.groups * 2 * 32 * p.tiles * c.dim * sizeof(float);
     p.ml_bytes = (size_t)p.groups * 2 * 32 * p.tiles * sizeof(float2);
