@@ -2,10 +2,14 @@
 // fp64, their sine and cosine and the products in fp32, one rounding to the
 // tokens' type.
 //
-// rotate_kernel: a thread has 8 pairs of a token (two pieces of 8 elements) and
-// walks some of its heads, so that 8 sines and cosines serve all of them; pieces of
-// neighbouring threads are neighbours in memory.  rotate_any_kernel takes the sizes,
-// strides and addresses that pieces do not fit, one pair at a time.
+// Bound by memory.  rotate_kernel: a thread has 8 pairs of a token (two pieces of 8 elements)
+// and walks some of its heads, so that 8 sines and cosines serve all of them; pieces of
+// neighbouring threads are neighbours in memory.  6000 tokens of 40 heads of 128 in bf16
+// (123 MB in and out) 26.8 us, 4.6 TB/s; half of each head, interleaved 30.4 us; 3000 in fp32 36 us.
+//
+// rotate_any_kernel has one pair at a time: for the sizes, strides and addresses that pieces
+// do not fit (there it takes 51 and 59 us for the first two), and for small calls, where eight
+// sines one after another are the longest wait: 1 x 32 heads of 128 2.5 us (pieces 3.0).
 #include "common.hpp"
 #include "launch_serving.hpp"
 
@@ -96,10 +100,9 @@ struct Piece {
     }
 };
 
-template <bool BF16, bool kInter>
+template <bool BF16, bool kInter, int kDeep>  // kDeep: heads whose pieces are in flight
 __global__ __launch_bounds__(kThreads) void rotate_kernel(RotateArgs a)
 {
-    constexpr int kDeep = 4;  // heads whose pieces are in flight
     uint32_t slot, lane;
     int64_t token;
     if (!rotate_place(a, slot, lane, token)) return;
@@ -194,6 +197,13 @@ __global__ __launch_bounds__(kThreads) void rotate_any_kernel(RotateArgs a)
     }
 }
 
+template <int kDeep>
+auto pieces_kernel(bool bf16, bool interleaved) -> void (*)(RotateArgs)
+{
+    return interleaved ? (bf16 ? rotate_kernel<true, true, kDeep> : rotate_kernel<false, true, kDeep>)
+                       : (bf16 ? rotate_kernel<true, false, kDeep> : rotate_kernel<false, false, kDeep>);
+}
+
 }  // namespace
 
 hipError_t launch_rotate(const Rope& rope, const void* x, bool bf16, int64_t tokens, int heads, int dim,
@@ -204,11 +214,17 @@ hipError_t launch_rotate(const Rope& rope, const void* x, bool bf16, int64_t tok
     const bool same = x == out && x_token == out_token && x_head == out_head;
     const int rest = same ? 0 : dim - rope.dims;  // copied
     const int64_t unit = bf16 ? 8 : 4;            // elements of 16 bytes
-    const bool pieces = rope.dims % 16 == 0 && dim % 8 == 0 && x_token % unit == 0 && x_head % unit == 0 &&
+    // pieces, pairs: 64 x 32 heads of 128 3.2 us, 2.8; 160 x 32 (328 k threads of pairs) 3.4, 3.3; 200 x 32
+    // (410 k) 3.4, 3.7; 500 x 32 4.2, 4.8; half of a head, 64 x 40 (246 k) 3.2, 3.0, 128 x 40 (492 k) 3.4, 3.8
+    constexpr int64_t kFewThreads = 3 << 17;
+    const bool pieces = tokens * heads * (int64_t)(rope.dims / 2 + rest) > kFewThreads &&
+                        rope.dims % 16 == 0 && dim % 8 == 0 && x_token % unit == 0 && x_head % unit == 0 &&
                         out_token % unit == 0 && out_head % unit == 0 &&
                         ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(out)) & 15) == 0;
     a.slots = pieces ? rope.dims / 16 + ceil_div(rest, 16) : rope.dims / 2 + rest;
-    // heads of a thread: as many as leave kFill threads
+    // Heads of a thread: as many as leave kFill threads (6000 x 40 heads of 128 26.8 us; 2^16 threads 26.5,
+    // 2^20 37.2; 1700 x 36 of 256 13.1; 14.2, 18.4), four of them in flight (one 28.0 us, two 28.9,
+    // eight 26.8 and 40 in fp32 for 36); a thread with one head asks for no more.
     constexpr int64_t kFill = 1 << 18;
     const int64_t most = tokens * heads * (int64_t)a.slots / kFill;
     const int per = (int)(most < 1 ? 1 : (most > 8 ? 8 : most));
@@ -220,8 +236,7 @@ hipError_t launch_rotate(const Rope& rope, const void* x, bool bf16, int64_t tok
         a.tokens = (uint32_t)(tokens - from < step ? tokens - from : step);
         const dim3 grid((unsigned)ceil_div(a.tokens * token_threads, kThreads));
         if (pieces)
-            (rope.interleaved ? (bf16 ? rotate_kernel<true, true> : rotate_kernel<false, true>)
-                              : (bf16 ? rotate_kernel<true, false> : rotate_kernel<false, false>))
+            (per == 1 ? pieces_kernel<1>(bf16, rope.interleaved) : pieces_kernel<4>(bf16, rope.interleaved))
                 <<<grid, kThreads, 0, stream>>>(a);
         else
             (bf16 ? rotate_any_kernel<true> : rotate_any_kernel<false>)<<<grid, kThreads, 0, stream>>>(a);

@@ -72,6 +72,16 @@ def test_rotate(case, kind):
         assert bool((wide[:, :lead] == 7).all()) and bool((wide[:, :, D:] == 7).all())
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("case", [(700, 33, 72, 16, True), (800, 9, 136, 128, False), (1500, 7, 256, 256, True),
+                                  (5000, 9, 80, 64, False), (9000, 33, 64, 64, True), (70000, 1, 24, 16, False),
+                                  (700, 33, 72, 18, True)])
+def test_rotate_many_tokens(case, kind):
+    """Calls that work by pieces of eight dimensions: one head a thread and several, a rest of one piece and of
+    many, both orders of pairs; and one whose pairs are no pieces."""
+    test_rotate(case, kind)
+
+
 def test_rotate_special_values():
     """NaN and infinities stay in their pairs; the unrotated rest keeps its bits."""
     t = torch()
