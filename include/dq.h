@@ -461,7 +461,15 @@ dq_status dq_draft_tree(const int32_t* parents, const int32_t* starts, const int
  * what dq_cache4_attention takes, makes all of a sequence's rows NaN.
  *   mask        device, [tokens, mask_words] int32, 4-byte aligned
  *   mask_words  1 .. DQ_MAX_MASK_WORDS
- * Everything else as there. */
+ * q in fp16 after a power of two, statistics and sums fp32.  Keys, and values before the
+ * first 32 positions with a token of the call's own, are rounded: a scale to 11 bits and its
+ * product with the code again.  Far below the largest they have fewer: a key's element is off
+ * by up to 2^-18 of the largest of its position (where 32 positions' largest lie within 2^6 of
+ * each other, of theirs), a value by 2^-20 of the largest of its group of dimensions so far.
+ * Weights have 11 bits, down to 2^-20 of a row's largest, then to 2^-31 of it.  From the
+ * first 32 positions with a token of the call's own on, values are exact, a weight times a
+ * value's scale is rounded once to 11 bits, and what a row does not see has no part in its
+ * rounding.  A call repeated gives the same bits.  Everything else as there. */
 size_t dq_cache4_tree_attention_workspace(const dq_cache4* cache, int64_t count, int64_t tokens,
                                           int32_t q_heads, int64_t max_q, int64_t max_len);
 dq_status dq_cache4_tree_attention(const dq_cache4* cache, const dq_cache4_batch* batch, const uint16_t* q,

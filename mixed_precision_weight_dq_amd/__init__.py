@@ -1358,8 +1358,8 @@ def verify_drafts(probs, ids, parents, starts, uniforms, draft_probs=None, works
     Without draft_probs a row's children are candidates of any origin, tried in order; with them
     (float32 [tokens, vocab]) a row's first child, drawn from its draft_probs, is tried alone.  The tokens
     that come out are distributed as the target's (the rule: ``dq_verify_drafts`` in include/dq.h).
-    path: from starts[b] on, the accepted[b] rows of sequence b, its root first, then -1; next: the token
-    drawn behind the last of them.  workspace: uint8 tensor to use instead of a new one."""
+    path: from starts[b] on, the accepted[b] rows of sequence b, its root first, then -1 (rows of no sequence:
+    any value); next: the token drawn behind the last of them.  workspace: uint8 tensor to use instead of a new one."""
     torch = _torch()
     dev = _gpu_index(probs, "probs")
     _fast_need(ids, "ids", torch.int32, 1, dev)

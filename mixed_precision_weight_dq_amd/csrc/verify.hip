@@ -19,11 +19,14 @@
 // Sums of a vocabulary, and what is compared, are fp64: fp32 sums of 10^5 terms would move
 // the borders between tokens by 10^-6, and some draw in a batch would go the other way.
 //
-// Bound by one row of p (and of q) per sequence.  Children have larger rows than
-// their parents, so a walk is one pass over a sequence's rows, 64 of them in a wave's
-// lanes.  verify_sums_kernel: every wave walks for itself (no barrier, and the loads of
-// all waves of a sequence are the same) and sums one stretch of kStretch tokens;
-// verify_draw_kernel: a workgroup per sequence finds the stretch, and the token in it.
+// Bound by one row of p (and of q) per sequence, and where those are few by the trips to memory that
+// wait for each other (starts, parents and ids, probabilities, the row; the sums, the stretch).
+// Children have larger rows than their parents, so a walk is one pass over a sequence's rows, 64 of
+// them in a wave's lanes.  verify_sums_kernel: every wave walks for itself (no barrier, and the
+// loads of all waves of a sequence are the same) and sums one stretch of kStretch tokens;
+// verify_draw_kernel: a workgroup per sequence finds the stretch, and the token in it.  6 rows of 32000
+// with draft probabilities 4.8 + 3.5 us, 16 trees of 32 rows of 50001 5.7 + 4.7, 48 x 7 of 128000 with draft
+// probabilities (49 MB) 12 + 5, the sums at 4.0 TB/s.
 #include "common.hpp"
 #include "launch_serving.hpp"
 
@@ -32,7 +35,8 @@ namespace dq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kStretch = 1024;  // tokens of a stretch: 48 rows of 128000 16.7 us, of 32000 7.6 (2048: 18.4, 9.2; 512: 18.2, 7.1)
+// Tokens of a stretch: 1 x 6 x 32000 7.6 us, 48 x 7 x 128000 16.7 (2048: 9.2, 18.4; 512: 7.1, 18.2).
+constexpr int kStretch = 1024;
 constexpr int kEach = kStretch / kWave;
 
 // Rows of sequence b, within the call's.
@@ -261,7 +265,7 @@ __device__ __forceinline__ int64_t find_stretch(int64_t chunks, float u, F sum_o
     return last;
 }
 
-// Four waves per sequence: each finds the stretch for itself, a thread has 8 of its tokens.
+// Four waves per sequence: each finds the stretch for itself, a thread has 4 of its tokens.
 template <bool kDraft>
 __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a)
 {
@@ -352,7 +356,7 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a)
     }
 }
 
-// Mask and position of every drafted row: the bits of itself and its ancestors, and the cached
+// Mask and position of every drafted row, a thread each (latency: a tree's depth of parents): the bits of itself and its ancestors, and the cached
 // tokens before the call's own plus its depth.  A row that is no tree's (its parent is neither -1
 // nor an earlier row) is a root.
 __global__ __launch_bounds__(kThreads) void draft_tree_kernel(const int32_t* __restrict__ parents,
