@@ -440,6 +440,8 @@ dq_status dq_cache4_append_rope(const dq_cache4* cache, const dq_cache4_batch* b
 /* Drafted tokens.  A sequence's rows of a call are a tree: parents[t] is the row, counted
  * within the sequence, of token t's parent, an earlier one; -1 (any other value) is a
  * root.  Its root, row 0, is the last token known, the others are drafted behind it.
+ * A sequence's rows from DQ_MAX_DRAFTS on are roots whatever parents says: no path
+ * reaches them.
  *
  * dq_draft_tree: what the attention and the rotation of such a tree need.
  *   mask       out  device, [tokens, words] int32: bit j % 32 of word j / 32 says that the row
@@ -449,6 +451,7 @@ dq_status dq_cache4_append_rope(const dq_cache4* cache, const dq_cache4_batch* b
  *                   plus the row's depth
  *   words           1 .. DQ_MAX_MASK_WORDS
  * Rows of no sequence are left as they were. */
+#define DQ_MAX_DRAFTS 4096
 #define DQ_MAX_MASK_WORDS 65536
 dq_status dq_draft_tree(const int32_t* parents, const int32_t* starts, const int32_t* lens, int64_t count,
                         int64_t tokens, int64_t words, int32_t* mask, int32_t* positions, void* stream);

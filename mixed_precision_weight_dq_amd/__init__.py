@@ -1264,7 +1264,7 @@ def cache4_attention(cache: Cache4, q, starts, lens, table, scale=None, max_q=No
 def draft_tree(parents, starts, lens=None, words=None):
     """What a tree of drafted tokens needs: (mask int32 [tokens, words], positions int32 [tokens]).
     parents int32 [tokens]: each token's parent, counted within its sequence's rows (starts int32
-    [count + 1]), an earlier row, -1 for a root.  Bit j % 32 of mask word j / 32 says that the token
+    [count + 1]), an earlier row, -1 for a root (as a sequence's rows from 4096 on are).  Bit j % 32 of mask word j / 32 says that the token
     sees its sequence's row j: itself or an ancestor.  words: the most rows of a sequence / 32,
     rounded up (default: enough for any sequence, tokens / 32).  positions: with ``lens`` (cached tokens, the rows
     included), where to rotate each: the context's length plus the row's depth; else None.  Rows of no

@@ -112,6 +112,8 @@ bool valid_rows(int64_t token, int64_t head, int32_t heads, int32_t dim)
     return head >= dim && head <= (1LL << 32) && token <= (1LL << 32) && token >= (heads - 1) * head + dim;
 }
 
+static_assert(dq::kMaxDrafts == DQ_MAX_DRAFTS);
+
 bool valid_batch(int64_t count, int64_t tokens)
 {
     return count >= 1 && count <= DQ_CACHE4_MAX_COUNT && tokens >= 1 && tokens <= 0x7fffffffLL;

@@ -53,6 +53,11 @@ hipError_t launch_rotate(const Rope& rope, const void* x, bool bf16, int64_t tok
                          int64_t x_token, int64_t x_head, const int32_t* positions, void* out,
                          int64_t out_token, int64_t out_head, hipStream_t stream);
 
+// Rows of a sequence that its tree can have.  Looking for ids that came before takes a pass over the rows
+// for each candidate, some 60 ms where all of these are one row's children: without a limit a call could
+// run for minutes.
+constexpr int64_t kMaxDrafts = 4096;
+
 struct VerifyArgs {
     const float* probs;  // [tokens, vocab], rows probs_stride apart
     int64_t probs_stride;

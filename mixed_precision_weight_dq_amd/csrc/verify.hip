@@ -79,12 +79,13 @@ __device__ __forceinline__ uint64_t children(const Lanes& r, int64_t cur)
     return __ballot(i > cur && r.parent == cur);
 }
 
-// f(token) of every child of cur (all were tried).
+// f(token) of every child of cur before row end (all were tried).
 template <class F>
-__device__ __forceinline__ void each_child(const VerifyArgs& a, int64_t first, int64_t n, int64_t cur, int64_t end, F f)
+__device__ __forceinline__ void each_child(const VerifyArgs& a, int64_t first, int64_t cur, int64_t end, F f)
 {
+    if (end > kMaxDrafts) end = kMaxDrafts;
     for (int64_t base = cur & ~(int64_t)(kWave - 1); base < end; base += kWave) {
-        const Lanes r = load_lanes(a, first, end < n ? end : n, base);
+        const Lanes r = load_lanes(a, first, end, base);
         for (uint64_t left = children(r, cur); left; left &= left - 1) f(read_lane(r.token, __builtin_ctzll(left)));
     }
 }
@@ -102,9 +103,10 @@ __device__ __forceinline__ Walked walk(const VerifyArgs& a, int64_t b, int64_t f
     Walked w{0, false};
     int64_t at = 1;
     double rest = 1.0;
+    const int64_t drafts = n < kMaxDrafts ? n : kMaxDrafts;
     if (write && lane == 0) a.path[first] = 0;
-    for (int64_t base = 0; base < n && !w.less; base += kWave) {
-        const Lanes r = load_lanes(a, first, n, base);
+    for (int64_t base = 0; base < drafts && !w.less; base += kWave) {
+        const Lanes r = load_lanes(a, first, drafts, base);
         const int64_t i = base + lane;
         // what each row would be tried with
         float u = 0.0f, p = 0.0f, q = 0.0f;
@@ -131,7 +133,7 @@ __device__ __forceinline__ Walked walk(const VerifyArgs& a, int64_t b, int64_t f
                 // a token that was tried before
                 bool again = (children(r, w.cur) & __ballot(r.token == token) & ((1ull << l) - 1)) != 0;
                 if (base > w.cur)
-                    each_child(a, first, n, w.cur, base, [&](int other) { again |= other == token; });
+                    each_child(a, first, w.cur, base, [&](int other) { again |= other == token; });
                 if (again) pl = 0.0;
                 take = ul * rest < pl;
                 rest -= pl;
@@ -211,7 +213,7 @@ __global__ __launch_bounds__(kThreads) void verify_sums_kernel(VerifyArgs a)
             sum += x0 + e * kWave + lane < a.vocab ? left_of(positive(v[e]), d[e]) : 0.0;
     } else {
         if (!kDraft)
-            each_child(a, first, n, w.cur, n, [&](int token) {
+            each_child(a, first, w.cur, n, [&](int token) {
                 const int64_t at = token - x0;
                 if (at < 0 || at >= kStretch) return;
 #pragma unroll
@@ -310,7 +312,7 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a)
 #pragma unroll
             for (int e = 0; e < kMine; ++e) v[e] = left_of(v[e], q[place(e)]);
         } else if (!kDraft) {
-            each_child(a, first, n, cur, n, [&](int token) {
+            each_child(a, first, cur, n, [&](int token) {
 #pragma unroll
                 for (int e = 0; e < kMine; ++e)
                     if (token == x0 + e) v[e] = 0.0;
@@ -357,8 +359,8 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a)
 }
 
 // Mask and position of every drafted row, a thread each (latency: a tree's depth of parents): the bits of itself and its ancestors, and the cached
-// tokens before the call's own plus its depth.  A row that is no tree's (its parent is neither -1
-// nor an earlier row) is a root.
+// tokens before the call's own plus its depth.  A row that is no tree's (its parent is no earlier
+// row, or it lies past kMaxDrafts) is a root.
 __global__ __launch_bounds__(kThreads) void draft_tree_kernel(const int32_t* __restrict__ parents,
                                                               const int32_t* __restrict__ starts,
                                                               const int32_t* __restrict__ lens, int64_t tokens,
@@ -381,7 +383,7 @@ __global__ __launch_bounds__(kThreads) void draft_tree_kernel(const int32_t* __r
                 bits = 0;
             }
             if (to < words) bits |= 1u << (at & 31);
-            const int64_t up = parents[first + at];
+            const int64_t up = at < kMaxDrafts ? parents[first + at] : -1;
             if (up < 0 || up >= at) break;
             at = up;
             ++depth;

@@ -246,6 +246,44 @@ def test_draft_tree():
     assert mask.shape == (T, -(-T // 32))
 
 
+def test_rows_past_the_largest_tree():
+    """A sequence's rows from 4096 on are roots that no path reaches: chains of 4095, 4096 and 4200 rows."""
+    sizes = [4095, 4200, 4096, 3]
+    starts = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    T = int(starts[-1])
+    parents = np.concatenate([np.arange(-1, n - 1) for n in sizes]).astype(np.int32)
+    lens = (np.array(sizes) + 50).astype(np.int32)
+    mask, pos = dq.draft_tree(ints(parents), ints(starts), ints(lens), words=132)
+    mask, pos = mask.cpu().numpy(), pos.cpu().numpy()
+    for b, n in enumerate(sizes):
+        i = np.arange(n)
+        sees = (i[None] <= i[:, None]) & (i[:, None] < 4096) | (i[None] == i[:, None])
+        assert np.array_equal(mask[starts[b]:starts[b + 1]], mask_words(sees, 132))
+        assert np.array_equal(pos[starts[b]:starts[b + 1]], 50 + np.where(i < 4096, i, 0))
+    g = np.random.default_rng(2)
+    probs = softmax(g.standard_normal((T, 9)))
+    ids, u = g.integers(0, 9, T).astype(np.int32), np.zeros(T, np.float32)
+    u[starts[:-1]] = 0.5
+    path, accepted, drawn = (x.cpu().numpy() for x in dq.verify_drafts(gpu(probs), ints(ids), ints(parents),
+                                                                       ints(starts), gpu(u)))
+    assert list(accepted) == [min(n, 4096) for n in sizes]
+    for b, n in enumerate(sizes):
+        i = np.arange(n)
+        assert np.array_equal(path[starts[b]:starts[b + 1]], np.where(i < 4096, i, -1))
+        last = probs[starts[b] + accepted[b] - 1].astype(np.float64)  # its child, if any, is past the tree
+        assert drawn[b] == np.flatnonzero(np.cumsum(last) > 0.5 * last.sum())[0]
+    # children of one row, all refused: each id once, as far as the tree reaches
+    parents[starts[1]:starts[2]] = 0
+    ids[starts[1]:starts[2]] = np.where(np.arange(4200) < 4096, np.arange(4200) % 3, 5)
+    u[starts[1]:starts[2]] = 0.999999
+    probs[starts[1]] = np.float32(1 / 9)
+    _, accepted, drawn = dq.verify_drafts(gpu(probs), ints(ids), ints(parents), ints(starts), gpu(u))
+    assert int(accepted[1]) == 1 and int(drawn[1]) == 8
+    u[starts[1]] = 0.4  # of ids 3 .. 8
+    _, accepted, drawn = dq.verify_drafts(gpu(probs), ints(ids), ints(parents), ints(starts), gpu(u))
+    assert int(accepted[1]) == 1 and int(drawn[1]) == 5
+
+
 # ------------------------------------------------------------------- verify
 
 def softmax(x):
