@@ -4,9 +4,8 @@
 //
 // A tree has 8 to 64 tokens, so a kv head has some 32 to 500 rows (token, query head),
 // between the one tile of 16 that cache4_attention_kernel is made for and the
-// thousands of a prompt.  Here a wave expands the codes of 32 positions in registers, once,
-// for T tiles of 32 rows (T = 1 or 2: 64 rows by 128 dimensions of output are 128
-// registers), and the four waves of a workgroup take neighbouring positions, each with a
+// thousands of a prompt.  Here a wave expands the codes of 32 positions in registers for a
+// tile of 32 rows (32 by 128 of output are 64 registers), and the four waves of a workgroup take neighbouring positions, each with a
 // softmax of its own; they meet only at the end of a unit.  Both products run on
 // v_mfma_f32_32x32x16_f16 in transposed form, S^T = K Q^T and O^T = V^T P^T: lane & 31 is a
 // row throughout, and S^T comes out in the lane and order in which P^T goes in.  Rows of q
@@ -15,14 +14,15 @@
 // a load in flight (registers instead of the ring: 245 us for the first case below, the ring 146).
 //
 // Bound by vector work and matrix work in turn.  A step of 32 positions and 32 rows of 128 is 16
-// matrix instructions (512 cycles) and, counted over a call, 380 vector ones (T = 2: 238), of
-// which 181 expand codes and 100 are the softmax: 151 k cycles of vector and 47 k of matrix
-// instructions in the 218 k that a wave lives (second case below), so two waves hardly overlap; a third
-// (168 registers, 3 x 52 KB of LDS) changed nothing.  T = 2 of heads of 128 spills 48 to 58 registers
-// outside the loop, T = 4 312.  With 8 kv heads of 128, g = 32: 64 tokens of 32 heads over 65000
-// positions 126 us and their join 10 (68 GFLOP, 0.51 PFLOP/s), 24 sequences of 24 tokens of 40 heads
-// over up to 6000 116 us and 7 (42 GFLOP, 0.34 PFLOP/s; 1.2 TB/s of cache), 8 of 6 tokens over 1100
-// (16 / 4 heads of 64) 8.3 us and 5.
+// matrix instructions (512 cycles) and, counted over a call, 380 vector ones, of which 181
+// expand codes and 100 are the softmax: 151 k cycles of vector and 47 k of matrix instructions in
+// the 218 k that a wave lives (second case below), so two waves hardly overlap; a third (168
+// registers, 3 x 52 KB of LDS) changed nothing.  Two tiles of rows a wave, which halve the expansion,
+// spill 56 registers: 132 us for the first case, but wrong results where a workgroup has several
+// units, so they are not built.  With 8 kv heads of 128, g = 32: 64 tokens of 32 heads over 65000
+// positions 144 us with their join (68 GFLOP, 0.47 PFLOP/s), 24 sequences of 24 tokens of 40 heads over
+// up to 6000 116 us and 7 (42 GFLOP, 0.34 PFLOP/s; 1.2 TB/s of cache), 8 of 6 tokens over 1100 (16 / 4
+// heads of 64) 8.3 us and 5.
 //
 // Expansion.  A code u in bits 0..3 (or 4..7) of a half is the fp16 subnormal u 2^-24 (u
 // 2^-20), so (u - 8) * scale is one packed fma, u 2^-24 * S - 8 2^-24 * S, with S the scale
@@ -58,6 +58,8 @@ struct TreeArgs {
     int64_t words;
 };
 
+constexpr int kTiles = 1;  // tiles of 32 rows of a wave
+using TreeCut = Cut<32 * kTiles, kThreads>;
 constexpr uint32_t kTopBits = 0x7fe000u;  // mantissa of 65504, fp16's largest
 
 __device__ __forceinline__ f16x2_t twice(float v)
@@ -200,10 +202,11 @@ __device__ __forceinline__ void read_values(const uint32_t (&v)[4], uint32_t (&w
 #undef READ16
 }
 
-template <int D, int G, int T>
+template <int D, int G>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel(TreeArgs args)
 {
-    using C = Cut<32 * T, kThreads>;
+    constexpr int T = kTiles;
+    using C = TreeCut;
     using R = Ring<D, G>;
     constexpr int S = 2;  // steps of the ring
     constexpr int NC = D / 32;    // 32-dimension steps of a dot product, and tiles of the output
@@ -907,20 +910,12 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void cache4_tree_kernel
 // The launch's shape; a step is 128 positions, a stretch what one workgroup takes of the line.
 struct TreePlan {
     int64_t rows, units, groups;
-    int tiles;       // T
     int step_shift;  // 31: a unit is one step, and nothing is joined
     size_t part_bytes, ml_bytes;
 };
 constexpr int64_t kMaxUnits = 1LL << 23;
 // The choices, in us, 32 query / 8 kv heads of 128, g = 32, sequences x tokens over positions:
 //
-// Two tiles of rows a wave where units are long: T = 2 reads and expands a position once for 64 rows, but
-// has the longer way into a unit and out of it (14 us against 8).
-//     T = 1, T = 2:  8 x 32 over 16000 94, 107;  4 x 64 over 16000 102, 105;  1 x 64 over 16000 57, 64;
-//                    4 x 64 over 24000 141, 138;  8 x 32 over 24000 142, 153;  4 x 64 over 32000 191, 182;
-//                    16 x 16 over 32000 225, 189;  1 x 64 over 65000 144, 132
-// so from 192 steps (24576 positions) on, given 16 steps for each of the CUs' workgroups.
-constexpr int64_t kLongSteps = 192;
 // Units that are cut into stretches need a second launch, and memory for the parts; whole ones leave CUs idle
 // at the end.
 //     whole, 512 stretches:  16 x 16 over 1000 20, 46;  64 x 8 over 1500 35, 52;  4 x 32 over 2000 30, 35;
@@ -939,12 +934,8 @@ TreePlan plan_of(const Cache4& c, int64_t count, int64_t tokens, int q_heads, in
     if (max_len > 0x7fffffffLL) max_len = 0x7fffffffLL;
     p.rows = max_q * (q_heads / c.heads);
     const int64_t heads = count * c.heads, steps = ceil_div(max_len, kStride);
-    const auto units_of = [&](int64_t rows) {
-        const int64_t tiles = ceil_div(p.rows, rows);
-        return tiles > kMaxUnits / heads ? kMaxUnits : heads * tiles;
-    };
-    p.tiles = c.dim != 256 && p.rows > 32 && steps >= kLongSteps && units_of(64) * steps >= 16 * fill ? 2 : 1;
-    p.units = units_of(32 * p.tiles);
+    const int64_t tiles = ceil_div(p.rows, TreeCut::kRows);
+    p.units = tiles > kMaxUnits / heads ? kMaxUnits : heads * tiles;
     const int64_t total = p.units * steps;  // (below 2^48)
     const bool whole = p.units > fill ? steps <= kWholeSteps
                                       : steps <= 4 || (4 * p.units >= fill && steps - total / fill <= kWholeSteps);
@@ -956,34 +947,26 @@ TreePlan plan_of(const Cache4& c, int64_t count, int64_t tokens, int q_heads, in
     p.step_shift = 7;
     p.groups = total / 4 < fill ? total / 4 : fill;  // (a stretch of fewer than 4 steps is mostly its ends)
     if (p.groups < 256) p.groups = total < 256 ? total : 256;
-    p.part_bytes = (size_t)p.groups * 2 * 32 * p.tiles * c.dim * sizeof(float);
-    p.ml_bytes = (size_t)p.groups * 2 * 32 * p.tiles * sizeof(float2);
+    p.part_bytes = (size_t)p.groups * 2 * TreeCut::kRows * c.dim * sizeof(float);
+    p.ml_bytes = (size_t)p.groups * 2 * TreeCut::kRows * sizeof(float2);
     return p;
-}
-
-template <int D, int G, int T>
-hipError_t launch_tiles(const TreeArgs& t, const TreePlan& p, hipStream_t stream)
-{
-    using C = Cut<32 * T, kThreads>;
-    const AttnArgs& a = t.a;
-    cache4_tree_kernel<D, G, T><<<(unsigned)a.groups, kThreads, 0, stream>>>(t);
-    if (a.groups > 1 && a.step_shift < 31) {
-        if (p.units * 2 > a.groups) {
-            cache4_join_edges_kernel<D, C><<<dim3((unsigned)a.groups - 1, 2 * T), kThreads, 0, stream>>>(a);
-        } else {
-            const dim3 grid((unsigned)p.rows, (unsigned)a.c.heads, (unsigned)a.bt.count);
-            cache4_join_kernel<D, C><<<grid, kThreads, 0, stream>>>(a);
-        }
-    }
-    return hipGetLastError();
 }
 
 template <int D, int G>
 hipError_t launch_dg(const TreeArgs& t, const TreePlan& p, hipStream_t stream)
 {
-    if constexpr (D != 256)
-        if (p.tiles == 2) return launch_tiles<D, G, 2>(t, p, stream);
-    return launch_tiles<D, G, 1>(t, p, stream);
+    const AttnArgs& a = t.a;
+    cache4_tree_kernel<D, G><<<(unsigned)a.groups, kThreads, 0, stream>>>(t);
+    if (a.groups > 1 && a.step_shift < 31) {
+        if (p.units * 2 > a.groups) {
+            cache4_join_edges_kernel<D, TreeCut>
+                <<<dim3((unsigned)a.groups - 1, TreeCut::kRows / 16), kThreads, 0, stream>>>(a);
+        } else {
+            const dim3 grid((unsigned)p.rows, (unsigned)a.c.heads, (unsigned)a.bt.count);
+            cache4_join_kernel<D, TreeCut><<<grid, kThreads, 0, stream>>>(a);
+        }
+    }
+    return hipGetLastError();
 }
 
 }  // namespace

@@ -453,3 +453,15 @@ def test_pages_past_4_gib():
         outs.append((out, *dq.cache4_read(cache, T, full, lens, tab)))
     for a, b in zip(*outs):
         assert t.equal(a, b)
+
+
+@pytest.mark.parametrize("D,g", GEOMETRY)
+@pytest.mark.parametrize("kind", ["tree", "any"])
+@pytest.mark.parametrize("H,per,max_len", [(8, 8, 30000), (8, 2, 4000), (2, 3, 30000)])
+def test_several_units_of_a_workgroup(D, g, kind, H, per, max_len):
+    """Stretches that hold several units, whole ones and parts: short sequences under hints of long ones."""
+    batch = Batch(60, [35, 160, 115, 17, 17, 565, 130], [2, 32, 100, 17, 1, 65, 2], 32)
+    cache, kv = filled(160, batch, H, D, g)
+    sees = masks(np.random.default_rng(60), batch, kind)
+    report("tree attention, several units D=%d g=%d %s H=%d per=%d" % (D, g, kind, H, per))
+    check(*attend(cache, kv, batch, H, per, sees, seed=60, words=5, max_q=100, max_len=max_len))
