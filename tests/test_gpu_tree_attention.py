@@ -373,7 +373,7 @@ def test_streams_and_graphs():
 @pytest.mark.parametrize("D,g", GEOMETRY)
 @pytest.mark.parametrize("hints", [dict(max_q=64, max_len=200000), dict(max_q=8, max_len=300), dict(max_q=20, max_len=4000)])
 def test_every_shape_of_the_launch(D, g, hints):
-    """Tiles of 64 rows, whole units and stretches (what the hints ask for), on lengths that are none of those:
+    """Whole units and stretches (what the hints ask for), on lengths that are none of those:
     several tiles, several masked steps of a wave, units that end inside a stretch."""
     batch = Batch(3, [700, 333, 150], [290, 21, 150], 32)
     cache, kv = filled(11, batch, 2, D, g)
